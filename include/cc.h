@@ -537,6 +537,109 @@ cc_status_t cc_int8_ef_workspace_size(const cc_config_t* cfg, int nranks, size_t
 /* count + 4 ceil(count / CC_QUANT_BLOCK): the bytes of one rank's message. */
 cc_status_t cc_int8_message_bytes(size_t count, size_t* bytes);
 
+/* ---- The model's side of the exchanges: what makes the gradient that an
+ * AllReduce sums (embedding), what makes the rows and counts of an MoE
+ * dispatch (routing), and what the experts compute between dispatch and
+ * combine (gated feed-forward block), with the gradients of each.
+ * Common to these calls: dtype is CC_FLOAT32 or CC_BFLOAT16 (CC_ERR_UNSUPPORTED
+ * otherwise); values are computed and summed in float32 and rounded once to
+ * dtype, except where a call says more; cfg.algo must be CC_ALGO_RING,
+ * fuse_depth and grid_sync 0 (CC_ERR_UNSUPPORTED otherwise); blocks_per_cu
+ * caps the embedding kernels and has no effect on the others.  Every buffer
+ * is rank-strided device memory, rows back to back inside a rank; no output
+ * may overlap another buffer of the call.  Workspaces are cfg->workspace, 16-byte
+ * aligned, of the size their *_workspace_size call gives; they hold nothing
+ * between calls, and two calls that may run at the same time need two.  All
+ * results are the same from call to call: no sum depends on the order in
+ * which workgroups run. */
+
+/* Embedding lookup: out[t] = scale * table[ids[t]] for the rank's `tokens`
+ * int32 ids, rows of `width` elements; an id outside [0, vocab) (padding)
+ * gives a zero row.  table.rank_stride_bytes may be 0: one table that all
+ * ranks read. */
+cc_status_t cc_embedding(cc_rankbuf_t table, cc_rankbuf_t ids, cc_rankbuf_t out, size_t vocab, size_t tokens,
+                         size_t width, float scale, cc_dtype_t dtype, int nranks, const cc_config_t* cfg,
+                         cc_stream_t stream);
+
+/* The table's gradient of each rank: dtable[v] = scale * the sum of grad[t]
+ * over the rank's t with ids[t] = v, for every v (all vocab rows are written;
+ * zeros for words the rank does not hold; ids outside [0, vocab) add nothing).
+ * The sums run in the order of t, in pieces of 32 for words that repeat. */
+cc_status_t cc_embedding_grad(cc_rankbuf_t grad, cc_rankbuf_t ids, cc_rankbuf_t dtable, size_t vocab, size_t tokens,
+                              size_t width, float scale, cc_dtype_t dtype, int nranks, const cc_config_t* cfg,
+                              cc_stream_t stream);
+
+/* The same gradient summed over the ranks, on every rank: cc_embedding_grad
+ * and the AllReduce of its result in one call, without the N dense gradients
+ * in memory.  The sum runs in the order of (rank, t) and is rounded once (the
+ * two calls round each rank's gradient too, and fold in the ring's order). */
+cc_status_t cc_all_reduce_embedding_grad(cc_rankbuf_t grad, cc_rankbuf_t ids, cc_rankbuf_t dtable, size_t vocab,
+                                         size_t tokens, size_t width, float scale, cc_dtype_t dtype, int nranks,
+                                         const cc_config_t* cfg, cc_stream_t stream);
+
+/* Workspace of both gradients. */
+cc_status_t cc_embedding_grad_workspace_size(int nranks, size_t vocab, size_t tokens, size_t width, size_t* bytes);
+
+/* Routing of each rank's tokens to nexperts (at most CC_MAX_ROUTE_EXPERTS)
+ * experts.  logits: [tokens][nexperts].  A token's topk (at most 64) experts
+ * are its largest logits, ties to the lowest index, largest first; a logit of
+ * -inf (masked) or NaN is never chosen.
+ *  experts [tokens][topk] int32: the chosen; -1 where none was left.
+ *  weights [tokens][topk] float32: their softmax probabilities over all
+ *    experts, divided by the sum of the chosen ones if `normalize` is 1; 0
+ *    where the expert is -1; NaN in a row that holds a NaN or +inf.
+ *  order [tokens * topk] int32: the assignments t * topk + slot sorted by
+ *    expert, then by themselves: the rank's token-side rows for
+ *    cc_moe_dispatch_padded or cc_all_to_all, row j holding token
+ *    order[j] / topk; then -1 for each empty slot.
+ *  counts [nexperts] int32: rows per expert (the dispatch's counts, once on
+ *    the host). */
+#define CC_MAX_ROUTE_EXPERTS 1024
+cc_status_t cc_moe_route(cc_rankbuf_t logits, cc_rankbuf_t experts, cc_rankbuf_t weights, cc_rankbuf_t order,
+                         cc_rankbuf_t counts, size_t tokens, int nexperts, int topk, int normalize, cc_dtype_t dtype,
+                         int nranks, const cc_config_t* cfg, cc_stream_t stream);
+cc_status_t cc_moe_route_workspace_size(int nranks, size_t tokens, int nexperts, int topk, size_t* bytes);
+
+/* The logits' gradient (dtype) from the weights' gradient (dweights, float32,
+ * laid out as weights) and the experts that cc_moe_route chose; entries of
+ * dweights whose expert is outside [0, nexperts) are not used, and a token's
+ * experts are distinct.  Every element of dlogits is written: 0 for experts
+ * without probability (and with `normalize` for those not chosen), NaN in a
+ * row whose logits hold a NaN or +inf.  Takes no workspace. */
+cc_status_t cc_moe_route_grad(cc_rankbuf_t logits, cc_rankbuf_t experts, cc_rankbuf_t dweights, cc_rankbuf_t dlogits,
+                              size_t tokens, int nexperts, int topk, int normalize, cc_dtype_t dtype, int nranks,
+                              const cc_config_t* cfg, cc_stream_t stream);
+
+/* Gated feed-forward block of the experts, on the expert side of
+ * cc_moe_dispatch_padded: for the kept rows x of every expert
+ *   [g | u] = x w_in^T,  h = act(g) * u,  y = h w_out^T.
+ * counts, nexperts and capacity as in the dispatch (counts host [nranks *
+ * nexperts]); x, y: E * capacity rows of `width` per rank, in the dispatch's
+ * layout.  Rank j's weights, one local expert after the other: w_in
+ * [2 * hidden][width] (gate rows, then up rows), w_out [width][hidden].  pre
+ * (base may be NULL) keeps [g | u], 2 * hidden elements a row in x's layout,
+ * for the gradient.  Rows behind a block's kept ones are neither read nor
+ * written.  h is rounded to dtype between the products.  A dense block is one
+ * expert with capacity rows.  SiLU is g / (1 + exp(-g)), GELU the exact one
+ * (g times the normal distribution function). */
+typedef enum { CC_ACT_SILU = 0, CC_ACT_GELU = 1, CC_ACT_MAX_ENUM = 0x7fffffff } cc_act_t;
+cc_status_t cc_moe_ffn(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t pre, cc_rankbuf_t y,
+                       const size_t* counts, int nexperts, size_t capacity, size_t width, size_t hidden, cc_act_t act,
+                       cc_dtype_t dtype, int nranks, const cc_config_t* cfg, cc_stream_t stream);
+
+/* Its gradients from dy (y's layout), with pre as the forward pass kept it:
+ * dx (x's layout, kept rows only), dw_in and dw_out (the weights' layout,
+ * every element written; zeros for an expert without rows).  The gradients of
+ * g, u and h are rounded to dtype between the products. */
+cc_status_t cc_moe_ffn_grad(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t pre, cc_rankbuf_t dy,
+                            cc_rankbuf_t dx, cc_rankbuf_t dw_in, cc_rankbuf_t dw_out, const size_t* counts,
+                            int nexperts, size_t capacity, size_t width, size_t hidden, cc_act_t act, cc_dtype_t dtype,
+                            int nranks, const cc_config_t* cfg, cc_stream_t stream);
+
+/* Workspace of cc_moe_ffn (grad 0) or cc_moe_ffn_grad (grad 1). */
+cc_status_t cc_moe_ffn_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width, size_t hidden,
+                                      cc_dtype_t dtype, int nranks, int grad, size_t* bytes);
+
 const char* cc_status_string(cc_status_t status);
 const char* cc_last_error(void);
 const char* cc_version(void);

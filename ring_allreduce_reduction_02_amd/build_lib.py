@@ -23,7 +23,9 @@ LIB = os.path.join(HERE, "libcc.so")
 
 SOURCES = [os.path.join(CSRC, f) for f in (
     "cc_kernels.hip", "cc_trees.hip", "cc_steps.hip", "cc_quant.hip", "cc_hier.hip", "cc_copy.hip", "cc_noalloc.hip",
-    "cc_api.cpp", "cc_sched.cpp", "cc_alltoall.cpp", "cc_compress.cpp")]
+    "cc_sort.hip", "cc_embed.hip", "cc_route.hip", "cc_ffn.hip",
+    "cc_api.cpp", "cc_sched.cpp", "cc_alltoall.cpp", "cc_compress.cpp",
+    "cc_model.cpp")]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -119,6 +119,25 @@ EXPORTS = {
     "cc_int8_ef_workspace_size": [ctypes.POINTER(Config), ctypes.c_int, ctypes.c_size_t, ctypes.c_int,
                                   ctypes.POINTER(ctypes.c_size_t)],
     "cc_int8_message_bytes": [ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)],
+    "cc_embedding": [RankBuf] * 3 + [ctypes.c_size_t] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int,
+                                                             ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_embedding_grad": [RankBuf] * 3 + [ctypes.c_size_t] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int,
+                                                                  ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_all_reduce_embedding_grad": [RankBuf] * 3 + [ctypes.c_size_t] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_int,
+                                                                             ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_embedding_grad_workspace_size": [ctypes.c_int, ctypes.c_size_t, ctypes.c_size_t, ctypes.c_size_t,
+                                         ctypes.POINTER(ctypes.c_size_t)],
+    "cc_moe_route": [RankBuf] * 5 + [ctypes.c_size_t] + [ctypes.c_int] * 5 + [ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_moe_route_workspace_size": [ctypes.c_int, ctypes.c_size_t, ctypes.c_int, ctypes.c_int,
+                                    ctypes.POINTER(ctypes.c_size_t)],
+    "cc_moe_route_grad": [RankBuf] * 4 + [ctypes.c_size_t] + [ctypes.c_int] * 5 + [ctypes.POINTER(Config),
+                                                                                  ctypes.c_void_p],
+    "cc_moe_ffn": [RankBuf] * 5 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                  + [ctypes.c_int] * 3 + [ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_moe_ffn_grad": [RankBuf] * 8 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                       + [ctypes.c_int] * 3 + [ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_moe_ffn_workspace_size": [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                                 + [ctypes.c_int] * 3 + [ctypes.POINTER(ctypes.c_size_t)],
     "cc_status_string": [ctypes.c_int],
     "cc_last_error": [],
     "cc_version": [],
@@ -538,6 +557,198 @@ def int8_message_bytes(count: int) -> int:
     out = ctypes.c_size_t(0)
     _check(load().cc_int8_message_bytes(count, ctypes.byref(out)))
     return out.value
+
+
+# ---- the model's side of the exchanges: embedding, routing, expert feed-forward
+
+ACTS = {"silu": 0, "gelu": 1}
+
+
+def _operand(t, name: str, n: int, length: int, dtype=None) -> RankBuf:
+    """A rank-strided operand [n, length] on the current device."""
+    import torch
+    if tuple(t.shape) != (n, length):
+        raise ValueError(f"{name} must be [{n}, {length}], got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    b = rankbuf(t)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+    return b
+
+
+def _operand_stream(stream, workspace=None) -> ctypes.c_void_p:
+    """The call's stream; it and the workspace belong to the current device."""
+    import torch
+    if stream is not None and stream.device_index != torch.cuda.current_device():
+        raise ValueError("the stream belongs to another device")
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.device.index != torch.cuda.current_device():
+            raise ValueError("the workspace must be on the current device")
+        if not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
+    return _stream(stream)
+
+
+def _rows(t, width: int, name: str) -> int:
+    if t.dim() != 2 or width < 1 or t.shape[1] % width:
+        raise ValueError(f"{name} must be [nranks, rows * {width}]")
+    return t.shape[1] // width
+
+
+def embedding(table, ids, out, width: int, scale: float = 1.0, stream=None, blocks_per_cu: int = 0) -> None:
+    """out [N, T * width] = scale * the rows ids [N, T] (int32) of table
+    [N, V * width]; zero rows for ids outside [0, V).  A table expanded over
+    the ranks (stride 0) is one table that all ranks read."""
+    import torch
+    N, T, V = ids.shape[0], ids.shape[1], _rows(table, width, "table")
+    args = (_operand(table, "table", N, V * width), _operand(ids, "ids", N, T, torch.int32),
+            _operand(out, "out", N, T * width, table.dtype))
+    cfg = config("ring", 0, None, blocks_per_cu)
+    _check(load().cc_embedding(*args, V, T, width, float(scale), DTYPES[dtype_name(table)], N, ctypes.byref(cfg),
+                               _operand_stream(stream)))
+
+
+def embedding_grad_workspace_size(nranks: int, vocab: int, tokens: int, width: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().cc_embedding_grad_workspace_size(nranks, vocab, tokens, width, ctypes.byref(out)))
+    return out.value
+
+
+def make_embedding_grad_workspace(nranks: int, vocab: int, tokens: int, width: int, dtype: str = "f32", device="cuda"):
+    """Allocate (with torch) the workspace of either embedding gradient, or None."""
+    import torch
+    n = embedding_grad_workspace_size(nranks, vocab, tokens, width)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _embedding_grad(call: str, grad, ids, dtable, width, scale, workspace, stream, blocks_per_cu) -> None:
+    import torch
+    N, T, V = ids.shape[0], ids.shape[1], _rows(dtable, width, "dtable")
+    args = (_operand(grad, "grad", N, T * width), _operand(ids, "ids", N, T, torch.int32),
+            _operand(dtable, "dtable", N, V * width, grad.dtype))
+    cfg = config("ring", 0, workspace, blocks_per_cu)
+    _check(getattr(load(), call)(*args, V, T, width, float(scale), DTYPES[dtype_name(grad)], N, ctypes.byref(cfg),
+                                 _operand_stream(stream, workspace)))
+
+
+def embedding_grad(grad, ids, dtable, width: int, scale: float = 1.0, workspace=None, stream=None,
+                   blocks_per_cu: int = 0) -> None:
+    """dtable [N, V * width]: each rank's gradient of its table from grad
+    [N, T * width] at ids [N, T]; every row is written."""
+    _embedding_grad("cc_embedding_grad", grad, ids, dtable, width, scale, workspace, stream, blocks_per_cu)
+
+
+def all_reduce_embedding_grad(grad, ids, dtable, width: int, scale: float = 1.0, workspace=None, stream=None,
+                              blocks_per_cu: int = 0) -> None:
+    """dtable [N, V * width]: the gradient summed over all ranks, on every rank."""
+    _embedding_grad("cc_all_reduce_embedding_grad", grad, ids, dtable, width, scale, workspace, stream, blocks_per_cu)
+
+
+def moe_route_workspace_size(nranks: int, tokens: int, nexperts: int, topk: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().cc_moe_route_workspace_size(nranks, tokens, nexperts, topk, ctypes.byref(out)))
+    return out.value
+
+
+def make_moe_route_workspace(nranks: int, tokens: int, nexperts: int, topk: int, device="cuda"):
+    """Allocate (with torch) the workspace of moe_route, or None."""
+    import torch
+    n = moe_route_workspace_size(nranks, tokens, nexperts, topk)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def moe_route(logits, experts, weights, order, counts, topk: int, normalize: bool = False, workspace=None,
+              stream=None) -> None:
+    """logits [N, T * E] -> experts (int32) and weights (f32) [N, T * topk],
+    order (int32) [N, T * topk], counts (int32) [N, E]."""
+    import torch
+    N, E = counts.shape
+    T = _rows(logits, E, "logits")
+    args = (_operand(logits, "logits", N, T * E), _operand(experts, "experts", N, T * topk, torch.int32),
+            _operand(weights, "weights", N, T * topk, torch.float32),
+            _operand(order, "order", N, T * topk, torch.int32), _operand(counts, "counts", N, E, torch.int32))
+    cfg = config("ring", 0, workspace)
+    _check(load().cc_moe_route(*args, T, E, topk, int(bool(normalize)), DTYPES[dtype_name(logits)], N,
+                               ctypes.byref(cfg), _operand_stream(stream, workspace)))
+
+
+def moe_route_grad(logits, experts, dweights, dlogits, topk: int, normalize: bool = False, stream=None) -> None:
+    """dlogits [N, T * E] from dweights (f32) [N, T * topk] at the experts moe_route chose."""
+    import torch
+    N, T = experts.shape[0], _rows(experts, topk, "experts")
+    E = _experts_of(logits, N, T)
+    args = (_operand(logits, "logits", N, T * E), _operand(experts, "experts", N, T * topk, torch.int32),
+            _operand(dweights, "dweights", N, T * topk, torch.float32),
+            _operand(dlogits, "dlogits", N, T * E, logits.dtype))
+    cfg = config("ring", 0, None)
+    _check(load().cc_moe_route_grad(*args, T, E, topk, int(bool(normalize)), DTYPES[dtype_name(logits)], N,
+                                    ctypes.byref(cfg), _operand_stream(stream)))
+
+
+def _experts_of(logits, n: int, tokens: int) -> int:
+    if logits.dim() != 2 or (tokens and logits.shape[1] % tokens):
+        raise ValueError(f"logits must be [{n}, {tokens} * nexperts]")
+    return logits.shape[1] // tokens if tokens else 1
+
+
+def moe_ffn_workspace_size(counts: Sequence[Sequence[int]], capacity: int, width: int, hidden: int, dtype: str,
+                           grad: bool = False) -> int:
+    N, E = len(counts), len(counts[0]) if len(counts) else 0
+    out = ctypes.c_size_t(0)
+    _check(load().cc_moe_ffn_workspace_size(_sizes(counts, N, E, "counts"), E, capacity, width, hidden, DTYPES[dtype],
+                                            N, int(bool(grad)), ctypes.byref(out)))
+    return out.value
+
+
+def make_moe_ffn_workspace(counts, capacity: int, width: int, hidden: int, dtype: str, grad: bool = False,
+                           device="cuda"):
+    """Allocate (with torch) the workspace of moe_ffn (or moe_ffn_grad)."""
+    import torch
+    n = moe_ffn_workspace_size(counts, capacity, width, hidden, dtype, grad)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _ffn_operands(x, w_in, w_out, counts, capacity, width):
+    """(N, E, hidden, expert-side length, counts array) of a feed-forward call."""
+    N, E = x.shape[0], len(counts[0]) if len(counts) else 0
+    arr = _sizes(counts, N, E, "counts")
+    if E < N or E % N:
+        raise ValueError(f"{E} experts are not a multiple of {N} ranks")
+    hidden = _rows(w_out, E // N * width, "w_out")
+    return N, E, hidden, E * capacity * width, arr
+
+
+def moe_ffn(x, w_in, w_out, y, counts: Sequence[Sequence[int]], capacity: int, width: int, pre=None, act: str = "silu",
+            workspace=None, stream=None) -> None:
+    """Gated feed-forward of the experts on the expert side of
+    moe_dispatch_padded: x, y [N, E * capacity * width], w_in
+    [N, E/N * 2 * hidden * width], w_out [N, E/N * width * hidden], counts
+    N x E; pre [N, E * capacity * 2 * hidden] keeps the pre-activations."""
+    N, E, hidden, side, arr = _ffn_operands(x, w_in, w_out, counts, capacity, width)
+    per, dt = E // N, x.dtype
+    args = (_operand(x, "x", N, side), _operand(w_in, "w_in", N, per * 2 * hidden * width, dt),
+            _operand(w_out, "w_out", N, per * width * hidden, dt),
+            RankBuf(None, 0) if pre is None else _operand(pre, "pre", N, E * capacity * 2 * hidden, dt),
+            _operand(y, "y", N, side, dt))
+    cfg = config("ring", 0, workspace)
+    _check(load().cc_moe_ffn(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N,
+                             ctypes.byref(cfg), _operand_stream(stream, workspace)))
+
+
+def moe_ffn_grad(x, w_in, w_out, pre, dy, dx, dw_in, dw_out, counts: Sequence[Sequence[int]], capacity: int,
+                 width: int, act: str = "silu", workspace=None, stream=None) -> None:
+    """The gradients of moe_ffn from dy, with pre as moe_ffn kept it."""
+    N, E, hidden, side, arr = _ffn_operands(x, w_in, w_out, counts, capacity, width)
+    per, dt = E // N, x.dtype
+    wi, wo = per * 2 * hidden * width, per * width * hidden
+    args = (_operand(x, "x", N, side), _operand(w_in, "w_in", N, wi, dt), _operand(w_out, "w_out", N, wo, dt),
+            _operand(pre, "pre", N, E * capacity * 2 * hidden, dt), _operand(dy, "dy", N, side, dt),
+            _operand(dx, "dx", N, side, dt), _operand(dw_in, "dw_in", N, wi, dt),
+            _operand(dw_out, "dw_out", N, wo, dt))
+    cfg = config("ring", 0, workspace)
+    _check(load().cc_moe_ffn_grad(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N,
+                                  ctypes.byref(cfg), _operand_stream(stream, workspace)))
 
 
 def raw(fn: str, *args):

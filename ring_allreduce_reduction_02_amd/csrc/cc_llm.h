@@ -1,0 +1,128 @@
+// Internal interface between the C ABI of the model-side operators
+// (cc_model.cpp) and their kernels (cc_sort.hip, cc_embed.hip, cc_route.hip,
+// cc_ffn.hip).  Host-side only; not installed.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cc_launch.h"
+
+namespace cc {
+
+// ---- stable sort of int32 keys with their positions, in `segs` segments of
+// n keys each.  Keys outside [0, nkeys) sort last, as the key nkeys.
+// Segment g's keys start at keys + g * key_stride; with `flat` every segment
+// is n / flat_n rows of flat_n keys, key_stride bytes apart (one segment over
+// all ranks' keys).
+struct SortPlan {
+  int segs;
+  uint64_t n;        // keys per segment, < 2^31
+  uint32_t nkeys;
+  int passes;        // of 8 bits
+  uint64_t tiles;    // per segment and pass
+  uint64_t bytes;    // of workspace
+};
+SortPlan sort_plan(int segs, uint64_t n, uint32_t nkeys);
+struct SortLaunch {
+  SortPlan p;
+  const char* keys;
+  uint64_t key_stride;   // bytes between segments (or between rows, flat)
+  uint64_t row_n;        // keys per row: n, or the row length of a flat segment
+  char* ws;              // p.bytes, 16-byte aligned
+  // outputs inside ws, [segs][n] int32: sorted keys and their positions
+  const int* sorted_keys;
+  const int* sorted_vals;
+  hipStream_t st;
+};
+hipError_t launch_sort(SortLaunch* L);
+
+// ---- embedding
+struct EmbedLaunch {
+  const char* table;
+  uint64_t table_stride;
+  const char* ids;
+  uint64_t ids_stride;
+  char* out;
+  uint64_t out_stride;
+  uint64_t vocab, tokens, width;
+  float scale;
+  int N, dt, vec_ok, blocks_per_cu;
+  hipStream_t st;
+};
+hipError_t launch_embed(const EmbedLaunch& L);
+
+constexpr int kEmbedPiece = 32;   // sorted positions per partial sum of a long run
+struct EmbedGradLaunch {
+  const char* grad;
+  uint64_t grad_stride;
+  char* out;
+  uint64_t out_stride;
+  const int* keys;       // sorted, [segs][n]
+  const int* vals;
+  float* partial;        // [segs][n / kEmbedPiece][width]
+  uint64_t n;            // keys per segment
+  uint64_t vocab, tokens, width;
+  float scale;
+  int N, dt, vec_ok, blocks_per_cu;
+  int summed;            // one segment over all ranks, the result on every rank
+  hipStream_t st;
+};
+hipError_t launch_embed_grad(const EmbedGradLaunch& L);
+
+// ---- MoE routing
+constexpr int kMaxRouteExperts = 1024;
+struct RouteLaunch {
+  const char* logits;
+  uint64_t logits_stride;
+  char* experts;         // int32 [tokens][topk]
+  uint64_t experts_stride;
+  char* weights;         // float32 [tokens][topk]; dweights of the gradient
+  uint64_t weights_stride;
+  char* order;           // int32 [tokens * topk]
+  uint64_t order_stride;
+  char* counts;          // int32 [nexperts]
+  uint64_t counts_stride;
+  char* dlogits;
+  uint64_t dlogits_stride;
+  uint64_t tokens;
+  int nexperts, topk, normalize;
+  int N, dt;
+  hipStream_t st;
+};
+hipError_t launch_route(const RouteLaunch& L);
+hipError_t launch_route_order(const RouteLaunch& L, const int* keys, const int* vals);
+hipError_t launch_route_grad(const RouteLaunch& L);
+
+// ---- gated feed-forward block of the experts.  Compact rows: the kept rows
+// of all experts back to back, expert by expert, source by source.
+constexpr int kFfnRowTile = 128;        // rows per tile of the row products
+struct FfnShape {
+  int N, E;              // ranks, experts
+  uint64_t cap;
+  uint64_t W, F;         // width, hidden
+  uint64_t rows;         // kept rows of all experts
+  uint64_t mtiles;       // row tiles of all experts
+  int dt, act;
+};
+// Workspace: row starts [E + 1], row tiles [mtiles] (expert, first row), row
+// map [rows] (row in the rank's buffer), kept counts [N * E], h [rows][F],
+// and for the gradient d(gate | up) [rows][2F].
+struct FfnWs {
+  uint64_t kept, start, mtab, rowmap, h, dgu, bytes;
+};
+FfnWs ffn_ws(const FfnShape& s, int grad);
+struct FfnLaunch {
+  FfnShape s;
+  FfnWs o;
+  char* ws;
+  const uint32_t* kept;  // host, [E][N]: kept rows of expert e from source i
+  Side x, w_in, w_out, pre, y;      // pre.base may be NULL (forward)
+  Side dy, dx, dw_in, dw_out;       // gradient
+  int vec_ok;
+  hipStream_t st;
+};
+hipError_t launch_ffn(const FfnLaunch& L);
+hipError_t launch_ffn_grad(const FfnLaunch& L);
+
+}  // namespace cc

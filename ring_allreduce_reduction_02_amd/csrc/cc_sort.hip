@@ -1,0 +1,183 @@
+// Stable sort of small integer keys with their positions: the rows of one
+// expert, or of one word of a vocabulary, brought together in the order they
+// came in.
+//
+// Least significant digit first, 8 bits a pass.  A pass is three kernels: the
+// digit counts of every tile, their exclusive prefix in (digit, tile) order,
+// and the scatter, in which a key's place inside its tile is the number of
+// equal digits before it: in its wave's earlier rounds, in the lanes below it
+// (one ballot per bit), and in the waves before it.  Every place is a count,
+// so nothing depends on the order in which workgroups run.
+
+#include "cc_device.h"
+#include "cc_llm.h"
+
+namespace cc {
+namespace {
+
+constexpr int kSortBlock = 256;
+constexpr int kSortWaves = kSortBlock / 64;
+constexpr int kSortRounds = 4;                              // keys per lane
+constexpr int kSortTile = kSortBlock * kSortRounds;         // 1024 keys
+constexpr int kDigits = 256;
+
+struct SortArgs {
+  const char* keys;      // first pass: the caller's keys
+  uint64_t key_stride;
+  uint64_t row_n;
+  const int* kin;        // later passes
+  const int* vin;
+  int* kout;
+  int* vout;
+  uint32_t* hist;        // [segs][kDigits][tiles]
+  uint64_t n;
+  uint32_t nkeys;
+  uint32_t tiles;
+  int shift;
+  int first;
+};
+
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint64_t seg, uint64_t i) {
+  if (!a.first) return (uint32_t)a.kin[seg * a.n + i];
+  // a flat segment walks rows of row_n keys; otherwise row_n == n
+  const uint64_t row = a.row_n == a.n ? seg : i / a.row_n;
+  const uint64_t col = a.row_n == a.n ? i : i - row * a.row_n;
+  const uint32_t k = (uint32_t)((const int*)(a.keys + row * a.key_stride))[col];
+  return k < a.nkeys ? k : a.nkeys;
+}
+
+__global__ __launch_bounds__(kSortBlock) void k_sort_hist(SortArgs a) {
+  __shared__ uint32_t h[kDigits];
+  h[threadIdx.x] = 0;
+  __syncthreads();
+  const uint64_t i0 = (uint64_t)blockIdx.x * kSortTile;
+  for (int q = 0; q < kSortRounds; ++q) {
+    const uint64_t i = i0 + (uint64_t)q * kSortBlock + threadIdx.x;
+    if (i < a.n) atomicAdd(&h[(sort_key(a, blockIdx.y, i) >> a.shift) & (kDigits - 1)], 1u);
+  }
+  __syncthreads();
+  a.hist[((uint64_t)blockIdx.y * kDigits + threadIdx.x) * a.tiles + blockIdx.x] = h[threadIdx.x];
+}
+
+// Exclusive prefix over a segment's kDigits * tiles counts, in place.
+constexpr int kScanBlock = 1024;
+__global__ __launch_bounds__(kScanBlock) void k_sort_scan(uint32_t* hist, uint64_t count) {
+  __shared__ uint32_t wsum[kScanBlock / 64];
+  __shared__ uint32_t carry_s;
+  uint32_t* h = hist + (uint64_t)blockIdx.x * count;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (threadIdx.x == 0) carry_s = 0;
+  __syncthreads();
+  for (uint64_t b = 0; b < count; b += kScanBlock) {
+    const uint64_t i = b + threadIdx.x;
+    const uint32_t v = i < count ? h[i] : 0u;
+    uint32_t s = v;
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t t = __shfl_up(s, d);
+      if (lane >= d) s += t;
+    }
+    if (lane == 63) wsum[wave] = s;
+    __syncthreads();
+    uint32_t base = carry_s, all = 0;
+    for (int w = 0; w < kScanBlock / 64; ++w) {
+      if (w < wave) base += wsum[w];
+      all += wsum[w];
+    }
+    if (i < count) h[i] = base + s - v;
+    __syncthreads();
+    if (threadIdx.x == 0) carry_s += all;
+    __syncthreads();
+  }
+}
+
+__global__ __launch_bounds__(kSortBlock) void k_sort_scatter(SortArgs a) {
+  __shared__ uint32_t cnt[kSortWaves][kDigits];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int d = threadIdx.x; d < kSortWaves * kDigits; d += kSortBlock) (&cnt[0][0])[d] = 0;
+  __syncthreads();
+  // wave w holds the tile's keys [w, w + 1) * 64 * rounds, 64 a round
+  const uint64_t i0 = (uint64_t)blockIdx.x * kSortTile + (uint64_t)wave * 64 * kSortRounds;
+  uint32_t key[kSortRounds], place[kSortRounds];
+  int val[kSortRounds];
+  const uint64_t below = (1ull << lane) - 1;
+  for (int q = 0; q < kSortRounds; ++q) {
+    const uint64_t i = i0 + (uint64_t)q * 64 + lane;
+    const bool in = i < a.n;
+    key[q] = in ? sort_key(a, blockIdx.y, i) : 0u;
+    val[q] = in ? (a.first ? (int)i : a.vin[(uint64_t)blockIdx.y * a.n + i]) : 0;
+    const uint32_t d = (key[q] >> a.shift) & (kDigits - 1);
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < 8; ++b) {
+      const uint64_t one = __ballot((d >> b) & 1u);
+      same &= ((d >> b) & 1u) ? one : ~one;
+    }
+    // lanes of one digit read its count, then the lowest of them adds theirs
+    // (a wave's LDS accesses complete in program order; volatile keeps it)
+    volatile uint32_t* c = &cnt[wave][d];
+    const uint32_t before = *c;
+    place[q] = before + (uint32_t)__popcll(same & below);
+    if (in && (same & below) == 0) *c = before + (uint32_t)__popcll(same);
+  }
+  __syncthreads();
+  {
+    const int d = threadIdx.x;   // kSortBlock == kDigits
+    uint32_t at = a.hist[((uint64_t)blockIdx.y * kDigits + d) * a.tiles + blockIdx.x];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = cnt[w][d];
+      cnt[w][d] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  for (int q = 0; q < kSortRounds; ++q) {
+    const uint64_t i = i0 + (uint64_t)q * 64 + lane;
+    if (i >= a.n) continue;
+    const uint32_t d = (key[q] >> a.shift) & (kDigits - 1);
+    const uint64_t to = (uint64_t)blockIdx.y * a.n + cnt[wave][d] + place[q];
+    a.kout[to] = (int)key[q];
+    a.vout[to] = val[q];
+  }
+}
+
+uint64_t up(uint64_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+SortPlan sort_plan(int segs, uint64_t n, uint32_t nkeys) {
+  SortPlan p;
+  p.segs = segs;
+  p.n = n;
+  p.nkeys = nkeys;
+  p.passes = 1;
+  while (p.passes < 4 && (nkeys >> (8 * p.passes)) != 0) ++p.passes;   // the key nkeys itself is sorted too
+  p.tiles = (n + kSortTile - 1) / kSortTile;
+  const uint64_t arr = up((uint64_t)segs * n * 4);
+  p.bytes = 4 * arr + up((uint64_t)segs * kDigits * p.tiles * 4);
+  return p;
+}
+
+hipError_t launch_sort(SortLaunch* L) {
+  const SortPlan& p = L->p;
+  const uint64_t arr = up((uint64_t)p.segs * p.n * 4);
+  int* k[2] = {(int*)L->ws, (int*)(L->ws + 2 * arr)};
+  int* v[2] = {(int*)(L->ws + arr), (int*)(L->ws + 3 * arr)};
+  uint32_t* hist = (uint32_t*)(L->ws + 4 * arr);
+  SortArgs a;
+  a.keys = L->keys; a.key_stride = L->key_stride; a.row_n = L->row_n;
+  a.hist = hist; a.n = p.n; a.nkeys = p.nkeys; a.tiles = (uint32_t)p.tiles;
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.segs), blk(kSortBlock);
+  for (int pass = 0; pass < p.passes; ++pass) {
+    a.first = pass == 0;
+    a.shift = 8 * pass;
+    a.kin = k[(pass + 1) & 1]; a.vin = v[(pass + 1) & 1];
+    a.kout = k[pass & 1]; a.vout = v[pass & 1];
+    CC_LAUNCH(k_sort_hist, grid, blk, 0, L->st, a);
+    CC_LAUNCH(k_sort_scan, dim3((unsigned)p.segs), dim3(kScanBlock), 0, L->st, hist, (uint64_t)kDigits * p.tiles);
+    CC_LAUNCH(k_sort_scatter, grid, blk, 0, L->st, a);
+  }
+  L->sorted_keys = k[(p.passes - 1) & 1];
+  L->sorted_vals = v[(p.passes - 1) & 1];
+  return hipGetLastError();
+}
+
+}  // namespace cc
