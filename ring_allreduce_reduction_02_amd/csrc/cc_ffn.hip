@@ -151,26 +151,40 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
   }
 }
 
+// Column tiles: a line per summed index, R columns long.  bf16 columns are read
+// with the transposing LDS load (16 lanes give the addresses of 4 summed
+// lines x 16 columns and get 4 summed elements of one column each); their
+// 32-byte pieces are permuted by the line's low bits, so that the 4 lines a
+// group reads lie in different banks.
+template <int DT, int R>
+__device__ __forceinline__ int col_at(int k, int col) {
+  if constexpr (DT == DT_BF16) return k * R * 2 + (((col >> 4) ^ (k & 3)) << 5) + (col & 15) * 2;
+  else return (k * R + col) * 4;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ u32x2 lds_transposed(const char* p) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+}
+
 // The 16 bytes of a lane for unit u of 32 lines from i0: line i0 + lane % 32,
 // elements of half lane / 32 of the unit.
 template <int DT, bool COL, int R>
 __device__ __forceinline__ u32x4 frag(const char* t, int u, int i0, int lane) {
-  const int i = i0 + (lane & 31), half = lane >> 5;
+  const int half = lane >> 5;
   if constexpr (!COL) {
-    return *(const u32x4*)(t + row_at(i, 2 * u + half));
+    return *(const u32x4*)(t + row_at(i0 + (lane & 31), 2 * u + half));
   } else if constexpr (DT == DT_BF16) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = 16 * u + 8 * half + 2 * j;
-      w[j] = (uint32_t)*(const uint16_t*)(t + (k * R + i) * 2) |
-             (uint32_t)*(const uint16_t*)(t + ((k + 1) * R + i) * 2) << 16;
-    }
-    return u32x4{w[0], w[1], w[2], w[3]};
+    const int k = 16 * u + 8 * half + ((lane & 15) >> 2), c = i0 + (lane & 16) + 4 * (lane & 3);
+    const u32x2 lo = lds_transposed(t + col_at<DT, R>(k, c)), hi = lds_transposed(t + col_at<DT, R>(k + 4, c));
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
   } else {
+    const int k = 8 * u + 4 * half, c = i0 + (lane & 31);
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = *(const uint32_t*)(t + ((8 * u + 4 * half + j) * R + i) * 4);
+    for (int j = 0; j < 4; ++j) w[j] = *(const uint32_t*)(t + col_at<DT, R>(k + j, c));
     return u32x4{w[0], w[1], w[2], w[3]};
   }
 }
@@ -194,7 +208,7 @@ __device__ __forceinline__ void stage_elems(char* t, const char* const* lp, int6
       const int k = e / R, c = e % R;
       const char* p = lp[k];
       if (p && c0 + c < C) v = SZ == 2 ? *(const uint16_t*)(p + (c0 + c) * SZ) : *(const uint32_t*)(p + (c0 + c) * SZ);
-      at = (k * R + c) * SZ;
+      at = col_at<DT, R>(k, c);
     }
     if constexpr (SZ == 2) *(uint16_t*)(t + at) = (uint16_t)v;
     else *(uint32_t*)(t + at) = v;
@@ -262,152 +276,117 @@ __device__ __forceinline__ void load4(const char* p, float* v, int n) {
 // columns of one row.  K_GATEUP takes BN / 2 hidden columns: the tile's lines
 // alternate 32 gate rows and the 32 up rows of the same columns, so that one
 // lane holds both.
-template <int DT, int KIND, bool VEC, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_gemm(GemmArgs g) {
-  constexpr int NT = 64 * (BM / WM) * (BN / WN);
-  constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ;
-  constexpr int TM = WM / 32, TN = WN / 32;
-  constexpr bool ACOL = KIND == K_DW, BCOL = KIND == K_DHID || KIND == K_DX || KIND == K_DW;
-  static_assert(KIND != K_GATEUP || TN == 2, "a wave holds 32 gate and the same 32 up columns");
-  __shared__ __attribute__((aligned(16))) char ta[BM * kKBytes];
-  __shared__ __attribute__((aligned(16))) char tb[BN * kKBytes];
-  __shared__ const char* la[ACOL ? BK : BM];
-  __shared__ const char* lb[BCOL ? BK : BN];
+template <int KIND, int BN>
+constexpr int tile_cols() {
+  return KIND == K_GATEUP ? BN / 2 : BN;
+}
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % (BM / WM), wn = wave / (BM / WM);
-  int e, p0, p1, m0, n0;   // expert, its rows from here, their end, tile origin
+struct Part {
+  int e, rank, local;
+  int p0, p1;   // compact rows: the tile's first, the expert's end
+  int m0, n0;   // origin in the result (row products: m0 = 0, rows from p0)
+  int64_t K;
+};
+
+// Workgroups go round the 8 XCDs in turn; each XCD gets one run of tiles, in
+// which 4 row tiles share the columns' weights and a few columns the rows.
+template <int KIND, int BM, int BN>
+__device__ __forceinline__ Part tile_of(const GemmArgs& g) {
+  const uint32_t n = gridDim.x, x = blockIdx.x & 7, q = n >> 3, r = n & 7;
+  const uint32_t b = x * q + (x < r ? x : r) + (blockIdx.x >> 3);
+  Part t;
+  const uint32_t mt = (uint32_t)g.mtiles, nt = (uint32_t)g.ntiles;
+  uint32_t tb = b;
   if constexpr (KIND == K_DW) {
-    const int per_e = g.mtiles * g.ntiles;
-    e = blockIdx.x / per_e;
-    const int t = blockIdx.x - e * per_e;
-    m0 = (t % g.mtiles) * BM;
-    n0 = (t / g.mtiles) * BN;
-    p0 = g.start[e];
-    p1 = g.start[e + 1];
+    t.e = (int)(b / (mt * nt));
+    tb = b - (uint32_t)t.e * mt * nt;
+  }
+  const uint32_t grp = tb / (4 * nt), in = tb - grp * 4 * nt, left = mt - grp * 4, rows = left < 4 ? left : 4;
+  const uint32_t m = grp * 4 + in % rows;
+  t.n0 = (int)(in / rows) * tile_cols<KIND, BN>();
+  if constexpr (KIND == K_DW) {
+    t.m0 = (int)m * BM;
+    t.p0 = g.start[t.e];
+    t.p1 = g.start[t.e + 1];
+    t.K = t.p1 - t.p0;
   } else {
-    const int2 mt = g.mtab[blockIdx.x % g.mtiles];
-    e = mt.x;
-    p0 = mt.y;
-    p1 = g.start[e + 1];
-    m0 = 0;
-    n0 = (blockIdx.x / g.mtiles) * (KIND == K_GATEUP ? BN / 2 : BN);
+    const int2 at = g.mtab[m];
+    t.e = at.x;
+    t.p0 = at.y;
+    t.p1 = g.start[t.e + 1];
+    t.m0 = 0;
+    t.K = g.K;
   }
-  const int rank = e / g.per, local = e % g.per;
-  const int64_t K = KIND == K_DW ? p1 - p0 : g.K;
+  t.rank = t.e / g.per;
+  t.local = t.e % g.per;
+  return t;
+}
 
-  // lines that stay for the whole product
-  if constexpr (!ACOL)
-    for (int r = tid; r < BM; r += NT) la[r] = p0 + r < p1 ? row_ptr(g.a, rank, p0 + r) : nullptr;
-  if constexpr (!BCOL) {
-    const char* w = wt_ptr(g.b, rank, local);
-    for (int r = tid; r < BN; r += NT) {
-      int64_t row;
-      bool in;
-      if constexpr (KIND == K_GATEUP) {
-        const int f = n0 + (r / 64) * 32 + (r & 31);
-        in = f < g.F;
-        row = (int64_t)((r >> 5) & 1) * g.F + f;
-      } else {
-        in = n0 + r < g.N;
-        row = n0 + r;
-      }
-      lb[r] = in ? w + row * (int64_t)g.b.pitch : nullptr;
-    }
+// The weight row of line r of a row tile of weights, or -1.
+template <int KIND>
+__device__ __forceinline__ int64_t weight_line(const GemmArgs& g, const Part& t, int r) {
+  if constexpr (KIND == K_GATEUP) {
+    const int f = t.n0 + (r >> 6) * 32 + (r & 31);
+    return f < g.F ? (int64_t)((r >> 5) & 1) * g.F + f : -1;
+  } else {
+    return t.n0 + r < g.N ? t.n0 + r : -1;
   }
+}
 
-  f32x16 acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
-
-  for (int64_t k0 = 0; k0 < K; k0 += BK) {
-    __syncthreads();
-    if constexpr (ACOL || BCOL) {
-      if (tid < BK) {
-        const int64_t k = k0 + tid;
-        if constexpr (ACOL) la[tid] = k < K ? row_ptr(g.a, rank, (int)(p0 + k)) : nullptr;
-        if constexpr (KIND == K_DW) lb[tid] = k < K ? row_ptr(g.b_rows, rank, (int)(p0 + k)) : nullptr;
-        else lb[tid] = k < K ? wt_ptr(g.b, rank, local) + k * (int64_t)g.b.pitch : nullptr;
-      }
-      __syncthreads();
-    }
-    stage_elems<DT, ACOL, BM, NT>(ta, la, k0, K, m0, g.M);
-    stage_elems<DT, BCOL, BN, NT>(tb, lb, k0, K, n0, g.N);
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      u32x4 fa[TM], fb[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = frag<DT, ACOL, BM>(ta, u, wm * WM + 32 * i, lane);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = frag<DT, BCOL, BN>(tb, u, wn * WN + 32 * j, lane);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[j], fa[i], acc[i][j]);
-    }
-  }
-
-  // a lane's results: row m (of the tile) = lane % 32 of a 32-tile, columns
-  // 8 q + 4 (lane / 32) + 0..3 of it for q = 0..3
+// The wave's results, rows from m and columns from n of the tile: a lane
+// holds row lane % 32 of a 32 x 32 tile, columns 8 q + 4 (lane / 32) + 0..3 of
+// it for q = 0..3.
+template <int DT, int KIND, bool VEC, int TM, int TN>
+__device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f32x16 (&acc)[TM][TN], int mw, int nw,
+                                       int lane) {
+  constexpr int SZ = Ty<DT>::SZ;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int m = wm * WM + 32 * i + (lane & 31);
-    const bool in = KIND == K_DW ? m0 + m < g.M : p0 + m < p1;
+    const int m = mw + 32 * i + (lane & 31);
+    const bool in = KIND == K_DW ? t.m0 + m < g.M : t.p0 + m < t.p1;
     if (!in) continue;
-    if constexpr (KIND == K_DW) {
-      char* o = wt_ptr(g.wout, rank, local) + (uint64_t)(m0 + m) * g.wout.pitch;
+    if constexpr (KIND == K_DW || KIND == K_DOWN || KIND == K_DX) {
+      char* o = KIND == K_DW ? wt_ptr(g.wout, t.rank, t.local) + (uint64_t)(t.m0 + m) * g.wout.pitch
+                             : row_ptr(g.out, t.rank, t.p0 + m);
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int n = n0 + wn * WN + 32 * j + 8 * q + 4 * (lane >> 5);
-          const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          store4<DT, VEC>(o + (int64_t)n * SZ, v, g.N - n);
-        }
-    } else if constexpr (KIND == K_DOWN || KIND == K_DX) {
-      char* o = row_ptr(g.out, rank, p0 + m);
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int n = n0 + wn * WN + 32 * j + 8 * q + 4 * (lane >> 5);
+          const int n = t.n0 + nw + 32 * j + 8 * q + 4 * (lane >> 5);
           const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
           store4<DT, VEC>(o + (int64_t)n * SZ, v, g.N - n);
         }
     } else if constexpr (KIND == K_GATEUP) {
-      char* o = row_ptr(g.out, rank, p0 + m);
-      char* pre = g.pre.base ? row_ptr(g.pre, rank, p0 + m) : nullptr;
+      char* o = row_ptr(g.out, t.rank, t.p0 + m);
+      char* pre = g.pre.base ? row_ptr(g.pre, t.rank, t.p0 + m) : nullptr;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int f = n0 + wn * 32 + 8 * q + 4 * (lane >> 5);
-        float gt[4], up[4], h[4];
+      for (int j = 0; j < TN; j += 2)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          gt[x] = acc[i][0][4 * q + x];
-          up[x] = acc[i][1][4 * q + x];
-          h[x] = act_of(gt[x], g.act) * up[x];
+        for (int q = 0; q < 4; ++q) {
+          const int f = t.n0 + (nw >> 1) + 16 * j + 8 * q + 4 * (lane >> 5);
+          float gt[4], up[4], h[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            gt[x] = acc[i][j][4 * q + x];
+            up[x] = acc[i][j + 1][4 * q + x];
+            h[x] = act_of(gt[x], g.act) * up[x];
+          }
+          store4<DT, VEC>(o + (int64_t)f * SZ, h, g.F - f);
+          if (pre) {
+            store4<DT, VEC>(pre + (int64_t)f * SZ, gt, g.F - f);
+            store4<DT, VEC>(pre + ((int64_t)g.F + f) * SZ, up, g.F - f);
+          }
         }
-        store4<DT, VEC>(o + (int64_t)f * SZ, h, g.F - f);
-        if (pre) {
-          store4<DT, VEC>(pre + (int64_t)f * SZ, gt, g.F - f);
-          store4<DT, VEC>(pre + ((int64_t)g.F + f) * SZ, up, g.F - f);
-        }
-      }
     } else {   // K_DHID
-      char* o = row_ptr(g.out, rank, p0 + m);
-      char* oh = row_ptr(g.h, rank, p0 + m);
-      const char* pre = row_ptr(g.pre, rank, p0 + m);
+      char* o = row_ptr(g.out, t.rank, t.p0 + m);
+      char* oh = row_ptr(g.h, t.rank, t.p0 + m);
+      const char* pre = row_ptr(g.pre, t.rank, t.p0 + m);
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int f = n0 + wn * WN + 32 * j + 8 * q + 4 * (lane >> 5);
-          float gt[4], up[4], dg[4], du[4], h[4];
+          const int f = t.n0 + nw + 32 * j + 8 * q + 4 * (lane >> 5);
+          float gt[4] = {}, up[4] = {}, dg[4], du[4], h[4];
           load4<DT, VEC>(pre + (int64_t)f * SZ, gt, g.F - f);
           load4<DT, VEC>(pre + ((int64_t)g.F + f) * SZ, up, g.F - f);
 #pragma unroll
@@ -427,28 +406,282 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_gemm(GemmArg
   }
 }
 
-template <int DT, int KIND, bool VEC>
-hipError_t run_gemm(GemmArgs g, hipStream_t st) {
-  constexpr int BM = kFfnRowTile, BN = 128;
-  const int cols = KIND == K_GATEUP ? g.F : g.N;
-  g.ntiles = (cols + (KIND == K_GATEUP ? BN / 2 : BN) - 1) / (KIND == K_GATEUP ? BN / 2 : BN);
-  uint64_t blocks;
-  if constexpr (KIND == K_DW) {
-    g.mtiles = (g.M + BM - 1) / BM;
-    blocks = (uint64_t)g.E * g.mtiles * g.ntiles;
-  } else {
-    blocks = (uint64_t)g.mtiles * g.ntiles;
+// One stage's products of a wave: the next unit's fragments are read while the
+// matrix instructions of the last ones run.
+template <int DT, bool ACOL, bool BCOL, int BM, int BN, int TM, int TN>
+__device__ __forceinline__ void multiply(const char* ta, const char* tb, f32x16 (&acc)[TM][TN], int mw, int nw,
+                                         int lane) {
+  u32x4 fa[2][TM], fb[2][TN];
+  auto read = [&](int u) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[u & 1][j] = frag<DT, BCOL, BN>(tb, u, nw + 32 * j, lane);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[u & 1][i] = frag<DT, ACOL, BM>(ta, u, mw + 32 * i, lane);
+  };
+  read(0);
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    if (u + 1 < kUnits) read(u + 1);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);   // keeps at most two units' fragments in registers
   }
-  if (blocks == 0) return hipSuccess;
-  CC_LAUNCH((k_ffn_gemm<DT, KIND, VEC, BM, BN, 64, 64>), dim3((unsigned)blocks), dim3(256), 0, st, g);
+}
+
+template <int TM, int TN>
+__device__ __forceinline__ void clear(f32x16 (&acc)[TM][TN]) {
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+}
+
+// Any alignment: every element staged by itself, one stage after the other.
+template <int DT, int KIND, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmArgs g) {
+  constexpr int NT = 64 * (BM / WM) * (BN / WN);
+  constexpr int BK = kKBytes / Ty<DT>::SZ;
+  constexpr int TM = WM / 32, TN = WN / 32;
+  constexpr bool ACOL = KIND == K_DW, BCOL = KIND == K_DHID || KIND == K_DX || KIND == K_DW;
+  __shared__ __attribute__((aligned(16))) char ta[BM * kKBytes];
+  __shared__ __attribute__((aligned(16))) char tb[BN * kKBytes];
+  __shared__ const char* la[ACOL ? BK : BM];
+  __shared__ const char* lb[BCOL ? BK : BN];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int mw = (wave % (BM / WM)) * WM, nw = (wave / (BM / WM)) * WN;
+  const Part t = tile_of<KIND, BM, BN>(g);
+  if constexpr (!ACOL)
+    for (int r = tid; r < BM; r += NT) la[r] = t.p0 + r < t.p1 ? row_ptr(g.a, t.rank, t.p0 + r) : nullptr;
+  if constexpr (!BCOL) {
+    const char* w = wt_ptr(g.b, t.rank, t.local);
+    for (int r = tid; r < BN; r += NT) {
+      const int64_t row = weight_line<KIND>(g, t, r);
+      lb[r] = row >= 0 ? w + row * (int64_t)g.b.pitch : nullptr;
+    }
+  }
+  f32x16 acc[TM][TN];
+  clear(acc);
+  for (int64_t k0 = 0; k0 < t.K; k0 += BK) {
+    __syncthreads();
+    if constexpr (ACOL || BCOL) {
+      if (tid < BK) {
+        const int64_t k = k0 + tid;
+        if constexpr (ACOL) la[tid] = k < t.K ? row_ptr(g.a, t.rank, (int)(t.p0 + k)) : nullptr;
+        if constexpr (KIND == K_DW) lb[tid] = k < t.K ? row_ptr(g.b_rows, t.rank, (int)(t.p0 + k)) : nullptr;
+        else lb[tid] = k < t.K ? wt_ptr(g.b, t.rank, t.local) + k * (int64_t)g.b.pitch : nullptr;
+      }
+      __syncthreads();
+    }
+    stage_elems<DT, ACOL, BM, NT>(ta, la, k0, t.K, t.m0, g.M);
+    stage_elems<DT, BCOL, BN, NT>(tb, lb, k0, t.K, t.n0, g.N);
+    __syncthreads();
+    multiply<DT, ACOL, BCOL, BM, BN>(ta, tb, acc, mw, nw, lane);
+  }
+  finish<DT, KIND, false>(g, t, acc, mw, nw, lane);
+}
+
+// ---- aligned rows: tiles come by direct loads to LDS, 16 bytes a lane
+
+__device__ const uint32_t g_zero[4] = {0, 0, 0, 0};
+
+__device__ __forceinline__ void load_lds(const char* from, char* to) {
+  typedef const __attribute__((address_space(1))) void gv;
+  typedef __attribute__((address_space(3))) void lv;
+  __builtin_amdgcn_global_load_lds((gv*)from, (lv*)to, 16, 0, 0);
+}
+
+// One operand's tile of R lines, loaded by NW waves: a wave's load fills 1 KiB
+// of LDS in lane order, so the lane fetches the chunk that the permuted layout
+// has at its place.  Lines and columns outside the matrix repeat the last
+// one (their results are not stored); summed elements outside read zeros.
+template <int DT, bool COL, int R, int NW>
+struct Loader {
+  static constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ;
+  static constexpr int Q = R / 8 / NW;                  // loads per wave and stage
+  static constexpr int LANES = COL ? R * SZ / 16 : 8;   // lanes per line
+  const char* p[Q];      // this lane's address at stage 0 (COL: of the line's first byte, plus the chunk)
+  int chunk[Q];          // row tiles: 16-byte chunk of the stage; column tiles: byte offset of the column chunk
+  uint64_t step;         // bytes per stage (0: lines by number, from a row map)
+  int first;             // summed line of load 0 in the stage (COL)
+
+  __device__ __forceinline__ static int line_of(int wave, int q, int lane) {
+    return (wave * Q + q) * (64 / LANES) + lane / LANES;
+  }
+  // load q of stage s
+  __device__ __forceinline__ void issue(char* t, int wave, int lane, int64_t s, int64_t K, bool tail) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const char* from = p[q] + s * (int64_t)step;
+      if (tail) {
+        const bool in = COL ? s * BK + line_of(wave, q, lane) < K : s * kKBytes + chunk[q] * 16 < K * SZ;
+        from = in ? from : (const char*)g_zero;
+      }
+      load_lds(from, t + (wave * Q + q) * 1024);
+    }
+  }
+  // load q of stage s, the summed lines being rows[p0 + ...]; idx: their rows
+  __device__ __forceinline__ void issue_rows(char* t, int wave, int lane, int64_t s, int64_t K, bool tail,
+                                             const char* base, uint64_t pitch, const int (&idx)[Q]) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const char* from = base + (uint64_t)(uint32_t)idx[q] * pitch + chunk[q];
+      if (tail && s * BK + line_of(wave, q, lane) >= K) from = (const char*)g_zero;
+      load_lds(from, t + (wave * Q + q) * 1024);
+    }
+  }
+  // the rows of stage s
+  __device__ __forceinline__ void rows(int (&idx)[Q], const int* map, int p0, int64_t K, int wave, int lane,
+                                       int64_t s) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      int64_t k = s * BK + line_of(wave, q, lane);
+      k = k < K ? k : K - 1;
+      idx[q] = map ? map[p0 + k] : (int)(p0 + k);
+    }
+  }
+  // column chunks of this lane (COL), clamped to the last of C columns
+  __device__ __forceinline__ void columns(int wave, int lane, int c0, int C) {
+    const int slot = lane % LANES, last = (C - c0) * SZ - 16;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int k = line_of(wave, q, lane);
+      const int c = 16 * (DT == DT_BF16 ? ((slot >> 1) ^ (k & 3)) * 2 + (slot & 1) : slot);
+      chunk[q] = c0 * SZ + (c < last ? c : last);
+    }
+  }
+  // row tiles: the chunk of a line's place is the place's number, permuted
+  __device__ __forceinline__ void chunks(int lane) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) chunk[q] = (lane & 7) ^ (lane >> 3);
+    step = kKBytes;
+  }
+};
+
+template <int DT, int KIND, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArgs g) {
+  constexpr int NW = (BM / WM) * (BN / WN);
+  constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ;
+  constexpr int TM = WM / 32, TN = WN / 32;
+  constexpr bool ACOL = KIND == K_DW, BCOL = KIND == K_DHID || KIND == K_DX || KIND == K_DW;
+  __shared__ __attribute__((aligned(16))) char ta0[BM * kKBytes], tb0[BN * kKBytes];
+  __shared__ __attribute__((aligned(16))) char ta1[BM * kKBytes], tb1[BN * kKBytes];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mw = (wave % (BM / WM)) * WM, nw = (wave / (BM / WM)) * WN;
+  const Part t = tile_of<KIND, BM, BN>(g);
+  typedef Loader<DT, ACOL, BM, NW> LA;
+  typedef Loader<DT, BCOL, BN, NW> LB;
+  LA la;
+  LB lb;
+  const char *abase = nullptr, *bbase = nullptr;
+  int ia[LA::Q], ib[LB::Q];
+  if constexpr (!ACOL) {
+    la.chunks(lane);
+#pragma unroll
+    for (int q = 0; q < LA::Q; ++q) {
+      int r = t.p0 + LA::line_of(wave, q, lane);
+      r = r < t.p1 ? r : t.p1 - 1;
+      la.p[q] = row_ptr(g.a, t.rank, r) + la.chunk[q] * 16;
+    }
+  } else {
+    la.columns(wave, lane, t.m0, g.M);
+    abase = g.a.map ? g.a.base + (uint64_t)t.rank * g.a.rank_stride : g.a.base;
+  }
+  if constexpr (!BCOL) {
+    const char* w = wt_ptr(g.b, t.rank, t.local);
+    lb.chunks(lane);
+#pragma unroll
+    for (int q = 0; q < LB::Q; ++q) {
+      int64_t row = weight_line<KIND>(g, t, LB::line_of(wave, q, lane));
+      row = row >= 0 ? row : 0;
+      lb.p[q] = w + row * (int64_t)g.b.pitch + lb.chunk[q] * 16;
+    }
+  } else if constexpr (KIND == K_DW) {
+    lb.columns(wave, lane, t.n0, g.N);
+    bbase = g.b_rows.map ? g.b_rows.base + (uint64_t)t.rank * g.b_rows.rank_stride : g.b_rows.base;
+  } else {
+    const char* w = wt_ptr(g.b, t.rank, t.local);
+    lb.columns(wave, lane, t.n0, g.N);
+    lb.step = (uint64_t)BK * g.b.pitch;
+#pragma unroll
+    for (int q = 0; q < LB::Q; ++q) lb.p[q] = w + (uint64_t)LB::line_of(wave, q, lane) * g.b.pitch + lb.chunk[q];
+  }
+
+  f32x16 acc[TM][TN];
+  clear(acc);
+  const int64_t S = (t.K + 2 * BK - 1) / (2 * BK) * 2;   // an odd last stage is zeros
+  auto rows = [&](int64_t s) {
+    if constexpr (KIND == K_DW) {
+      la.rows(ia, g.a.map, t.p0, t.K, wave, lane, s);
+      lb.rows(ib, g.b_rows.map, t.p0, t.K, wave, lane, s);
+    }
+  };
+  auto issue = [&](char* a, char* b, int64_t s) {
+    const bool tail = (s + 1) * BK > t.K;
+    if constexpr (KIND == K_DW) {
+      la.issue_rows(a, wave, lane, s, t.K, tail, abase, g.a.pitch, ia);
+      lb.issue_rows(b, wave, lane, s, t.K, tail, bbase, g.b_rows.pitch, ib);
+      if (s + 1 < S) rows(s + 1);
+    } else {
+      la.issue(a, wave, lane, s, t.K, tail);
+      lb.issue(b, wave, lane, s, t.K, tail);
+    }
+  };
+  if (S) {
+    rows(0);
+    issue(ta0, tb0, 0);
+  }
+  for (int64_t s = 0; s < S; s += 2) {
+    __syncthreads();
+    issue(ta1, tb1, s + 1);
+    multiply<DT, ACOL, BCOL, BM, BN>(ta0, tb0, acc, mw, nw, lane);
+    __syncthreads();
+    if (s + 2 < S) issue(ta0, tb0, s + 2);
+    multiply<DT, ACOL, BCOL, BM, BN>(ta1, tb1, acc, mw, nw, lane);
+  }
+  finish<DT, KIND, true>(g, t, acc, mw, nw, lane);
+}
+
+// rows per tile of a call's row products
+int row_tile(const FfnLaunch& L) { return L.vec_ok && 4 * L.s.rows >= 3 * 256 * L.s.mtiles256 ? 256 : kFfnRowTile; }
+
+template <int KIND, int BM, int BN>
+uint64_t tiles_of(GemmArgs* g) {
+  const int cols = KIND == K_GATEUP ? g->F : g->N, bn = tile_cols<KIND, BN>();
+  g->ntiles = (cols + bn - 1) / bn;
+  if constexpr (KIND == K_DW) {
+    g->mtiles = (g->M + BM - 1) / BM;
+    return (uint64_t)g->E * g->mtiles * g->ntiles;
+  }
+  return (uint64_t)g->mtiles * g->ntiles;
+}
+
+template <int DT, int KIND>
+hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
+  if (!L.vec_ok) {
+    const uint64_t blocks = tiles_of<KIND, 128, 128>(&g);
+    if (blocks == 0) return hipSuccess;
+    CC_LAUNCH((k_ffn_elems<DT, KIND, 128, 128, 64, 64>), dim3((unsigned)blocks), dim3(256), 0, L.st, g);
+  } else if (row_tile(L) == 256) {
+    const uint64_t blocks = tiles_of<KIND, 256, 256>(&g);
+    if (blocks == 0) return hipSuccess;
+    CC_LAUNCH((k_ffn_tile<DT, KIND, 256, 256, 128, 64>), dim3((unsigned)blocks), dim3(512), 0, L.st, g);
+  } else {
+    const uint64_t blocks = tiles_of<KIND, 128, 128>(&g);
+    if (blocks == 0) return hipSuccess;
+    CC_LAUNCH((k_ffn_tile<DT, KIND, 128, 128, 64, 64>), dim3((unsigned)blocks), dim3(256), 0, L.st, g);
+  }
   return hipGetLastError();
 }
 
 template <int KIND>
 hipError_t pick_gemm(const GemmArgs& g, const FfnLaunch& L) {
-  if (L.s.dt == DT_F32)
-    return L.vec_ok ? run_gemm<DT_F32, KIND, true>(g, L.st) : run_gemm<DT_F32, KIND, false>(g, L.st);
-  return L.vec_ok ? run_gemm<DT_BF16, KIND, true>(g, L.st) : run_gemm<DT_BF16, KIND, false>(g, L.st);
+  return L.s.dt == DT_F32 ? run_gemm<DT_F32, KIND>(g, L) : run_gemm<DT_BF16, KIND>(g, L);
 }
 
 uint64_t up256(uint64_t v) { return (v + 255) / 256 * 256; }
@@ -483,7 +716,7 @@ GemmArgs gemm_args(const FfnLaunch& L) {
   GemmArgs g = {};
   g.start = (const int*)(L.ws + L.o.start);
   g.mtab = (const int2*)(L.ws + L.o.mtab);
-  g.mtiles = (int)L.s.mtiles;
+  g.mtiles = (int)(row_tile(L) == 256 ? L.s.mtiles256 : L.s.mtiles);
   g.E = L.s.E;
   g.per = L.s.E / L.s.N;
   g.F = (int)L.s.F;
@@ -525,7 +758,7 @@ FfnWs ffn_ws(const FfnShape& s, int grad) {
 
 hipError_t launch_ffn(const FfnLaunch& L) {
   const uint64_t W = L.s.W, F = L.s.F;
-  hipError_t e = plan(L, kFfnRowTile);
+  hipError_t e = plan(L, row_tile(L));
   if (e != hipSuccess) return e;
   GemmArgs g = gemm_args(L);
   g.K = (int)W;
@@ -546,7 +779,7 @@ hipError_t launch_ffn(const FfnLaunch& L) {
 
 hipError_t launch_ffn_grad(const FfnLaunch& L) {
   const uint64_t W = L.s.W, F = L.s.F;
-  hipError_t e = plan(L, kFfnRowTile);
+  hipError_t e = plan(L, row_tile(L));
   if (e != hipSuccess) return e;
   GemmArgs g = gemm_args(L);
   g.K = (int)W;

@@ -102,7 +102,8 @@ struct FfnShape {
   uint64_t cap;
   uint64_t W, F;         // width, hidden
   uint64_t rows;         // kept rows of all experts
-  uint64_t mtiles;       // row tiles of all experts
+  uint64_t mtiles;       // row tiles of all experts, of kFfnRowTile rows
+  uint64_t mtiles256;    // and of 256
   int dt, act;
 };
 // Workspace: row starts [E + 1], row tiles [mtiles] (expert, first row), row
