@@ -219,14 +219,19 @@ __device__ __forceinline__ void stage_elems(char* t, const char* const* lp, int6
 
 enum Act { ACT_SILU = 0, ACT_GELU = 1 };
 
+// 1 / (1 + exp(-g)) from the hardware's exp2 and reciprocal (1 ulp each): off by
+// at most (|g| + 4) 2^-24 of its value
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * g));
+}
 __device__ __forceinline__ float act_of(float g, int act) {
-  if (act == ACT_SILU) return g / (1.0f + expf(-g));
+  if (act == ACT_SILU) return g * sigmoid(g);
   return 0.5f * g * erfcf(-g * 0.70710678118654752f);
 }
 // the activation and its derivative
 __device__ __forceinline__ void act_both(float g, int act, float* a, float* d) {
   if (act == ACT_SILU) {
-    const float s = 1.0f / (1.0f + expf(-g));
+    const float s = sigmoid(g);
     *a = g * s;
     *d = s * (1.0f + g * (1.0f - s));
   } else {
@@ -236,35 +241,26 @@ __device__ __forceinline__ void act_both(float g, int act, float* a, float* d) {
   }
 }
 
-// four consecutive elements of a row, n of them inside it
-template <int DT, bool VEC>
-__device__ __forceinline__ void store4(char* p, const float* v, int n) {
+// V (4 or 8) consecutive elements of a row, n of them inside it
+template <int DT, bool VEC, int V>
+__device__ __forceinline__ void store_n(char* p, const float* v, int n) {
   if constexpr (VEC) {
     if (n <= 0) return;
-    if constexpr (DT == DT_BF16)
-      *(u32x2*)p = u32x2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
-    else
-      *(u32x4*)p = pack<DT_F32>(v);
+    static_assert(V * Ty<DT>::SZ == 16, "one vector");
+    *(u32x4*)p = pack<DT>(v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < V; ++i)
       if (i < n) st1<DT>(p + i * Ty<DT>::SZ, v[i]);
   }
 }
-template <int DT, bool VEC>
-__device__ __forceinline__ void load4(const char* p, float* v, int n) {
+template <int DT, bool VEC, int V>
+__device__ __forceinline__ void load_n(const char* p, float* v, int n) {
   if constexpr (VEC) {
-    if (n <= 0) return;
-    if constexpr (DT == DT_BF16) {
-      const u32x2 w = *(const u32x2*)p;
-      v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
-      v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else {
-      unpack<DT_F32>(*(const u32x4*)p, v);
-    }
+    unpack<DT>(n > 0 ? *(const u32x4*)p : u32x4{0u, 0u, 0u, 0u}, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < n ? ld1<DT>(p + i * Ty<DT>::SZ) : 0.0f;
+    for (int i = 0; i < V; ++i) v[i] = i < n ? ld1<DT>(p + i * Ty<DT>::SZ) : 0.0f;
   }
 }
 
@@ -279,6 +275,24 @@ __device__ __forceinline__ void load4(const char* p, float* v, int n) {
 template <int KIND, int BN>
 constexpr int tile_cols() {
   return KIND == K_GATEUP ? BN / 2 : BN;
+}
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// LDS written by a wave's lanes is read by others of the same wave: its LDS
+// accesses complete in program order, which the compiler has to keep.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int V>
+__device__ __forceinline__ void read_row(const char* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const f32x4 w = *(const f32x4*)(p + 4 * i);
+    v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
+  }
 }
 
 struct Part {
@@ -333,76 +347,80 @@ __device__ __forceinline__ int64_t weight_line(const GemmArgs& g, const Part& t,
   }
 }
 
-// The wave's results, rows from m and columns from n of the tile: a lane
+// The wave's results, rows from mw and columns from nw of the tile.  A lane
 // holds row lane % 32 of a 32 x 32 tile, columns 8 q + 4 (lane / 32) + 0..3 of
-// it for q = 0..3.
+// it for q = 0..3.  They go through the wave's own piece of LDS (32 rows of
+// WN floats, 16 bytes of padding a row so that the rows lie in different
+// banks), so that a group of lanes holds a row's consecutive columns and
+// stores (and, K_DHID, loads) whole runs of them.
+template <int WN>
+constexpr int finish_bytes() {
+  return 32 * (WN * 4 + 16);
+}
+
 template <int DT, int KIND, bool VEC, int TM, int TN>
 __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f32x16 (&acc)[TM][TN], int mw, int nw,
-                                       int lane) {
-  constexpr int SZ = Ty<DT>::SZ;
+                                       int lane, char* lds) {
+  constexpr int SZ = Ty<DT>::SZ, V = Ty<DT>::V, WN = 32 * TN, PITCH = WN * 4 + 16;
+  constexpr int COLS = KIND == K_GATEUP ? WN / 2 : WN;   // result columns of the wave
+  constexpr int LPR = COLS / V, RPP = 64 / LPR;          // lanes per row, rows per pass
+  const int cl = (lane % LPR) * V;
+  // K_GATEUP: columns alternate 32 gate and 32 up
+  const int at = KIND == K_GATEUP ? (cl / 32) * 64 + cl % 32 : cl;
+  const int n = t.n0 + (KIND == K_GATEUP ? nw / 2 : nw) + cl;
+  const int left = (KIND == K_GATEUP ? g.F : g.N) - n;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int m = mw + 32 * i + (lane & 31);
-    const bool in = KIND == K_DW ? t.m0 + m < g.M : t.p0 + m < t.p1;
-    if (!in) continue;
-    if constexpr (KIND == K_DW || KIND == K_DOWN || KIND == K_DX) {
-      char* o = KIND == K_DW ? wt_ptr(g.wout, t.rank, t.local) + (uint64_t)(t.m0 + m) * g.wout.pitch
-                             : row_ptr(g.out, t.rank, t.p0 + m);
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int n = t.n0 + nw + 32 * j + 8 * q + 4 * (lane >> 5);
-          const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          store4<DT, VEC>(o + (int64_t)n * SZ, v, g.N - n);
+      for (int q = 0; q < 4; ++q)
+        *(f32x4*)(lds + (lane & 31) * PITCH + (32 * j + 8 * q + 4 * (lane >> 5)) * 4) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    wave_lds_sync();
+#pragma unroll
+    for (int r = 0; r < 32; r += RPP) {
+      const int row = r + lane / LPR, m = mw + 32 * i + row;
+      const bool in = KIND == K_DW ? t.m0 + m < g.M : t.p0 + m < t.p1;
+      if (!in) continue;
+      float v[V];
+      read_row<V>(lds + row * PITCH + at * 4, v);
+      if constexpr (KIND == K_DW) {
+        store_n<DT, VEC, V>(wt_ptr(g.wout, t.rank, t.local) + (uint64_t)(t.m0 + m) * g.wout.pitch + (int64_t)n * SZ, v,
+                            left);
+      } else if constexpr (KIND == K_DOWN || KIND == K_DX) {
+        store_n<DT, VEC, V>(row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ, v, left);
+      } else if constexpr (KIND == K_GATEUP) {
+        float up[V], h[V];
+        read_row<V>(lds + row * PITCH + (at + 32) * 4, up);
+#pragma unroll
+        for (int x = 0; x < V; ++x) h[x] = act_of(v[x], g.act) * up[x];
+        store_n<DT, VEC, V>(row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ, h, left);
+        if (g.pre.base) {
+          char* pre = row_ptr(g.pre, t.rank, t.p0 + m) + (int64_t)n * SZ;
+          store_n<DT, VEC, V>(pre, v, left);
+          store_n<DT, VEC, V>(pre + (int64_t)g.F * SZ, up, left);
         }
-    } else if constexpr (KIND == K_GATEUP) {
-      char* o = row_ptr(g.out, t.rank, t.p0 + m);
-      char* pre = g.pre.base ? row_ptr(g.pre, t.rank, t.p0 + m) : nullptr;
+      } else {   // K_DHID
+        const char* pre = row_ptr(g.pre, t.rank, t.p0 + m) + (int64_t)n * SZ;
+        float gt[V], up[V], du[V];
+        load_n<DT, VEC, V>(pre, gt, left);
+        load_n<DT, VEC, V>(pre + (int64_t)g.F * SZ, up, left);
 #pragma unroll
-      for (int j = 0; j < TN; j += 2)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int f = t.n0 + (nw >> 1) + 16 * j + 8 * q + 4 * (lane >> 5);
-          float gt[4], up[4], h[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            gt[x] = acc[i][j][4 * q + x];
-            up[x] = acc[i][j + 1][4 * q + x];
-            h[x] = act_of(gt[x], g.act) * up[x];
-          }
-          store4<DT, VEC>(o + (int64_t)f * SZ, h, g.F - f);
-          if (pre) {
-            store4<DT, VEC>(pre + (int64_t)f * SZ, gt, g.F - f);
-            store4<DT, VEC>(pre + ((int64_t)g.F + f) * SZ, up, g.F - f);
-          }
+        for (int x = 0; x < V; ++x) {
+          float a, d;
+          act_both(gt[x], g.act, &a, &d);
+          du[x] = v[x] * a;
+          v[x] = v[x] * up[x] * d;
+          up[x] *= a;
         }
-    } else {   // K_DHID
-      char* o = row_ptr(g.out, t.rank, t.p0 + m);
-      char* oh = row_ptr(g.h, t.rank, t.p0 + m);
-      const char* pre = row_ptr(g.pre, t.rank, t.p0 + m);
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int f = t.n0 + nw + 32 * j + 8 * q + 4 * (lane >> 5);
-          float gt[4] = {}, up[4] = {}, dg[4], du[4], h[4];
-          load4<DT, VEC>(pre + (int64_t)f * SZ, gt, g.F - f);
-          load4<DT, VEC>(pre + ((int64_t)g.F + f) * SZ, up, g.F - f);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float dh = acc[i][j][4 * q + x];
-            float a, d;
-            act_both(gt[x], g.act, &a, &d);
-            dg[x] = dh * up[x] * d;
-            du[x] = dh * a;
-            h[x] = a * up[x];
-          }
-          store4<DT, VEC>(o + (int64_t)f * SZ, dg, g.F - f);
-          store4<DT, VEC>(o + ((int64_t)g.F + f) * SZ, du, g.F - f);
-          store4<DT, VEC>(oh + (int64_t)f * SZ, h, g.F - f);
-        }
+        char* o = row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ;
+        store_n<DT, VEC, V>(o, v, left);
+        store_n<DT, VEC, V>(o + (int64_t)g.F * SZ, du, left);
+        store_n<DT, VEC, V>(row_ptr(g.h, t.rank, t.p0 + m) + (int64_t)n * SZ, up, left);
+      }
     }
+    wave_lds_sync();
   }
 }
 
@@ -449,6 +467,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmAr
   constexpr bool ACOL = KIND == K_DW, BCOL = KIND == K_DHID || KIND == K_DX || KIND == K_DW;
   __shared__ __attribute__((aligned(16))) char ta[BM * kKBytes];
   __shared__ __attribute__((aligned(16))) char tb[BN * kKBytes];
+  __shared__ __attribute__((aligned(16))) char fin[(NT / 64) * finish_bytes<WN>()];
   __shared__ const char* la[ACOL ? BK : BM];
   __shared__ const char* lb[BCOL ? BK : BN];
 
@@ -482,7 +501,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmAr
     __syncthreads();
     multiply<DT, ACOL, BCOL, BM, BN>(ta, tb, acc, mw, nw, lane);
   }
-  finish<DT, KIND, false>(g, t, acc, mw, nw, lane);
+  finish<DT, KIND, false>(g, t, acc, mw, nw, lane, fin + wave * finish_bytes<WN>());
 }
 
 // ---- aligned rows: tiles come by direct loads to LDS, 16 bytes a lane
@@ -644,7 +663,12 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
     if (s + 2 < S) issue(ta0, tb0, s + 2);
     multiply<DT, ACOL, BCOL, BM, BN>(ta1, tb1, acc, mw, nw, lane);
   }
-  finish<DT, KIND, true>(g, t, acc, mw, nw, lane);
+  __syncthreads();   // other waves may still read the last tiles
+  static_assert(NW * finish_bytes<WN>() <= 2 * BM * kKBytes + 2 * BN * kKBytes, "the results pass through the tiles' LDS");
+  constexpr int PER = BM * kKBytes / finish_bytes<WN>();   // waves that one tile buffer serves
+  char* fin = wave < PER ? ta0 : wave < 2 * PER ? tb0 : wave < 3 * PER ? ta1 : tb1;
+  static_assert(NW <= 4 * PER && BM == BN, "every wave has its piece");
+  finish<DT, KIND, true>(g, t, acc, mw, nw, lane, fin + (wave % PER) * finish_bytes<WN>());
 }
 
 // rows per tile of a call's row products
