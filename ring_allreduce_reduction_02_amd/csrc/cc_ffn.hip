@@ -134,9 +134,12 @@ struct GemmArgs {
 // ------------------------------------------------------------------ LDS tiles
 
 // Lines along the summed axis ("row" tiles: R lines of 128 bytes): 16-byte
-// chunks permuted by the line's low bits, so that a fragment's lanes, one
-// line each, spread over the banks.
-__device__ __forceinline__ int row_at(int r, int chunk) { return r * kKBytes + ((chunk ^ (r & 7)) << 4); }
+// chunks permuted by the line's number, so that a fragment's lanes, one line
+// each, spread over all 64 banks (256 bytes: two lines) for any 16 lines in
+// a row.  The plain line number (8 places) measured 4 conflict cycles in the 8
+// of every fragment read.
+__device__ __forceinline__ int row_place(int r, int chunk) { return chunk ^ ((r >> 1) & 7); }
+__device__ __forceinline__ int row_at(int r, int chunk) { return r * kKBytes + (row_place(r, chunk) << 4); }
 
 template <int DT>
 __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
@@ -153,13 +156,19 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
 
 // Column tiles: a line per summed index, R columns long.  bf16 columns are read
 // with the transposing LDS load (16 lanes give the addresses of 4 summed
-// lines x 16 columns and get 4 summed elements of one column each); their
-// 32-byte pieces are permuted by the line's low bits, so that the 4 lines a
-// group reads lie in different banks.
+// lines x 16 columns and get 4 summed elements of one column each); 32-byte
+// pieces are permuted by the line's number, so that the 4 lines and 2 pieces
+// (or 2 line groups) that 32 lanes read lie in different banks.  float32
+// columns are read one element a lane, from two lines 4 apart at a time.
+template <int DT>
+__device__ __forceinline__ int col_place(int k, int chunk) {   // of a 16-byte chunk in its line
+  if constexpr (DT == DT_BF16) return chunk ^ ((k & 3) << 2) ^ ((k & 8) >> 2);
+  else return chunk ^ ((k & 4) << 1);
+}
 template <int DT, int R>
 __device__ __forceinline__ int col_at(int k, int col) {
-  if constexpr (DT == DT_BF16) return k * R * 2 + (((col >> 4) ^ (k & 3)) << 5) + (col & 15) * 2;
-  else return (k * R + col) * 4;
+  constexpr int SZ = Ty<DT>::SZ;
+  return k * R * SZ + (col_place<DT>(k, col * SZ / 16) << 4) + col * SZ % 16;
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -569,14 +578,14 @@ struct Loader {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int k = line_of(wave, q, lane);
-      const int c = 16 * (DT == DT_BF16 ? ((slot >> 1) ^ (k & 3)) * 2 + (slot & 1) : slot);
+      const int c = 16 * col_place<DT>(k, slot);   // its own inverse
       chunk[q] = c0 * SZ + (c < last ? c : last);
     }
   }
-  // row tiles: the chunk of a line's place is the place's number, permuted
-  __device__ __forceinline__ void chunks(int lane) {
+  // row tiles: the chunk that lies at this lane's place of its line
+  __device__ __forceinline__ void chunks(int wave, int lane) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) chunk[q] = (lane & 7) ^ (lane >> 3);
+    for (int q = 0; q < Q; ++q) chunk[q] = row_place(line_of(wave, q, lane), lane & 7);
     step = kKBytes;
   }
 };
@@ -600,7 +609,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   const char *abase = nullptr, *bbase = nullptr;
   int ia[LA::Q], ib[LB::Q];
   if constexpr (!ACOL) {
-    la.chunks(lane);
+    la.chunks(wave, lane);
 #pragma unroll
     for (int q = 0; q < LA::Q; ++q) {
       int r = t.p0 + LA::line_of(wave, q, lane);
@@ -613,7 +622,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   }
   if constexpr (!BCOL) {
     const char* w = wt_ptr(g.b, t.rank, t.local);
-    lb.chunks(lane);
+    lb.chunks(wave, lane);
 #pragma unroll
     for (int q = 0; q < LB::Q; ++q) {
       int64_t row = weight_line<KIND>(g, t, LB::line_of(wave, q, lane));
