@@ -12,6 +12,8 @@
 // float32; h, dg and du are rounded once to the buffers' type between two
 // products, because the matrix cores read that type.
 
+#include <algorithm>
+
 #include "cc_device.h"
 #include "cc_llm.h"
 
@@ -24,8 +26,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 enum Kind { K_GATEUP = 0, K_DOWN = 1, K_DHID = 2, K_DX = 3, K_DW = 4 };
 
-constexpr int kKBytes = 128;   // bytes of the summed axis per stage and line
-constexpr int kUnits = 4;      // matrix instruction steps per stage: 32 bytes of the summed axis each
+constexpr int kKBytes = 64;   // bytes of the summed axis per stage and line
+constexpr int kUnits = 2;     // matrix instruction steps per stage: 32 bytes of the summed axis each
+constexpr int kStages = 4;    // stages in LDS
 
 // ------------------------------------------------------------------ plan
 
@@ -97,6 +100,7 @@ struct RowSide {
   uint64_t rank_stride;
   uint64_t pitch;
   const int* map;
+  uint64_t span;   // bytes that 32-bit offsets may reach: a rank's buffer, or the rows of one expert
 };
 // One matrix an expert.
 struct WtSide {
@@ -133,12 +137,13 @@ struct GemmArgs {
 
 // ------------------------------------------------------------------ LDS tiles
 
-// Lines along the summed axis ("row" tiles: R lines of 128 bytes): 16-byte
+// Lines along the summed axis ("row" tiles: R lines of 64 bytes): 16-byte
 // chunks permuted by the line's number, so that a fragment's lanes, one line
-// each, spread over all 64 banks (256 bytes: two lines) for any 16 lines in
-// a row.  The plain line number (8 places) measured 4 conflict cycles in the 8
-// of every fragment read.
-__device__ __forceinline__ int row_place(int r, int chunk) { return chunk ^ ((r >> 1) & 7); }
+// each, spread over all 64 banks (256 bytes: four lines) for any 16 lines in a
+// row.  (With 128-byte lines permuted by r & 7, 8 places, 4 of the 8 cycles of
+// every fragment read were conflicts.)
+constexpr int kChunks = kKBytes / 16;
+__device__ __forceinline__ int row_place(int r, int chunk) { return chunk ^ ((r / (16 / kChunks)) & (kChunks - 1)); }
 __device__ __forceinline__ int row_at(int r, int chunk) { return r * kKBytes + (row_place(r, chunk) << 4); }
 
 template <int DT>
@@ -513,14 +518,29 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmAr
   finish<DT, KIND, false>(g, t, acc, mw, nw, lane, fin + wave * finish_bytes<WN>());
 }
 
-// ---- aligned rows: tiles come by direct loads to LDS, 16 bytes a lane
+// ---- aligned rows: tiles come by direct loads to LDS, 16 bytes a lane.  Buffer
+// loads, because the compiler counts them apart from the LDS reads around
+// them (behind a global load to LDS it waits for all LDS reads before it uses
+// any).  An offset outside the buffer (kOutside) reads as zeros.
 
-__device__ const uint32_t g_zero[4] = {0, 0, 0, 0};
+constexpr uint32_t kOutside = 0xfffffff0u;
+constexpr uint64_t kMaxSpan = 0xfff00000ull;   // bytes that offsets reach, below kOutside
 
-__device__ __forceinline__ void load_lds(const char* from, char* to) {
-  typedef const __attribute__((address_space(1))) void gv;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char* base, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)(uint32_t)bytes, 0x00020000);
+}
+
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t uniform_off, char* to) {
   typedef __attribute__((address_space(3))) void lv;
-  __builtin_amdgcn_global_load_lds((gv*)from, (lv*)to, 16, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lv*)to, 16, (int)off, (int)uniform_off, 0, 0);
+}
+
+// until at most N of the wave's loads are under way, and none of its LDS reads
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  asm volatile("" ::: "memory");
 }
 
 // One operand's tile of R lines, loaded by NW waves: a wave's load fills 1 KiB
@@ -530,65 +550,69 @@ __device__ __forceinline__ void load_lds(const char* from, char* to) {
 template <int DT, bool COL, int R, int NW>
 struct Loader {
   static constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ;
-  static constexpr int Q = R / 8 / NW;                  // loads per wave and stage
-  static constexpr int LANES = COL ? R * SZ / 16 : 8;   // lanes per line
-  const char* p[Q];      // this lane's address at stage 0 (COL: of the line's first byte, plus the chunk)
-  int chunk[Q];          // row tiles: 16-byte chunk of the stage; column tiles: byte offset of the column chunk
-  uint64_t step;         // bytes per stage (0: lines by number, from a row map)
-  int first;             // summed line of load 0 in the stage (COL)
+  static constexpr int Q = R * kKBytes / 1024 / NW;           // loads per wave and stage
+  static constexpr int LANES = COL ? R * SZ / 16 : kChunks;   // lanes per line
+  __amdgpu_buffer_rsrc_t buf;
+  uint32_t off[Q];      // this lane's bytes at stage 0 (summed lines by a row map: the column chunk's)
+  int last[Q];          // stages in which they lie inside the summed elements
+  uint32_t step;        // bytes per stage
 
   __device__ __forceinline__ static int line_of(int wave, int q, int lane) {
     return (wave * Q + q) * (64 / LANES) + lane / LANES;
   }
-  // load q of stage s
-  __device__ __forceinline__ void issue(char* t, int wave, int lane, int64_t s, int64_t K, bool tail) const {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const char* from = p[q] + s * (int64_t)step;
-      if (tail) {
-        const bool in = COL ? s * BK + line_of(wave, q, lane) < K : s * kKBytes + chunk[q] * 16 < K * SZ;
-        from = in ? from : (const char*)g_zero;
-      }
-      load_lds(from, t + (wave * Q + q) * 1024);
-    }
+  // chunk of a row tile's line that lies at this lane's place
+  __device__ __forceinline__ static int chunk_of(int wave, int q, int lane) {
+    return row_place(line_of(wave, q, lane), lane % kChunks);
   }
-  // load q of stage s, the summed lines being rows[p0 + ...]; idx: their rows
-  __device__ __forceinline__ void issue_rows(char* t, int wave, int lane, int64_t s, int64_t K, bool tail,
-                                             const char* base, uint64_t pitch, const int (&idx)[Q]) const {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const char* from = base + (uint64_t)(uint32_t)idx[q] * pitch + chunk[q];
-      if (tail && s * BK + line_of(wave, q, lane) >= K) from = (const char*)g_zero;
-      load_lds(from, t + (wave * Q + q) * 1024);
-    }
-  }
-  // the rows of stage s
-  __device__ __forceinline__ void rows(int (&idx)[Q], const int* map, int p0, int64_t K, int wave, int lane,
-                                       int64_t s) const {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      int64_t k = s * BK + line_of(wave, q, lane);
-      k = k < K ? k : K - 1;
-      idx[q] = map ? map[p0 + k] : (int)(p0 + k);
-    }
-  }
-  // column chunks of this lane (COL), clamped to the last of C columns
-  __device__ __forceinline__ void columns(int wave, int lane, int c0, int C) {
-    const int slot = lane % LANES, last = (C - c0) * SZ - 16;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int k = line_of(wave, q, lane);
-      const int c = 16 * col_place<DT>(k, slot);   // its own inverse
-      chunk[q] = c0 * SZ + (c < last ? c : last);
-    }
-  }
-  // row tiles: the chunk that lies at this lane's place of its line
-  __device__ __forceinline__ void chunks(int wave, int lane) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) chunk[q] = row_place(line_of(wave, q, lane), lane & 7);
+  // row tiles: off[] are the lines' first bytes
+  __device__ __forceinline__ void lines(int wave, int lane, int K) {
     step = kKBytes;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int c = 16 * chunk_of(wave, q, lane);
+      off[q] += c;
+      last[q] = (int)(((int64_t)K * SZ - c + kKBytes - 1) / kKBytes);
+    }
+  }
+  // column tiles: off[] become the column chunks' bytes, columns c0.. of C
+  __device__ __forceinline__ void columns(int wave, int lane, int c0, int C, int K) {
+    const int end = (C - c0) * SZ - 16;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int k = line_of(wave, q, lane), c = 16 * col_place<DT>(k, lane % LANES);   // its own inverse
+      off[q] = (uint32_t)(c0 * SZ + (c < end ? c : end));
+      last[q] = (K - k + BK - 1) / BK;
+    }
+  }
+  // the loads of stage s (zeros past the end)
+  __device__ __forceinline__ void issue(char* t, int wave, int s, int s_end) const {
+    const uint32_t at = (uint32_t)(s < s_end ? s : s_end) * step;   // never past the buffer by itself
+#pragma unroll
+    for (int q = 0; q < Q; ++q) load_lds(buf, s < last[q] ? off[q] : kOutside, at, t + (wave * Q + q) * 1024);
+  }
+  // the same with the summed lines' rows, idx
+  __device__ __forceinline__ void issue_rows(char* t, int wave, int s, uint32_t pitch, const int (&idx)[Q]) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      load_lds(buf, s < last[q] ? (uint32_t)idx[q] * pitch + off[q] : kOutside, 0, t + (wave * Q + q) * 1024);
+  }
+  // the rows of stage s: from the map, or counted from the expert's first
+  __device__ __forceinline__ void rows(int (&idx)[Q], const int* map, int p0, int K, int wave, int lane,
+                                       int s) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      int k = s * BK + line_of(wave, q, lane);
+      k = k < K ? k : K - 1;
+      idx[q] = map ? map[p0 + k] : k;
+    }
   }
 };
+
+// The buffer that a row operand's offsets count in: the rank's, or for compact
+// rows the part from row p0 on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const RowSide& s, int rank, int p0) {
+  return buffer_of(s.map ? s.base + (uint64_t)rank * s.rank_stride : s.base + (uint64_t)p0 * s.pitch, s.span);
+}
 
 template <int DT, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArgs g) {
@@ -596,8 +620,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ;
   constexpr int TM = WM / 32, TN = WN / 32;
   constexpr bool ACOL = KIND == K_DW, BCOL = KIND == K_DHID || KIND == K_DX || KIND == K_DW;
-  __shared__ __attribute__((aligned(16))) char ta0[BM * kKBytes], tb0[BN * kKBytes];
-  __shared__ __attribute__((aligned(16))) char ta1[BM * kKBytes], tb1[BN * kKBytes];
+  // separate arrays: the compiler then knows which of them a load to LDS fills,
+  // and waits for no other
+  __shared__ __attribute__((aligned(16))) char t0[(BM + BN) * kKBytes], t1[(BM + BN) * kKBytes];
+  __shared__ __attribute__((aligned(16))) char t2[(BM + BN) * kKBytes], t3[(BM + BN) * kKBytes];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mw = (wave % (BM / WM)) * WM, nw = (wave / (BM / WM)) * WN;
@@ -606,82 +632,129 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   typedef Loader<DT, BCOL, BN, NW> LB;
   LA la;
   LB lb;
-  const char *abase = nullptr, *bbase = nullptr;
+  const int K = (int)t.K;
   int ia[LA::Q], ib[LB::Q];
+  la.buf = rows_buffer(g.a, t.rank, t.p0);
   if constexpr (!ACOL) {
-    la.chunks(wave, lane);
 #pragma unroll
     for (int q = 0; q < LA::Q; ++q) {
-      int r = t.p0 + LA::line_of(wave, q, lane);
-      r = r < t.p1 ? r : t.p1 - 1;
-      la.p[q] = row_ptr(g.a, t.rank, r) + la.chunk[q] * 16;
+      int r = LA::line_of(wave, q, lane);
+      r = t.p0 + r < t.p1 ? r : t.p1 - 1 - t.p0;
+      la.off[q] = (uint32_t)(g.a.map ? g.a.map[t.p0 + r] : r) * (uint32_t)g.a.pitch;
     }
+    la.lines(wave, lane, K);
   } else {
-    la.columns(wave, lane, t.m0, g.M);
-    abase = g.a.map ? g.a.base + (uint64_t)t.rank * g.a.rank_stride : g.a.base;
+    la.columns(wave, lane, t.m0, g.M, K);
   }
-  if constexpr (!BCOL) {
-    const char* w = wt_ptr(g.b, t.rank, t.local);
-    lb.chunks(wave, lane);
-#pragma unroll
-    for (int q = 0; q < LB::Q; ++q) {
-      int64_t row = weight_line<KIND>(g, t, LB::line_of(wave, q, lane));
-      row = row >= 0 ? row : 0;
-      lb.p[q] = w + row * (int64_t)g.b.pitch + lb.chunk[q] * 16;
-    }
-  } else if constexpr (KIND == K_DW) {
-    lb.columns(wave, lane, t.n0, g.N);
-    bbase = g.b_rows.map ? g.b_rows.base + (uint64_t)t.rank * g.b_rows.rank_stride : g.b_rows.base;
+  if constexpr (KIND == K_DW) {
+    lb.buf = rows_buffer(g.b_rows, t.rank, t.p0);
+    lb.columns(wave, lane, t.n0, g.N, K);
   } else {
-    const char* w = wt_ptr(g.b, t.rank, t.local);
-    lb.columns(wave, lane, t.n0, g.N);
-    lb.step = (uint64_t)BK * g.b.pitch;
+    lb.buf = buffer_of(wt_ptr(g.b, t.rank, t.local), g.b.expert_stride);
+    if constexpr (BCOL) {
+      lb.columns(wave, lane, t.n0, g.N, K);
+      lb.step = (uint32_t)BK * (uint32_t)g.b.pitch;
 #pragma unroll
-    for (int q = 0; q < LB::Q; ++q) lb.p[q] = w + (uint64_t)LB::line_of(wave, q, lane) * g.b.pitch + lb.chunk[q];
+      for (int q = 0; q < LB::Q; ++q) lb.off[q] += (uint32_t)LB::line_of(wave, q, lane) * (uint32_t)g.b.pitch;
+    } else {
+#pragma unroll
+      for (int q = 0; q < LB::Q; ++q) {
+        const int64_t row = weight_line<KIND>(g, t, LB::line_of(wave, q, lane));
+        lb.off[q] = (uint32_t)(row >= 0 ? row : 0) * (uint32_t)g.b.pitch;
+      }
+      lb.lines(wave, lane, K);
+    }
   }
 
   f32x16 acc[TM][TN];
   clear(acc);
-  const int64_t S = (t.K + 2 * BK - 1) / (2 * BK) * 2;   // an odd last stage is zeros
-  auto rows = [&](int64_t s) {
+  const int S = (K + kStages * BK - 1) / (kStages * BK) * kStages;   // stages past the end are zeros
+  const int s_end = (K + BK - 1) / BK - 1;                      // the last stage with elements
+  auto issue = [&](char* to, int s) {
     if constexpr (KIND == K_DW) {
-      la.rows(ia, g.a.map, t.p0, t.K, wave, lane, s);
-      lb.rows(ib, g.b_rows.map, t.p0, t.K, wave, lane, s);
+      // the next stage's rows first, so that the loads to LDS stay the newest
+      int na[LA::Q], nb[LB::Q];
+      la.rows(na, g.a.map, t.p0, K, wave, lane, s + 1);
+      lb.rows(nb, g.b_rows.map, t.p0, K, wave, lane, s + 1);
+      la.issue_rows(to, wave, s, (uint32_t)g.a.pitch, ia);
+      lb.issue_rows(to + BM * kKBytes, wave, s, (uint32_t)g.b_rows.pitch, ib);
+#pragma unroll
+      for (int q = 0; q < LA::Q; ++q) ia[q] = na[q];
+#pragma unroll
+      for (int q = 0; q < LB::Q; ++q) ib[q] = nb[q];
+    } else {
+      la.issue(to, wave, s, s_end);
+      lb.issue(to + BM * kKBytes, wave, s, s_end);
     }
   };
-  auto issue = [&](char* a, char* b, int64_t s) {
-    const bool tail = (s + 1) * BK > t.K;
-    if constexpr (KIND == K_DW) {
-      la.issue_rows(a, wave, lane, s, t.K, tail, abase, g.a.pitch, ia);
-      lb.issue_rows(b, wave, lane, s, t.K, tail, bbase, g.b_rows.pitch, ib);
-      if (s + 1 < S) rows(s + 1);
-    } else {
-      la.issue(a, wave, lane, s, t.K, tail);
-      lb.issue(b, wave, lane, s, t.K, tail);
+  constexpr int LOADS = LA::Q + LB::Q;
+  u32x4 fa[2][TM], fb[2][TN];
+  auto read = [&](const char* from, int u) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[u & 1][j] = frag<DT, BCOL, BN>(from + BM * kKBytes, u, nw + 32 * j, lane);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[u & 1][i] = frag<DT, ACOL, BM>(from, u, mw + 32 * i, lane);
+  };
+  auto multiply_unit = [&](int u) {
+    __builtin_amdgcn_sched_barrier(0);   // the reads before the matrix instructions that hide them
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Stage s: its tile and the next one's are in LDS (this wave's loads by the
+  // count, every wave's by the barrier), the buffer of stage s - 1 is free.
+  // The next unit's fragments, the next stage's first among them, are read
+  // while the matrix instructions of the last ones run.
+  auto stage = [&](const char* now, const char* next, char* free, int s) {
+    wait_loads<(kStages - 3) * LOADS>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    issue(free, s + kStages - 1);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      if (u + 1 < kUnits) read(now, u + 1);
+      else read(next, 0);
+      multiply_unit(u);
     }
   };
   if (S) {
-    rows(0);
-    issue(ta0, tb0, 0);
+    if constexpr (KIND == K_DW) {
+      la.rows(ia, g.a.map, t.p0, K, wave, lane, 0);
+      lb.rows(ib, g.b_rows.map, t.p0, K, wave, lane, 0);
+    }
+    issue(t0, 0);
+    issue(t1, 1);
+    issue(t2, 2);
+    wait_loads<2 * LOADS>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(t0, 0);
   }
-  for (int64_t s = 0; s < S; s += 2) {
-    __syncthreads();
-    issue(ta1, tb1, s + 1);
-    multiply<DT, ACOL, BCOL, BM, BN>(ta0, tb0, acc, mw, nw, lane);
-    __syncthreads();
-    if (s + 2 < S) issue(ta0, tb0, s + 2);
-    multiply<DT, ACOL, BCOL, BM, BN>(ta1, tb1, acc, mw, nw, lane);
+  for (int s = 0; s < S; s += kStages) {
+    stage(t0, t1, t3, s);
+    stage(t1, t2, t0, s + 1);
+    stage(t2, t3, t1, s + 2);
+    stage(t3, t0, t2, s + 3);
   }
   __syncthreads();   // other waves may still read the last tiles
-  static_assert(NW * finish_bytes<WN>() <= 2 * BM * kKBytes + 2 * BN * kKBytes, "the results pass through the tiles' LDS");
-  constexpr int PER = BM * kKBytes / finish_bytes<WN>();   // waves that one tile buffer serves
-  char* fin = wave < PER ? ta0 : wave < 2 * PER ? tb0 : wave < 3 * PER ? ta1 : tb1;
-  static_assert(NW <= 4 * PER && BM == BN, "every wave has its piece");
+  constexpr int PER = (BM + BN) * kKBytes / finish_bytes<WN>();   // waves that one stage's LDS serves
+  static_assert(NW <= 4 * PER, "every wave has its piece");
+  char* fin = wave < PER ? t0 : wave < 2 * PER ? t1 : wave < 3 * PER ? t2 : t3;
   finish<DT, KIND, true>(g, t, acc, mw, nw, lane, fin + (wave % PER) * finish_bytes<WN>());
 }
 
+// whether the products run as aligned tiles: rows of whole 16-byte vectors, and
+// operands that 32-bit offsets reach
+bool tiled(const FfnLaunch& L) {
+  const uint64_t es = elem_size(L.s.dt), row = std::max(L.s.W, 2 * L.s.F) * es;
+  return L.vec_ok && (uint64_t)L.s.E * L.s.cap * L.s.W * es <= kMaxSpan && L.s.most * row <= kMaxSpan &&
+         2 * L.s.F * L.s.W * es <= kMaxSpan;
+}
+
 // rows per tile of a call's row products
-int row_tile(const FfnLaunch& L) { return L.vec_ok && 4 * L.s.rows >= 3 * 256 * L.s.mtiles256 ? 256 : kFfnRowTile; }
+int row_tile(const FfnLaunch& L) { return tiled(L) && 4 * L.s.rows >= 3 * 256 * L.s.mtiles256 ? 256 : kFfnRowTile; }
 
 template <int KIND, int BM, int BN>
 uint64_t tiles_of(GemmArgs* g) {
@@ -696,7 +769,7 @@ uint64_t tiles_of(GemmArgs* g) {
 
 template <int DT, int KIND>
 hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
-  if (!L.vec_ok) {
+  if (!tiled(L)) {
     const uint64_t blocks = tiles_of<KIND, 128, 128>(&g);
     if (blocks == 0) return hipSuccess;
     CC_LAUNCH((k_ffn_elems<DT, KIND, 128, 128, 64, 64>), dim3((unsigned)blocks), dim3(256), 0, L.st, g);
@@ -758,10 +831,12 @@ GemmArgs gemm_args(const FfnLaunch& L) {
 }
 
 RowSide rows_of(const FfnLaunch& L, const Side& s, uint64_t cols) {
-  return RowSide{s.base, s.stride, cols * elem_size(L.s.dt), (const int*)(L.ws + L.o.rowmap)};
+  const uint64_t pitch = cols * elem_size(L.s.dt);
+  return RowSide{s.base, s.stride, pitch, (const int*)(L.ws + L.o.rowmap), (uint64_t)L.s.E * L.s.cap * pitch};
 }
 RowSide compact(const FfnLaunch& L, uint64_t off, uint64_t cols) {
-  return RowSide{L.ws + off, 0, cols * elem_size(L.s.dt), nullptr};
+  const uint64_t pitch = cols * elem_size(L.s.dt);
+  return RowSide{L.ws + off, 0, pitch, nullptr, L.s.most * pitch};
 }
 WtSide wts(const FfnLaunch& L, const Side& s, uint64_t r, uint64_t c) {
   const uint64_t es = elem_size(L.s.dt);

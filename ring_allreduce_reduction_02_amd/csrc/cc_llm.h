@@ -101,7 +101,7 @@ struct FfnShape {
   int N, E;              // ranks, experts
   uint64_t cap;
   uint64_t W, F;         // width, hidden
-  uint64_t rows;         // kept rows of all experts
+  uint64_t rows, most;   // kept rows of all experts, and of the one with most
   uint64_t mtiles;       // row tiles of all experts, of kFfnRowTile rows
   uint64_t mtiles256;    // and of 256
   int dt, act;
