@@ -26,9 +26,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 enum Kind { K_GATEUP = 0, K_DOWN = 1, K_DHID = 2, K_DX = 3, K_DW = 4 };
 
-constexpr int kKBytes = 64;   // bytes of the summed axis per stage and line
-constexpr int kUnits = 2;     // matrix instruction steps per stage: 32 bytes of the summed axis each
-constexpr int kStages = 4;    // stages in LDS
+constexpr int kKBytes = 128;   // bytes of the summed axis per stage and line: a cache line
+constexpr int kUnits = 4;      // matrix instruction steps per stage: 32 bytes of the summed axis each
 
 // ------------------------------------------------------------------ plan
 
@@ -137,11 +136,11 @@ struct GemmArgs {
 
 // ------------------------------------------------------------------ LDS tiles
 
-// Lines along the summed axis ("row" tiles: R lines of 64 bytes): 16-byte
+// Lines along the summed axis ("row" tiles: R lines of 128 bytes): 16-byte
 // chunks permuted by the line's number, so that a fragment's lanes, one line
-// each, spread over all 64 banks (256 bytes: four lines) for any 16 lines in a
-// row.  (With 128-byte lines permuted by r & 7, 8 places, 4 of the 8 cycles of
-// every fragment read were conflicts.)
+// each, spread over all 64 banks (256 bytes: two lines) for any 16 lines in a
+// row.  (Permuted by r & 7, 8 places, 4 of the 8 cycles of every fragment read
+// were conflicts.)
 constexpr int kChunks = kKBytes / 16;
 __device__ __forceinline__ int row_place(int r, int chunk) { return chunk ^ ((r / (16 / kChunks)) & (kChunks - 1)); }
 __device__ __forceinline__ int row_at(int r, int chunk) { return r * kKBytes + (row_place(r, chunk) << 4); }
@@ -623,7 +622,6 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   // separate arrays: the compiler then knows which of them a load to LDS fills,
   // and waits for no other
   __shared__ __attribute__((aligned(16))) char t0[(BM + BN) * kKBytes], t1[(BM + BN) * kKBytes];
-  __shared__ __attribute__((aligned(16))) char t2[(BM + BN) * kKBytes], t3[(BM + BN) * kKBytes];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mw = (wave % (BM / WM)) * WM, nw = (wave / (BM / WM)) * WN;
@@ -668,7 +666,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
 
   f32x16 acc[TM][TN];
   clear(acc);
-  const int S = (K + kStages * BK - 1) / (kStages * BK) * kStages;   // stages past the end are zeros
+  const int S = (K + 2 * BK - 1) / (2 * BK) * 2;                // an odd last stage is zeros
   const int s_end = (K + BK - 1) / BK - 1;                      // the last stage with elements
   auto issue = [&](char* to, int s) {
     if constexpr (KIND == K_DW) {
@@ -703,21 +701,23 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
       for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stage s: its tile and the next one's are in LDS (this wave's loads by the
-  // count, every wave's by the barrier), the buffer of stage s - 1 is free.
-  // The next unit's fragments, the next stage's first among them, are read
-  // while the matrix instructions of the last ones run.
-  auto stage = [&](const char* now, const char* next, char* free, int s) {
-    wait_loads<(kStages - 3) * LOADS>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    issue(free, s + kStages - 1);
+  // Stage s.  The next unit's fragments are read while the matrix instructions
+  // of the last ones run.  Before the last unit's, every wave has read all of
+  // this stage and its loads of the next one have come (a whole stage after
+  // they were sent): the barrier then frees this stage's LDS for the stage
+  // after the next, and the next stage's first fragments are read.
+  auto stage = [&](char* now, const char* next, int s) {
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      if (u + 1 < kUnits) read(now, u + 1);
-      else read(next, 0);
+    for (int u = 0; u + 1 < kUnits; ++u) {
+      read(now, u + 1);
       multiply_unit(u);
     }
+    wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    issue(now, s + 2);
+    read(next, 0);
+    multiply_unit(kUnits - 1);
   };
   if (S) {
     if constexpr (KIND == K_DW) {
@@ -726,22 +726,19 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
     }
     issue(t0, 0);
     issue(t1, 1);
-    issue(t2, 2);
-    wait_loads<2 * LOADS>();
+    wait_loads<LOADS>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     read(t0, 0);
   }
-  for (int s = 0; s < S; s += kStages) {
-    stage(t0, t1, t3, s);
-    stage(t1, t2, t0, s + 1);
-    stage(t2, t3, t1, s + 2);
-    stage(t3, t0, t2, s + 3);
+  for (int s = 0; s < S; s += 2) {
+    stage(t0, t1, s);
+    stage(t1, t0, s + 1);
   }
   __syncthreads();   // other waves may still read the last tiles
   constexpr int PER = (BM + BN) * kKBytes / finish_bytes<WN>();   // waves that one stage's LDS serves
-  static_assert(NW <= 4 * PER, "every wave has its piece");
-  char* fin = wave < PER ? t0 : wave < 2 * PER ? t1 : wave < 3 * PER ? t2 : t3;
+  static_assert(NW <= 2 * PER, "every wave has its piece");
+  char* fin = wave < PER ? t0 : t1;
   finish<DT, KIND, true>(g, t, acc, mw, nw, lane, fin + (wave % PER) * finish_bytes<WN>());
 }
 
