@@ -583,17 +583,14 @@ struct Loader {
       last[q] = (K - k + BK - 1) / BK;
     }
   }
-  // the loads of stage s (zeros past the end)
-  __device__ __forceinline__ void issue(char* t, int wave, int s, int s_end) const {
+  // load q of stage s (zeros past the end, s_end the last stage inside)
+  __device__ __forceinline__ void issue(char* t, int wave, int q, int s, int s_end) const {
     const uint32_t at = (uint32_t)(s < s_end ? s : s_end) * step;   // never past the buffer by itself
-#pragma unroll
-    for (int q = 0; q < Q; ++q) load_lds(buf, s < last[q] ? off[q] : kOutside, at, t + (wave * Q + q) * 1024);
+    load_lds(buf, s < last[q] ? off[q] : kOutside, at, t + (wave * Q + q) * 1024);
   }
-  // the same with the summed lines' rows, idx
-  __device__ __forceinline__ void issue_rows(char* t, int wave, int s, uint32_t pitch, const int (&idx)[Q]) const {
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      load_lds(buf, s < last[q] ? (uint32_t)idx[q] * pitch + off[q] : kOutside, 0, t + (wave * Q + q) * 1024);
+  // the same with the summed line's row
+  __device__ __forceinline__ void issue_row(char* t, int wave, int q, int s, uint32_t pitch, int row) const {
+    load_lds(buf, s < last[q] ? (uint32_t)row * pitch + off[q] : kOutside, 0, t + (wave * Q + q) * 1024);
   }
   // the rows of stage s: from the map, or counted from the expert's first
   __device__ __forceinline__ void rows(int (&idx)[Q], const int* map, int p0, int K, int wave, int lane,
@@ -668,24 +665,20 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   clear(acc);
   const int S = (K + 2 * BK - 1) / (2 * BK) * 2;                // an odd last stage is zeros
   const int s_end = (K + BK - 1) / BK - 1;                      // the last stage with elements
-  auto issue = [&](char* to, int s) {
+  auto issue_a = [&](char* to, int s, int q) {
+    if constexpr (KIND == K_DW) la.issue_row(to, wave, q, s, (uint32_t)g.a.pitch, ia[q]);
+    else la.issue(to, wave, q, s, s_end);
+  };
+  auto issue_b = [&](char* to, int s, int q) {
+    if constexpr (KIND == K_DW) lb.issue_row(to + BM * kKBytes, wave, q, s, (uint32_t)g.b_rows.pitch, ib[q]);
+    else lb.issue(to + BM * kKBytes, wave, q, s, s_end);
+  };
+  auto rows = [&](int s) {
     if constexpr (KIND == K_DW) {
-      // the next stage's rows first, so that the loads to LDS stay the newest
-      int na[LA::Q], nb[LB::Q];
-      la.rows(na, g.a.map, t.p0, K, wave, lane, s + 1);
-      lb.rows(nb, g.b_rows.map, t.p0, K, wave, lane, s + 1);
-      la.issue_rows(to, wave, s, (uint32_t)g.a.pitch, ia);
-      lb.issue_rows(to + BM * kKBytes, wave, s, (uint32_t)g.b_rows.pitch, ib);
-#pragma unroll
-      for (int q = 0; q < LA::Q; ++q) ia[q] = na[q];
-#pragma unroll
-      for (int q = 0; q < LB::Q; ++q) ib[q] = nb[q];
-    } else {
-      la.issue(to, wave, s, s_end);
-      lb.issue(to + BM * kKBytes, wave, s, s_end);
+      la.rows(ia, g.a.map, t.p0, K, wave, lane, s);
+      lb.rows(ib, g.b_rows.map, t.p0, K, wave, lane, s);
     }
   };
-  constexpr int LOADS = LA::Q + LB::Q;
   u32x4 fa[2][TM], fb[2][TN];
   auto read = [&](const char* from, int u) {
 #pragma unroll
@@ -693,42 +686,61 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
 #pragma unroll
     for (int i = 0; i < TM; ++i) fa[u & 1][i] = frag<DT, ACOL, BM>(from, u, mw + 32 * i, lane);
   };
-  auto multiply_unit = [&](int u) {
+  // unit u's matrix instructions; after each TN of them, one of TM calls between
+  auto multiply_unit = [&](int u, auto between) {
     __builtin_amdgcn_sched_barrier(0);   // the reads before the matrix instructions that hide them
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
-    __builtin_amdgcn_sched_barrier(0);
+      between(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
+  auto nothing = [](int) {};
   // Stage s.  The next unit's fragments are read while the matrix instructions
   // of the last ones run.  Before the last unit's, every wave has read all of
-  // this stage and its loads of the next one have come (a whole stage after
-  // they were sent): the barrier then frees this stage's LDS for the stage
-  // after the next, and the next stage's first fragments are read.
-  auto stage = [&](char* now, const char* next, int s) {
+  // this stage and its loads of the next one have come (three units or more
+  // after they were sent): the barrier then frees this stage's LDS for the
+  // stage after the next, whose loads go out between the matrix instructions
+  // of this unit and the next one, and the next stage's first fragments are
+  // read.
+  auto stage = [&](char* now, char* next, int s) {
 #pragma unroll
     for (int u = 0; u + 1 < kUnits; ++u) {
       read(now, u + 1);
-      multiply_unit(u);
+      if (u == 0) {
+        multiply_unit(u, [&](int i) {
+#pragma unroll
+          for (int q = i; q < LB::Q; q += TM) issue_b(next, s + 1, q);
+        });
+        rows(s + 2);
+      } else {
+        multiply_unit(u, nothing);
+      }
     }
     wait_loads<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    issue(now, s + 2);
     read(next, 0);
-    multiply_unit(kUnits - 1);
+    multiply_unit(kUnits - 1, [&](int i) {
+#pragma unroll
+      for (int q = i; q < LA::Q; q += TM) issue_a(now, s + 2, q);
+    });
   };
   if (S) {
-    if constexpr (KIND == K_DW) {
-      la.rows(ia, g.a.map, t.p0, K, wave, lane, 0);
-      lb.rows(ib, g.b_rows.map, t.p0, K, wave, lane, 0);
-    }
-    issue(t0, 0);
-    issue(t1, 1);
-    wait_loads<LOADS>();
+    // stage 0, and of stage 1 what a stage sends before its first unit
+    rows(0);
+#pragma unroll
+    for (int q = 0; q < LA::Q; ++q) issue_a(t0, 0, q);
+#pragma unroll
+    for (int q = 0; q < LB::Q; ++q) issue_b(t0, 0, q);
+    rows(1);
+    wait_loads<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < LA::Q; ++q) issue_a(t1, 1, q);
     read(t0, 0);
   }
   for (int s = 0; s < S; s += 2) {
