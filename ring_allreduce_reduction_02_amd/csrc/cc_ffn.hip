@@ -237,20 +237,57 @@ enum Act { ACT_SILU = 0, ACT_GELU = 1 };
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * g));
 }
-__device__ __forceinline__ float act_of(float g, int act) {
-  if (act == ACT_SILU) return g * sigmoid(g);
-  return 0.5f * g * erfcf(-g * 0.70710678118654752f);
-}
-// the activation and its derivative
-__device__ __forceinline__ void act_both(float g, int act, float* a, float* d) {
+// the normal distribution function
+__device__ __forceinline__ float normal_cdf(float g) { return 0.5f * erfcf(-g * 0.70710678118654752f); }
+
+// h = act(g) u
+template <int V>
+__device__ __forceinline__ void gate(const float* g, const float* u, int act, float* h) {
   if (act == ACT_SILU) {
-    const float s = sigmoid(g);
-    *a = g * s;
-    *d = s * (1.0f + g * (1.0f - s));
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = g[i] * sigmoid(g[i]) * u[i];
   } else {
-    const float c = 0.5f * erfcf(-g * 0.70710678118654752f);
-    *a = g * c;
-    *d = c + g * expf(-0.5f * g * g) * 0.39894228040143268f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = g[i] * normal_cdf(g[i]) * u[i];
+  }
+}
+// dh -> dg, du and h
+template <int V>
+__device__ __forceinline__ void gate_grad(const float* g, const float* u, int act, const float* dh, float* dg,
+                                          float* du, float* h) {
+  if (act == ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float s = sigmoid(g[i]), a = g[i] * s, d = s * (1.0f + g[i] * (1.0f - s));
+      dg[i] = dh[i] * u[i] * d;
+      du[i] = dh[i] * a;
+      h[i] = a * u[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float c = normal_cdf(g[i]), a = g[i] * c, d = c + g[i] * expf(-0.5f * g[i] * g[i]) * 0.39894228040143268f;
+      dg[i] = dh[i] * u[i] * d;
+      du[i] = dh[i] * a;
+      h[i] = a * u[i];
+    }
+  }
+}
+
+// V floats in one 16-byte vector; bf16 by the hardware's conversion (nearest,
+// ties to even), one instruction for two elements
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <int DT>
+__device__ __forceinline__ u32x4 pack_row(const float* v) {
+  if constexpr (DT == DT_BF16) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[2 * i], v[2 * i + 1]}), bf16x2));
+    return w;
+  } else {
+    return pack<DT>(v);
   }
 }
 
@@ -260,7 +297,7 @@ __device__ __forceinline__ void store_n(char* p, const float* v, int n) {
   if constexpr (VEC) {
     if (n <= 0) return;
     static_assert(V * Ty<DT>::SZ == 16, "one vector");
-    *(u32x4*)p = pack<DT>(v);
+    *(u32x4*)p = pack_row<DT>(v);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -404,10 +441,10 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
       } else if constexpr (KIND == K_DOWN || KIND == K_DX) {
         store_n<DT, VEC, V>(row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ, v, left);
       } else if constexpr (KIND == K_GATEUP) {
+        // the row's place in the rank's buffer, when the pre-activations are kept
         float up[V], h[V];
         read_row<V>(lds + row * PITCH + (at + 32) * 4, up);
-#pragma unroll
-        for (int x = 0; x < V; ++x) h[x] = act_of(v[x], g.act) * up[x];
+        gate<V>(v, up, g.act, h);
         store_n<DT, VEC, V>(row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ, h, left);
         if (g.pre.base) {
           char* pre = row_ptr(g.pre, t.rank, t.p0 + m) + (int64_t)n * SZ;
@@ -416,21 +453,14 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
         }
       } else {   // K_DHID
         const char* pre = row_ptr(g.pre, t.rank, t.p0 + m) + (int64_t)n * SZ;
-        float gt[V], up[V], du[V];
+        float gt[V], up[V], dg[V], du[V], h[V];
         load_n<DT, VEC, V>(pre, gt, left);
         load_n<DT, VEC, V>(pre + (int64_t)g.F * SZ, up, left);
-#pragma unroll
-        for (int x = 0; x < V; ++x) {
-          float a, d;
-          act_both(gt[x], g.act, &a, &d);
-          du[x] = v[x] * a;
-          v[x] = v[x] * up[x] * d;
-          up[x] *= a;
-        }
+        gate_grad<V>(gt, up, g.act, v, dg, du, h);
         char* o = row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ;
-        store_n<DT, VEC, V>(o, v, left);
+        store_n<DT, VEC, V>(o, dg, left);
         store_n<DT, VEC, V>(o + (int64_t)g.F * SZ, du, left);
-        store_n<DT, VEC, V>(row_ptr(g.h, t.rank, t.p0 + m) + (int64_t)n * SZ, up, left);
+        store_n<DT, VEC, V>(row_ptr(g.h, t.rank, t.p0 + m) + (int64_t)n * SZ, h, left);
       }
     }
     wave_lds_sync();
