@@ -59,124 +59,255 @@ struct EmbedGradArgs {
   uint64_t gs;
   char* out;
   uint64_t os;
-  const int* keys;
+  const int* keys;   // each rank's sorted ids and their positions, [N][tokens]
   const int* vals;
-  float* partial;
-  uint64_t n;
+  float* partial;    // [N][pieces][width]
   uint64_t vocab, tokens, width;
-  uint64_t pieces;   // n / kEmbedPiece
+  uint64_t pieces;   // of kEmbedPiece sorted positions per rank; 0: no partial sums
   float scale;
   int N;
 };
 
-// The grad row of sorted position p in segment seg: a summed segment holds
-// all ranks' tokens, rank by rank.
-template <int DT, bool SUM>
-__device__ __forceinline__ const char* grad_row(const EmbedGradArgs& a, uint64_t seg, int val) {
-  uint64_t r = seg, t = (uint32_t)val;
-  if constexpr (SUM) {
-    r = (uint32_t)val / (uint32_t)a.tokens;
-    t = (uint32_t)val - (uint32_t)r * (uint32_t)a.tokens;
-  }
-  return a.grad + r * a.gs + t * a.width * Ty<DT>::SZ;
-}
+// A wave's columns: CB blocks of 64 lanes, V consecutive elements a lane.
+// Enough of them that a row of 2048 bf16 takes one walk over its tokens.
+template <int DT, bool VEC>
+struct Cols {
+  static constexpr int V = VEC ? Ty<DT>::V : 1;
+  static constexpr int CB = VEC ? 4 : 8;
+  static constexpr int STEP = 64 * V * CB;
+};
 
-template <int DT, bool VEC, bool SUM>
-__device__ __forceinline__ void add_rows(const EmbedGradArgs& a, uint64_t seg, uint64_t lo, uint64_t hi, uint64_t c,
-                                         float* acc) {
-  constexpr int V = VEC ? Ty<DT>::V : 1;
-  const int* vals = a.vals + seg * a.n;
-  for (uint64_t p = lo; p < hi; ++p) {
-    const char* g = grad_row<DT, SUM>(a, seg, vals[p]) + c * Ty<DT>::SZ;
-    if constexpr (VEC) {
-      float x[V];
-      unpack<DT>(*(const u32x4*)g, x);
+// acc += the rows of grad at the sorted positions [lo, hi) of rank r, columns
+// c0 + 64 V i + V lane.  Positions are fetched 64 at a time, and their rows
+// four at a time, so that a lane has 4 CB loads under way.
+template <int DT, bool VEC>
+__device__ __forceinline__ void add_rows(const EmbedGradArgs& a, uint64_t r, uint64_t lo, uint64_t hi, uint64_t c0,
+                                         int lane, float (&acc)[Cols<DT, VEC>::CB][Cols<DT, VEC>::V]) {
+  constexpr int V = Cols<DT, VEC>::V, CB = Cols<DT, VEC>::CB, SZ = Ty<DT>::SZ;
+  const int* vals = a.vals + r * a.tokens;
+  const char* base = a.grad + r * a.gs + (c0 + lane * V) * SZ;
+  const uint64_t left = a.width - c0;
+  for (uint64_t p0 = lo; p0 < hi; p0 += 64) {
+    const int n = (int)(hi - p0 < 64 ? hi - p0 : 64);
+    const int mine = lane < n ? vals[p0 + lane] : 0;
+    for (int k = 0; k < n; k += 4) {
+      u32x4 w[4][CB];
+      float x1[4][CB];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += x[i];
-    } else {
-      acc[0] += ld1<DT>(g);
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t t = (uint32_t)__builtin_amdgcn_readlane(mine, k + q < n ? k + q : k);
+        const char* g = base + (uint64_t)t * a.width * SZ;
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+          const bool in = (uint64_t)(i * 64 + lane) * V < left;
+          if constexpr (VEC) w[q][i] = in ? *(const u32x4*)(g + i * 64 * V * SZ) : u32x4{0u, 0u, 0u, 0u};
+          else x1[q][i] = in ? ld1<DT>(g + i * 64 * SZ) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (k + q >= n) break;
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+          if constexpr (VEC) {
+            float x[V];
+            unpack<DT>(w[q][i], x);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[i][e] += x[e];
+          } else {
+            acc[i][0] += x1[q][i];
+          }
+        }
+      }
     }
   }
 }
 
-// Partial sums of the pieces (kEmbedPiece sorted positions) that lie inside
-// one word's run, so that a frequent word is summed by many workgroups.
-template <int DT, bool VEC, bool SUM>
-__global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
-  const uint64_t piece = blockIdx.x, seg = blockIdx.y;
-  const uint64_t p0 = piece * kEmbedPiece;
-  const int* keys = a.keys + seg * a.n;
-  const uint32_t k = (uint32_t)keys[p0];
-  if (k >= a.vocab || k != (uint32_t)keys[p0 + kEmbedPiece - 1]) return;
-  float* o = a.partial + (seg * a.pieces + piece) * a.width;
-  constexpr int V = VEC ? Ty<DT>::V : 1;
-  for (uint64_t c = (uint64_t)threadIdx.x * V; c < a.width; c += kEmbedBlock * V) {
-    float acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    add_rows<DT, VEC, SUM>(a, seg, p0, p0 + kEmbedPiece, c, acc);
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[c + i] = acc[i];
-  }
-}
-
 // first sorted position whose key is at least k
-__device__ __forceinline__ uint64_t lower_bound(const int* keys, uint64_t n, uint32_t k) {
-  uint64_t lo = 0, hi = n;
+__device__ __forceinline__ uint32_t lower_bound(const int* keys, uint32_t n, uint32_t k) {
+  uint32_t lo = 0, hi = n;
   while (lo < hi) {
-    const uint64_t mid = (lo + hi) >> 1;
+    const uint32_t mid = (lo + hi) >> 1;
     if ((uint32_t)keys[mid] < k) lo = mid + 1; else hi = mid;
   }
   return lo;
 }
 
-constexpr int kEmbedRows = 8;   // table rows per workgroup
+// Partial sums of the pieces (kEmbedPiece sorted positions) that lie inside
+// one word's run of kEmbedLong or more, one wave each, so that a frequent word
+// is summed by many.
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
+  typedef Cols<DT, VEC> C;
+  const int lane = threadIdx.x & 63;
+  const uint64_t piece = (uint64_t)blockIdx.x * (kEmbedBlock / 64) + (threadIdx.x >> 6), r = blockIdx.y;
+  if (piece >= a.pieces) return;
+  const uint64_t p0 = piece * kEmbedPiece;
+  const int* keys = a.keys + r * a.tokens;
+  const uint32_t k = (uint32_t)keys[p0];
+  if (k >= a.vocab || k != (uint32_t)keys[p0 + kEmbedPiece - 1]) return;
+  const uint32_t end = lower_bound(keys, (uint32_t)a.tokens, k + (lane & 1));   // the run's first and last + 1
+  if (__builtin_amdgcn_readlane(end, 1) - __builtin_amdgcn_readlane(end, 0) < kEmbedLong) return;
+  float* o = a.partial + (r * a.pieces + piece) * a.width;
+  for (uint64_t c0 = 0; c0 < a.width; c0 += C::STEP) {
+    float acc[C::CB][C::V] = {};
+    add_rows<DT, VEC>(a, r, p0, p0 + kEmbedPiece, c0, lane, acc);
+#pragma unroll
+    for (int i = 0; i < C::CB; ++i)
+#pragma unroll
+      for (int e = 0; e < C::V; ++e) {
+        const uint64_t c = c0 + (uint64_t)(i * 64 + lane) * C::V + e;
+        if (c < a.width) o[c] = acc[i][e];
+      }
+  }
+}
+
+// acc += the sorted positions [lo, hi) of rank r, part of a run of `run`
+// positions: of a long run, whole pieces come as their partial sums.
+template <int DT, bool VEC>
+__device__ __forceinline__ void add_run(const EmbedGradArgs& a, uint64_t r, uint64_t lo, uint64_t hi, uint64_t run,
+                                        uint64_t c0, int lane, float (&acc)[Cols<DT, VEC>::CB][Cols<DT, VEC>::V]) {
+  typedef Cols<DT, VEC> C;
+  const uint64_t f = (lo + kEmbedPiece - 1) / kEmbedPiece, l = hi / kEmbedPiece;
+  if (a.pieces == 0 || run < kEmbedLong || f >= l) {
+    add_rows<DT, VEC>(a, r, lo, hi, c0, lane, acc);
+    return;
+  }
+  add_rows<DT, VEC>(a, r, lo, f * kEmbedPiece, c0, lane, acc);
+  const float* part = a.partial + (r * a.pieces + f) * a.width + c0 + lane * C::V;
+  for (uint64_t p = f; p < l; ++p, part += a.width)
+#pragma unroll
+    for (int k = 0; k < C::CB; ++k)
+      if (c0 + (uint64_t)(k * 64 + lane) * C::V < a.width)
+#pragma unroll
+        for (int e = 0; e < C::V; ++e) acc[k][e] += part[k * 64 * C::V + e];
+  add_rows<DT, VEC>(a, r, l * kEmbedPiece, hi, c0, lane, acc);
+}
+
+// columns of acc, scaled, to the ranks [r0, r0 + nr)
+template <int DT, bool VEC>
+__device__ __forceinline__ void put_row(const EmbedGradArgs& a, char* o, int r0, int nr, uint64_t c0, int lane,
+                                        float (&acc)[Cols<DT, VEC>::CB][Cols<DT, VEC>::V]) {
+  typedef Cols<DT, VEC> C;
+#pragma unroll
+  for (int k = 0; k < C::CB; ++k) {
+    const uint64_t c = c0 + (uint64_t)(k * 64 + lane) * C::V;
+    if (c >= a.width) continue;
+#pragma unroll
+    for (int e = 0; e < C::V; ++e) acc[k][e] *= a.scale;
+    for (int r = r0; r < r0 + nr; ++r) {
+      char* to = o + (uint64_t)r * a.os + c * Ty<DT>::SZ;
+      if constexpr (VEC) stg(to, pack<DT>(acc[k]));
+      else st1<DT>(to, acc[k][0]);
+    }
+  }
+}
+
+// a row of zeros: whole vectors wherever the row starts
+template <int DT>
+__device__ __forceinline__ void zero_row(char* o, uint64_t bytes, int lane) {
+  const uint64_t head = (16 - ((uintptr_t)o & 15u)) & 15u, h = head < bytes ? head : bytes;
+  constexpr int SZ = Ty<DT>::SZ;
+  if ((uint64_t)lane * SZ < h) st1<DT>(o + lane * SZ, 0.0f);
+  const uint64_t body = (bytes - h) / 16 * 16;
+  for (uint64_t c = (uint64_t)lane * 16; c < body; c += 1024) stg(o + h + c, u32x4{0u, 0u, 0u, 0u});
+  const uint64_t tail = h + body + (uint64_t)lane * SZ;
+  if (tail < bytes) st1<DT>(o + tail, 0.0f);
+}
+
+// A workgroup takes every gridDim.x-th table row, up to 16 of them (frequent
+// words have neighbouring ids and so fall to different workgroups).  Where a
+// row's tokens lie in the sorted ids is found by binary search, all rows (and
+// ranks) of the workgroup at once.  Most rows have none and are written as
+// zeros; a wave sums a row of a few tokens by itself, and the four waves a
+// row of kEmbedShared or more, each a quarter of them.  SUM: the tokens of all
+// ranks, rank by rank, and the row on every rank; else of the workgroup's rank.
+constexpr int kEmbedRows = 16;
+constexpr uint32_t kEmbedShared = 16;
+constexpr int kEmbedWaves = kEmbedBlock / 64;
 
 template <int DT, bool VEC, bool SUM>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
-  __shared__ uint64_t begin[kEmbedRows + 1];
-  const uint64_t seg = blockIdx.y, v0 = (uint64_t)blockIdx.x * kEmbedRows;
-  if (threadIdx.x <= kEmbedRows) begin[threadIdx.x] = lower_bound(a.keys + seg * a.n, a.n, (uint32_t)(v0 + threadIdx.x));
+  typedef Cols<DT, VEC> C;
+  constexpr int SZ = Ty<DT>::SZ, NR = SUM ? kMaxRanks : 1;
+  __shared__ uint32_t begin[NR][kEmbedRows], end[NR][kEmbedRows];
+  __shared__ uint32_t total[kEmbedRows];
+  __shared__ float part[kEmbedWaves - 1][C::STEP];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r0 = SUM ? 0 : (int)blockIdx.y, nr = SUM ? a.N : 1;
+  const uint64_t v0 = blockIdx.x, dv = gridDim.x;
+  const int rows = (int)((a.vocab - v0 + dv - 1) / dv);
+  for (int i = threadIdx.x; i < nr * 2 * kEmbedRows; i += kEmbedBlock) {
+    const int r = i / (2 * kEmbedRows), row = (i / 2) % kEmbedRows;
+    const uint32_t at = row < rows ? lower_bound(a.keys + (uint64_t)(r0 + r) * a.tokens, (uint32_t)a.tokens,
+                                                 (uint32_t)(v0 + row * dv) + (i & 1))
+                                   : 0u;
+    if (i & 1) end[r][row] = at; else begin[r][row] = at;
+  }
   __syncthreads();
-  const int rows = (int)(a.vocab - v0 < kEmbedRows ? a.vocab - v0 : kEmbedRows);
-  constexpr int V = VEC ? Ty<DT>::V : 1;
+  if (threadIdx.x < kEmbedRows) {
+    uint32_t n = 0;
+    for (int r = 0; r < nr; ++r) n += end[r][threadIdx.x] - begin[r][threadIdx.x];
+    total[threadIdx.x] = n;
+  }
+  __syncthreads();
+  for (int i = wave; i < rows; i += kEmbedWaves) {
+    if (total[i] >= kEmbedShared) continue;
+    char* const o = a.out + (v0 + i * dv) * a.width * SZ;
+    if (total[i] == 0) {
+      for (int r = r0; r < r0 + nr; ++r) zero_row<DT>(o + (uint64_t)r * a.os, a.width * SZ, lane);
+      continue;
+    }
+    for (uint64_t c0 = 0; c0 < a.width; c0 += C::STEP) {
+      float acc[C::CB][C::V] = {};
+      for (int r = 0; r < nr; ++r)
+        if (begin[r][i] < end[r][i]) add_rows<DT, VEC>(a, r0 + r, begin[r][i], end[r][i], c0, lane, acc);
+      put_row<DT, VEC>(a, o, r0, nr, c0, lane, acc);
+    }
+  }
   for (int i = 0; i < rows; ++i) {
-    const uint64_t lo = begin[i], hi = begin[i + 1];
-    // whole pieces of a long run come as their partial sums
-    const uint64_t f = (lo + kEmbedPiece - 1) / kEmbedPiece, l = hi / kEmbedPiece;
-    for (uint64_t c = (uint64_t)threadIdx.x * V; c < a.width; c += kEmbedBlock * V) {
-      float acc[V];
-#pragma unroll
-      for (int q = 0; q < V; ++q) acc[q] = 0.0f;
-      if (f < l) {
-        add_rows<DT, VEC, SUM>(a, seg, lo, f * kEmbedPiece, c, acc);
-        for (uint64_t p = f; p < l; ++p)
-#pragma unroll
-          for (int q = 0; q < V; ++q) acc[q] += a.partial[(seg * a.pieces + p) * a.width + c + q];
-        add_rows<DT, VEC, SUM>(a, seg, l * kEmbedPiece, hi, c, acc);
-      } else {
-        add_rows<DT, VEC, SUM>(a, seg, lo, hi, c, acc);
+    if (total[i] < kEmbedShared) continue;
+    // this wave's quarter of the tokens, counted over the ranks
+    const uint32_t w0 = (uint32_t)((uint64_t)total[i] * wave / kEmbedWaves);
+    const uint32_t w1 = (uint32_t)((uint64_t)total[i] * (wave + 1) / kEmbedWaves);
+    for (uint64_t c0 = 0; c0 < a.width; c0 += C::STEP) {
+      float acc[C::CB][C::V] = {};
+      uint32_t before = 0;
+      for (int r = 0; r < nr; ++r) {
+        const uint32_t lo = begin[r][i], n = end[r][i] - lo;
+        const uint32_t f = w0 > before ? w0 - before : 0, l = w1 > before ? w1 - before : 0;
+        if (f < n && l) add_run<DT, VEC>(a, r0 + r, lo + f, lo + (l < n ? l : n), n, c0, lane, acc);
+        before += n;
       }
+      __syncthreads();   // the last columns' parts are read
+      if (wave)
 #pragma unroll
-      for (int q = 0; q < V; ++q) acc[q] *= a.scale;
-      const uint64_t at = ((v0 + i) * a.width + c) * Ty<DT>::SZ;
-      const int r0 = SUM ? 0 : (int)seg, r1 = SUM ? a.N : r0 + 1;
-      for (int r = r0; r < r1; ++r) {
-        char* o = a.out + (uint64_t)r * a.os + at;
-        if constexpr (VEC) *(u32x4*)o = pack<DT>(acc);
-        else st1<DT>(o, acc[0]);
+        for (int k = 0; k < C::CB; ++k)
+#pragma unroll
+          for (int e = 0; e < C::V; ++e) part[wave - 1][(k * C::V + e) * 64 + lane] = acc[k][e];
+      __syncthreads();
+      if (wave == 0) {
+        for (int w = 0; w < kEmbedWaves - 1; ++w)
+#pragma unroll
+          for (int k = 0; k < C::CB; ++k)
+#pragma unroll
+            for (int e = 0; e < C::V; ++e) acc[k][e] += part[w][(k * C::V + e) * 64 + lane];
+        put_row<DT, VEC>(a, a.out + (v0 + i * dv) * a.width * SZ, r0, nr, c0, lane, acc);
       }
     }
   }
 }
 
-template <int DT, bool VEC, bool SUM>
+template <int DT, bool VEC>
 hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
-  const unsigned segs = SUM ? 1 : (unsigned)L.N;
-  if (a.pieces)
-    CC_LAUNCH((k_embed_pieces<DT, VEC, SUM>), dim3((unsigned)a.pieces, segs), dim3(kEmbedBlock), 0, L.st, a);
+  if (a.pieces) {
+    const unsigned blocks = (unsigned)((a.pieces + kEmbedBlock / 64 - 1) / (kEmbedBlock / 64));
+    CC_LAUNCH((k_embed_pieces<DT, VEC>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), 0, L.st, a);
+  }
   const unsigned blocks = (unsigned)((a.vocab + kEmbedRows - 1) / kEmbedRows);
-  CC_LAUNCH((k_embed_grad<DT, VEC, SUM>), dim3(blocks, segs), dim3(kEmbedBlock), 0, L.st, a);
+  const unsigned lds = L.blocks_per_cu > 0 ? lds_for_blocks_per_cu(L.blocks_per_cu) : 0;
+  if (L.summed) CC_LAUNCH((k_embed_grad<DT, VEC, true>), dim3(blocks), dim3(kEmbedBlock), lds, L.st, a);
+  else CC_LAUNCH((k_embed_grad<DT, VEC, false>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), lds, L.st, a);
   return hipGetLastError();
 }
 
@@ -196,14 +327,10 @@ hipError_t launch_embed(const EmbedLaunch& L) {
 }
 
 hipError_t launch_embed_grad(const EmbedGradLaunch& L) {
-  EmbedGradArgs a{L.grad, L.grad_stride, L.out, L.out_stride, L.keys, L.vals, L.partial, L.n,
-                  L.vocab, L.tokens, L.width, L.n / kEmbedPiece, L.scale, L.N};
-  if (L.dt == DT_F32) {
-    if (L.vec_ok) return L.summed ? run_embed_grad<DT_F32, true, true>(a, L) : run_embed_grad<DT_F32, true, false>(a, L);
-    return L.summed ? run_embed_grad<DT_F32, false, true>(a, L) : run_embed_grad<DT_F32, false, false>(a, L);
-  }
-  if (L.vec_ok) return L.summed ? run_embed_grad<DT_BF16, true, true>(a, L) : run_embed_grad<DT_BF16, true, false>(a, L);
-  return L.summed ? run_embed_grad<DT_BF16, false, true>(a, L) : run_embed_grad<DT_BF16, false, false>(a, L);
+  EmbedGradArgs a{L.grad, L.grad_stride, L.out, L.out_stride, L.keys, L.vals, L.partial,
+                  L.vocab, L.tokens, L.width, embed_pieces(L.tokens), L.scale, L.N};
+  if (L.dt == DT_F32) return L.vec_ok ? run_embed_grad<DT_F32, true>(a, L) : run_embed_grad<DT_F32, false>(a, L);
+  return L.vec_ok ? run_embed_grad<DT_BF16, true>(a, L) : run_embed_grad<DT_BF16, false>(a, L);
 }
 
 }  // namespace cc

@@ -10,27 +10,23 @@
 
 namespace cc {
 
-// ---- stable sort of int32 keys with their positions, in `segs` segments of
-// n keys each.  Keys outside [0, nkeys) sort last, as the key nkeys.
-// Segment g's keys start at keys + g * key_stride; with `flat` every segment
-// is n / flat_n rows of flat_n keys, key_stride bytes apart (one segment over
-// all ranks' keys).
+// ---- stable sort of each rank's n int32 keys with their positions.  Keys
+// outside [0, nkeys) sort last, as the key nkeys.
 struct SortPlan {
-  int segs;
-  uint64_t n;        // keys per segment, < 2^31
+  int N;
+  uint64_t n;        // keys per rank, < 2^31
   uint32_t nkeys;
   int passes;        // of 8 bits
-  uint64_t tiles;    // per segment and pass
+  uint64_t tiles;    // per rank and pass; 0: one workgroup sorts a rank's keys in LDS
   uint64_t bytes;    // of workspace
 };
-SortPlan sort_plan(int segs, uint64_t n, uint32_t nkeys);
+SortPlan sort_plan(int N, uint64_t n, uint32_t nkeys);
 struct SortLaunch {
   SortPlan p;
-  const char* keys;
-  uint64_t key_stride;   // bytes between segments (or between rows, flat)
-  uint64_t row_n;        // keys per row: n, or the row length of a flat segment
+  const char* keys;      // rank-strided
+  uint64_t key_stride;
   char* ws;              // p.bytes, 16-byte aligned
-  // outputs inside ws, [segs][n] int32: sorted keys and their positions
+  // outputs inside ws, [N][n] int32: sorted keys and their positions
   const int* sorted_keys;
   const int* sorted_vals;
   hipStream_t st;
@@ -52,20 +48,24 @@ struct EmbedLaunch {
 };
 hipError_t launch_embed(const EmbedLaunch& L);
 
-constexpr int kEmbedPiece = 32;   // sorted positions per partial sum of a long run
+// Sorted positions per partial sum of a long run, the shortest run that has
+// them, and how many a rank's tokens have; none up to 512 tokens, where a
+// workgroup sums a whole run itself in the time of the extra launch.
+constexpr int kEmbedPiece = 32;
+constexpr uint32_t kEmbedLong = 128;
+inline uint64_t embed_pieces(uint64_t tokens) { return tokens > 512 ? tokens / kEmbedPiece : 0; }
 struct EmbedGradLaunch {
   const char* grad;
   uint64_t grad_stride;
   char* out;
   uint64_t out_stride;
-  const int* keys;       // sorted, [segs][n]
+  const int* keys;       // sorted, [N][tokens]
   const int* vals;
-  float* partial;        // [segs][n / kEmbedPiece][width]
-  uint64_t n;            // keys per segment
+  float* partial;        // [N][embed_pieces][width]
   uint64_t vocab, tokens, width;
   float scale;
   int N, dt, vec_ok, blocks_per_cu;
-  int summed;            // one segment over all ranks, the result on every rank
+  int summed;            // over all ranks, the result on every rank
   hipStream_t st;
 };
 hipError_t launch_embed_grad(const EmbedGradLaunch& L);

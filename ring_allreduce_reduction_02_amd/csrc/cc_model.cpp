@@ -96,19 +96,16 @@ cc_status_t embed_sizes(int nranks, uint64_t vocab, uint64_t tokens, uint64_t wi
   return CC_OK;
 }
 
-// the sort of each rank's ids (or of all ranks' together) and the partial
-// sums of its whole pieces
+// the sort of each rank's ids and the partial sums of its pieces
 struct EmbedWs {
   SortPlan sort;
   uint64_t partial, bytes;
 };
-EmbedWs embed_ws(int N, uint64_t vocab, uint64_t tokens, uint64_t width, bool summed) {
+EmbedWs embed_ws(int N, uint64_t vocab, uint64_t tokens, uint64_t width) {
   EmbedWs w;
-  const int segs = summed ? 1 : N;
-  const uint64_t n = summed ? (uint64_t)N * tokens : tokens;
-  w.sort = sort_plan(segs, n, (uint32_t)vocab);
+  w.sort = sort_plan(N, tokens, (uint32_t)vocab);
   w.partial = w.sort.bytes;
-  w.bytes = w.partial + rup((uint64_t)segs * (n / kEmbedPiece) * width * 4, 256);
+  w.bytes = tokens ? w.partial + rup((uint64_t)N * embed_pieces(tokens) * width * 4, 256) : 0;
   return w;
 }
 
@@ -123,8 +120,8 @@ cc_status_t embed_grad(cc_rankbuf_t grad, cc_rankbuf_t ids, cc_rankbuf_t dtable,
                    {&dtable, (u128)vocab * width * es, "dtable", true, N}};
   const u128 whole = (u128)N * tokens * width * 4 + (u128)N * tokens * 64;
   if (whole >= kByteLimit) return fail(CC_ERR_INVALID_ARG, "grad is too large");
-  const EmbedWs w = embed_ws(N, vocab, tokens, width, summed);
-  if ((s = check_bufs(b, 3, cfg, tokens ? w.bytes : 0, "cc_embedding_grad_workspace_size")) ||
+  const EmbedWs w = embed_ws(N, vocab, tokens, width);
+  if ((s = check_bufs(b, 3, cfg, w.bytes, "cc_embedding_grad_workspace_size")) ||
       (s = check_elems(grad, es, "grad")) || (s = check_elems(ids, 4, "ids")) || (s = check_elems(dtable, es, "dtable")))
     return s;
   if ((s = device_ready())) return s;
@@ -132,7 +129,6 @@ cc_status_t embed_grad(cc_rankbuf_t grad, cc_rankbuf_t ids, cc_rankbuf_t dtable,
   so.p = w.sort;
   so.keys = (const char*)ids.base;
   so.key_stride = ids.rank_stride_bytes;
-  so.row_n = tokens;
   so.ws = (char*)cfg.workspace;
   so.st = st;
   if (tokens) {
@@ -144,7 +140,6 @@ cc_status_t embed_grad(cc_rankbuf_t grad, cc_rankbuf_t ids, cc_rankbuf_t dtable,
   L.out = (char*)dtable.base; L.out_stride = dtable.rank_stride_bytes;
   L.keys = so.sorted_keys; L.vals = so.sorted_vals;
   L.partial = (float*)((char*)cfg.workspace + w.partial);
-  L.n = w.sort.n;
   L.vocab = vocab; L.tokens = tokens; L.width = width;
   L.scale = scale;
   L.N = N; L.dt = (int)dtype; L.blocks_per_cu = cfg.blocks_per_cu;
@@ -302,9 +297,7 @@ cc_status_t cc_embedding_grad_workspace_size(int nranks, size_t vocab, size_t to
   if (!bytes) return fail(CC_ERR_INVALID_ARG, "bytes is NULL");
   if ((u128)nranks * tokens * width * 4 + (u128)nranks * tokens * 64 >= kByteLimit)
     return fail(CC_ERR_INVALID_ARG, "grad is too large");
-  *bytes = tokens == 0 ? 0
-                       : (size_t)std::max(embed_ws(nranks, vocab, tokens, width, false).bytes,
-                                          embed_ws(nranks, vocab, tokens, width, true).bytes);
+  *bytes = (size_t)embed_ws(nranks, vocab, tokens, width).bytes;
   return ok();
 }
 
@@ -339,9 +332,8 @@ cc_status_t cc_moe_route(cc_rankbuf_t logits, cc_rankbuf_t experts, cc_rankbuf_t
     hipError_t e = launch_route(L);
     if (e != hipSuccess) return hip_status(e, "MoE routing");
     so.p = p;
-    so.keys = experts.base ? (const char*)experts.base : nullptr;
+    so.keys = (const char*)experts.base;
     so.key_stride = experts.rank_stride_bytes;
-    so.row_n = (uint64_t)tokens * topk;
     so.ws = (char*)cfg.workspace;
     so.st = (hipStream_t)stream;
     if ((e = launch_sort(&so)) != hipSuccess) return hip_status(e, "MoE routing (sort)");

@@ -24,12 +24,11 @@ constexpr int kDigits = 256;
 struct SortArgs {
   const char* keys;      // first pass: the caller's keys
   uint64_t key_stride;
-  uint64_t row_n;
   const int* kin;        // later passes
   const int* vin;
   int* kout;
   int* vout;
-  uint32_t* hist;        // [segs][kDigits][tiles]
+  uint32_t* hist;        // [N][kDigits][tiles]
   uint64_t n;
   uint32_t nkeys;
   uint32_t tiles;
@@ -37,13 +36,104 @@ struct SortArgs {
   int first;
 };
 
-__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint64_t seg, uint64_t i) {
-  if (!a.first) return (uint32_t)a.kin[seg * a.n + i];
-  // a flat segment walks rows of row_n keys; otherwise row_n == n
-  const uint64_t row = a.row_n == a.n ? seg : i / a.row_n;
-  const uint64_t col = a.row_n == a.n ? i : i - row * a.row_n;
-  const uint32_t k = (uint32_t)((const int*)(a.keys + row * a.key_stride))[col];
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint64_t rank, uint64_t i) {
+  if (!a.first) return (uint32_t)a.kin[rank * a.n + i];
+  const uint32_t k = (uint32_t)((const int*)(a.keys + rank * a.key_stride))[i];
   return k < a.nkeys ? k : a.nkeys;
+}
+
+// The lanes of a wave whose digit is d, for every lane of `in`.
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, bool in) {
+  uint64_t same = __ballot(in);
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const uint64_t one = __ballot((d >> b) & 1u);
+    same &= ((d >> b) & 1u) ? one : ~one;
+  }
+  return same;
+}
+
+// Up to kLdsSortMax keys of a rank, all passes in one workgroup: keys and
+// positions stay in registers between passes and change places through LDS.
+// Wave w holds the keys [w, w + 1) * 64 R, 64 a round, as in a tile below.
+// 4096 keys of 15 bits: 2 passes in one launch instead of six launches.
+constexpr int kLdsSortBlock = 1024;
+constexpr int kLdsSortWaves = kLdsSortBlock / 64;
+constexpr int kLdsSortMax = 8192;
+
+template <int R>
+__global__ __launch_bounds__(kLdsSortBlock) void k_sort_lds(SortArgs a, int passes) {
+  __shared__ uint32_t cnt[kLdsSortWaves][kDigits];
+  __shared__ uint32_t base[kDigits];
+  __shared__ uint32_t wsum[kDigits / 64];
+  __shared__ uint2 kv[R * kLdsSortBlock];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t n = (uint32_t)a.n, i0 = wave * 64 * R + lane;
+  const uint64_t rank = blockIdx.x, below = (1ull << lane) - 1;
+  uint32_t key[R], val[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const uint32_t i = i0 + q * 64;
+    key[q] = i < n ? sort_key(a, rank, i) : 0u;
+    val[q] = i;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    for (int d = threadIdx.x; d < kLdsSortWaves * kDigits; d += kLdsSortBlock) (&cnt[0][0])[d] = 0;
+    __syncthreads();
+    uint32_t place[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const bool in = i0 + q * 64 < n;
+      const uint32_t d = (key[q] >> (8 * pass)) & (kDigits - 1);
+      const uint64_t same = same_digit(d, in);
+      volatile uint32_t* c = &cnt[wave][d];
+      const uint32_t before = *c;
+      place[q] = before + (uint32_t)__popcll(same & below);
+      if (in && (same & below) == 0) *c = before + (uint32_t)__popcll(same);
+    }
+    __syncthreads();
+    // exclusive prefix over (digit, wave)
+    if (threadIdx.x < kDigits) {
+      uint32_t all = 0;
+#pragma unroll
+      for (int w = 0; w < kLdsSortWaves; ++w) {
+        const uint32_t c = cnt[w][threadIdx.x];
+        cnt[w][threadIdx.x] = all;
+        all += c;
+      }
+      uint32_t s = all;
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t t = __shfl_up(s, d);
+        if (lane >= d) s += t;
+      }
+      base[threadIdx.x] = s - all;
+      if (lane == 63) wsum[wave] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      if (i0 + q * 64 >= n) continue;
+      const uint32_t d = (key[q] >> (8 * pass)) & (kDigits - 1);
+      uint32_t at = base[d] + cnt[wave][d] + place[q];
+      for (uint32_t w = 0; w < (d >> 6); ++w) at += wsum[w];
+      kv[at] = make_uint2(key[q], val[q]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const uint32_t i = i0 + q * 64;
+      if (i >= n) continue;
+      key[q] = kv[i].x;
+      val[q] = kv[i].y;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const uint32_t i = i0 + q * 64;
+    if (i >= n) continue;
+    a.kout[rank * a.n + i] = (int)key[q];
+    a.vout[rank * a.n + i] = (int)val[q];
+  }
 }
 
 __global__ __launch_bounds__(kSortBlock) void k_sort_hist(SortArgs a) {
@@ -59,7 +149,7 @@ __global__ __launch_bounds__(kSortBlock) void k_sort_hist(SortArgs a) {
   a.hist[((uint64_t)blockIdx.y * kDigits + threadIdx.x) * a.tiles + blockIdx.x] = h[threadIdx.x];
 }
 
-// Exclusive prefix over a segment's kDigits * tiles counts, in place.
+// Exclusive prefix over a rank's kDigits * tiles counts, in place.
 constexpr int kScanBlock = 1024;
 __global__ __launch_bounds__(kScanBlock) void k_sort_scan(uint32_t* hist, uint64_t count) {
   __shared__ uint32_t wsum[kScanBlock / 64];
@@ -106,11 +196,7 @@ __global__ __launch_bounds__(kSortBlock) void k_sort_scatter(SortArgs a) {
     key[q] = in ? sort_key(a, blockIdx.y, i) : 0u;
     val[q] = in ? (a.first ? (int)i : a.vin[(uint64_t)blockIdx.y * a.n + i]) : 0;
     const uint32_t d = (key[q] >> a.shift) & (kDigits - 1);
-    uint64_t same = __ballot(in);
-    for (int b = 0; b < 8; ++b) {
-      const uint64_t one = __ballot((d >> b) & 1u);
-      same &= ((d >> b) & 1u) ? one : ~one;
-    }
+    const uint64_t same = same_digit(d, in);
     // lanes of one digit read its count, then the lowest of them adds theirs
     // (a wave's LDS accesses complete in program order; volatile keeps it)
     volatile uint32_t* c = &cnt[wave][d];
@@ -143,36 +229,51 @@ uint64_t up(uint64_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-SortPlan sort_plan(int segs, uint64_t n, uint32_t nkeys) {
+SortPlan sort_plan(int N, uint64_t n, uint32_t nkeys) {
   SortPlan p;
-  p.segs = segs;
+  p.N = N;
   p.n = n;
   p.nkeys = nkeys;
   p.passes = 1;
   while (p.passes < 4 && (nkeys >> (8 * p.passes)) != 0) ++p.passes;   // the key nkeys itself is sorted too
-  p.tiles = (n + kSortTile - 1) / kSortTile;
-  const uint64_t arr = up((uint64_t)segs * n * 4);
-  p.bytes = 4 * arr + up((uint64_t)segs * kDigits * p.tiles * 4);
+  p.tiles = n <= kLdsSortMax ? 0 : (n + kSortTile - 1) / kSortTile;
+  const uint64_t arr = up((uint64_t)N * n * 4);
+  p.bytes = (p.tiles && p.passes > 1 ? 4 : 2) * arr + up((uint64_t)N * kDigits * p.tiles * 4);
   return p;
 }
 
 hipError_t launch_sort(SortLaunch* L) {
   const SortPlan& p = L->p;
-  const uint64_t arr = up((uint64_t)p.segs * p.n * 4);
-  int* k[2] = {(int*)L->ws, (int*)(L->ws + 2 * arr)};
-  int* v[2] = {(int*)(L->ws + arr), (int*)(L->ws + 3 * arr)};
-  uint32_t* hist = (uint32_t*)(L->ws + 4 * arr);
-  SortArgs a;
-  a.keys = L->keys; a.key_stride = L->key_stride; a.row_n = L->row_n;
-  a.hist = hist; a.n = p.n; a.nkeys = p.nkeys; a.tiles = (uint32_t)p.tiles;
-  const dim3 grid((unsigned)p.tiles, (unsigned)p.segs), blk(kSortBlock);
+  const uint64_t arr = up((uint64_t)p.N * p.n * 4);
+  SortArgs a = {};
+  a.keys = L->keys; a.key_stride = L->key_stride;
+  a.n = p.n; a.nkeys = p.nkeys;
+  if (p.tiles == 0) {
+    a.first = 1;
+    a.kout = (int*)L->ws;
+    a.vout = (int*)(L->ws + arr);
+    const dim3 grid((unsigned)p.N), blk(kLdsSortBlock);
+    if (p.n <= 1024) CC_LAUNCH(k_sort_lds<1>, grid, blk, 0, L->st, a, p.passes);
+    else if (p.n <= 2048) CC_LAUNCH(k_sort_lds<2>, grid, blk, 0, L->st, a, p.passes);
+    else if (p.n <= 4096) CC_LAUNCH(k_sort_lds<4>, grid, blk, 0, L->st, a, p.passes);
+    else CC_LAUNCH(k_sort_lds<8>, grid, blk, 0, L->st, a, p.passes);
+    L->sorted_keys = a.kout;
+    L->sorted_vals = a.vout;
+    return hipGetLastError();
+  }
+  const int two = p.passes > 1;
+  int* k[2] = {(int*)L->ws, (int*)(L->ws + 2 * two * arr)};
+  int* v[2] = {(int*)(L->ws + arr), (int*)(L->ws + 3 * two * arr)};
+  a.hist = (uint32_t*)(L->ws + (two ? 4 : 2) * arr);
+  a.tiles = (uint32_t)p.tiles;
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.N), blk(kSortBlock);
   for (int pass = 0; pass < p.passes; ++pass) {
     a.first = pass == 0;
     a.shift = 8 * pass;
     a.kin = k[(pass + 1) & 1]; a.vin = v[(pass + 1) & 1];
     a.kout = k[pass & 1]; a.vout = v[pass & 1];
     CC_LAUNCH(k_sort_hist, grid, blk, 0, L->st, a);
-    CC_LAUNCH(k_sort_scan, dim3((unsigned)p.segs), dim3(kScanBlock), 0, L->st, hist, (uint64_t)kDigits * p.tiles);
+    CC_LAUNCH(k_sort_scan, dim3((unsigned)p.N), dim3(kScanBlock), 0, L->st, a.hist, (uint64_t)kDigits * p.tiles);
     CC_LAUNCH(k_sort_scatter, grid, blk, 0, L->st, a);
   }
   L->sorted_keys = k[(p.passes - 1) & 1];
