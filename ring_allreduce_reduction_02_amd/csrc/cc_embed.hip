@@ -8,6 +8,8 @@
 // elements, the gradient reads tokens * width and writes all vocab * width
 // (most rows are zeros: a batch holds few of a vocabulary's words).
 
+#include <algorithm>
+
 #include "cc_device.h"
 #include "cc_llm.h"
 
@@ -77,6 +79,8 @@ struct Cols {
   static constexpr int STEP = 64 * V * CB;
 };
 
+constexpr int kEmbedBatch = 4;   // token rows under way per wave
+
 // acc += the rows of grad at the sorted positions [lo, hi) of rank r, columns
 // c0 + 64 V i + V lane.  Positions are fetched 64 at a time, and their rows
 // four at a time, so that a lane has 4 CB loads under way.
@@ -90,11 +94,11 @@ __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, uint64_t r, uin
   for (uint64_t p0 = lo; p0 < hi; p0 += 64) {
     const int n = (int)(hi - p0 < 64 ? hi - p0 : 64);
     const int mine = lane < n ? vals[p0 + lane] : 0;
-    for (int k = 0; k < n; k += 4) {
-      u32x4 w[4][CB];
-      float x1[4][CB];
+    for (int k = 0; k < n; k += kEmbedBatch) {
+      u32x4 w[kEmbedBatch][CB];
+      float x1[kEmbedBatch][CB];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kEmbedBatch; ++q) {
         const uint32_t t = (uint32_t)__builtin_amdgcn_readlane(mine, k + q < n ? k + q : k);
         const char* g = base + (uint64_t)t * a.width * SZ;
 #pragma unroll
@@ -105,7 +109,7 @@ __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, uint64_t r, uin
         }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kEmbedBatch; ++q) {
         if (k + q >= n) break;
 #pragma unroll
         for (int i = 0; i < CB; ++i) {
@@ -153,12 +157,12 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
     float acc[C::CB][C::V] = {};
     add_rows<DT, VEC>(a, r, p0, p0 + kEmbedPiece, c0, lane, acc);
 #pragma unroll
-    for (int i = 0; i < C::CB; ++i)
-#pragma unroll
-      for (int e = 0; e < C::V; ++e) {
-        const uint64_t c = c0 + (uint64_t)(i * 64 + lane) * C::V + e;
-        if (c < a.width) o[c] = acc[i][e];
-      }
+    for (int i = 0; i < C::CB; ++i) {
+      const uint64_t c = c0 + (uint64_t)(i * 64 + lane) * C::V;
+      if (c >= a.width) continue;
+      if constexpr (VEC) stw_vec<DT>((char*)(o + c), acc[i]);
+      else o[c] = acc[i][0];
+    }
   }
 }
 
@@ -177,10 +181,17 @@ __device__ __forceinline__ void add_run(const EmbedGradArgs& a, uint64_t r, uint
   const float* part = a.partial + (r * a.pieces + f) * a.width + c0 + lane * C::V;
   for (uint64_t p = f; p < l; ++p, part += a.width)
 #pragma unroll
-    for (int k = 0; k < C::CB; ++k)
-      if (c0 + (uint64_t)(k * 64 + lane) * C::V < a.width)
+    for (int k = 0; k < C::CB; ++k) {
+      if (c0 + (uint64_t)(k * 64 + lane) * C::V >= a.width) continue;
+      if constexpr (VEC) {
+        float x[C::V];
+        ldw_vec<DT>((const char*)(part + k * 64 * C::V), x);
 #pragma unroll
-        for (int e = 0; e < C::V; ++e) acc[k][e] += part[k * 64 * C::V + e];
+        for (int e = 0; e < C::V; ++e) acc[k][e] += x[e];
+      } else {
+        acc[k][0] += part[k * 64];
+      }
+    }
   add_rows<DT, VEC>(a, r, l * kEmbedPiece, hi, c0, lane, acc);
 }
 
@@ -229,12 +240,14 @@ constexpr int kEmbedWaves = kEmbedBlock / 64;
 template <int DT, bool VEC, bool SUM>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
   typedef Cols<DT, VEC> C;
-  constexpr int SZ = Ty<DT>::SZ, NR = SUM ? kMaxRanks : 1;
-  __shared__ uint32_t begin[NR][kEmbedRows], end[NR][kEmbedRows];
+  constexpr int SZ = Ty<DT>::SZ;
+  extern __shared__ uint32_t runs[];   // [nr][kEmbedRows] begin, then end
+  uint32_t(*const begin)[kEmbedRows] = (uint32_t(*)[kEmbedRows])runs;
   __shared__ uint32_t total[kEmbedRows];
-  __shared__ float part[kEmbedWaves - 1][C::STEP];
+  __shared__ float part[2][C::STEP];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r0 = SUM ? 0 : (int)blockIdx.y, nr = SUM ? a.N : 1;
+  uint32_t(*const end)[kEmbedRows] = begin + nr;
   const uint64_t v0 = blockIdx.x, dv = gridDim.x;
   const int rows = (int)((a.vocab - v0 + dv - 1) / dv);
   for (int i = threadIdx.x; i < nr * 2 * kEmbedRows; i += kEmbedBlock) {
@@ -279,21 +292,23 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
         if (f < n && l) add_run<DT, VEC>(a, r0 + r, lo + f, lo + (l < n ? l : n), n, c0, lane, acc);
         before += n;
       }
-      __syncthreads();   // the last columns' parts are read
-      if (wave)
-#pragma unroll
-        for (int k = 0; k < C::CB; ++k)
-#pragma unroll
-          for (int e = 0; e < C::V; ++e) part[wave - 1][(k * C::V + e) * 64 + lane] = acc[k][e];
-      __syncthreads();
-      if (wave == 0) {
-        for (int w = 0; w < kEmbedWaves - 1; ++w)
+      // join: waves 2 and 3 into 0 and 1, then 1 into 0
+      for (int half = kEmbedWaves / 2; half; half >>= 1) {
+        __syncthreads();   // the last parts are read
+        if (wave >= half && wave < 2 * half)
 #pragma unroll
           for (int k = 0; k < C::CB; ++k)
 #pragma unroll
-            for (int e = 0; e < C::V; ++e) acc[k][e] += part[w][(k * C::V + e) * 64 + lane];
-        put_row<DT, VEC>(a, a.out + (v0 + i * dv) * a.width * SZ, r0, nr, c0, lane, acc);
+            for (int e = 0; e < C::V; ++e) part[wave - half][(k * C::V + e) * 64 + lane] = acc[k][e];
+        __syncthreads();
+        if (wave < half)
+#pragma unroll
+          for (int k = 0; k < C::CB; ++k)
+#pragma unroll
+            for (int e = 0; e < C::V; ++e) acc[k][e] += part[wave][(k * C::V + e) * 64 + lane];
       }
+      if (wave == 0)
+        put_row<DT, VEC>(a, a.out + (v0 + i * dv) * a.width * SZ, r0, nr, c0, lane, acc);
     }
   }
 }
@@ -305,7 +320,9 @@ hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
     CC_LAUNCH((k_embed_pieces<DT, VEC>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), 0, L.st, a);
   }
   const unsigned blocks = (unsigned)((a.vocab + kEmbedRows - 1) / kEmbedRows);
-  const unsigned lds = L.blocks_per_cu > 0 ? lds_for_blocks_per_cu(L.blocks_per_cu) : 0;
+  const unsigned need = (L.summed ? L.N : 1) * 2 * kEmbedRows * 4;
+  const unsigned cap = lds_for_blocks_per_cu(L.blocks_per_cu), fixed = sizeof(float) * (2 * Cols<DT, VEC>::STEP + kEmbedRows);
+  const unsigned lds = std::max(need, cap > fixed ? cap - fixed : 0u);
   if (L.summed) CC_LAUNCH((k_embed_grad<DT, VEC, true>), dim3(blocks), dim3(kEmbedBlock), lds, L.st, a);
   else CC_LAUNCH((k_embed_grad<DT, VEC, false>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), lds, L.st, a);
   return hipGetLastError();
@@ -316,12 +333,13 @@ hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
 hipError_t launch_embed(const EmbedLaunch& L) {
   EmbedArgs a{L.table, L.table_stride, L.ids, L.ids_stride, L.out, L.out_stride, L.vocab, L.tokens, L.width, L.scale};
   const dim3 grid((unsigned)L.tokens, (unsigned)L.N), blk(kEmbedBlock);
+  const unsigned lds = lds_for_blocks_per_cu(L.blocks_per_cu);
   if (L.dt == DT_F32) {
-    if (L.vec_ok) CC_LAUNCH((k_embed<DT_F32, true>), grid, blk, 0, L.st, a);
-    else CC_LAUNCH((k_embed<DT_F32, false>), grid, blk, 0, L.st, a);
+    if (L.vec_ok) CC_LAUNCH((k_embed<DT_F32, true>), grid, blk, lds, L.st, a);
+    else CC_LAUNCH((k_embed<DT_F32, false>), grid, blk, lds, L.st, a);
   } else {
-    if (L.vec_ok) CC_LAUNCH((k_embed<DT_BF16, true>), grid, blk, 0, L.st, a);
-    else CC_LAUNCH((k_embed<DT_BF16, false>), grid, blk, 0, L.st, a);
+    if (L.vec_ok) CC_LAUNCH((k_embed<DT_BF16, true>), grid, blk, lds, L.st, a);
+    else CC_LAUNCH((k_embed<DT_BF16, false>), grid, blk, lds, L.st, a);
   }
   return hipGetLastError();
 }
