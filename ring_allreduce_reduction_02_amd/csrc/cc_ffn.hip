@@ -44,37 +44,37 @@ __global__ __launch_bounds__(256) void k_ffn_put(PutArgs a) {
 struct PlanArgs {
   uint32_t v[kPlanCounts];
   const uint32_t* kept;   // in memory, or NULL: v
-  int N, E, tile;
+  int N, E;
   uint64_t cap;
   int* start;
-  int2* mtab;
+  int2* mtab[kFfnTiles];
   int* rowmap;
 };
 
 // Workgroup e writes expert e's first compact row, its row tiles and its rows'
 // places in the rank's buffer.
 __global__ __launch_bounds__(256) void k_ffn_plan(PlanArgs a) {
-  __shared__ uint32_t red[2][256];
+  __shared__ uint32_t red[1 + kFfnTiles][256];
   const int e = blockIdx.x, tid = threadIdx.x, N = a.N;
   const uint32_t* kept = a.kept ? a.kept : a.v;
-  uint32_t rows = 0, tiles = 0;
+  uint32_t sum[1 + kFfnTiles] = {};
   for (int x = tid; x < e; x += 256) {
     uint32_t n = 0;
     for (int i = 0; i < N; ++i) n += kept[x * N + i];
-    rows += n;
-    tiles += (n + a.tile - 1) / a.tile;
+    sum[0] += n;
+#pragma unroll
+    for (int k = 0; k < kFfnTiles; ++k) sum[1 + k] += (n + kFfnTile[k] - 1) / kFfnTile[k];
   }
-  red[0][tid] = rows;
-  red[1][tid] = tiles;
+#pragma unroll
+  for (int k = 0; k <= kFfnTiles; ++k) red[k][tid] = sum[k];
   __syncthreads();
   for (int d = 128; d; d >>= 1) {
-    if (tid < d) {
-      red[0][tid] += red[0][tid + d];
-      red[1][tid] += red[1][tid + d];
-    }
+    if (tid < d)
+#pragma unroll
+      for (int k = 0; k <= kFfnTiles; ++k) red[k][tid] += red[k][tid + d];
     __syncthreads();
   }
-  const uint32_t r0 = red[0][0], t0 = red[1][0];
+  const uint32_t r0 = red[0][0];
   const int per = a.E / N, l = e % per;
   uint32_t at = r0;
   for (int i = 0; i < N; ++i) {
@@ -83,8 +83,11 @@ __global__ __launch_bounds__(256) void k_ffn_plan(PlanArgs a) {
     for (uint32_t s = tid; s < n; s += 256) a.rowmap[at + s] = (int)(src + s);
     at += n;
   }
-  const uint32_t nt = (at - r0 + a.tile - 1) / a.tile;
-  for (uint32_t t = tid; t < nt; t += 256) a.mtab[t0 + t] = make_int2(e, (int)(r0 + t * a.tile));
+#pragma unroll
+  for (int k = 0; k < kFfnTiles; ++k) {
+    const uint32_t nt = (at - r0 + kFfnTile[k] - 1) / kFfnTile[k], t0 = red[1 + k][0];
+    for (uint32_t t = tid; t < nt; t += 256) a.mtab[k][t0 + t] = make_int2(e, (int)(r0 + t * kFfnTile[k]));
+  }
   if (tid == 0) {
     a.start[e] = (int)r0;
     if (e == a.E - 1) a.start[a.E] = (int)at;
@@ -164,15 +167,17 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
 // pieces are permuted by the line's number, so that the 4 lines and 2 pieces
 // (or 2 line groups) that 32 lanes read lie in different banks.  float32
 // columns are read one element a lane, from two lines 4 apart at a time.
-template <int DT>
+template <int DT, int R>
 __device__ __forceinline__ int col_place(int k, int chunk) {   // of a 16-byte chunk in its line
-  if constexpr (DT == DT_BF16) return chunk ^ ((k & 3) << 2) ^ ((k & 8) >> 2);
-  else return chunk ^ ((k & 4) << 1);
+  if constexpr (DT == DT_F32) return chunk ^ ((k & 4) << 1);
+  else if constexpr (R * 2 >= 256) return chunk ^ ((k & 3) << 2) ^ ((k & 8) >> 2);
+  else return chunk ^ ((k & 2) << 1) ^ ((k & 8) >> 2);         // 128-byte lines: two of them span the banks
 }
 template <int DT, int R>
 __device__ __forceinline__ int col_at(int k, int col) {
   constexpr int SZ = Ty<DT>::SZ;
-  return k * R * SZ + (col_place<DT>(k, col * SZ / 16) << 4) + col * SZ % 16;
+  static_assert(R >= 64, "a line holds every permuted place");
+  return k * R * SZ + (col_place<DT, R>(k, col * SZ / 16) << 4) + col * SZ % 16;
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -206,27 +211,30 @@ __device__ __forceinline__ u32x4 frag(const char* t, int u, int i0, int lane) {
 // r's first byte (NULL: zeros), elements [k0, K).  Column tiles: lp[k] is
 // summed line k0 + k (NULL: zeros), columns [c0, C).
 template <int DT, bool COL, int R, int NT>
-__device__ __forceinline__ void stage_elems(char* t, const char* const* lp, int64_t k0, int64_t K, int64_t c0,
-                                            int64_t C) {
-  constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ;
-  for (int e = threadIdx.x; e < R * BK; e += NT) {
-    uint32_t v = 0;
-    int at;
-    if constexpr (!COL) {
-      const int r = e / BK, k = e % BK;
-      const char* p = lp[r];
-      if (p && k0 + k < K) v = SZ == 2 ? *(const uint16_t*)(p + (k0 + k) * SZ) : *(const uint32_t*)(p + (k0 + k) * SZ);
-      at = row_at(r, k * SZ / 16) + (k * SZ) % 16;
-    } else {
-      const int k = e / R, c = e % R;
-      const char* p = lp[k];
-      if (p && c0 + c < C) v = SZ == 2 ? *(const uint16_t*)(p + (c0 + c) * SZ) : *(const uint32_t*)(p + (c0 + c) * SZ);
-      at = col_at<DT, R>(k, c);
+struct Elems {
+  static constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ, Q = R * BK / NT;
+  uint32_t v[Q];
+  __device__ __forceinline__ void load(const char* const* lp, int64_t k0, int64_t K, int64_t c0, int64_t C) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int e = threadIdx.x + q * NT;
+      const int line = COL ? e / R : e / BK;
+      const int64_t at = COL ? c0 + e % R : k0 + e % BK;
+      const char* p = lp[line];
+      v[q] = 0;
+      if (p && at < (COL ? C : K)) v[q] = SZ == 2 ? *(const uint16_t*)(p + at * SZ) : *(const uint32_t*)(p + at * SZ);
     }
-    if constexpr (SZ == 2) *(uint16_t*)(t + at) = (uint16_t)v;
-    else *(uint32_t*)(t + at) = v;
   }
-}
+  __device__ __forceinline__ void store(char* t) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int e = threadIdx.x + q * NT;
+      const int at = COL ? col_at<DT, R>(e / R, e % R) : row_at(e / BK, e % BK * SZ / 16) + (e % BK * SZ) % 16;
+      if constexpr (SZ == 2) *(uint16_t*)(t + at) = (uint16_t)v[q];
+      else *(uint32_t*)(t + at) = v[q];
+    }
+  }
+};
 
 // ------------------------------------------------------------------ activations
 
@@ -501,7 +509,8 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TM][TN]) {
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 }
 
-// Any alignment: every element staged by itself, one stage after the other.
+// Any alignment: every element staged by itself, through registers, the next
+// stage's on their way while this one's products run.
 template <int DT, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmArgs g) {
   constexpr int NT = 64 * (BM / WM) * (BN / WN);
@@ -511,8 +520,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmAr
   __shared__ __attribute__((aligned(16))) char ta[BM * kKBytes];
   __shared__ __attribute__((aligned(16))) char tb[BN * kKBytes];
   __shared__ __attribute__((aligned(16))) char fin[(NT / 64) * finish_bytes<WN>()];
+  // lines of the tile, or (column tiles) of a stage's summed lines
   __shared__ const char* la[ACOL ? BK : BM];
   __shared__ const char* lb[BCOL ? BK : BN];
+  static_assert(BK <= NT, "a thread sets a summed line");
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int mw = (wave % (BM / WM)) * WM, nw = (wave / (BM / WM)) * WN;
@@ -526,22 +537,34 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmAr
       lb[r] = row >= 0 ? w + row * (int64_t)g.b.pitch : nullptr;
     }
   }
+  auto summed_lines = [&](int64_t k0) {
+    if (tid < BK) {
+      const int64_t k = k0 + tid;
+      if constexpr (ACOL) la[tid] = k < t.K ? row_ptr(g.a, t.rank, (int)(t.p0 + k)) : nullptr;
+      if constexpr (KIND == K_DW) lb[tid] = k < t.K ? row_ptr(g.b_rows, t.rank, (int)(t.p0 + k)) : nullptr;
+      else if constexpr (BCOL) lb[tid] = k < t.K ? wt_ptr(g.b, t.rank, t.local) + k * (int64_t)g.b.pitch : nullptr;
+    }
+  };
+  Elems<DT, ACOL, BM, NT> ea;
+  Elems<DT, BCOL, BN, NT> eb;
   f32x16 acc[TM][TN];
   clear(acc);
+  summed_lines(0);
+  __syncthreads();
+  if (t.K > 0) {
+    ea.load(la, 0, t.K, t.m0, g.M);
+    eb.load(lb, 0, t.K, t.n0, g.N);
+  }
   for (int64_t k0 = 0; k0 < t.K; k0 += BK) {
+    __syncthreads();   // the last stage's tiles and lines are read
+    ea.store(ta);
+    eb.store(tb);
+    summed_lines(k0 + BK);
     __syncthreads();
-    if constexpr (ACOL || BCOL) {
-      if (tid < BK) {
-        const int64_t k = k0 + tid;
-        if constexpr (ACOL) la[tid] = k < t.K ? row_ptr(g.a, t.rank, (int)(t.p0 + k)) : nullptr;
-        if constexpr (KIND == K_DW) lb[tid] = k < t.K ? row_ptr(g.b_rows, t.rank, (int)(t.p0 + k)) : nullptr;
-        else lb[tid] = k < t.K ? wt_ptr(g.b, t.rank, t.local) + k * (int64_t)g.b.pitch : nullptr;
-      }
-      __syncthreads();
+    if (k0 + BK < t.K) {
+      ea.load(la, k0 + BK, t.K, t.m0, g.M);
+      eb.load(lb, k0 + BK, t.K, t.n0, g.N);
     }
-    stage_elems<DT, ACOL, BM, NT>(ta, la, k0, t.K, t.m0, g.M);
-    stage_elems<DT, BCOL, BN, NT>(tb, lb, k0, t.K, t.n0, g.N);
-    __syncthreads();
     multiply<DT, ACOL, BCOL, BM, BN>(ta, tb, acc, mw, nw, lane);
   }
   finish<DT, KIND, false>(g, t, acc, mw, nw, lane, fin + wave * finish_bytes<WN>());
@@ -608,7 +631,7 @@ struct Loader {
     const int end = (C - c0) * SZ - 16;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const int k = line_of(wave, q, lane), c = 16 * col_place<DT>(k, lane % LANES);   // its own inverse
+      const int k = line_of(wave, q, lane), c = 16 * col_place<DT, R>(k, lane % LANES);   // its own inverse
       off[q] = (uint32_t)(c0 * SZ + (c < end ? c : end));
       last[q] = (K - k + BK - 1) / BK;
     }
@@ -792,34 +815,55 @@ bool tiled(const FfnLaunch& L) {
          2 * L.s.F * L.s.W * es <= kMaxSpan;
 }
 
-// rows per tile of a call's row products
-int row_tile(const FfnLaunch& L) { return tiled(L) && 4 * L.s.rows >= 3 * 256 * L.s.mtiles256 ? 256 : kFfnRowTile; }
-
-template <int KIND, int BM, int BN>
-uint64_t tiles_of(GemmArgs* g) {
-  const int cols = KIND == K_GATEUP ? g->F : g->N, bn = tile_cols<KIND, BN>();
+// workgroups of a product in tiles of kFfnTile[k]
+template <int KIND>
+uint64_t tiles_of(GemmArgs* g, const FfnLaunch& L, int k) {
+  const int cols = KIND == K_GATEUP ? g->F : g->N, bn = KIND == K_GATEUP ? kFfnTile[k] / 2 : kFfnTile[k];
   g->ntiles = (cols + bn - 1) / bn;
+  g->mtab = (const int2*)(L.ws + L.o.mtab[k]);
   if constexpr (KIND == K_DW) {
-    g->mtiles = (g->M + BM - 1) / BM;
+    g->mtiles = (g->M + kFfnTile[k] - 1) / kFfnTile[k];
     return (uint64_t)g->E * g->mtiles * g->ntiles;
   }
+  g->mtiles = (int)L.s.mtiles[k];
   return (uint64_t)g->mtiles * g->ntiles;
+}
+
+// The tile whose workgroups, dealt out over the compute units, take least: a
+// larger tile moves fewer bytes for a product, a smaller one leaves fewer
+// units idle.  Measured cost of equal areas: 1, 1.25 and 1.9.
+template <int KIND>
+int pick_tile(GemmArgs g, const FfnLaunch& L, int first) {
+  static constexpr double kArea[kFfnTiles] = {16.0, 4.0 * 1.25, 1.9};
+  const int cus = dev_info().cus > 0 ? dev_info().cus : 256;
+  int best = first;
+  double least = 0.0;
+  for (int k = first; k < kFfnTiles; ++k) {
+    const double t = (double)((tiles_of<KIND>(&g, L, k) + cus - 1) / cus) * kArea[k];
+    if (k == first || t < least) {
+      least = t;
+      best = k;
+    }
+  }
+  return best;
 }
 
 template <int DT, int KIND>
 hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
-  if (!tiled(L)) {
-    const uint64_t blocks = tiles_of<KIND, 128, 128>(&g);
-    if (blocks == 0) return hipSuccess;
-    CC_LAUNCH((k_ffn_elems<DT, KIND, 128, 128, 64, 64>), dim3((unsigned)blocks), dim3(256), 0, L.st, g);
-  } else if (row_tile(L) == 256) {
-    const uint64_t blocks = tiles_of<KIND, 256, 256>(&g);
-    if (blocks == 0) return hipSuccess;
-    CC_LAUNCH((k_ffn_tile<DT, KIND, 256, 256, 128, 64>), dim3((unsigned)blocks), dim3(512), 0, L.st, g);
+  const bool fast = tiled(L);
+  const int k = pick_tile<KIND>(g, L, fast ? 0 : 1);
+  const uint64_t blocks = tiles_of<KIND>(&g, L, k);
+  if (blocks == 0) return hipSuccess;
+  const dim3 grid((unsigned)blocks);
+  if (!fast) {
+    if (k == 1) CC_LAUNCH((k_ffn_elems<DT, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, L.st, g);
+    else CC_LAUNCH((k_ffn_elems<DT, KIND, 64, 64, 32, 64>), grid, dim3(128), 0, L.st, g);
+  } else if (k == 0) {
+    CC_LAUNCH((k_ffn_tile<DT, KIND, 256, 256, 128, 64>), grid, dim3(512), 0, L.st, g);
+  } else if (k == 1) {
+    CC_LAUNCH((k_ffn_tile<DT, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, L.st, g);
   } else {
-    const uint64_t blocks = tiles_of<KIND, 128, 128>(&g);
-    if (blocks == 0) return hipSuccess;
-    CC_LAUNCH((k_ffn_tile<DT, KIND, 128, 128, 64, 64>), dim3((unsigned)blocks), dim3(256), 0, L.st, g);
+    CC_LAUNCH((k_ffn_tile<DT, KIND, 64, 64, 32, 64>), grid, dim3(128), 0, L.st, g);
   }
   return hipGetLastError();
 }
@@ -832,7 +876,7 @@ hipError_t pick_gemm(const GemmArgs& g, const FfnLaunch& L) {
 uint64_t up256(uint64_t v) { return (v + 255) / 256 * 256; }
 
 // the tables, from the counts in the launch's arguments or (many) in memory
-hipError_t plan(const FfnLaunch& L, int tile) {
+hipError_t plan(const FfnLaunch& L) {
   PlanArgs a;
   const int n = L.s.N * L.s.E;
   a.kept = nullptr;
@@ -849,9 +893,9 @@ hipError_t plan(const FfnLaunch& L, int tile) {
     }
     a.kept = to;
   }
-  a.N = L.s.N; a.E = L.s.E; a.tile = tile; a.cap = L.s.cap;
+  a.N = L.s.N; a.E = L.s.E; a.cap = L.s.cap;
   a.start = (int*)(L.ws + L.o.start);
-  a.mtab = (int2*)(L.ws + L.o.mtab);
+  for (int k = 0; k < kFfnTiles; ++k) a.mtab[k] = (int2*)(L.ws + L.o.mtab[k]);
   a.rowmap = (int*)(L.ws + L.o.rowmap);
   CC_LAUNCH(k_ffn_plan, dim3((unsigned)L.s.E), dim3(256), 0, L.st, a);
   return hipGetLastError();
@@ -860,8 +904,6 @@ hipError_t plan(const FfnLaunch& L, int tile) {
 GemmArgs gemm_args(const FfnLaunch& L) {
   GemmArgs g = {};
   g.start = (const int*)(L.ws + L.o.start);
-  g.mtab = (const int2*)(L.ws + L.o.mtab);
-  g.mtiles = (int)(row_tile(L) == 256 ? L.s.mtiles256 : L.s.mtiles);
   g.E = L.s.E;
   g.per = L.s.E / L.s.N;
   g.F = (int)L.s.F;
@@ -895,7 +937,7 @@ FfnWs ffn_ws(const FfnShape& s, int grad) {
   };
   o.kept = take((uint64_t)s.N * s.E * 4);
   o.start = take(((uint64_t)s.E + 1) * 4);
-  o.mtab = take(s.mtiles * 8);
+  for (int k = 0; k < kFfnTiles; ++k) o.mtab[k] = take(s.mtiles[k] * 8);
   o.rowmap = take(s.rows * 4);
   o.h = take(s.rows * s.F * es);
   o.dgu = grad ? take(s.rows * 2 * s.F * es) : 0;
@@ -905,7 +947,7 @@ FfnWs ffn_ws(const FfnShape& s, int grad) {
 
 hipError_t launch_ffn(const FfnLaunch& L) {
   const uint64_t W = L.s.W, F = L.s.F;
-  hipError_t e = plan(L, row_tile(L));
+  hipError_t e = plan(L);
   if (e != hipSuccess) return e;
   GemmArgs g = gemm_args(L);
   g.K = (int)W;
@@ -926,7 +968,7 @@ hipError_t launch_ffn(const FfnLaunch& L) {
 
 hipError_t launch_ffn_grad(const FfnLaunch& L) {
   const uint64_t W = L.s.W, F = L.s.F;
-  hipError_t e = plan(L, row_tile(L));
+  hipError_t e = plan(L);
   if (e != hipSuccess) return e;
   GemmArgs g = gemm_args(L);
   g.K = (int)W;

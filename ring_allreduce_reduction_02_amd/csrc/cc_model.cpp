@@ -177,7 +177,7 @@ cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uin
   if (W >= (1ull << 24) || F >= (1ull << 24)) return fail(CC_ERR_INVALID_ARG, "width or hidden too large");
   if ((u128)E * cap >= (1ull << 31)) return fail(CC_ERR_INVALID_ARG, "nexperts * capacity must be below 2^31 rows");
   kept->assign((size_t)E * N, 0);
-  uint64_t rows = 0, most = 0, tiles = 0, tiles256 = 0;
+  uint64_t rows = 0, most = 0, tiles[kFfnTiles] = {};
   for (int e = 0; e < E; ++e) {
     uint64_t n = 0;
     for (int i = 0; i < N; ++i) {
@@ -187,14 +187,13 @@ cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uin
     }
     rows += n;
     most = std::max(most, n);
-    tiles += (n + kFfnRowTile - 1) / kFfnRowTile;
-    tiles256 += (n + 255) / 256;
+    for (int k = 0; k < kFfnTiles; ++k) tiles[k] += (n + kFfnTile[k] - 1) / kFfnTile[k];
     if (rows >= (1ull << 31)) return fail(CC_ERR_INVALID_ARG, "2^31 rows or more in one call");
   }
-  const uint64_t wt = (2 * F + 63) / 64, wn = (W + 63) / 64;
-  if (tiles * std::max(wt, wn) >= kMaxBlocks || (u128)E * wt * wn >= kMaxBlocks)
+  const uint64_t wt = (2 * F + 63) / 64, wn = (W + 63) / 64;   // the smallest tile's
+  if ((u128)tiles[kFfnTiles - 1] * std::max(wt, wn) >= kMaxBlocks || (u128)E * wt * wn >= kMaxBlocks)
     return fail(CC_ERR_INVALID_ARG, "too many tiles for one launch");
-  *sh = FfnShape{N, E, cap, W, F, rows, most, tiles, tiles256, (int)dtype, 0};
+  *sh = FfnShape{N, E, cap, W, F, rows, most, {tiles[0], tiles[1], tiles[2]}, (int)dtype, 0};
   return CC_OK;
 }
 
