@@ -134,6 +134,7 @@ struct GemmArgs {
   RowSide out;           // rows out
   RowSide pre;           // gate and up pre-activations (base NULL: not kept)
   RowSide h;             // compact h (K_DHID)
+  const int* map;        // compact rows' places in their rank's buffer
   WtSide wout;           // K_DW
 };
 
@@ -422,13 +423,48 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
   constexpr int SZ = Ty<DT>::SZ, V = Ty<DT>::V, WN = 32 * TN, PITCH = WN * 4 + 16;
   constexpr int COLS = KIND == K_GATEUP ? WN / 2 : WN;   // result columns of the wave
   constexpr int LPR = COLS / V, RPP = 64 / LPR;          // lanes per row, rows per pass
+  constexpr int PASSES = 32 / RPP;
   const int cl = (lane % LPR) * V;
   // K_GATEUP: columns alternate 32 gate and 32 up
   const int at = KIND == K_GATEUP ? (cl / 32) * 64 + cl % 32 : cl;
   const int n = t.n0 + (KIND == K_GATEUP ? nw / 2 : nw) + cl;
   const int left = (KIND == K_GATEUP ? g.F : g.N) - n;
+  const int rows = KIND == K_DW ? g.M - t.m0 : t.p1 - t.p0;
+  // the rows' places in the rank's buffer, 64 rows of the wave a register
+  constexpr bool MAPPED = KIND != K_DW;
+  int place[(TM + 1) / 2];
+  if constexpr (MAPPED) {
+#pragma unroll
+    for (int k = 0; k < (TM + 1) / 2; ++k) {
+      const int m = mw + 64 * k + lane;
+      place[k] = KIND == K_GATEUP && !g.pre.base ? 0 : m < rows ? g.map[t.p0 + m] : 0;
+    }
+  }
+  auto place_of = [&](int i, int row) { return __shfl(place[i / 2], (i & 1) * 32 + row); };
+  auto mapped = [&](const RowSide& s, int place) {
+    return s.base + (uint64_t)t.rank * s.rank_stride + (uint64_t)(uint32_t)place * s.pitch + (int64_t)n * SZ;
+  };
+  auto packed = [&](const RowSide& s, int m) { return s.base + (uint64_t)(t.p0 + m) * s.pitch + (int64_t)n * SZ; };
+  // K_DHID: the pre-activations, loaded 32 rows ahead (bf16; of float32 they
+  // would fill the registers)
+  constexpr bool AHEAD = KIND == K_DHID && VEC && PASSES <= 4;
+  u32x4 fg[2][PASSES], fu[2][PASSES];
+  auto ahead = [&](int i) {
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int r = 0; r < PASSES; ++r) {
+        const int row = r * RPP + lane / LPR;
+        const char* pre = mapped(g.pre, place_of(i, row));
+        const bool in = mw + 32 * i + row < rows && left > 0;
+        fg[i & 1][r] = in ? *(const u32x4*)pre : u32x4{0u, 0u, 0u, 0u};
+        fu[i & 1][r] = in ? *(const u32x4*)(pre + (int64_t)g.F * SZ) : u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+  };
+  ahead(0);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
+    if (i + 1 < TM) ahead(i + 1);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -437,38 +473,43 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
             f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     wave_lds_sync();
 #pragma unroll
-    for (int r = 0; r < 32; r += RPP) {
-      const int row = r + lane / LPR, m = mw + 32 * i + row;
-      const bool in = KIND == K_DW ? t.m0 + m < g.M : t.p0 + m < t.p1;
-      if (!in) continue;
+    for (int r = 0; r < PASSES; ++r) {
+      const int row = r * RPP + lane / LPR, m = mw + 32 * i + row;
+      int at_row = 0;
+      if constexpr (MAPPED) at_row = place_of(i, row);
+      if (m >= rows) continue;
       float v[V];
       read_row<V>(lds + row * PITCH + at * 4, v);
       if constexpr (KIND == K_DW) {
         store_n<DT, VEC, V>(wt_ptr(g.wout, t.rank, t.local) + (uint64_t)(t.m0 + m) * g.wout.pitch + (int64_t)n * SZ, v,
                             left);
       } else if constexpr (KIND == K_DOWN || KIND == K_DX) {
-        store_n<DT, VEC, V>(row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ, v, left);
+        store_n<DT, VEC, V>(mapped(g.out, at_row), v, left);
       } else if constexpr (KIND == K_GATEUP) {
-        // the row's place in the rank's buffer, when the pre-activations are kept
         float up[V], h[V];
         read_row<V>(lds + row * PITCH + (at + 32) * 4, up);
         gate<V>(v, up, g.act, h);
-        store_n<DT, VEC, V>(row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ, h, left);
+        store_n<DT, VEC, V>(packed(g.out, m), h, left);
         if (g.pre.base) {
-          char* pre = row_ptr(g.pre, t.rank, t.p0 + m) + (int64_t)n * SZ;
+          char* pre = mapped(g.pre, at_row);
           store_n<DT, VEC, V>(pre, v, left);
           store_n<DT, VEC, V>(pre + (int64_t)g.F * SZ, up, left);
         }
       } else {   // K_DHID
-        const char* pre = row_ptr(g.pre, t.rank, t.p0 + m) + (int64_t)n * SZ;
         float gt[V], up[V], dg[V], du[V], h[V];
-        load_n<DT, VEC, V>(pre, gt, left);
-        load_n<DT, VEC, V>(pre + (int64_t)g.F * SZ, up, left);
+        if constexpr (AHEAD) {
+          unpack<DT>(fg[i & 1][r], gt);
+          unpack<DT>(fu[i & 1][r], up);
+        } else {
+          const char* pre = mapped(g.pre, at_row);
+          load_n<DT, VEC, V>(pre, gt, left);
+          load_n<DT, VEC, V>(pre + (int64_t)g.F * SZ, up, left);
+        }
         gate_grad<V>(gt, up, g.act, v, dg, du, h);
-        char* o = row_ptr(g.out, t.rank, t.p0 + m) + (int64_t)n * SZ;
+        char* o = packed(g.out, m);
         store_n<DT, VEC, V>(o, dg, left);
         store_n<DT, VEC, V>(o + (int64_t)g.F * SZ, du, left);
-        store_n<DT, VEC, V>(row_ptr(g.h, t.rank, t.p0 + m) + (int64_t)n * SZ, h, left);
+        store_n<DT, VEC, V>(packed(g.h, m), h, left);
       }
     }
     wave_lds_sync();
@@ -904,6 +945,7 @@ hipError_t plan(const FfnLaunch& L) {
 GemmArgs gemm_args(const FfnLaunch& L) {
   GemmArgs g = {};
   g.start = (const int*)(L.ws + L.o.start);
+  g.map = (const int*)(L.ws + L.o.rowmap);
   g.E = L.s.E;
   g.per = L.s.E / L.s.N;
   g.F = (int)L.s.F;
