@@ -306,7 +306,7 @@ __device__ __forceinline__ void store_n(char* p, const float* v, int n) {
   if constexpr (VEC) {
     if (n <= 0) return;
     static_assert(V * Ty<DT>::SZ == 16, "one vector");
-    *(u32x4*)p = pack_row<DT>(v);
+    stg(p, pack_row<DT>(v));   // past the caches, which the operands' tiles need
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)

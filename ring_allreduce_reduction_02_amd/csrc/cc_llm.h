@@ -26,9 +26,15 @@ struct SortLaunch {
   const char* keys;      // rank-strided
   uint64_t key_stride;
   char* ws;              // p.bytes, 16-byte aligned
-  // outputs inside ws, [N][n] int32: sorted keys and their positions
+  // Without `counts`: sorted keys and their positions, [N][n] int32 inside ws
   const int* sorted_keys;
   const int* sorted_vals;
+  // With it (both rank-strided): the positions, -1 for keys outside [0, nkeys), and
+  // the number of each key
+  char* order;
+  uint64_t order_stride;
+  char* counts;
+  uint64_t counts_stride;
   hipStream_t st;
 };
 hipError_t launch_sort(SortLaunch* L);
@@ -79,10 +85,6 @@ struct RouteLaunch {
   uint64_t experts_stride;
   char* weights;         // float32 [tokens][topk]; dweights of the gradient
   uint64_t weights_stride;
-  char* order;           // int32 [tokens * topk]
-  uint64_t order_stride;
-  char* counts;          // int32 [nexperts]
-  uint64_t counts_stride;
   char* dlogits;
   uint64_t dlogits_stride;
   uint64_t tokens;
@@ -91,7 +93,6 @@ struct RouteLaunch {
   hipStream_t st;
 };
 hipError_t launch_route(const RouteLaunch& L);
-hipError_t launch_route_order(const RouteLaunch& L, const int* keys, const int* vals);
 hipError_t launch_route_grad(const RouteLaunch& L);
 
 // ---- gated feed-forward block of the experts.  Compact rows: the kept rows

@@ -322,22 +322,19 @@ cc_status_t cc_moe_route(cc_rankbuf_t logits, cc_rankbuf_t experts, cc_rankbuf_t
   L.logits = (const char*)logits.base; L.logits_stride = logits.rank_stride_bytes;
   L.experts = (char*)experts.base; L.experts_stride = experts.rank_stride_bytes;
   L.weights = (char*)weights.base; L.weights_stride = weights.rank_stride_bytes;
-  L.order = (char*)order.base; L.order_stride = order.rank_stride_bytes;
-  L.counts = (char*)counts.base; L.counts_stride = counts.rank_stride_bytes;
   L.tokens = tokens; L.nexperts = nexperts; L.topk = topk; L.normalize = normalize;
   L.N = N; L.dt = (int)dtype; L.st = (hipStream_t)stream;
+  hipError_t e = tokens ? launch_route(L) : hipSuccess;
+  if (e != hipSuccess) return hip_status(e, "MoE routing");
   SortLaunch so = {};
-  if (tokens) {
-    hipError_t e = launch_route(L);
-    if (e != hipSuccess) return hip_status(e, "MoE routing");
-    so.p = p;
-    so.keys = (const char*)experts.base;
-    so.key_stride = experts.rank_stride_bytes;
-    so.ws = (char*)cfg.workspace;
-    so.st = (hipStream_t)stream;
-    if ((e = launch_sort(&so)) != hipSuccess) return hip_status(e, "MoE routing (sort)");
-  }
-  return hip_status(launch_route_order(L, so.sorted_keys, so.sorted_vals), "MoE routing (order)");
+  so.p = p;
+  so.keys = (const char*)experts.base;
+  so.key_stride = experts.rank_stride_bytes;
+  so.ws = (char*)cfg.workspace;
+  so.order = (char*)order.base; so.order_stride = order.rank_stride_bytes;
+  so.counts = (char*)counts.base; so.counts_stride = counts.rank_stride_bytes;
+  so.st = (hipStream_t)stream;
+  return hip_status(launch_sort(&so), "MoE routing (order)");
 }
 
 cc_status_t cc_moe_route_workspace_size(int nranks, size_t tokens, int nexperts, int topk, size_t* bytes) {

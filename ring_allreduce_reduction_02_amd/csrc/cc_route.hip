@@ -40,13 +40,38 @@ __device__ __forceinline__ uint32_t rank_bits(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Reductions over a wave by data-parallel moves (within 16 lanes, then across
+// rows), the result on every lane: a tenth of the latency of shuffles through
+// LDS.  The order is fixed.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t x, uint32_t none) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, CTRL, 0xf, 0xf, false);
+}
+template <class F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t x, uint32_t none, F f) {
+  x = f(x, moved<0x111>(x, none));   // row_shr 1, 2, 4, 8
+  x = f(x, moved<0x112>(x, none));
+  x = f(x, moved<0x114>(x, none));
+  x = f(x, moved<0x118>(x, none));
+  x = f(x, moved<0x142>(x, none));   // row_bcast 15, 31
+  x = f(x, moved<0x143>(x, none));
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
+  return wave_reduce(x, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ uint32_t wave_umin(uint32_t x) {
+  return wave_reduce(x, 0xffffffffu, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
 __device__ __forceinline__ float wave_max(float x) {
-  for (int d = 32; d; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
-  return x;
+  return __uint_as_float(wave_reduce(__float_as_uint(x), 0xff800000u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
 }
 __device__ __forceinline__ float wave_sum(float x) {
-  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
-  return x;
+  return __uint_as_float(wave_reduce(__float_as_uint(x), 0u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
 // A token's logits over a wave, V a lane: lane l holds experts q * 64 + l.
@@ -72,8 +97,8 @@ __device__ __forceinline__ float load_exp(const char* row, int E, int lane, floa
   return wave_sum(s);
 }
 
-// One wave a token.  The chosen experts one after the other: the largest
-// (bits, lowest index) of the wave, then taken out.
+// One wave a token.  The chosen experts one after the other: the largest bits
+// of the wave, the lowest index that has them, then taken out.
 template <int DT, int V>
 __global__ __launch_bounds__(kRouteBlock) void k_route(RouteArgs a) {
   const int lane = threadIdx.x & 63;
@@ -81,21 +106,25 @@ __global__ __launch_bounds__(kRouteBlock) void k_route(RouteArgs a) {
   if (t >= a.tokens) return;
   float x[V], ex[V];
   const float all = load_exp<DT, V>(a.logits + r * a.ls + t * a.E * Ty<DT>::SZ, a.E, lane, x, ex);
-  uint64_t key[V];
+  uint32_t key[V];
 #pragma unroll
-  for (int q = 0; q < V; ++q) key[q] = ((uint64_t)rank_bits(x[q]) << 32) | (uint32_t)~(q * 64 + lane);
+  for (int q = 0; q < V; ++q) key[q] = rank_bits(x[q]);
   int my_e = -1;       // slot `lane`
   float my_p = 0.0f, chosen = 0.0f;
   for (int s = 0; s < a.K; ++s) {
-    uint64_t best = key[0];
+    uint32_t mine = key[0], first = 0;
 #pragma unroll
-    for (int q = 1; q < V; ++q) best = key[q] > best ? key[q] : best;
-    for (int d = 32; d; d >>= 1) {
-      const uint64_t o = __shfl_xor((unsigned long long)best, d);
-      best = o > best ? o : best;
-    }
-    if ((best >> 32) == 0) break;
-    const int e = (int)~(uint32_t)best;
+    for (int q = 1; q < V; ++q)
+      if (key[q] > mine) {
+        mine = key[q];
+        first = q;
+      }
+    const uint32_t best = wave_umax(mine);
+    if (best == 0) break;
+    // the lowest index that has it
+    int e;
+    if constexpr (V == 1) e = __builtin_ctzll(__ballot(mine == best));
+    else e = (int)wave_umin(mine == best ? first * 64 + lane : 0xffffffffu);
     float p = 0.0f;
 #pragma unroll
     for (int q = 0; q < V; ++q) {
@@ -104,7 +133,7 @@ __global__ __launch_bounds__(kRouteBlock) void k_route(RouteArgs a) {
         p = ex[q];
       }
     }
-    p = __shfl(p, e & 63);
+    p = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(p), e & 63));
     chosen += p;
     if (lane == s) {
       my_e = e;
@@ -134,8 +163,8 @@ __global__ __launch_bounds__(kRouteBlock) void k_route_grad(RouteArgs a) {
 #pragma unroll
   for (int q = 0; q < V; ++q) u[q] = 0.0f;
   for (int s = 0; s < a.K; ++s) {
-    const int e = __shfl(my_e, s);
-    const float d = __shfl(my_d, s);
+    const int e = __builtin_amdgcn_readlane(my_e, s);
+    const float d = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_d), s));
 #pragma unroll
     for (int q = 0; q < V; ++q) {
       if (q * 64 + lane == e) {
@@ -170,36 +199,6 @@ __global__ __launch_bounds__(kRouteBlock) void k_route_grad(RouteArgs a) {
   }
 }
 
-struct OrderArgs {
-  const int* keys;
-  const int* vals;
-  char* order;
-  uint64_t os;
-  char* counts;
-  uint64_t cs;
-  uint64_t n;
-  int E;
-};
-
-// The sorted assignments without the empty slots, and the rows of each expert.
-__global__ __launch_bounds__(kRouteBlock) void k_route_order(OrderArgs a) {
-  const uint64_t r = blockIdx.y, i = (uint64_t)blockIdx.x * kRouteBlock + threadIdx.x;
-  const int* keys = a.keys + r * a.n;
-  if (i < a.n) ((int*)(a.order + r * a.os))[i] = keys[i] < a.E ? a.vals[r * a.n + i] : -1;
-  if (i < (uint64_t)a.E) {
-    uint64_t b[2];
-    for (int s = 0; s < 2; ++s) {
-      uint64_t lo = 0, hi = a.n;
-      while (lo < hi) {
-        const uint64_t mid = (lo + hi) >> 1;
-        if (keys[mid] < (int)i + s) lo = mid + 1; else hi = mid;
-      }
-      b[s] = lo;
-    }
-    ((int*)(a.counts + r * a.cs))[i] = (int)(b[1] - b[0]);
-  }
-}
-
 template <bool GRAD, int DT, int V>
 hipError_t run_route(const RouteArgs& a, const RouteLaunch& L) {
   const dim3 grid((unsigned)((L.tokens + kRouteWaves - 1) / kRouteWaves), (unsigned)L.N), blk(kRouteBlock);
@@ -230,15 +229,6 @@ hipError_t launch_route(const RouteLaunch& L) {
 
 hipError_t launch_route_grad(const RouteLaunch& L) {
   return L.dt == DT_F32 ? pick_route<true, DT_F32>(route_args(L), L) : pick_route<true, DT_BF16>(route_args(L), L);
-}
-
-hipError_t launch_route_order(const RouteLaunch& L, const int* keys, const int* vals) {
-  const uint64_t n = L.tokens * (uint64_t)L.topk;
-  OrderArgs a{keys, vals, L.order, L.order_stride, L.counts, L.counts_stride, n, L.nexperts};
-  const uint64_t m = n > (uint64_t)L.nexperts ? n : (uint64_t)L.nexperts;
-  CC_LAUNCH(k_route_order, dim3((unsigned)((m + kRouteBlock - 1) / kRouteBlock), (unsigned)L.N), dim3(kRouteBlock), 0,
-            L.st, a);
-  return hipGetLastError();
 }
 
 }  // namespace cc

@@ -9,6 +9,8 @@
 // (one ballot per bit), and in the waves before it.  Every place is a count,
 // so nothing depends on the order in which workgroups run.
 
+#include <algorithm>
+
 #include "cc_device.h"
 #include "cc_llm.h"
 
@@ -28,6 +30,10 @@ struct SortArgs {
   const int* vin;
   int* kout;
   int* vout;
+  char* order;
+  uint64_t os;
+  char* counts;          // set: the pass gives positions and counts
+  uint64_t cs;
   uint32_t* hist;        // [N][kDigits][tiles]
   uint64_t n;
   uint32_t nkeys;
@@ -127,6 +133,26 @@ __global__ __launch_bounds__(kLdsSortBlock) void k_sort_lds(SortArgs a, int pass
       val[q] = kv[i].y;
     }
   }
+  if (a.counts) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const uint32_t i = i0 + q * 64;
+      if (i < n) ((int*)(a.order + rank * a.os))[i] = key[q] < a.nkeys ? (int)val[q] : -1;
+    }
+    for (uint32_t e = threadIdx.x; e < a.nkeys; e += kLdsSortBlock) {
+      uint32_t b[2];
+      for (int s = 0; s < 2; ++s) {   // first sorted place of the key e + s
+        uint32_t lo = 0, hi = n;
+        while (lo < hi) {
+          const uint32_t mid = (lo + hi) >> 1;
+          if (kv[mid].x < e + s) lo = mid + 1; else hi = mid;
+        }
+        b[s] = lo;
+      }
+      ((int*)(a.counts + rank * a.cs))[e] = (int)(b[1] - b[0]);
+    }
+    return;
+  }
 #pragma unroll
   for (int q = 0; q < R; ++q) {
     const uint32_t i = i0 + q * 64;
@@ -149,34 +175,70 @@ __global__ __launch_bounds__(kSortBlock) void k_sort_hist(SortArgs a) {
   a.hist[((uint64_t)blockIdx.y * kDigits + threadIdx.x) * a.tiles + blockIdx.x] = h[threadIdx.x];
 }
 
-// Exclusive prefix over a rank's kDigits * tiles counts, in place.
+// Exclusive prefix over a rank's kDigits * tiles counts, in place, 8 of them a
+// thread.  (tiles * kDigits is a multiple of 8.)
 constexpr int kScanBlock = 1024;
+constexpr int kScanEach = 8;
 __global__ __launch_bounds__(kScanBlock) void k_sort_scan(uint32_t* hist, uint64_t count) {
   __shared__ uint32_t wsum[kScanBlock / 64];
-  __shared__ uint32_t carry_s;
   uint32_t* h = hist + (uint64_t)blockIdx.x * count;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (threadIdx.x == 0) carry_s = 0;
-  __syncthreads();
-  for (uint64_t b = 0; b < count; b += kScanBlock) {
-    const uint64_t i = b + threadIdx.x;
-    const uint32_t v = i < count ? h[i] : 0u;
-    uint32_t s = v;
+  uint32_t carry = 0;
+  for (uint64_t b = 0; b < count; b += kScanBlock * kScanEach) {
+    const uint64_t i = b + (uint64_t)threadIdx.x * kScanEach;
+    uint32_t v[kScanEach] = {}, own = 0;
+    if (i < count) {
+      const u32x4 lo = *(const u32x4*)(h + i), hi = *(const u32x4*)(h + i + 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = lo[k];
+        v[4 + k] = hi[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kScanEach; ++k) own += v[k];
+    uint32_t s = own;
     for (int d = 1; d < 64; d <<= 1) {
       const uint32_t t = __shfl_up(s, d);
       if (lane >= d) s += t;
     }
+    __syncthreads();   // the last round's wsum is read
     if (lane == 63) wsum[wave] = s;
     __syncthreads();
-    uint32_t base = carry_s, all = 0;
+    uint32_t at = carry + s - own;
     for (int w = 0; w < kScanBlock / 64; ++w) {
-      if (w < wave) base += wsum[w];
-      all += wsum[w];
+      if (w < wave) at += wsum[w];
+      carry += wsum[w];
     }
-    if (i < count) h[i] = base + s - v;
-    __syncthreads();
-    if (threadIdx.x == 0) carry_s += all;
-    __syncthreads();
+    if (i < count) {
+      u32x4 lo, hi;
+#pragma unroll
+      for (int k = 0; k < kScanEach; ++k) {
+        if (k < 4) lo[k] = at; else hi[k - 4] = at;
+        at += v[k];
+      }
+      *(u32x4*)(h + i) = lo;
+      *(u32x4*)(h + i + 4) = hi;
+    }
+  }
+}
+
+// Positions and counts from sorted keys (more than one pass of tiles).
+__global__ __launch_bounds__(kSortBlock) void k_sort_order(SortArgs a) {
+  const uint64_t r = blockIdx.y, i = (uint64_t)blockIdx.x * kSortBlock + threadIdx.x;
+  const int* keys = a.kin + r * a.n;
+  if (i < a.n) ((int*)(a.order + r * a.os))[i] = (uint32_t)keys[i] < a.nkeys ? a.vin[r * a.n + i] : -1;
+  if (i < a.nkeys) {
+    uint64_t b[2];
+    for (int s = 0; s < 2; ++s) {
+      uint64_t lo = 0, hi = a.n;
+      while (lo < hi) {
+        const uint64_t mid = (lo + hi) >> 1;
+        if ((uint64_t)keys[mid] < i + s) lo = mid + 1; else hi = mid;
+      }
+      b[s] = lo;
+    }
+    ((int*)(a.counts + r * a.cs))[i] = (int)(b[1] - b[0]);
   }
 }
 
@@ -207,7 +269,11 @@ __global__ __launch_bounds__(kSortBlock) void k_sort_scatter(SortArgs a) {
   __syncthreads();
   {
     const int d = threadIdx.x;   // kSortBlock == kDigits
-    uint32_t at = a.hist[((uint64_t)blockIdx.y * kDigits + d) * a.tiles + blockIdx.x];
+    const uint32_t* first = a.hist + ((uint64_t)blockIdx.y * kDigits + d) * a.tiles;
+    uint32_t at = first[blockIdx.x];
+    // one pass: a digit is a key, and nkeys < kDigits of them have a next one
+    if (a.counts && blockIdx.x == 0 && (uint32_t)d < a.nkeys)
+      ((int*)(a.counts + (uint64_t)blockIdx.y * a.cs))[d] = (int)(first[a.tiles] - first[0]);
     for (int w = 0; w < kSortWaves; ++w) {
       const uint32_t c = cnt[w][d];
       cnt[w][d] = at;
@@ -219,9 +285,13 @@ __global__ __launch_bounds__(kSortBlock) void k_sort_scatter(SortArgs a) {
     const uint64_t i = i0 + (uint64_t)q * 64 + lane;
     if (i >= a.n) continue;
     const uint32_t d = (key[q] >> a.shift) & (kDigits - 1);
-    const uint64_t to = (uint64_t)blockIdx.y * a.n + cnt[wave][d] + place[q];
-    a.kout[to] = (int)key[q];
-    a.vout[to] = val[q];
+    const uint64_t to = cnt[wave][d] + place[q];
+    if (a.counts) {
+      ((int*)(a.order + (uint64_t)blockIdx.y * a.os))[to] = key[q] < a.nkeys ? val[q] : -1;
+    } else {
+      a.kout[(uint64_t)blockIdx.y * a.n + to] = (int)key[q];
+      a.vout[(uint64_t)blockIdx.y * a.n + to] = val[q];
+    }
   }
 }
 
@@ -248,7 +318,9 @@ hipError_t launch_sort(SortLaunch* L) {
   SortArgs a = {};
   a.keys = L->keys; a.key_stride = L->key_stride;
   a.n = p.n; a.nkeys = p.nkeys;
-  if (p.tiles == 0) {
+  a.order = L->order; a.os = L->order_stride; a.cs = L->counts_stride;
+  if (p.n == 0 || p.tiles == 0) {
+    a.counts = L->counts;
     a.first = 1;
     a.kout = (int*)L->ws;
     a.vout = (int*)(L->ws + arr);
@@ -272,12 +344,20 @@ hipError_t launch_sort(SortLaunch* L) {
     a.shift = 8 * pass;
     a.kin = k[(pass + 1) & 1]; a.vin = v[(pass + 1) & 1];
     a.kout = k[pass & 1]; a.vout = v[pass & 1];
+    a.counts = p.passes == 1 ? L->counts : nullptr;
     CC_LAUNCH(k_sort_hist, grid, blk, 0, L->st, a);
     CC_LAUNCH(k_sort_scan, dim3((unsigned)p.N), dim3(kScanBlock), 0, L->st, a.hist, (uint64_t)kDigits * p.tiles);
     CC_LAUNCH(k_sort_scatter, grid, blk, 0, L->st, a);
   }
   L->sorted_keys = k[(p.passes - 1) & 1];
   L->sorted_vals = v[(p.passes - 1) & 1];
+  if (L->counts && p.passes > 1) {
+    a.counts = L->counts;
+    a.kin = L->sorted_keys;
+    a.vin = L->sorted_vals;
+    const uint64_t m = std::max<uint64_t>(p.n, p.nkeys);
+    CC_LAUNCH(k_sort_order, dim3((unsigned)((m + kSortBlock - 1) / kSortBlock), (unsigned)p.N), blk, 0, L->st, a);
+  }
   return hipGetLastError();
 }
 
