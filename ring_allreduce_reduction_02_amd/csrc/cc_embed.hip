@@ -29,6 +29,41 @@ struct EmbedArgs {
   float scale;
 };
 
+// 16 bytes of a row: with VEC rows are 16-byte aligned; otherwise they start
+// anywhere (global memory takes whole vectors at any element), and the row's
+// last vector, `left` elements short of V, goes by elements.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int DT, bool VEC>
+__device__ __forceinline__ u32x4 load_part(const char* p, int64_t left) {
+  if constexpr (VEC) {
+    return left > 0 ? *(const u32x4*)p : u32x4{0u, 0u, 0u, 0u};
+  } else {
+    if (left >= Ty<DT>::V) return *(const u32x4_any*)p;
+    float x[Ty<DT>::V] = {};
+#pragma unroll
+    for (int i = 0; i < Ty<DT>::V; ++i)
+      if (i < left) x[i] = ld1<DT>(p + i * Ty<DT>::SZ);
+    return pack<DT>(x);   // widened and packed again: the same bits
+  }
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_part(char* p, u32x4 w, int64_t left) {
+  if constexpr (VEC) {
+    if (left > 0) stg(p, w);
+  } else {
+    if (left >= Ty<DT>::V) {
+      *(u32x4_any*)p = w;
+      return;
+    }
+    float x[Ty<DT>::V];
+    unpack<DT>(w, x);
+#pragma unroll
+    for (int i = 0; i < Ty<DT>::V; ++i)
+      if (i < left) st1<DT>(p + i * Ty<DT>::SZ, x[i]);
+  }
+}
+
 // One workgroup a token row and rank.
 template <int DT, bool VEC>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed(EmbedArgs a) {
@@ -37,22 +72,18 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed(EmbedArgs a) {
   const bool in = (uint32_t)id < a.vocab;
   char* o = a.out + r * a.os + t * a.width * Ty<DT>::SZ;
   const char* s = a.table + r * a.ts + (in ? (uint64_t)id : 0) * a.width * Ty<DT>::SZ;
-  constexpr int V = VEC ? Ty<DT>::V : 1;
+  constexpr int V = Ty<DT>::V;
   for (uint64_t c = (uint64_t)threadIdx.x * V; c < a.width; c += kEmbedBlock * V) {
-    float x[V];
+    const int64_t left = (int64_t)(a.width - c);
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (in) {
+      float x[V];
+      unpack<DT>(load_part<DT, VEC>(s + c * Ty<DT>::SZ, left), x);
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = 0.0f;
-    if constexpr (VEC) {
-      if (in) {
-        unpack<DT>(*(const u32x4*)(s + c * Ty<DT>::SZ), x);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] *= a.scale;
-      }
-      *(u32x4*)(o + c * Ty<DT>::SZ) = pack<DT>(x);
-    } else {
-      if (in) x[0] = ld1<DT>(s + c * Ty<DT>::SZ) * a.scale;
-      st1<DT>(o + c * Ty<DT>::SZ, x[0]);
+      for (int i = 0; i < V; ++i) x[i] *= a.scale;
+      w = pack<DT>(x);
     }
+    store_part<DT, VEC>(o + c * Ty<DT>::SZ, w, left);
   }
 }
 
@@ -63,8 +94,8 @@ struct EmbedGradArgs {
   uint64_t os;
   const int* keys;   // each rank's sorted ids and their positions, [N][tokens]
   const int* vals;
-  float* partial;    // [N][pieces][width]
-  uint64_t vocab, tokens, width;
+  float* partial;    // [N][pieces][pitch]
+  uint64_t vocab, tokens, width, pitch;
   uint64_t pieces;   // of kEmbedPiece sorted positions per rank; 0: no partial sums
   float scale;
   int N;
@@ -72,10 +103,10 @@ struct EmbedGradArgs {
 
 // A wave's columns: CB blocks of 64 lanes, V consecutive elements a lane.
 // Enough of them that a row of 2048 bf16 takes one walk over its tokens.
-template <int DT, bool VEC>
+template <int DT>
 struct Cols {
-  static constexpr int V = VEC ? Ty<DT>::V : 1;
-  static constexpr int CB = VEC ? 4 : 8;
+  static constexpr int V = Ty<DT>::V;
+  static constexpr int CB = 4;
   static constexpr int STEP = 64 * V * CB;
 };
 
@@ -86,41 +117,32 @@ constexpr int kEmbedBatch = 4;   // token rows under way per wave
 // four at a time, so that a lane has 4 CB loads under way.
 template <int DT, bool VEC>
 __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, uint64_t r, uint64_t lo, uint64_t hi, uint64_t c0,
-                                         int lane, float (&acc)[Cols<DT, VEC>::CB][Cols<DT, VEC>::V]) {
-  constexpr int V = Cols<DT, VEC>::V, CB = Cols<DT, VEC>::CB, SZ = Ty<DT>::SZ;
+                                         int lane, float (&acc)[Cols<DT>::CB][Cols<DT>::V]) {
+  constexpr int V = Cols<DT>::V, CB = Cols<DT>::CB, SZ = Ty<DT>::SZ;
   const int* vals = a.vals + r * a.tokens;
   const char* base = a.grad + r * a.gs + (c0 + lane * V) * SZ;
-  const uint64_t left = a.width - c0;
+  const int64_t left = (int64_t)(a.width - c0) - lane * V;
   for (uint64_t p0 = lo; p0 < hi; p0 += 64) {
     const int n = (int)(hi - p0 < 64 ? hi - p0 : 64);
     const int mine = lane < n ? vals[p0 + lane] : 0;
     for (int k = 0; k < n; k += kEmbedBatch) {
       u32x4 w[kEmbedBatch][CB];
-      float x1[kEmbedBatch][CB];
 #pragma unroll
       for (int q = 0; q < kEmbedBatch; ++q) {
         const uint32_t t = (uint32_t)__builtin_amdgcn_readlane(mine, k + q < n ? k + q : k);
         const char* g = base + (uint64_t)t * a.width * SZ;
 #pragma unroll
-        for (int i = 0; i < CB; ++i) {
-          const bool in = (uint64_t)(i * 64 + lane) * V < left;
-          if constexpr (VEC) w[q][i] = in ? *(const u32x4*)(g + i * 64 * V * SZ) : u32x4{0u, 0u, 0u, 0u};
-          else x1[q][i] = in ? ld1<DT>(g + i * 64 * SZ) : 0.0f;
-        }
+        for (int i = 0; i < CB; ++i) w[q][i] = load_part<DT, VEC>(g + i * 64 * V * SZ, left - i * 64 * V);
       }
 #pragma unroll
       for (int q = 0; q < kEmbedBatch; ++q) {
         if (k + q >= n) break;
 #pragma unroll
         for (int i = 0; i < CB; ++i) {
-          if constexpr (VEC) {
-            float x[V];
-            unpack<DT>(w[q][i], x);
+          float x[V];
+          unpack<DT>(w[q][i], x);
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[i][e] += x[e];
-          } else {
-            acc[i][0] += x1[q][i];
-          }
+          for (int e = 0; e < V; ++e) acc[i][e] += x[e];
         }
       }
     }
@@ -142,7 +164,7 @@ __device__ __forceinline__ uint32_t lower_bound(const int* keys, uint32_t n, uin
 // is summed by many.
 template <int DT, bool VEC>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
-  typedef Cols<DT, VEC> C;
+  typedef Cols<DT> C;
   const int lane = threadIdx.x & 63;
   const uint64_t piece = (uint64_t)blockIdx.x * (kEmbedBlock / 64) + (threadIdx.x >> 6), r = blockIdx.y;
   if (piece >= a.pieces) return;
@@ -152,16 +174,14 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
   if (k >= a.vocab || k != (uint32_t)keys[p0 + kEmbedPiece - 1]) return;
   const uint32_t end = lower_bound(keys, (uint32_t)a.tokens, k + (lane & 1));   // the run's first and last + 1
   if (__builtin_amdgcn_readlane(end, 1) - __builtin_amdgcn_readlane(end, 0) < kEmbedLong) return;
-  float* o = a.partial + (r * a.pieces + piece) * a.width;
+  float* o = a.partial + (r * a.pieces + piece) * a.pitch;
   for (uint64_t c0 = 0; c0 < a.width; c0 += C::STEP) {
     float acc[C::CB][C::V] = {};
     add_rows<DT, VEC>(a, r, p0, p0 + kEmbedPiece, c0, lane, acc);
 #pragma unroll
     for (int i = 0; i < C::CB; ++i) {
       const uint64_t c = c0 + (uint64_t)(i * 64 + lane) * C::V;
-      if (c >= a.width) continue;
-      if constexpr (VEC) stw_vec<DT>((char*)(o + c), acc[i]);
-      else o[c] = acc[i][0];
+      if (c < a.width) stw_vec<DT>((char*)(o + c), acc[i]);
     }
   }
 }
@@ -170,27 +190,23 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
 // positions: of a long run, whole pieces come as their partial sums.
 template <int DT, bool VEC>
 __device__ __forceinline__ void add_run(const EmbedGradArgs& a, uint64_t r, uint64_t lo, uint64_t hi, uint64_t run,
-                                        uint64_t c0, int lane, float (&acc)[Cols<DT, VEC>::CB][Cols<DT, VEC>::V]) {
-  typedef Cols<DT, VEC> C;
+                                        uint64_t c0, int lane, float (&acc)[Cols<DT>::CB][Cols<DT>::V]) {
+  typedef Cols<DT> C;
   const uint64_t f = (lo + kEmbedPiece - 1) / kEmbedPiece, l = hi / kEmbedPiece;
   if (a.pieces == 0 || run < kEmbedLong || f >= l) {
     add_rows<DT, VEC>(a, r, lo, hi, c0, lane, acc);
     return;
   }
   add_rows<DT, VEC>(a, r, lo, f * kEmbedPiece, c0, lane, acc);
-  const float* part = a.partial + (r * a.pieces + f) * a.width + c0 + lane * C::V;
-  for (uint64_t p = f; p < l; ++p, part += a.width)
+  const float* part = a.partial + (r * a.pieces + f) * a.pitch + c0 + lane * C::V;
+  for (uint64_t p = f; p < l; ++p, part += a.pitch)
 #pragma unroll
     for (int k = 0; k < C::CB; ++k) {
       if (c0 + (uint64_t)(k * 64 + lane) * C::V >= a.width) continue;
-      if constexpr (VEC) {
-        float x[C::V];
-        ldw_vec<DT>((const char*)(part + k * 64 * C::V), x);
+      float x[C::V];
+      ldw_vec<DT>((const char*)(part + k * 64 * C::V), x);
 #pragma unroll
-        for (int e = 0; e < C::V; ++e) acc[k][e] += x[e];
-      } else {
-        acc[k][0] += part[k * 64];
-      }
+      for (int e = 0; e < C::V; ++e) acc[k][e] += x[e];
     }
   add_rows<DT, VEC>(a, r, l * kEmbedPiece, hi, c0, lane, acc);
 }
@@ -198,8 +214,8 @@ __device__ __forceinline__ void add_run(const EmbedGradArgs& a, uint64_t r, uint
 // columns of acc, scaled, to the ranks [r0, r0 + nr)
 template <int DT, bool VEC>
 __device__ __forceinline__ void put_row(const EmbedGradArgs& a, char* o, int r0, int nr, uint64_t c0, int lane,
-                                        float (&acc)[Cols<DT, VEC>::CB][Cols<DT, VEC>::V]) {
-  typedef Cols<DT, VEC> C;
+                                        float (&acc)[Cols<DT>::CB][Cols<DT>::V]) {
+  typedef Cols<DT> C;
 #pragma unroll
   for (int k = 0; k < C::CB; ++k) {
     const uint64_t c = c0 + (uint64_t)(k * 64 + lane) * C::V;
@@ -207,9 +223,7 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs& a, char* o, int r0,
 #pragma unroll
     for (int e = 0; e < C::V; ++e) acc[k][e] *= a.scale;
     for (int r = r0; r < r0 + nr; ++r) {
-      char* to = o + (uint64_t)r * a.os + c * Ty<DT>::SZ;
-      if constexpr (VEC) stg(to, pack<DT>(acc[k]));
-      else st1<DT>(to, acc[k][0]);
+      store_part<DT, VEC>(o + (uint64_t)r * a.os + c * Ty<DT>::SZ, pack<DT>(acc[k]), (int64_t)(a.width - c));
     }
   }
 }
@@ -239,7 +253,7 @@ constexpr int kEmbedWaves = kEmbedBlock / 64;
 
 template <int DT, bool VEC, bool SUM>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
-  typedef Cols<DT, VEC> C;
+  typedef Cols<DT> C;
   constexpr int SZ = Ty<DT>::SZ;
   extern __shared__ uint32_t runs[];   // [nr][kEmbedRows] begin, then end
   uint32_t(*const begin)[kEmbedRows] = (uint32_t(*)[kEmbedRows])runs;
@@ -321,7 +335,7 @@ hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
   }
   const unsigned blocks = (unsigned)((a.vocab + kEmbedRows - 1) / kEmbedRows);
   const unsigned need = (L.summed ? L.N : 1) * 2 * kEmbedRows * 4;
-  const unsigned cap = lds_for_blocks_per_cu(L.blocks_per_cu), fixed = sizeof(float) * (2 * Cols<DT, VEC>::STEP + kEmbedRows);
+  const unsigned cap = lds_for_blocks_per_cu(L.blocks_per_cu), fixed = sizeof(float) * (2 * Cols<DT>::STEP + kEmbedRows);
   const unsigned lds = std::max(need, cap > fixed ? cap - fixed : 0u);
   if (L.summed) CC_LAUNCH((k_embed_grad<DT, VEC, true>), dim3(blocks), dim3(kEmbedBlock), lds, L.st, a);
   else CC_LAUNCH((k_embed_grad<DT, VEC, false>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), lds, L.st, a);
@@ -346,7 +360,7 @@ hipError_t launch_embed(const EmbedLaunch& L) {
 
 hipError_t launch_embed_grad(const EmbedGradLaunch& L) {
   EmbedGradArgs a{L.grad, L.grad_stride, L.out, L.out_stride, L.keys, L.vals, L.partial,
-                  L.vocab, L.tokens, L.width, embed_pieces(L.tokens), L.scale, L.N};
+                  L.vocab, L.tokens, L.width, embed_partial_pitch(L.width), embed_pieces(L.tokens), L.scale, L.N};
   if (L.dt == DT_F32) return L.vec_ok ? run_embed_grad<DT_F32, true>(a, L) : run_embed_grad<DT_F32, false>(a, L);
   return L.vec_ok ? run_embed_grad<DT_BF16, true>(a, L) : run_embed_grad<DT_BF16, false>(a, L);
 }

@@ -208,31 +208,66 @@ __device__ __forceinline__ u32x4 frag(const char* t, int u, int i0, int lane) {
   }
 }
 
-// Element-wise staging of a tile: any alignment.  Row tiles: lp[r] is line
-// r's first byte (NULL: zeros), elements [k0, K).  Column tiles: lp[k] is
-// summed line k0 + k (NULL: zeros), columns [c0, C).
+// V floats in one 16-byte vector; bf16 by the hardware's conversion (nearest,
+// ties to even), one instruction for two elements
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <int DT>
+__device__ __forceinline__ u32x4 pack_row(const float* v) {
+  if constexpr (DT == DT_BF16) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[2 * i], v[2 * i + 1]}), bf16x2));
+    return w;
+  } else {
+    return pack<DT>(v);
+  }
+}
+
+// Staging of a tile of lines that start anywhere, through registers: 16-byte
+// chunks (global memory takes whole vectors at any element), a line's last
+// one by elements.  Row tiles: lp[r] is line r's first byte (the last line
+// repeated past the end), elements [k0, K).  Column tiles: lp[k] is summed line
+// k0 + k (NULL past the end: zeros), columns [c0, C).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 template <int DT, bool COL, int R, int NT>
-struct Elems {
-  static constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ, Q = R * BK / NT;
-  uint32_t v[Q];
+struct Chunks {
+  static constexpr int SZ = Ty<DT>::SZ, V = Ty<DT>::V, Q = R * kKBytes / 16 / NT;
+  static constexpr int PER = COL ? R * SZ / 16 : kKBytes / 16;   // chunks per line
+  u32x4 v[Q];
   __device__ __forceinline__ void load(const char* const* lp, int64_t k0, int64_t K, int64_t c0, int64_t C) {
+    if (k0 + kKBytes / SZ <= K && (!COL || c0 + R <= C)) {   // whole chunks only
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int e = threadIdx.x + q * NT;
+        v[q] = *(const u32x4_any*)(lp[e / PER] + ((COL ? c0 : k0) + (int64_t)(e % PER) * V) * SZ);
+      }
+      return;
+    }
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int e = threadIdx.x + q * NT;
-      const int line = COL ? e / R : e / BK;
-      const int64_t at = COL ? c0 + e % R : k0 + e % BK;
-      const char* p = lp[line];
-      v[q] = 0;
-      if (p && at < (COL ? C : K)) v[q] = SZ == 2 ? *(const uint16_t*)(p + at * SZ) : *(const uint32_t*)(p + at * SZ);
+      const int64_t at = (COL ? c0 : k0) + (int64_t)(e % PER) * V, left = (COL ? C : K) - at;
+      const char* p = lp[e / PER];
+      v[q] = u32x4{0u, 0u, 0u, 0u};
+      if (p && left >= V) {
+        v[q] = *(const u32x4_any*)(p + at * SZ);
+      } else if (p && left > 0) {
+        float x[V] = {};
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < left) x[i] = ld1<DT>(p + (at + i) * SZ);
+        v[q] = pack_row<DT>(x);   // widened and packed again: the same bits
+      }
     }
   }
   __device__ __forceinline__ void store(char* t) const {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int e = threadIdx.x + q * NT;
-      const int at = COL ? col_at<DT, R>(e / R, e % R) : row_at(e / BK, e % BK * SZ / 16) + (e % BK * SZ) % 16;
-      if constexpr (SZ == 2) *(uint16_t*)(t + at) = (uint16_t)v[q];
-      else *(uint32_t*)(t + at) = v[q];
+      *(u32x4*)(t + (COL ? col_at<DT, R>(e / PER, e % PER * V) : row_at(e / PER, e % PER))) = v[q];
     }
   }
 };
@@ -283,23 +318,6 @@ __device__ __forceinline__ void gate_grad(const float* g, const float* u, int ac
   }
 }
 
-// V floats in one 16-byte vector; bf16 by the hardware's conversion (nearest,
-// ties to even), one instruction for two elements
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-template <int DT>
-__device__ __forceinline__ u32x4 pack_row(const float* v) {
-  if constexpr (DT == DT_BF16) {
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[2 * i], v[2 * i + 1]}), bf16x2));
-    return w;
-  } else {
-    return pack<DT>(v);
-  }
-}
-
 // V (4 or 8) consecutive elements of a row, n of them inside it
 template <int DT, bool VEC, int V>
 __device__ __forceinline__ void store_n(char* p, const float* v, int n) {
@@ -307,6 +325,8 @@ __device__ __forceinline__ void store_n(char* p, const float* v, int n) {
     if (n <= 0) return;
     static_assert(V * Ty<DT>::SZ == 16, "one vector");
     stg(p, pack_row<DT>(v));   // past the caches, which the operands' tiles need
+  } else if (n >= V) {
+    *(u32x4_any*)p = pack_row<DT>(v);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -317,6 +337,8 @@ template <int DT, bool VEC, int V>
 __device__ __forceinline__ void load_n(const char* p, float* v, int n) {
   if constexpr (VEC) {
     unpack<DT>(n > 0 ? *(const u32x4*)p : u32x4{0u, 0u, 0u, 0u}, v);
+  } else if (n >= V) {
+    unpack<DT>(*(const u32x4_any*)p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = i < n ? ld1<DT>(p + i * Ty<DT>::SZ) : 0.0f;
@@ -550,10 +572,10 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TM][TN]) {
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 }
 
-// Any alignment: every element staged by itself, through registers, the next
-// stage's on their way while this one's products run.
+// Any alignment: tiles staged through registers, the next stage's on their way
+// while this one's products run.
 template <int DT, int KIND, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmArgs g) {
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_any(GemmArgs g) {
   constexpr int NT = 64 * (BM / WM) * (BN / WN);
   constexpr int BK = kKBytes / Ty<DT>::SZ;
   constexpr int TM = WM / 32, TN = WN / 32;
@@ -570,12 +592,12 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmAr
   const int mw = (wave % (BM / WM)) * WM, nw = (wave / (BM / WM)) * WN;
   const Part t = tile_of<KIND, BM, BN>(g);
   if constexpr (!ACOL)
-    for (int r = tid; r < BM; r += NT) la[r] = t.p0 + r < t.p1 ? row_ptr(g.a, t.rank, t.p0 + r) : nullptr;
+    for (int r = tid; r < BM; r += NT) la[r] = row_ptr(g.a, t.rank, t.p0 + r < t.p1 ? t.p0 + r : t.p1 - 1);
   if constexpr (!BCOL) {
     const char* w = wt_ptr(g.b, t.rank, t.local);
     for (int r = tid; r < BN; r += NT) {
       const int64_t row = weight_line<KIND>(g, t, r);
-      lb[r] = row >= 0 ? w + row * (int64_t)g.b.pitch : nullptr;
+      lb[r] = w + (row >= 0 ? row : 0) * (int64_t)g.b.pitch;
     }
   }
   auto summed_lines = [&](int64_t k0) {
@@ -586,8 +608,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_elems(GemmAr
       else if constexpr (BCOL) lb[tid] = k < t.K ? wt_ptr(g.b, t.rank, t.local) + k * (int64_t)g.b.pitch : nullptr;
     }
   };
-  Elems<DT, ACOL, BM, NT> ea;
-  Elems<DT, BCOL, BN, NT> eb;
+  Chunks<DT, ACOL, BM, NT> ea;
+  Chunks<DT, BCOL, BN, NT> eb;
   f32x16 acc[TM][TN];
   clear(acc);
   summed_lines(0);
@@ -897,8 +919,8 @@ hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
   if (blocks == 0) return hipSuccess;
   const dim3 grid((unsigned)blocks);
   if (!fast) {
-    if (k == 1) CC_LAUNCH((k_ffn_elems<DT, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, L.st, g);
-    else CC_LAUNCH((k_ffn_elems<DT, KIND, 64, 64, 32, 64>), grid, dim3(128), 0, L.st, g);
+    if (k == 1) CC_LAUNCH((k_ffn_any<DT, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, L.st, g);
+    else CC_LAUNCH((k_ffn_any<DT, KIND, 64, 64, 32, 64>), grid, dim3(128), 0, L.st, g);
   } else if (k == 0) {
     CC_LAUNCH((k_ffn_tile<DT, KIND, 256, 256, 128, 64>), grid, dim3(512), 0, L.st, g);
   } else if (k == 1) {

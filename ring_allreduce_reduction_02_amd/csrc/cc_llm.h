@@ -59,6 +59,7 @@ hipError_t launch_embed(const EmbedLaunch& L);
 // workgroup sums a whole run itself in the time of the extra launch.
 constexpr int kEmbedPiece = 32;
 constexpr uint32_t kEmbedLong = 128;
+inline uint64_t embed_partial_pitch(uint64_t width) { return (width + 7) / 8 * 8; }
 inline uint64_t embed_pieces(uint64_t tokens) { return tokens > 512 ? tokens / kEmbedPiece : 0; }
 struct EmbedGradLaunch {
   const char* grad;
@@ -67,7 +68,7 @@ struct EmbedGradLaunch {
   uint64_t out_stride;
   const int* keys;       // sorted, [N][tokens]
   const int* vals;
-  float* partial;        // [N][embed_pieces][width]
+  float* partial;        // [N][embed_pieces][embed_partial_pitch]
   uint64_t vocab, tokens, width;
   float scale;
   int N, dt, vec_ok, blocks_per_cu;

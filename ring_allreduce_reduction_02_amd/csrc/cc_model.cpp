@@ -105,7 +105,7 @@ EmbedWs embed_ws(int N, uint64_t vocab, uint64_t tokens, uint64_t width) {
   EmbedWs w;
   w.sort = sort_plan(N, tokens, (uint32_t)vocab);
   w.partial = w.sort.bytes;
-  w.bytes = tokens ? w.partial + rup((uint64_t)N * embed_pieces(tokens) * width * 4, 256) : 0;
+  w.bytes = tokens ? w.partial + rup((uint64_t)N * embed_pieces(tokens) * embed_partial_pitch(width) * 4, 256) : 0;
   return w;
 }
 
