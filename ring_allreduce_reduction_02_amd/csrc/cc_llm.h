@@ -55,12 +55,12 @@ struct EmbedLaunch {
 hipError_t launch_embed(const EmbedLaunch& L);
 
 // Sorted positions per partial sum of a long run, the shortest run that has
-// them, and how many a rank's tokens have; none up to 512 tokens, where a
+// them, and how many a rank's tokens have; none up to 1024 tokens, where a
 // workgroup sums a whole run itself in the time of the extra launch.
 constexpr int kEmbedPiece = 32;
 constexpr uint32_t kEmbedLong = 128;
 inline uint64_t embed_partial_pitch(uint64_t width) { return (width + 7) / 8 * 8; }
-inline uint64_t embed_pieces(uint64_t tokens) { return tokens > 512 ? tokens / kEmbedPiece : 0; }
+inline uint64_t embed_pieces(uint64_t tokens) { return tokens > 1024 ? tokens / kEmbedPiece : 0; }
 struct EmbedGradLaunch {
   const char* grad;
   uint64_t grad_stride;
