@@ -564,30 +564,44 @@ def int8_message_bytes(count: int) -> int:
 ACTS = {"silu": 0, "gelu": 1}
 
 
-def _operand(t, name: str, n: int, length: int, dtype=None) -> RankBuf:
-    """A rank-strided operand [n, length] on the current device."""
-    import torch
-    if tuple(t.shape) != (n, length):
-        raise ValueError(f"{name} must be [{n}, {length}], got {list(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    b = rankbuf(t)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
-    return b
+class _Call:
+    """The operands, stream and config of one call.  Everything belongs to the
+    current device, which is asked for once; a call with no workspace and no
+    occupancy cap passes no config (NULL is that config)."""
 
+    def __init__(self, stream, workspace=None, blocks_per_cu: int = 0):
+        import torch
+        dev = self.dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+        if stream is None:
+            self.stream = torch.cuda.current_stream().cuda_stream if dev is not None else None
+        else:
+            if stream.device_index != dev:
+                raise ValueError("the stream belongs to another device")
+            self.stream = stream.cuda_stream
+        self.cfg = None
+        if workspace is not None:
+            if not workspace.is_cuda or workspace.get_device() != dev:
+                raise ValueError("the workspace must be on the current device")
+            if not workspace.is_contiguous():
+                raise ValueError("the workspace must be contiguous")
+        if workspace is not None or blocks_per_cu:
+            self.cfg = ctypes.byref(config("ring", 0, workspace, blocks_per_cu))
 
-def _operand_stream(stream, workspace=None) -> ctypes.c_void_p:
-    """The call's stream; it and the workspace belong to the current device."""
-    import torch
-    if stream is not None and stream.device_index != torch.cuda.current_device():
-        raise ValueError("the stream belongs to another device")
-    if workspace is not None:
-        if not workspace.is_cuda or workspace.device.index != torch.cuda.current_device():
-            raise ValueError("the workspace must be on the current device")
-        if not workspace.is_contiguous():
-            raise ValueError("the workspace must be contiguous")
-    return _stream(stream)
+    def operand(self, t, name: str, n: int, length: int, dtype=None) -> RankBuf:
+        """A rank-strided operand [n, length] on the current device."""
+        shape = t.shape
+        if len(shape) != 2 or shape[0] != n or shape[1] != length:
+            raise ValueError(f"{name} must be [{n}, {length}], got {list(shape)}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: buffers must be device tensors")
+        if t.get_device() != self.dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is {self.dev}")
+        stride = t.stride()
+        if length > 1 and stride[1] != 1:
+            raise ValueError(f"{name}: each rank's row must be contiguous")
+        return RankBuf(t.data_ptr(), stride[0] * t.element_size())
 
 
 def _rows(t, width: int, name: str) -> int:
@@ -601,12 +615,10 @@ def embedding(table, ids, out, width: int, scale: float = 1.0, stream=None, bloc
     [N, V * width]; zero rows for ids outside [0, V).  A table expanded over
     the ranks (stride 0) is one table that all ranks read."""
     import torch
-    N, T, V = ids.shape[0], ids.shape[1], _rows(table, width, "table")
-    args = (_operand(table, "table", N, V * width), _operand(ids, "ids", N, T, torch.int32),
-            _operand(out, "out", N, T * width, table.dtype))
-    cfg = config("ring", 0, None, blocks_per_cu)
-    _check(load().cc_embedding(*args, V, T, width, float(scale), DTYPES[dtype_name(table)], N, ctypes.byref(cfg),
-                               _operand_stream(stream)))
+    (N, T), V, c = ids.shape, _rows(table, width, "table"), _Call(stream, None, blocks_per_cu)
+    _check(load().cc_embedding(c.operand(table, "table", N, V * width), c.operand(ids, "ids", N, T, torch.int32),
+                               c.operand(out, "out", N, T * width, table.dtype), V, T, width, scale,
+                               DTYPES[dtype_name(table)], N, c.cfg, c.stream))
 
 
 def embedding_grad_workspace_size(nranks: int, vocab: int, tokens: int, width: int) -> int:
@@ -624,12 +636,10 @@ def make_embedding_grad_workspace(nranks: int, vocab: int, tokens: int, width: i
 
 def _embedding_grad(call: str, grad, ids, dtable, width, scale, workspace, stream, blocks_per_cu) -> None:
     import torch
-    N, T, V = ids.shape[0], ids.shape[1], _rows(dtable, width, "dtable")
-    args = (_operand(grad, "grad", N, T * width), _operand(ids, "ids", N, T, torch.int32),
-            _operand(dtable, "dtable", N, V * width, grad.dtype))
-    cfg = config("ring", 0, workspace, blocks_per_cu)
-    _check(getattr(load(), call)(*args, V, T, width, float(scale), DTYPES[dtype_name(grad)], N, ctypes.byref(cfg),
-                                 _operand_stream(stream, workspace)))
+    (N, T), V, c = ids.shape, _rows(dtable, width, "dtable"), _Call(stream, workspace, blocks_per_cu)
+    _check(getattr(load(), call)(c.operand(grad, "grad", N, T * width), c.operand(ids, "ids", N, T, torch.int32),
+                                 c.operand(dtable, "dtable", N, V * width, grad.dtype), V, T, width, scale,
+                                 DTYPES[dtype_name(grad)], N, c.cfg, c.stream))
 
 
 def embedding_grad(grad, ids, dtable, width: int, scale: float = 1.0, workspace=None, stream=None,
@@ -664,26 +674,25 @@ def moe_route(logits, experts, weights, order, counts, topk: int, normalize: boo
     order (int32) [N, T * topk], counts (int32) [N, E]."""
     import torch
     N, E = counts.shape
-    T = _rows(logits, E, "logits")
-    args = (_operand(logits, "logits", N, T * E), _operand(experts, "experts", N, T * topk, torch.int32),
-            _operand(weights, "weights", N, T * topk, torch.float32),
-            _operand(order, "order", N, T * topk, torch.int32), _operand(counts, "counts", N, E, torch.int32))
-    cfg = config("ring", 0, workspace)
-    _check(load().cc_moe_route(*args, T, E, topk, int(bool(normalize)), DTYPES[dtype_name(logits)], N,
-                               ctypes.byref(cfg), _operand_stream(stream, workspace)))
+    T, c = _rows(logits, E, "logits"), _Call(stream, workspace)
+    _check(load().cc_moe_route(c.operand(logits, "logits", N, T * E),
+                               c.operand(experts, "experts", N, T * topk, torch.int32),
+                               c.operand(weights, "weights", N, T * topk, torch.float32),
+                               c.operand(order, "order", N, T * topk, torch.int32),
+                               c.operand(counts, "counts", N, E, torch.int32), T, E, topk, 1 if normalize else 0,
+                               DTYPES[dtype_name(logits)], N, c.cfg, c.stream))
 
 
 def moe_route_grad(logits, experts, dweights, dlogits, topk: int, normalize: bool = False, stream=None) -> None:
     """dlogits [N, T * E] from dweights (f32) [N, T * topk] at the experts moe_route chose."""
     import torch
     N, T = experts.shape[0], _rows(experts, topk, "experts")
-    E = _experts_of(logits, N, T)
-    args = (_operand(logits, "logits", N, T * E), _operand(experts, "experts", N, T * topk, torch.int32),
-            _operand(dweights, "dweights", N, T * topk, torch.float32),
-            _operand(dlogits, "dlogits", N, T * E, logits.dtype))
-    cfg = config("ring", 0, None)
-    _check(load().cc_moe_route_grad(*args, T, E, topk, int(bool(normalize)), DTYPES[dtype_name(logits)], N,
-                                    ctypes.byref(cfg), _operand_stream(stream)))
+    E, c = _experts_of(logits, N, T), _Call(stream)
+    _check(load().cc_moe_route_grad(c.operand(logits, "logits", N, T * E),
+                                    c.operand(experts, "experts", N, T * topk, torch.int32),
+                                    c.operand(dweights, "dweights", N, T * topk, torch.float32),
+                                    c.operand(dlogits, "dlogits", N, T * E, logits.dtype), T, E, topk,
+                                    1 if normalize else 0, DTYPES[dtype_name(logits)], N, c.cfg, c.stream))
 
 
 def _experts_of(logits, n: int, tokens: int) -> int:
@@ -726,29 +735,27 @@ def moe_ffn(x, w_in, w_out, y, counts: Sequence[Sequence[int]], capacity: int, w
     [N, E/N * 2 * hidden * width], w_out [N, E/N * width * hidden], counts
     N x E; pre [N, E * capacity * 2 * hidden] keeps the pre-activations."""
     N, E, hidden, side, arr = _ffn_operands(x, w_in, w_out, counts, capacity, width)
-    per, dt = E // N, x.dtype
-    args = (_operand(x, "x", N, side), _operand(w_in, "w_in", N, per * 2 * hidden * width, dt),
-            _operand(w_out, "w_out", N, per * width * hidden, dt),
-            RankBuf(None, 0) if pre is None else _operand(pre, "pre", N, E * capacity * 2 * hidden, dt),
-            _operand(y, "y", N, side, dt))
-    cfg = config("ring", 0, workspace)
-    _check(load().cc_moe_ffn(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N,
-                             ctypes.byref(cfg), _operand_stream(stream, workspace)))
+    per, dt, c = E // N, x.dtype, _Call(stream, workspace)
+    args = (c.operand(x, "x", N, side), c.operand(w_in, "w_in", N, per * 2 * hidden * width, dt),
+            c.operand(w_out, "w_out", N, per * width * hidden, dt),
+            RankBuf(None, 0) if pre is None else c.operand(pre, "pre", N, E * capacity * 2 * hidden, dt),
+            c.operand(y, "y", N, side, dt))
+    _check(load().cc_moe_ffn(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N, c.cfg,
+                             c.stream))
 
 
 def moe_ffn_grad(x, w_in, w_out, pre, dy, dx, dw_in, dw_out, counts: Sequence[Sequence[int]], capacity: int,
                  width: int, act: str = "silu", workspace=None, stream=None) -> None:
     """The gradients of moe_ffn from dy, with pre as moe_ffn kept it."""
     N, E, hidden, side, arr = _ffn_operands(x, w_in, w_out, counts, capacity, width)
-    per, dt = E // N, x.dtype
+    per, dt, c = E // N, x.dtype, _Call(stream, workspace)
     wi, wo = per * 2 * hidden * width, per * width * hidden
-    args = (_operand(x, "x", N, side), _operand(w_in, "w_in", N, wi, dt), _operand(w_out, "w_out", N, wo, dt),
-            _operand(pre, "pre", N, E * capacity * 2 * hidden, dt), _operand(dy, "dy", N, side, dt),
-            _operand(dx, "dx", N, side, dt), _operand(dw_in, "dw_in", N, wi, dt),
-            _operand(dw_out, "dw_out", N, wo, dt))
-    cfg = config("ring", 0, workspace)
-    _check(load().cc_moe_ffn_grad(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N,
-                                  ctypes.byref(cfg), _operand_stream(stream, workspace)))
+    args = (c.operand(x, "x", N, side), c.operand(w_in, "w_in", N, wi, dt), c.operand(w_out, "w_out", N, wo, dt),
+            c.operand(pre, "pre", N, E * capacity * 2 * hidden, dt), c.operand(dy, "dy", N, side, dt),
+            c.operand(dx, "dx", N, side, dt), c.operand(dw_in, "dw_in", N, wi, dt),
+            c.operand(dw_out, "dw_out", N, wo, dt))
+    _check(load().cc_moe_ffn_grad(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N, c.cfg,
+                                  c.stream))
 
 
 def raw(fn: str, *args):
