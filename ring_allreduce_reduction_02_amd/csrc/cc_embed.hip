@@ -240,39 +240,44 @@ __device__ __forceinline__ void zero_row(char* o, uint64_t bytes, int lane) {
   if (tail < bytes) st1<DT>(o + tail, 0.0f);
 }
 
-// A workgroup takes every gridDim.x-th table row, up to 16 of them (frequent
+// A workgroup takes every gridDim.x-th table row, up to 16 or 32 of them (frequent
 // words have neighbouring ids and so fall to different workgroups).  Where a
 // row's tokens lie in the sorted ids is found by binary search, all rows (and
 // ranks) of the workgroup at once.  Most rows have none and are written as
 // zeros; a wave sums a row of a few tokens by itself, and the four waves a
 // row of kEmbedShared or more, each a quarter of them.  SUM: the tokens of all
 // ranks, rank by rank, and the row on every rank; else of the workgroup's rank.
-constexpr int kEmbedRows = 16;
+// Rows: 32 of one rank, 16 of a sum (8 ranks x 4096 tokens, 32000 x 2048 bf16:
+// each rank's 275 us against 321 with 16 rows, the sum 288 against 319 with 32).
+template <bool SUM>
+constexpr int embed_rows() {
+  return SUM ? 16 : 32;
+}
 constexpr uint32_t kEmbedShared = 16;
 constexpr int kEmbedWaves = kEmbedBlock / 64;
 
 template <int DT, bool VEC, bool SUM>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
   typedef Cols<DT> C;
-  constexpr int SZ = Ty<DT>::SZ;
-  extern __shared__ uint32_t runs[];   // [nr][kEmbedRows] begin, then end
-  uint32_t(*const begin)[kEmbedRows] = (uint32_t(*)[kEmbedRows])runs;
-  __shared__ uint32_t total[kEmbedRows];
+  constexpr int SZ = Ty<DT>::SZ, ROWS = embed_rows<SUM>();
+  extern __shared__ uint32_t runs[];   // [nr][ROWS] begin, then end
+  uint32_t(*const begin)[ROWS] = (uint32_t(*)[ROWS])runs;
+  __shared__ uint32_t total[ROWS];
   __shared__ float part[2][C::STEP];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r0 = SUM ? 0 : (int)blockIdx.y, nr = SUM ? a.N : 1;
-  uint32_t(*const end)[kEmbedRows] = begin + nr;
+  uint32_t(*const end)[ROWS] = begin + nr;
   const uint64_t v0 = blockIdx.x, dv = gridDim.x;
   const int rows = (int)((a.vocab - v0 + dv - 1) / dv);
-  for (int i = threadIdx.x; i < nr * 2 * kEmbedRows; i += kEmbedBlock) {
-    const int r = i / (2 * kEmbedRows), row = (i / 2) % kEmbedRows;
+  for (int i = threadIdx.x; i < nr * 2 * ROWS; i += kEmbedBlock) {
+    const int r = i / (2 * ROWS), row = (i / 2) % ROWS;
     const uint32_t at = row < rows ? lower_bound(a.keys + (uint64_t)(r0 + r) * a.tokens, (uint32_t)a.tokens,
                                                  (uint32_t)(v0 + row * dv) + (i & 1))
                                    : 0u;
     if (i & 1) end[r][row] = at; else begin[r][row] = at;
   }
   __syncthreads();
-  if (threadIdx.x < kEmbedRows) {
+  if (threadIdx.x < ROWS) {
     uint32_t n = 0;
     for (int r = 0; r < nr; ++r) n += end[r][threadIdx.x] - begin[r][threadIdx.x];
     total[threadIdx.x] = n;
@@ -333,14 +338,15 @@ hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
     const unsigned blocks = (unsigned)((a.pieces + kEmbedBlock / 64 - 1) / (kEmbedBlock / 64));
     CC_LAUNCH((k_embed_pieces<DT, VEC>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), 0, L.st, a);
   }
-  const unsigned blocks = (unsigned)((a.vocab + kEmbedRows - 1) / kEmbedRows);
-  const unsigned need = (L.summed ? L.N : 1) * 2 * kEmbedRows * 4;
+  const int rows = L.summed ? embed_rows<true>() : embed_rows<false>();
+  const unsigned blocks = (unsigned)((a.vocab + rows - 1) / rows);
+  const unsigned need = (L.summed ? L.N : 1) * 2 * rows * 4;
   // A sum written to more than 4 ranks streams best from one workgroup a
   // compute unit (32000 x 2048 bf16 to 8 ranks 287 us against 334 uncapped, to
   // 4 ranks of a fourth of the tokens 110 either way, float32 x 1024 to 2 ranks
   // 93 against 86).
   const int blocks_per_cu = L.blocks_per_cu > 0 ? L.blocks_per_cu : L.summed && L.N > 4 ? 1 : 0;
-  const unsigned cap = lds_for_blocks_per_cu(blocks_per_cu), fixed = sizeof(float) * (2 * Cols<DT>::STEP + kEmbedRows);
+  const unsigned cap = lds_for_blocks_per_cu(blocks_per_cu), fixed = sizeof(float) * (2 * Cols<DT>::STEP + rows);
   const unsigned lds = std::max(need, cap > fixed ? cap - fixed : 0u);
   if (L.summed) CC_LAUNCH((k_embed_grad<DT, VEC, true>), dim3(blocks), dim3(kEmbedBlock), lds, L.st, a);
   else CC_LAUNCH((k_embed_grad<DT, VEC, false>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), lds, L.st, a);
