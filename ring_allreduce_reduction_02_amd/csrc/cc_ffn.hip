@@ -802,11 +802,17 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
 #pragma unroll
     for (int i = 0; i < TM; ++i) fa[u & 1][i] = frag<DT, ACOL, BM>(from, u, mw + 32 * i, lane);
   };
-  // unit u's matrix instructions; after each TN of them, one of TM calls between
-  auto multiply_unit = [&](int u, auto between) {
-    __builtin_amdgcn_sched_barrier(0);   // the reads before the matrix instructions that hide them
+  // unit u's matrix instructions; before each TN of them fragments of unit ru
+  // of the stage rd are read, and after them one of TM calls between
+  auto multiply_unit = [&](int u, const char* rd, int ru, auto between) {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
+#pragma unroll
+      for (int j = i; j < TN; j += TM)
+        fb[(u + 1) & 1][j] = frag<DT, BCOL, BN>(rd + BM * kKBytes, ru, nw + 32 * j, lane);
+      fa[(u + 1) & 1][i] = frag<DT, ACOL, BM>(rd, ru, mw + 32 * i, lane);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
       between(i);
@@ -814,8 +820,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
     }
   };
   auto nothing = [](int) {};
-  // Stage s.  The next unit's fragments are read while the matrix instructions
-  // of the last ones run.  Before the last unit's, every wave has read all of
+  // Stage s.  The next unit's fragments are read between the matrix instructions
+  // of the last ones.  Before the last unit's, every wave has read all of
   // this stage and its loads of the next one have come (three units or more
   // after they were sent): the barrier then frees this stage's LDS for the
   // stage after the next, whose loads go out between the matrix instructions
@@ -824,22 +830,20 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   auto stage = [&](char* now, char* next, int s) {
 #pragma unroll
     for (int u = 0; u + 1 < kUnits; ++u) {
-      read(now, u + 1);
       if (u == 0) {
-        multiply_unit(u, [&](int i) {
+        multiply_unit(u, now, u + 1, [&](int i) {
 #pragma unroll
           for (int q = i; q < LB::Q; q += TM) issue_b(next, s + 1, q);
         });
         rows(s + 2);
       } else {
-        multiply_unit(u, nothing);
+        multiply_unit(u, now, u + 1, nothing);
       }
     }
     wait_loads<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    read(next, 0);
-    multiply_unit(kUnits - 1, [&](int i) {
+    multiply_unit(kUnits - 1, next, 0, [&](int i) {
 #pragma unroll
       for (int q = i; q < LA::Q; q += TM) issue_a(now, s + 2, q);
     });
