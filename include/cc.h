@@ -613,13 +613,14 @@ cc_status_t cc_moe_route_grad(cc_rankbuf_t logits, cc_rankbuf_t experts, cc_rank
 /* Gated feed-forward block of the experts, on the expert side of
  * cc_moe_dispatch_padded: for the kept rows x of every expert
  *   [g | u] = x w_in^T,  h = act(g) * u,  y = h w_out^T.
- * counts, nexperts and capacity as in the dispatch (counts host [nranks *
- * nexperts]); x, y: E * capacity rows of `width` per rank, in the dispatch's
+ * counts, nexperts (at most 8192) and capacity as in the dispatch (counts
+ * host [nranks * nexperts]; the call has read them when it returns); x, y: E * capacity rows of `width` per rank, in the dispatch's
  * layout.  Rank j's weights, one local expert after the other: w_in
  * [2 * hidden][width] (gate rows, then up rows), w_out [width][hidden].  pre
  * (base may be NULL) keeps [g | u], 2 * hidden elements a row in x's layout,
  * for the gradient.  Rows behind a block's kept ones are neither read nor
- * written.  h is rounded to dtype between the products.  A dense block is one
+ * written.  Fewer than 2^31 kept rows, nexperts * capacity below 2^31.  h is
+ * rounded to dtype between the products.  A dense block is one
  * expert with capacity rows.  SiLU is g / (1 + exp(-g)), GELU the exact one
  * (g times the normal distribution function). */
 typedef enum { CC_ACT_SILU = 0, CC_ACT_GELU = 1, CC_ACT_MAX_ENUM = 0x7fffffff } cc_act_t;

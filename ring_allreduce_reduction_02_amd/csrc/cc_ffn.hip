@@ -573,7 +573,9 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TM][TN]) {
 }
 
 // Any alignment: tiles staged through registers, the next stage's on their way
-// while this one's products run.
+// while this one's products run.  2 x 333 tokens, top-2 of 6 experts, 515 x 331
+// float32: 32 and 20 us, bound by the latency of 17 and 11 stages (the products
+// are 9 us of the matrix units); element by element they took 54 and 35.
 template <int DT, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_any(GemmArgs g) {
   constexpr int NT = 64 * (BM / WM) * (BN / WN);
@@ -726,6 +728,19 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const RowSide& s, 
   return buffer_of(s.map ? s.base + (uint64_t)rank * s.rank_stride : s.base + (uint64_t)p0 * s.pitch, s.span);
 }
 
+// Two stages of whole 128-byte lines are in LDS (128 KiB of a 256 x 256 tile),
+// one barrier a stage.  Measured on 8 x 4096 tokens, top-2 of 16 experts,
+// 2048 x 2048 bf16 (60.7k rows): gate and up 1.04 ms (980 TFLOP/s), down 0.48-0.51
+// (1000-1060), hidden gradient 0.65 (780; it reads and writes 1.5 GB more), row
+// gradient 0.87 (1170), weight gradients 0.54 and 1.10 (930).  The matrix units
+// are busy 58-63% of the cycles, at 1.65-1.8 GHz: the card lowers its clock under
+// this load.  With the loads left out a stage took 1.36 us, with loads that
+// hit the L2 1.58, as it is 1.95.
+// What else was tried there: four stages of 64-byte lines (twice the cache
+// requests: 10% slower), 128 x 128 tiles two to a unit (10-25% slower), four
+// waves of 128 x 128 (faster per stage, slower results), loads of later
+// stages' lines into the L2 ahead (within 2%), row groups of 8 and 16 (0-5%
+// slower).
 template <int DT, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArgs g) {
   constexpr int NW = (BM / WM) * (BN / WN);
@@ -898,15 +913,18 @@ uint64_t tiles_of(GemmArgs* g, const FfnLaunch& L, int k) {
 
 // The tile whose workgroups, dealt out over the compute units, take least: a
 // larger tile moves fewer bytes for a product, a smaller one leaves fewer
-// units idle.  Measured cost of equal areas: 1, 1.25 and 1.9.
+// units idle.  Cost of equal areas, measured on all six products of 60.7k rows:
+// bf16 2048 x 2048 1, 1.21 and 1.92 (4.62, 5.62 and 8.87 ms), float32, whose
+// products take eight times as long, 1024 x 1024 1, 1 and 1.25 (9.79, 9.81 and
+// 12.24 ms; the weight gradients alone 1, 1 and 1.35, which is counted).
 template <int KIND>
 int pick_tile(GemmArgs g, const FfnLaunch& L, int first) {
-  static constexpr double kArea[kFfnTiles] = {16.0, 4.0 * 1.25, 1.9};
+  static constexpr double kArea[2][kFfnTiles] = {{16.0, 4.0 * 1.21, 1.92}, {16.0, 4.0, 1.35}};
   const int cus = dev_info().cus > 0 ? dev_info().cus : 256;
   int best = first;
   double least = 0.0;
   for (int k = first; k < kFfnTiles; ++k) {
-    const double t = (double)((tiles_of<KIND>(&g, L, k) + cus - 1) / cus) * kArea[k];
+    const double t = (double)((tiles_of<KIND>(&g, L, k) + cus - 1) / cus) * kArea[L.s.dt == DT_F32][k];
     if (k == first || t < least) {
       least = t;
       best = k;

