@@ -882,6 +882,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
     stage(t0, t1, s);
     stage(t1, t0, s + 1);
   }
+  wait_loads<0>();   // the zeros of stages past the end also land in LDS
   __syncthreads();   // other waves may still read the last tiles
   constexpr int PER = (BM + BN) * kKBytes / finish_bytes<WN>();   // waves that one stage's LDS serves
   static_assert(NW <= 2 * PER, "every wave has its piece");
