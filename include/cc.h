@@ -614,8 +614,8 @@ cc_status_t cc_moe_route_grad(cc_rankbuf_t logits, cc_rankbuf_t experts, cc_rank
  * cc_moe_dispatch_padded: for the kept rows x of every expert
  *   [g | u] = x w_in^T,  h = act(g) * u,  y = h w_out^T.
  * counts, nexperts (at most 8192) and capacity as in the dispatch (counts
- * host [nranks * nexperts]; the call has read them when it returns); x, y: E * capacity rows of `width` per rank, in the dispatch's
- * layout.  Rank j's weights, one local expert after the other: w_in
+ * host [nranks * nexperts]; the call has read them when it returns); x, y:
+ * E * capacity rows of `width` per rank, in the dispatch's layout.  Rank j's weights, one local expert after the other: w_in
  * [2 * hidden][width] (gate rows, then up rows), w_out [width][hidden].  pre
  * (base may be NULL) keeps [g | u], 2 * hidden elements a row in x's layout,
  * for the gradient.  Rows behind a block's kept ones are neither read nor
@@ -637,7 +637,9 @@ cc_status_t cc_moe_ffn_grad(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_ou
                             int nexperts, size_t capacity, size_t width, size_t hidden, cc_act_t act, cc_dtype_t dtype,
                             int nranks, const cc_config_t* cfg, cc_stream_t stream);
 
-/* Workspace of cc_moe_ffn (grad 0) or cc_moe_ffn_grad (grad 1). */
+/* Workspace of cc_moe_ffn (grad 0) or cc_moe_ffn_grad (grad 1).  Where rows of
+ * width or hidden elements are no whole 16-byte vectors it may hold padded
+ * copies of the weights and of the kept rows. */
 cc_status_t cc_moe_ffn_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width, size_t hidden,
                                       cc_dtype_t dtype, int nranks, int grad, size_t* bytes);
 

@@ -277,7 +277,7 @@ struct Chunks {
 enum Act { ACT_SILU = 0, ACT_GELU = 1 };
 
 // 1 / (1 + exp(-g)) from the hardware's exp2 and reciprocal (1 ulp each): off by
-// at most (|g| + 4) 2^-24 of its value
+// at most (|g| + 4) 2^-24 of its value; below 2^-126 it may be 0
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * g));
 }
@@ -333,15 +333,18 @@ __device__ __forceinline__ void store_n(char* p, const float* v, int n) {
       if (i < n) st1<DT>(p + i * Ty<DT>::SZ, v[i]);
   }
 }
-template <int DT, bool VEC, int V>
-__device__ __forceinline__ void load_n(const char* p, float* v, int n) {
+// their 16 bytes, zeros past the n
+template <int DT, bool VEC>
+__device__ __forceinline__ u32x4 load_n(const char* p, int n) {
+  constexpr int V = Ty<DT>::V;
   if constexpr (VEC) {
-    unpack<DT>(n > 0 ? *(const u32x4*)p : u32x4{0u, 0u, 0u, 0u}, v);
-  } else if (n >= V) {
-    unpack<DT>(*(const u32x4_any*)p, v);
+    return n > 0 ? *(const u32x4*)p : u32x4{0u, 0u, 0u, 0u};
   } else {
+    if (n >= V) return *(const u32x4_any*)p;
+    float x[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = i < n ? ld1<DT>(p + i * Ty<DT>::SZ) : 0.0f;
+    for (int i = 0; i < V; ++i) x[i] = i < n ? ld1<DT>(p + i * Ty<DT>::SZ) : 0.0f;
+    return pack_row<DT>(x);   // widened and packed again: the same bits
   }
 }
 
@@ -469,7 +472,7 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
   auto packed = [&](const RowSide& s, int m) { return s.base + (uint64_t)(t.p0 + m) * s.pitch + (int64_t)n * SZ; };
   // K_DHID: the pre-activations, loaded 32 rows ahead (bf16; of float32 they
   // would fill the registers)
-  constexpr bool AHEAD = KIND == K_DHID && VEC && PASSES <= 4;
+  constexpr bool AHEAD = KIND == K_DHID && PASSES <= 4;
   u32x4 fg[2][PASSES], fu[2][PASSES];
   auto ahead = [&](int i) {
     if constexpr (AHEAD) {
@@ -477,9 +480,9 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
       for (int r = 0; r < PASSES; ++r) {
         const int row = r * RPP + lane / LPR;
         const char* pre = mapped(g.pre, place_of(i, row));
-        const bool in = mw + 32 * i + row < rows && left > 0;
-        fg[i & 1][r] = in ? *(const u32x4*)pre : u32x4{0u, 0u, 0u, 0u};
-        fu[i & 1][r] = in ? *(const u32x4*)(pre + (int64_t)g.F * SZ) : u32x4{0u, 0u, 0u, 0u};
+        const int n = mw + 32 * i + row < rows ? left : 0;
+        fg[i & 1][r] = load_n<DT, VEC>(pre, n);
+        fu[i & 1][r] = load_n<DT, VEC>(pre + (int64_t)g.F * SZ, n);
       }
     }
   };
@@ -524,8 +527,8 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
           unpack<DT>(fu[i & 1][r], up);
         } else {
           const char* pre = mapped(g.pre, at_row);
-          load_n<DT, VEC, V>(pre, gt, left);
-          load_n<DT, VEC, V>(pre + (int64_t)g.F * SZ, up, left);
+          unpack<DT>(load_n<DT, VEC>(pre, left), gt);
+          unpack<DT>(load_n<DT, VEC>(pre + (int64_t)g.F * SZ, left), up);
         }
         gate_grad<V>(gt, up, g.act, v, dg, du, h);
         char* o = packed(g.out, m);
@@ -691,9 +694,10 @@ struct Loader {
       last[q] = (int)(((int64_t)K * SZ - c + kKBytes - 1) / kKBytes);
     }
   }
-  // column tiles: off[] become the column chunks' bytes, columns c0.. of C
+  // column tiles: off[] become the column chunks' bytes, columns c0.. of C (the
+  // padding of a copied row's last chunk among them: no result of it is stored)
   __device__ __forceinline__ void columns(int wave, int lane, int c0, int C, int K) {
-    const int end = (C - c0) * SZ - 16;
+    const int end = ((C - c0) * SZ + 15) / 16 * 16 - 16;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int k = line_of(wave, q, lane), c = 16 * col_place<DT, R>(k, lane % LANES);   // its own inverse
@@ -741,7 +745,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const RowSide& s, 
 // waves of 128 x 128 (faster per stage, slower results), loads of later
 // stages' lines into the L2 ahead (within 2%), row groups of 8 and 16 (0-5%
 // slower).
-template <int DT, int KIND, int BM, int BN, int WM, int WN>
+template <int DT, int KIND, bool VEC, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArgs g) {
   constexpr int NW = (BM / WM) * (BN / WN);
   constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ;
@@ -887,12 +891,104 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   constexpr int PER = (BM + BN) * kKBytes / finish_bytes<WN>();   // waves that one stage's LDS serves
   static_assert(NW <= 2 * PER, "every wave has its piece");
   char* fin = wave < PER ? t0 : t1;
-  finish<DT, KIND, true>(g, t, acc, mw, nw, lane, fin + (wave % PER) * finish_bytes<WN>());
+  finish<DT, KIND, VEC>(g, t, acc, mw, nw, lane, fin + (wave % PER) * finish_bytes<WN>());
+}
+
+// ------------------------------------------------------------------ aligned copies
+
+uint64_t up256(uint64_t v) { return (v + 255) / 256 * 256; }
+uint64_t line_pitch(const FfnShape& s, uint64_t cols) {   // whole cache lines
+  return (cols * elem_size(s.dt) + 127) / 128 * 128;
+}
+
+// Whether the operands are first copied into rows that direct loads can take:
+// whole 16-byte vectors, padded with zeros, the experts' rows compact.  For
+// rows that are none, or a side that 32-bit offsets do not reach.
+// Gradients always: 1.04 to 2.7 times faster than the tiles through registers
+// over 1 to 8192 rows an expert and 201 x 333 to 2047 x 2047 of both types
+// (16 experts, 2047 x 2047 bf16, 4 rows an expert 461 us against 747, 4096
+// rows 3605 against 10002).  The forward pass reads every operand once along
+// its rows, where the tiles through registers do better, so that the copies
+// pay from about 1024 rows an expert and 512 columns on: 2047 x 2047 bf16 128
+// rows 378 us against 285, 512 rows 504 against 507, 2048 rows 1072 against 1665;
+// 300 x 517 bf16 2048 rows 118 against 121, 201 x 333 float32 236 against 213.
+constexpr uint64_t kCopyRows = 1024, kCopyCols = 512;
+bool copied(const FfnShape& s, int grad) {
+  const uint64_t es = elem_size(s.dt), w = line_pitch(s, s.W), f = line_pitch(s, s.F), f2 = line_pitch(s, 2 * s.F);
+  if (s.rows == 0 || (s.W * es % 16 == 0 && s.F * es % 16 == 0 && s.E * s.cap * s.W * es <= kMaxSpan)) return false;
+  if (s.most * std::max(w, f2) > kMaxSpan || 2 * s.F * w > kMaxSpan || s.W * f > kMaxSpan) return false;
+  return grad || (s.rows >= kCopyRows * s.E && std::min(s.W, s.F) >= kCopyCols);
+}
+
+struct CopyArgs {
+  const int* start;
+  const int2* mtab;      // row tiles of 64
+  const int* map;
+  int per;
+  struct {
+    const char* from;
+    uint64_t rank_stride;
+    uint64_t lines, each;          // weights: lines in all, and of an expert; rows: tiles, 0
+    char* to;
+    uint64_t cols, pitch;
+  } job[4];
+  char* h;               // padding of the rows between the products
+  char* dgu;
+  uint64_t F, h_pitch, dgu_pitch;
+};
+
+constexpr int kCopyLines = kFfnTile[kFfnTiles - 1];
+
+// Workgroup x of job y copies 64 lines.  Bound by memory: 16 experts of
+// 2047 x 2047 bf16 weights, 800 MB in and out, about 175 us, 4.6 TB/s.
+template <int DT>
+__global__ __launch_bounds__(256) void k_ffn_copy(CopyArgs a) {
+  constexpr int V = Ty<DT>::V, SZ = Ty<DT>::SZ;
+  const auto& j = a.job[blockIdx.y];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool rows = j.each == 0;
+  uint64_t first, end;
+  const char* from = j.from;
+  if (rows) {
+    if (blockIdx.x >= j.lines) return;
+    const int2 at = a.mtab[blockIdx.x];
+    first = (uint64_t)at.y;
+    const uint64_t stop = (uint64_t)a.start[at.x + 1];
+    end = first + kCopyLines < stop ? first + kCopyLines : stop;
+    from += (uint64_t)(at.x / a.per) * j.rank_stride;
+  } else {
+    first = (uint64_t)blockIdx.x * kCopyLines;
+    if (first >= j.lines) return;
+    end = first + kCopyLines < j.lines ? first + kCopyLines : j.lines;
+  }
+  for (uint64_t l = first + wave; l < end; l += 4) {
+    const char* p;
+    if (rows) {
+      p = from + (uint64_t)a.map[l] * j.cols * SZ;
+    } else {
+      const uint64_t e = l / j.each, r = e / a.per;
+      if (a.start[e] == a.start[e + 1]) continue;   // no rows: never read
+      p = from + r * j.rank_stride + (l - r * a.per * j.each) * j.cols * SZ;
+    }
+    char* o = j.to + l * j.pitch;
+    for (uint64_t c = (uint64_t)lane * V; c * SZ < j.pitch; c += 64 * V) {
+      const int64_t left = (int64_t)(j.cols - c);
+      const u32x4 w = load_n<DT, false>(p + c * SZ, left < V ? (int)left : V);
+      *(u32x4*)(o + c * SZ) = w;
+    }
+    if (rows && blockIdx.y == 0) {
+      for (uint64_t c = a.F * SZ + lane * SZ; c < a.h_pitch; c += 64 * SZ) st1<DT>(a.h + l * a.h_pitch + c, 0.0f);
+      if (a.dgu)
+        for (uint64_t c = 2 * a.F * SZ + lane * SZ; c < a.dgu_pitch; c += 64 * SZ)
+          st1<DT>(a.dgu + l * a.dgu_pitch + c, 0.0f);
+    }
+  }
 }
 
 // whether the products run as aligned tiles: rows of whole 16-byte vectors, and
 // operands that 32-bit offsets reach
 bool tiled(const FfnLaunch& L) {
+  if (L.o.copied) return true;
   const uint64_t es = elem_size(L.s.dt), row = std::max(L.s.W, 2 * L.s.F) * es;
   return L.vec_ok && (uint64_t)L.s.E * L.s.cap * L.s.W * es <= kMaxSpan && L.s.most * row <= kMaxSpan &&
          2 * L.s.F * L.s.W * es <= kMaxSpan;
@@ -934,6 +1030,14 @@ int pick_tile(GemmArgs g, const FfnLaunch& L, int first) {
   return best;
 }
 
+template <int DT, int KIND, bool VEC>
+hipError_t launch_tile(const GemmArgs& g, int k, dim3 grid, hipStream_t st) {
+  if (k == 0) CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 256, 256, 128, 64>), grid, dim3(512), 0, st, g);
+  else if (k == 1) CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 128, 128, 64, 64>), grid, dim3(256), 0, st, g);
+  else CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 64, 64, 32, 64>), grid, dim3(128), 0, st, g);
+  return hipGetLastError();
+}
+
 template <int DT, int KIND>
 hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
   const bool fast = tiled(L);
@@ -941,16 +1045,10 @@ hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
   const uint64_t blocks = tiles_of<KIND>(&g, L, k);
   if (blocks == 0) return hipSuccess;
   const dim3 grid((unsigned)blocks);
-  if (!fast) {
-    if (k == 1) CC_LAUNCH((k_ffn_any<DT, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, L.st, g);
-    else CC_LAUNCH((k_ffn_any<DT, KIND, 64, 64, 32, 64>), grid, dim3(128), 0, L.st, g);
-  } else if (k == 0) {
-    CC_LAUNCH((k_ffn_tile<DT, KIND, 256, 256, 128, 64>), grid, dim3(512), 0, L.st, g);
-  } else if (k == 1) {
-    CC_LAUNCH((k_ffn_tile<DT, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, L.st, g);
-  } else {
-    CC_LAUNCH((k_ffn_tile<DT, KIND, 64, 64, 32, 64>), grid, dim3(128), 0, L.st, g);
-  }
+  if (fast && L.o.copied) return launch_tile<DT, KIND, false>(g, k, grid, L.st);   // results start anywhere
+  if (fast) return launch_tile<DT, KIND, true>(g, k, grid, L.st);
+  if (k == 1) CC_LAUNCH((k_ffn_any<DT, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, L.st, g);
+  else CC_LAUNCH((k_ffn_any<DT, KIND, 64, 64, 32, 64>), grid, dim3(128), 0, L.st, g);
   return hipGetLastError();
 }
 
@@ -958,8 +1056,6 @@ template <int KIND>
 hipError_t pick_gemm(const GemmArgs& g, const FfnLaunch& L) {
   return L.s.dt == DT_F32 ? run_gemm<DT_F32, KIND>(g, L) : run_gemm<DT_BF16, KIND>(g, L);
 }
-
-uint64_t up256(uint64_t v) { return (v + 255) / 256 * 256; }
 
 // the tables, from the counts in the launch's arguments or (many) in memory
 hipError_t plan(const FfnLaunch& L) {
@@ -1003,12 +1099,50 @@ RowSide rows_of(const FfnLaunch& L, const Side& s, uint64_t cols) {
   return RowSide{s.base, s.stride, pitch, (const int*)(L.ws + L.o.rowmap), (uint64_t)L.s.E * L.s.cap * pitch};
 }
 RowSide compact(const FfnLaunch& L, uint64_t off, uint64_t cols) {
-  const uint64_t pitch = cols * elem_size(L.s.dt);
+  const uint64_t pitch = L.o.copied ? line_pitch(L.s, cols) : cols * elem_size(L.s.dt);
   return RowSide{L.ws + off, 0, pitch, nullptr, L.s.most * pitch};
 }
 WtSide wts(const FfnLaunch& L, const Side& s, uint64_t r, uint64_t c) {
   const uint64_t es = elem_size(L.s.dt);
   return WtSide{s.base, s.stride, r * c * es, c * es};
+}
+
+// the operands as the products read them: the caller's, or their copies
+RowSide rows_in(const FfnLaunch& L, const Side& s, uint64_t copy) {
+  return L.o.copied ? compact(L, copy, L.s.W) : rows_of(L, s, L.s.W);
+}
+WtSide wts_in(const FfnLaunch& L, const Side& s, uint64_t copy, uint64_t r, uint64_t c) {
+  if (!L.o.copied) return wts(L, s, r, c);
+  const uint64_t p = line_pitch(L.s, c);
+  return WtSide{L.ws + copy, (uint64_t)(L.s.E / L.s.N) * r * p, r * p, p};
+}
+
+hipError_t copy_operands(const FfnLaunch& L, int grad) {
+  const uint64_t W = L.s.W, F = L.s.F, n = L.s.E, tiles = L.s.mtiles[kFfnTiles - 1];
+  CopyArgs a = {};
+  a.start = (const int*)(L.ws + L.o.start);
+  a.mtab = (const int2*)(L.ws + L.o.mtab[kFfnTiles - 1]);
+  a.map = (const int*)(L.ws + L.o.rowmap);
+  a.per = L.s.E / L.s.N;
+  a.job[0] = {L.x.base, L.x.stride, tiles, 0, L.ws + L.o.x, W, line_pitch(L.s, W)};
+  a.job[1] = {L.w_in.base, L.w_in.stride, n * 2 * F, 2 * F, L.ws + L.o.w_in, W, line_pitch(L.s, W)};
+  a.job[2] = {L.w_out.base, L.w_out.stride, n * W, W, L.ws + L.o.w_out, F, line_pitch(L.s, F)};
+  if (grad) a.job[3] = {L.dy.base, L.dy.stride, tiles, 0, L.ws + L.o.dy, W, line_pitch(L.s, W)};
+  a.h = L.ws + L.o.h;
+  a.dgu = grad ? L.ws + L.o.dgu : nullptr;
+  a.F = F;
+  a.h_pitch = line_pitch(L.s, F);
+  a.dgu_pitch = line_pitch(L.s, 2 * F);
+  const uint64_t blocks = std::max(tiles, (n * std::max(2 * F, W) + kCopyLines - 1) / kCopyLines);
+  const dim3 grid((unsigned)blocks, grad ? 4 : 3), blk(256);
+  if (L.s.dt == DT_F32) CC_LAUNCH(k_ffn_copy<DT_F32>, grid, blk, 0, L.st, a);
+  else CC_LAUNCH(k_ffn_copy<DT_BF16>, grid, blk, 0, L.st, a);
+  return hipGetLastError();
+}
+
+hipError_t prepare(const FfnLaunch& L, int grad) {
+  const hipError_t e = plan(L);
+  return e == hipSuccess && L.o.copied ? copy_operands(L, grad) : e;
 }
 
 }  // namespace
@@ -1026,21 +1160,32 @@ FfnWs ffn_ws(const FfnShape& s, int grad) {
   o.start = take(((uint64_t)s.E + 1) * 4);
   for (int k = 0; k < kFfnTiles; ++k) o.mtab[k] = take(s.mtiles[k] * 8);
   o.rowmap = take(s.rows * 4);
-  o.h = take(s.rows * s.F * es);
-  o.dgu = grad ? take(s.rows * 2 * s.F * es) : 0;
+  o.copied = copied(s, grad);
+  o.x = o.dy = o.w_in = o.w_out = 0;
+  if (o.copied) {
+    o.h = take(s.rows * line_pitch(s, s.F));
+    o.dgu = grad ? take(s.rows * line_pitch(s, 2 * s.F)) : 0;
+    o.x = take(s.rows * line_pitch(s, s.W));
+    if (grad) o.dy = take(s.rows * line_pitch(s, s.W));
+    o.w_in = take((uint64_t)s.E * 2 * s.F * line_pitch(s, s.W));
+    o.w_out = take((uint64_t)s.E * s.W * line_pitch(s, s.F));
+  } else {
+    o.h = take(s.rows * s.F * es);
+    o.dgu = grad ? take(s.rows * 2 * s.F * es) : 0;
+  }
   o.bytes = at;
   return o;
 }
 
 hipError_t launch_ffn(const FfnLaunch& L) {
   const uint64_t W = L.s.W, F = L.s.F;
-  hipError_t e = plan(L);
+  hipError_t e = prepare(L, 0);
   if (e != hipSuccess) return e;
   GemmArgs g = gemm_args(L);
   g.K = (int)W;
   g.N = (int)(2 * F);
-  g.a = rows_of(L, L.x, W);
-  g.b = wts(L, L.w_in, 2 * F, W);
+  g.a = rows_in(L, L.x, L.o.x);
+  g.b = wts_in(L, L.w_in, L.o.w_in, 2 * F, W);
   g.out = compact(L, L.o.h, F);
   g.pre = rows_of(L, L.pre, 2 * F);
   if ((e = pick_gemm<K_GATEUP>(g, L)) != hipSuccess) return e;
@@ -1048,20 +1193,20 @@ hipError_t launch_ffn(const FfnLaunch& L) {
   g.K = (int)F;
   g.N = (int)W;
   g.a = compact(L, L.o.h, F);
-  g.b = wts(L, L.w_out, W, F);
+  g.b = wts_in(L, L.w_out, L.o.w_out, W, F);
   g.out = rows_of(L, L.y, W);
   return pick_gemm<K_DOWN>(g, L);
 }
 
 hipError_t launch_ffn_grad(const FfnLaunch& L) {
   const uint64_t W = L.s.W, F = L.s.F;
-  hipError_t e = plan(L);
+  hipError_t e = prepare(L, 1);
   if (e != hipSuccess) return e;
   GemmArgs g = gemm_args(L);
   g.K = (int)W;
   g.N = (int)F;
-  g.a = rows_of(L, L.dy, W);
-  g.b = wts(L, L.w_out, W, F);
+  g.a = rows_in(L, L.dy, L.o.dy);
+  g.b = wts_in(L, L.w_out, L.o.w_out, W, F);
   g.out = compact(L, L.o.dgu, 2 * F);
   g.h = compact(L, L.o.h, F);
   g.pre = rows_of(L, L.pre, 2 * F);
@@ -1070,13 +1215,13 @@ hipError_t launch_ffn_grad(const FfnLaunch& L) {
   g.K = (int)(2 * F);
   g.N = (int)W;
   g.a = compact(L, L.o.dgu, 2 * F);
-  g.b = wts(L, L.w_in, 2 * F, W);
+  g.b = wts_in(L, L.w_in, L.o.w_in, 2 * F, W);
   g.out = rows_of(L, L.dx, W);
   if ((e = pick_gemm<K_DX>(g, L)) != hipSuccess) return e;
   g = gemm_args(L);
   g.M = (int)W;
   g.N = (int)F;
-  g.a = rows_of(L, L.dy, W);
+  g.a = rows_in(L, L.dy, L.o.dy);
   g.b_rows = compact(L, L.o.h, F);
   g.wout = wts(L, L.dw_out, W, F);
   if ((e = pick_gemm<K_DW>(g, L)) != hipSuccess) return e;
@@ -1084,7 +1229,7 @@ hipError_t launch_ffn_grad(const FfnLaunch& L) {
   g.M = (int)(2 * F);
   g.N = (int)W;
   g.a = compact(L, L.o.dgu, 2 * F);
-  g.b_rows = rows_of(L, L.x, W);
+  g.b_rows = rows_in(L, L.x, L.o.x);
   g.wout = wts(L, L.dw_in, 2 * F, W);
   return pick_gemm<K_DW>(g, L);
 }

@@ -110,9 +110,13 @@ struct FfnShape {
 };
 // Workspace: row starts [E + 1], row tiles of each size (expert, first row), row
 // map [rows] (row in the rank's buffer), kept counts [N * E], h [rows][F],
-// and for the gradient d(gate | up) [rows][2F].
+// and for the gradient d(gate | up) [rows][2F].  Where rows are no whole
+// 16-byte vectors it may hold aligned copies, lines padded with zeros to 128
+// bytes (h and d(gate | up) then too): x and dy by compact rows, the weights.
 struct FfnWs {
   uint64_t kept, start, mtab[kFfnTiles], rowmap, h, dgu, bytes;
+  int copied;
+  uint64_t x, dy, w_in, w_out;
 };
 FfnWs ffn_ws(const FfnShape& s, int grad);
 struct FfnLaunch {

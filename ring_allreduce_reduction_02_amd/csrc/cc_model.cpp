@@ -24,7 +24,7 @@ cc_status_t guarded(F f) {
   try {
     return f();
   } catch (const std::bad_alloc&) {
-    return CC_ERR_INVALID_ARG;
+    return fail(CC_ERR_INVALID_ARG, "no host memory for the counts");
   }
 }
 
