@@ -103,51 +103,62 @@ struct EmbedGradArgs {
   int N;
 };
 
-// A wave's columns: CB blocks of 64 lanes, V consecutive elements a lane.
-// Enough of them that a row of 2048 bf16 takes one walk over its tokens.
-template <int DT>
+// A wave's columns: CB blocks of 64 lanes, V consecutive elements a lane, as
+// many (1, 2 or 4) as a row has, so that a row of 2048 bf16 takes one walk over
+// its tokens and a narrow one has more token rows under way (4 ranks x 2000
+// tokens, 2000 x 512 bf16: 28 us with one block and 16 rows, 50 with four blocks and 4).
+template <int DT, int B>
 struct Cols {
   static constexpr int V = Ty<DT>::V;
-  static constexpr int CB = 4;
+  static constexpr int CB = B;
   static constexpr int STEP = 64 * V * CB;
+  static constexpr int BATCH = 16 / CB;   // token rows under way per wave
 };
 
-constexpr int kEmbedBatch = 4;   // token rows under way per wave
+// acc += Q token rows, the first n of them; g is the lane's first byte of row 0,
+// `mine` a position a lane, from lane k on.
+template <int DT, bool VEC, int B, int Q>
+__device__ __forceinline__ void add_batch(const char* g, uint64_t pitch, int64_t left, int mine, int k, int n,
+                                          float (&acc)[Cols<DT, B>::CB][Cols<DT, B>::V]) {
+  constexpr int V = Ty<DT>::V;
+  u32x4 w[Q][B];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const uint32_t t = (uint32_t)__builtin_amdgcn_readlane(mine, q < n ? k + q : k);
+#pragma unroll
+    for (int i = 0; i < B; ++i) w[q][i] = load_part<DT, VEC>(g + t * pitch + i * 64 * V * Ty<DT>::SZ, left - i * 64 * V);
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (q >= n) break;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      float x[V];
+      unpack<DT>(w[q][i], x);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[i][e] += x[e];
+    }
+  }
+}
 
 // acc += the rows of grad at the sorted positions [lo, hi) of rank r, columns
-// c0 + 64 V i + V lane.  Positions are fetched 64 at a time, and their rows
-// four at a time, so that a lane has 4 CB loads under way.
-template <int DT, bool VEC>
+// c0 + 64 V i + V lane.  Positions are fetched 64 at a time, their rows BATCH
+// at a time, so that a lane has 16 loads under way, and the last few by 4.
+template <int DT, bool VEC, int B>
 __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, uint64_t r, uint64_t lo, uint64_t hi, uint64_t c0,
-                                         int lane, float (&acc)[Cols<DT>::CB][Cols<DT>::V]) {
-  constexpr int V = Cols<DT>::V, CB = Cols<DT>::CB, SZ = Ty<DT>::SZ;
+                                         int lane, float (&acc)[Cols<DT, B>::CB][Cols<DT, B>::V]) {
+  constexpr int V = Ty<DT>::V, BATCH = Cols<DT, B>::BATCH, SZ = Ty<DT>::SZ;
   const int* vals = a.vals + r * a.tokens;
   const char* base = a.grad + r * a.gs + (c0 + lane * V) * SZ;
   const int64_t left = (int64_t)(a.width - c0) - lane * V;
   for (uint64_t p0 = lo; p0 < hi; p0 += 64) {
     const int n = (int)(hi - p0 < 64 ? hi - p0 : 64);
     const int mine = lane < n ? vals[p0 + lane] : 0;
-    for (int k = 0; k < n; k += kEmbedBatch) {
-      u32x4 w[kEmbedBatch][CB];
-#pragma unroll
-      for (int q = 0; q < kEmbedBatch; ++q) {
-        const uint32_t t = (uint32_t)__builtin_amdgcn_readlane(mine, k + q < n ? k + q : k);
-        const char* g = base + (uint64_t)t * a.width * SZ;
-#pragma unroll
-        for (int i = 0; i < CB; ++i) w[q][i] = load_part<DT, VEC>(g + i * 64 * V * SZ, left - i * 64 * V);
-      }
-#pragma unroll
-      for (int q = 0; q < kEmbedBatch; ++q) {
-        if (k + q >= n) break;
-#pragma unroll
-        for (int i = 0; i < CB; ++i) {
-          float x[V];
-          unpack<DT>(w[q][i], x);
-#pragma unroll
-          for (int e = 0; e < V; ++e) acc[i][e] += x[e];
-        }
-      }
-    }
+    int k = 0;
+    if constexpr (BATCH > 4)
+      for (; k + BATCH <= n; k += BATCH)
+        add_batch<DT, VEC, B, BATCH>(base, a.width * SZ, left, mine, k, BATCH, acc);
+    for (; k < n; k += 4) add_batch<DT, VEC, B, 4>(base, a.width * SZ, left, mine, k, n - k, acc);
   }
 }
 
@@ -164,9 +175,9 @@ __device__ __forceinline__ uint32_t lower_bound(const int* keys, uint32_t n, uin
 // Partial sums of the pieces (kEmbedPiece sorted positions) that lie inside
 // one word's run of kEmbedLong or more, one wave each, so that a frequent word
 // is summed by many.
-template <int DT, bool VEC>
+template <int DT, bool VEC, int B>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
-  typedef Cols<DT> C;
+  typedef Cols<DT, B> C;
   const int lane = threadIdx.x & 63;
   const uint64_t piece = (uint64_t)blockIdx.x * (kEmbedBlock / 64) + (threadIdx.x >> 6), r = blockIdx.y;
   if (piece >= a.pieces) return;
@@ -179,7 +190,7 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
   float* o = a.partial + (r * a.pieces + piece) * a.pitch;
   for (uint64_t c0 = 0; c0 < a.width; c0 += C::STEP) {
     float acc[C::CB][C::V] = {};
-    add_rows<DT, VEC>(a, r, p0, p0 + kEmbedPiece, c0, lane, acc);
+    add_rows<DT, VEC, B>(a, r, p0, p0 + kEmbedPiece, c0, lane, acc);
 #pragma unroll
     for (int i = 0; i < C::CB; ++i) {
       const uint64_t c = c0 + (uint64_t)(i * 64 + lane) * C::V;
@@ -190,16 +201,16 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_pieces(EmbedGradArgs a) {
 
 // acc += the sorted positions [lo, hi) of rank r, part of a run of `run`
 // positions: of a long run, whole pieces come as their partial sums.
-template <int DT, bool VEC>
+template <int DT, bool VEC, int B>
 __device__ __forceinline__ void add_run(const EmbedGradArgs& a, uint64_t r, uint64_t lo, uint64_t hi, uint64_t run,
-                                        uint64_t c0, int lane, float (&acc)[Cols<DT>::CB][Cols<DT>::V]) {
-  typedef Cols<DT> C;
+                                        uint64_t c0, int lane, float (&acc)[Cols<DT, B>::CB][Cols<DT, B>::V]) {
+  typedef Cols<DT, B> C;
   const uint64_t f = (lo + kEmbedPiece - 1) / kEmbedPiece, l = hi / kEmbedPiece;
   if (a.pieces == 0 || run < kEmbedLong || f >= l) {
-    add_rows<DT, VEC>(a, r, lo, hi, c0, lane, acc);
+    add_rows<DT, VEC, B>(a, r, lo, hi, c0, lane, acc);
     return;
   }
-  add_rows<DT, VEC>(a, r, lo, f * kEmbedPiece, c0, lane, acc);
+  add_rows<DT, VEC, B>(a, r, lo, f * kEmbedPiece, c0, lane, acc);
   const float* part = a.partial + (r * a.pieces + f) * a.pitch + c0 + lane * C::V;
   for (uint64_t p = f; p < l; ++p, part += a.pitch)
 #pragma unroll
@@ -210,14 +221,14 @@ __device__ __forceinline__ void add_run(const EmbedGradArgs& a, uint64_t r, uint
 #pragma unroll
       for (int e = 0; e < C::V; ++e) acc[k][e] += x[e];
     }
-  add_rows<DT, VEC>(a, r, l * kEmbedPiece, hi, c0, lane, acc);
+  add_rows<DT, VEC, B>(a, r, l * kEmbedPiece, hi, c0, lane, acc);
 }
 
 // columns of acc, scaled, to the ranks [r0, r0 + nr)
-template <int DT, bool VEC>
+template <int DT, bool VEC, int B>
 __device__ __forceinline__ void put_row(const EmbedGradArgs& a, char* o, int r0, int nr, uint64_t c0, int lane,
-                                        float (&acc)[Cols<DT>::CB][Cols<DT>::V]) {
-  typedef Cols<DT> C;
+                                        float (&acc)[Cols<DT, B>::CB][Cols<DT, B>::V]) {
+  typedef Cols<DT, B> C;
 #pragma unroll
   for (int k = 0; k < C::CB; ++k) {
     const uint64_t c = c0 + (uint64_t)(k * 64 + lane) * C::V;
@@ -263,9 +274,9 @@ constexpr int embed_rows() {
 constexpr uint32_t kEmbedShared = 16;
 constexpr int kEmbedWaves = kEmbedBlock / 64;
 
-template <int DT, bool VEC, bool SUM>
+template <int DT, bool VEC, bool SUM, int B>
 __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
-  typedef Cols<DT> C;
+  typedef Cols<DT, B> C;
   constexpr int SZ = Ty<DT>::SZ, ROWS = embed_rows<SUM>();
   extern __shared__ uint32_t runs[];   // [nr][ROWS] begin, then end
   uint32_t(*const begin)[ROWS] = (uint32_t(*)[ROWS])runs;
@@ -294,14 +305,14 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
     if (total[i] >= kEmbedShared) continue;
     char* const o = a.out + (v0 + i * dv) * a.width * SZ;
     if (total[i] == 0) {
-      for (int r = r0; r < r0 + nr; ++r) zero_row<DT>(o + (uint64_t)r * a.os, a.width * SZ, lane);
+      for (int r = r0; r < r0 + nr && blockIdx.z == 0; ++r) zero_row<DT>(o + (uint64_t)r * a.os, a.width * SZ, lane);
       continue;
     }
-    for (uint64_t c0 = 0; c0 < a.width; c0 += C::STEP) {
+    for (uint64_t c0 = blockIdx.z * C::STEP; c0 < a.width; c0 += gridDim.z * C::STEP) {
       float acc[C::CB][C::V] = {};
       for (int r = 0; r < nr; ++r)
-        if (begin[r][i] < end[r][i]) add_rows<DT, VEC>(a, r0 + r, begin[r][i], end[r][i], c0, lane, acc);
-      put_row<DT, VEC>(a, o, r0, nr, c0, lane, acc);
+        if (begin[r][i] < end[r][i]) add_rows<DT, VEC, B>(a, r0 + r, begin[r][i], end[r][i], c0, lane, acc);
+      put_row<DT, VEC, B>(a, o, r0, nr, c0, lane, acc);
     }
   }
   for (int i = 0; i < rows; ++i) {
@@ -309,13 +320,13 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
     // this wave's quarter of the tokens, counted over the ranks
     const uint32_t w0 = (uint32_t)((uint64_t)total[i] * wave / kEmbedWaves);
     const uint32_t w1 = (uint32_t)((uint64_t)total[i] * (wave + 1) / kEmbedWaves);
-    for (uint64_t c0 = 0; c0 < a.width; c0 += C::STEP) {
+    for (uint64_t c0 = blockIdx.z * C::STEP; c0 < a.width; c0 += gridDim.z * C::STEP) {
       float acc[C::CB][C::V] = {};
       uint32_t before = 0;
       for (int r = 0; r < nr; ++r) {
         const uint32_t lo = begin[r][i], n = end[r][i] - lo;
         const uint32_t f = w0 > before ? w0 - before : 0, l = w1 > before ? w1 - before : 0;
-        if (f < n && l) add_run<DT, VEC>(a, r0 + r, lo + f, lo + (l < n ? l : n), n, c0, lane, acc);
+        if (f < n && l) add_run<DT, VEC, B>(a, r0 + r, lo + f, lo + (l < n ? l : n), n, c0, lane, acc);
         before += n;
       }
       // join: waves 2 and 3 into 0 and 1, then 1 into 0
@@ -334,30 +345,54 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
             for (int e = 0; e < C::V; ++e) acc[k][e] += part[wave][(k * C::V + e) * 64 + lane];
       }
       if (wave == 0)
-        put_row<DT, VEC>(a, a.out + (v0 + i * dv) * a.width * SZ, r0, nr, c0, lane, acc);
+        put_row<DT, VEC, B>(a, a.out + (v0 + i * dv) * a.width * SZ, r0, nr, c0, lane, acc);
     }
   }
 }
 
-template <int DT, bool VEC>
+int compute_units() { return dev_info().cus > 0 ? dev_info().cus : 256; }
+
+// A small table has fewer rows a workgroup, so that all compute units have some
+// (8 ranks x 4096 tokens, 300 x 400 float32: 42 us against 78, the sum 63
+// against 190).  Where that makes less than two workgroups a unit, a row's
+// columns go to several too (the sum of 8 x 4096 tokens, 400 x 2048 bf16: 98 us
+// against 113, of 8 x 100 tokens, 300 x 2048: 26 against 20).
+unsigned embed_blocks(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
+  const uint64_t rows = L.summed ? embed_rows<true>() : embed_rows<false>();
+  const uint64_t fill = (uint64_t)(4 * compute_units() / (L.summed ? 1 : L.N));
+  return (unsigned)std::max((a.vocab + rows - 1) / rows, std::min(a.vocab, fill));
+}
+bool few_rows(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
+  return (uint64_t)embed_blocks(a, L) * (L.summed ? 1 : L.N) < (uint64_t)2 * compute_units();
+}
+
+template <int DT, bool VEC, int B>
 hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
   if (a.pieces) {
     const unsigned blocks = (unsigned)((a.pieces + kEmbedBlock / 64 - 1) / (kEmbedBlock / 64));
-    CC_LAUNCH((k_embed_pieces<DT, VEC>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), 0, L.st, a);
+    CC_LAUNCH((k_embed_pieces<DT, VEC, B>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), 0, L.st, a);
   }
   const int rows = L.summed ? embed_rows<true>() : embed_rows<false>();
-  const unsigned blocks = (unsigned)((a.vocab + rows - 1) / rows);
+  const unsigned blocks = embed_blocks(a, L);
+  const unsigned z = few_rows(a, L) ? (unsigned)std::min<uint64_t>((a.width - 1) / Cols<DT, B>::STEP + 1, 64) : 1;
   const unsigned need = (L.summed ? L.N : 1) * 2 * rows * 4;
   // A sum written to more than 4 ranks streams best from one workgroup a
   // compute unit (32000 x 2048 bf16 to 8 ranks 287 us against 334 uncapped, to
   // 4 ranks of a fourth of the tokens 110 either way, float32 x 1024 to 2 ranks
   // 93 against 86).
   const int blocks_per_cu = L.blocks_per_cu > 0 ? L.blocks_per_cu : L.summed && L.N > 4 ? 1 : 0;
-  const unsigned cap = lds_for_blocks_per_cu(blocks_per_cu), fixed = sizeof(float) * (2 * Cols<DT>::STEP + rows);
+  const unsigned cap = lds_for_blocks_per_cu(blocks_per_cu), fixed = sizeof(float) * (2 * Cols<DT, B>::STEP + rows);
   const unsigned lds = std::max(need, cap > fixed ? cap - fixed : 0u);
-  if (L.summed) CC_LAUNCH((k_embed_grad<DT, VEC, true>), dim3(blocks), dim3(kEmbedBlock), lds, L.st, a);
-  else CC_LAUNCH((k_embed_grad<DT, VEC, false>), dim3(blocks, (unsigned)L.N), dim3(kEmbedBlock), lds, L.st, a);
+  if (L.summed) CC_LAUNCH((k_embed_grad<DT, VEC, true, B>), dim3(blocks, 1, z), dim3(kEmbedBlock), lds, L.st, a);
+  else CC_LAUNCH((k_embed_grad<DT, VEC, false, B>), dim3(blocks, (unsigned)L.N, z), dim3(kEmbedBlock), lds, L.st, a);
   return hipGetLastError();
+}
+
+template <int DT, bool VEC>
+hipError_t pick_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
+  if (a.width <= (uint64_t)Cols<DT, 1>::STEP || few_rows(a, L)) return run_embed_grad<DT, VEC, 1>(a, L);
+  if (a.width <= (uint64_t)Cols<DT, 2>::STEP) return run_embed_grad<DT, VEC, 2>(a, L);
+  return run_embed_grad<DT, VEC, 4>(a, L);
 }
 
 }  // namespace
@@ -379,8 +414,8 @@ hipError_t launch_embed(const EmbedLaunch& L) {
 hipError_t launch_embed_grad(const EmbedGradLaunch& L) {
   EmbedGradArgs a{L.grad, L.grad_stride, L.out, L.out_stride, L.keys, L.vals, L.partial,
                   L.vocab, L.tokens, L.width, embed_partial_pitch(L.width), embed_pieces(L.tokens), L.scale, L.N};
-  if (L.dt == DT_F32) return L.vec_ok ? run_embed_grad<DT_F32, true>(a, L) : run_embed_grad<DT_F32, false>(a, L);
-  return L.vec_ok ? run_embed_grad<DT_BF16, true>(a, L) : run_embed_grad<DT_BF16, false>(a, L);
+  if (L.dt == DT_F32) return L.vec_ok ? pick_embed_grad<DT_F32, true>(a, L) : pick_embed_grad<DT_F32, false>(a, L);
+  return L.vec_ok ? pick_embed_grad<DT_BF16, true>(a, L) : pick_embed_grad<DT_BF16, false>(a, L);
 }
 
 }  // namespace cc
