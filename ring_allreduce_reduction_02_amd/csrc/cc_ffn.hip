@@ -24,8 +24,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-enum Kind { K_GATEUP = 0, K_DOWN = 1, K_DHID = 2, K_DX = 3, K_DW = 4 };
-
 constexpr int kKBytes = 128;   // bytes of the summed axis per stage and line: a cache line
 constexpr int kUnits = 4;      // matrix instruction steps per stage: 32 bytes of the summed axis each
 
@@ -644,7 +642,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_any(GemmArgs
 // any).  An offset outside the buffer (kOutside) reads as zeros.
 
 constexpr uint32_t kOutside = 0xfffffff0u;
-constexpr uint64_t kMaxSpan = 0xfff00000ull;   // bytes that offsets reach, below kOutside
+static_assert(kMaxSpan <= kOutside, "an offset inside a buffer is not kOutside");
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char* base, uint64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)(uint32_t)bytes, 0x00020000);
@@ -897,28 +895,6 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
 // ------------------------------------------------------------------ aligned copies
 
 uint64_t up256(uint64_t v) { return (v + 255) / 256 * 256; }
-uint64_t line_pitch(const FfnShape& s, uint64_t cols) {   // whole cache lines
-  return (cols * elem_size(s.dt) + 127) / 128 * 128;
-}
-
-// Whether the operands are first copied into rows that direct loads can take:
-// whole 16-byte vectors, padded with zeros, the experts' rows compact.  For
-// rows that are none, or a side that 32-bit offsets do not reach.
-// Gradients always: 1.04 to 2.7 times faster than the tiles through registers
-// over 1 to 8192 rows an expert and 201 x 333 to 2047 x 2047 of both types
-// (16 experts, 2047 x 2047 bf16, 4 rows an expert 461 us against 747, 4096
-// rows 3605 against 10002).  The forward pass reads every operand once along
-// its rows, where the tiles through registers do better, so that the copies
-// pay from about 1024 rows an expert and 512 columns on: 2047 x 2047 bf16 128
-// rows 378 us against 285, 512 rows 504 against 507, 2048 rows 1072 against 1665;
-// 300 x 517 bf16 2048 rows 118 against 121, 201 x 333 float32 236 against 213.
-constexpr uint64_t kCopyRows = 1024, kCopyCols = 512;
-bool copied(const FfnShape& s, int grad) {
-  const uint64_t es = elem_size(s.dt), w = line_pitch(s, s.W), f = line_pitch(s, s.F), f2 = line_pitch(s, 2 * s.F);
-  if (s.rows == 0 || (s.W * es % 16 == 0 && s.F * es % 16 == 0 && s.E * s.cap * s.W * es <= kMaxSpan)) return false;
-  if (s.most * std::max(w, f2) > kMaxSpan || 2 * s.F * w > kMaxSpan || s.W * f > kMaxSpan) return false;
-  return grad || (s.rows >= kCopyRows * s.E && std::min(s.W, s.F) >= kCopyCols);
-}
 
 struct CopyArgs {
   const int* start;
@@ -992,51 +968,6 @@ __global__ __launch_bounds__(256) void k_ffn_copy(CopyArgs a) {
   }
 }
 
-// whether the products run as aligned tiles: rows of whole 16-byte vectors, and
-// operands that 32-bit offsets reach
-bool tiled(const FfnLaunch& L) {
-  if (L.o.copied) return true;
-  const uint64_t es = elem_size(L.s.dt), row = std::max(L.s.W, 2 * L.s.F) * es;
-  return L.vec_ok && (uint64_t)L.s.E * L.s.cap * L.s.W * es <= kMaxSpan && L.s.most * row <= kMaxSpan &&
-         2 * L.s.F * L.s.W * es <= kMaxSpan;
-}
-
-// workgroups of a product in tiles of kFfnTile[k]
-template <int KIND>
-uint64_t tiles_of(GemmArgs* g, const FfnLaunch& L, int k) {
-  const int cols = KIND == K_GATEUP ? g->F : g->N, bn = KIND == K_GATEUP ? kFfnTile[k] / 2 : kFfnTile[k];
-  g->ntiles = (cols + bn - 1) / bn;
-  g->mtab = (const int2*)(L.ws + L.o.mtab[k]);
-  if constexpr (KIND == K_DW) {
-    g->mtiles = (g->M + kFfnTile[k] - 1) / kFfnTile[k];
-    return (uint64_t)g->E * g->mtiles * g->ntiles;
-  }
-  g->mtiles = (int)L.s.mtiles[k];
-  return (uint64_t)g->mtiles * g->ntiles;
-}
-
-// The tile whose workgroups, dealt out over the compute units, take least: a
-// larger tile moves fewer bytes for a product, a smaller one leaves fewer
-// units idle.  Cost of equal areas, measured on all six products of 60.7k rows:
-// bf16 2048 x 2048 1, 1.21 and 1.92 (4.62, 5.62 and 8.87 ms), float32, whose
-// products take eight times as long, 1024 x 1024 1, 1 and 1.25 (9.79, 9.81 and
-// 12.24 ms; the weight gradients alone 1, 1 and 1.35, which is counted).
-template <int KIND>
-int pick_tile(GemmArgs g, const FfnLaunch& L, int first) {
-  static constexpr double kArea[2][kFfnTiles] = {{16.0, 4.0 * 1.21, 1.92}, {16.0, 4.0, 1.35}};
-  const int cus = dev_info().cus > 0 ? dev_info().cus : 256;
-  int best = first;
-  double least = 0.0;
-  for (int k = first; k < kFfnTiles; ++k) {
-    const double t = (double)((tiles_of<KIND>(&g, L, k) + cus - 1) / cus) * kArea[L.s.dt == DT_F32][k];
-    if (k == first || t < least) {
-      least = t;
-      best = k;
-    }
-  }
-  return best;
-}
-
 template <int DT, int KIND, bool VEC>
 hipError_t launch_tile(const GemmArgs& g, int k, dim3 grid, hipStream_t st) {
   if (k == 0) CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 256, 256, 128, 64>), grid, dim3(512), 0, st, g);
@@ -1047,10 +978,15 @@ hipError_t launch_tile(const GemmArgs& g, int k, dim3 grid, hipStream_t st) {
 
 template <int DT, int KIND>
 hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
-  const bool fast = tiled(L);
-  const int k = pick_tile<KIND>(g, L, fast ? 0 : 1);
-  const uint64_t blocks = tiles_of<KIND>(&g, L, k);
+  const bool fast = ffn_tiled(L.s, L.o.copied, L.vec_ok);
+  const int cus = dev_info().cus > 0 ? dev_info().cus : 256, cols = KIND == K_GATEUP ? g.F : g.N;
+  const int k = ffn_pick_tile(L.s, KIND, g.M, cols, fast, cus);
+  const FfnGrid tiles = ffn_grid(L.s, KIND, g.M, cols, k);
+  const uint64_t blocks = tiles.blocks;
   if (blocks == 0) return hipSuccess;
+  g.mtiles = (int)tiles.mt;
+  g.ntiles = (int)tiles.nt;
+  g.mtab = (const int2*)(L.ws + L.o.mtab[k]);
   const dim3 grid((unsigned)blocks);
   if (fast && L.o.copied) return launch_tile<DT, KIND, false>(g, k, grid, L.st);   // results start anywhere
   if (fast) return launch_tile<DT, KIND, true>(g, k, grid, L.st);
@@ -1167,7 +1103,7 @@ FfnWs ffn_ws(const FfnShape& s, int grad) {
   o.start = take(((uint64_t)s.E + 1) * 4);
   for (int k = 0; k < kFfnTiles; ++k) o.mtab[k] = take(s.mtiles[k] * 8);
   o.rowmap = take(s.rows * 4);
-  o.copied = copied(s, grad);
+  o.copied = ffn_copied(s, grad);
   o.x = o.dy = o.w_in = o.w_out = 0;
   if (o.copied) {
     o.h = take(s.rows * line_pitch(s, s.F));

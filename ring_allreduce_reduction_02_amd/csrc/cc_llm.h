@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "cc_ffn_rule.h"
 #include "cc_launch.h"
 
 namespace cc {
@@ -98,16 +99,6 @@ hipError_t launch_route_grad(const RouteLaunch& L);
 
 // ---- gated feed-forward block of the experts.  Compact rows: the kept rows
 // of all experts back to back, expert by expert, source by source.
-constexpr int kFfnTiles = 3;            // tile sizes (rows and columns) of the products
-constexpr int kFfnTile[kFfnTiles] = {256, 128, 64};
-struct FfnShape {
-  int N, E;              // ranks, experts
-  uint64_t cap;
-  uint64_t W, F;         // width, hidden
-  uint64_t rows, most;   // kept rows of all experts, and of the one with most
-  uint64_t mtiles[kFfnTiles];   // row tiles of all experts, of each size
-  int dt, act;
-};
 // Workspace: row starts [E + 1], row tiles of each size (expert, first row), row
 // map [rows] (row in the rank's buffer), kept counts [N * E], h [rows][F],
 // and for the gradient d(gate | up) [rows][2F].  Where rows are no whole

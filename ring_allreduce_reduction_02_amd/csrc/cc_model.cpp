@@ -195,7 +195,7 @@ cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uin
   const uint64_t wt = (2 * F + 63) / 64, wn = (W + 63) / 64;   // the smallest tile's
   if ((u128)tiles[kFfnTiles - 1] * std::max(wt, wn) >= kMaxBlocks || (u128)E * wt * wn >= kMaxBlocks)
     return fail(CC_ERR_INVALID_ARG, "too many tiles for one launch");
-  *sh = FfnShape{N, E, cap, W, F, rows, most, {tiles[0], tiles[1], tiles[2]}, (int)dtype, 0};
+  *sh = FfnShape{N, E, cap, W, F, rows, most, {tiles[0], tiles[1], tiles[2]}, (int)dtype, elem_size((int)dtype), 0};
   return CC_OK;
 }
 
