@@ -614,7 +614,8 @@ cc_status_t cc_moe_route_grad(cc_rankbuf_t logits, cc_rankbuf_t experts, cc_rank
  * cc_moe_dispatch_padded: for the kept rows x of every expert
  *   [g | u] = x w_in^T,  h = act(g) * u,  y = h w_out^T.
  * counts, nexperts (at most 8192) and capacity as in the dispatch (counts
- * host [nranks * nexperts]; the call has read them when it returns); x, y:
+ * host [nranks * nexperts]; the call has read them when it returns; one above
+ * SIZE_MAX / 2 is a negative number and refused); x, y:
  * E * capacity rows of `width` per rank, in the dispatch's layout.  Rank j's weights, one local expert after the other: w_in
  * [2 * hidden][width] (gate rows, then up rows), w_out [width][hidden].  pre
  * (base may be NULL) keeps [g | u], 2 * hidden elements a row in x's layout,

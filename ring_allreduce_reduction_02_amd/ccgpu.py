@@ -408,7 +408,7 @@ def all_to_all(send, recv, counts: Sequence[Sequence[int]], elem_per_row: int = 
 
 def _sizes(rows: Sequence[Sequence[int]], n: int, m: int, what: str):
     flat = [int(v) for row in rows for v in row]
-    if len(flat) != n * m:
+    if len(flat) != n * m or any(len(row) != m for row in rows):
         raise ValueError(f"{what} must be {n} x {m}")
     return (ctypes.c_size_t * max(len(flat), 1))(*flat)
 

@@ -183,6 +183,8 @@ cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uin
   for (int e = 0; e < E; ++e) {
     uint64_t n = 0;
     for (int i = 0; i < N; ++i) {
+      if (counts[(size_t)i * E + e] > SIZE_MAX / 2)
+        return fail(CC_ERR_INVALID_ARG, "counts[%d][%d] is negative", i, e);
       const uint64_t k = std::min<uint64_t>(counts[(size_t)i * E + e], cap);
       (*kept)[(size_t)e * N + i] = (uint32_t)k;
       n += k;
