@@ -564,15 +564,21 @@ cc_status_t cc_embedding(cc_rankbuf_t table, cc_rankbuf_t ids, cc_rankbuf_t out,
 /* The table's gradient of each rank: dtable[v] = scale * the sum of grad[t]
  * over the rank's t with ids[t] = v, for every v (all vocab rows are written;
  * zeros for words the rank does not hold; ids outside [0, vocab) add nothing).
- * The sums run in the order of t, in pieces of 32 for words that repeat. */
+ * A word with n < 16 positions t is summed in the order of t.  From 16 on it is
+ * summed in four parts, part k the positions [n k / 4, n (k + 1) / 4) in the
+ * order of t, joined as (0 + 2) + (1 + 3).  Where tokens > 1024 and the rank
+ * holds the word 128 times or more, a part first sums each 32 of its positions
+ * that fill places [32 m, 32 m + 32) of the rank's ids sorted by (id, t), and
+ * adds that sum as one term. */
 cc_status_t cc_embedding_grad(cc_rankbuf_t grad, cc_rankbuf_t ids, cc_rankbuf_t dtable, size_t vocab, size_t tokens,
                               size_t width, float scale, cc_dtype_t dtype, int nranks, const cc_config_t* cfg,
                               cc_stream_t stream);
 
 /* The same gradient summed over the ranks, on every rank: cc_embedding_grad
  * and the AllReduce of its result in one call, without the N dense gradients
- * in memory.  The sum runs in the order of (rank, t) and is rounded once (the
- * two calls round each rank's gradient too, and fold in the ring's order). */
+ * in memory.  The sum runs as above over the positions (rank, t) in order, n of
+ * them on all ranks, and is rounded once (the two calls round each rank's
+ * gradient too, and fold in the ring's order). */
 cc_status_t cc_all_reduce_embedding_grad(cc_rankbuf_t grad, cc_rankbuf_t ids, cc_rankbuf_t dtable, size_t vocab,
                                          size_t tokens, size_t width, float scale, cc_dtype_t dtype, int nranks,
                                          const cc_config_t* cfg, cc_stream_t stream);

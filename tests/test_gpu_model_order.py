@@ -1,0 +1,91 @@
+"""The order in which the embedding's gradients are summed, as the header states
+it, replayed in float32 on the host: the same bits, for words of one position
+to runs of many pieces, of one rank and over the ranks."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV
+from ring_allreduce_reduction_02_amd import ccgpu
+from test_gpu_model import gen, ints, ranks, say
+
+pytestmark = pytest.mark.gpu
+F32 = np.float32
+SHARED, LONG, PIECE, FEW = 16, 128, 32, 1024
+
+
+def in_order(terms, acc=None):
+    acc = np.zeros(terms.shape[1], F32) if acc is None else acc
+    for t in terms:
+        acc = acc + t
+    return acc
+
+
+def fold(runs, tokens):
+    """One word's sum.  runs: per rank the word's first place in the rank's sorted ids and its rows, float32."""
+    n = sum(len(rows) for _, rows in runs)
+    if n < SHARED:
+        return in_order(np.concatenate([rows for _, rows in runs]))
+    quarter = []
+    for k in range(4):
+        lo, hi, before, acc = n * k // 4, n * (k + 1) // 4, 0, np.zeros(runs[0][1].shape[1], F32)
+        for first, rows in runs:
+            f, l = max(lo - before, 0), min(max(hi - before, 0), len(rows))
+            before += len(rows)
+            while f < l:
+                at = first + f
+                if tokens > FEW and len(rows) >= LONG and at % PIECE == 0 and f + PIECE <= l:
+                    acc = acc + in_order(rows[f:f + PIECE])
+                    f += PIECE
+                else:
+                    acc = acc + rows[f]
+                    f += 1
+        quarter.append(acc)
+    return (quarter[0] + quarter[2]) + (quarter[1] + quarter[3])
+
+
+def replay(grad, ids, V, scale, summed):
+    """float32 [N or 1][V][D] before the rounding to the buffers' type; and how many words the plain order differs in."""
+    N, T, D = grad.shape
+    out, other = np.zeros((1 if summed else N, V, D), F32), 0
+    runs = []
+    for r in range(N):
+        key = np.where((ids[r] >= 0) & (ids[r] < V), ids[r], V)
+        order = np.argsort(key, kind="stable")
+        first = np.searchsorted(key[order], np.arange(V + 1))
+        runs.append([(first[v], grad[r][order[first[v]:first[v + 1]]]) for v in range(V)])
+    for g in ([list(range(N))] if summed else [[r] for r in range(N)]):
+        for v in range(V):
+            mine = [runs[r][v] for r in g]
+            s = fold(mine, T)
+            other += not np.array_equal(s, in_order(np.concatenate([rows for _, rows in mine])))
+            out[0 if summed else g[0], v] = s * F32(scale)
+    return out, other
+
+
+# (ranks, tokens, vocab, width): no pieces; pieces, their borders anywhere; the last token count without them
+CASES = [(3, 700, 41, 5), (2, 3001, 23, 12), (5, 1024, 9, 8), (1, 1025, 6, 7)]
+
+
+@pytest.mark.parametrize("summed", [False, True], ids=["rank", "sum"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_order_of_the_sums(case, dtype, summed):
+    N, T, V, D = case
+    say("order", case, dtype, summed)
+    g = gen(T)
+    u = torch.rand((N, T), generator=g, device=DEV, dtype=torch.float64)
+    ids = ints(N, T, 3)
+    ids.copy_((u ** 3 * V).int().clamp(0, V - 1))                     # many positions of the first words, few of the last
+    ids[torch.rand((N, T), generator=g, device=DEV) < 0.05] = -1
+    grad = ranks(N, T * D, dtype, 8, 0, torch.randn((N, T, D), generator=g, device=DEV))
+    out = ranks(N, V * D, dtype, 16)
+    f = ccgpu.all_reduce_embedding_grad if summed else ccgpu.embedding_grad
+    f(grad, ids, out, D, scale=0.7, workspace=ccgpu.make_embedding_grad_workspace(N, V, T, D))
+    torch.cuda.synchronize()
+    want, other = replay(grad.float().cpu().numpy().reshape(N, T, D), ids.cpu().numpy(), V, 0.7, summed)
+    # the words distinguish it from the plain order (bf16 terms have 8 bits, and float32 sums of some tens of them are
+    # exact in any order, unless a term below 2^-16 of the sum is among them)
+    assert other > 0 or dtype == "bf16"
+    want = torch.from_numpy(want).to(out.dtype).expand(N, -1, -1)
+    assert torch.equal(out.cpu().reshape(N, V, D), want)
