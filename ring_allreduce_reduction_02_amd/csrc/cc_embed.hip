@@ -353,10 +353,10 @@ __global__ __launch_bounds__(kEmbedBlock) void k_embed_grad(EmbedGradArgs a) {
 int compute_units() { return dev_info().cus > 0 ? dev_info().cus : 256; }
 
 // A small table has fewer rows a workgroup, so that all compute units have some
-// (8 ranks x 4096 tokens, 300 x 400 float32: 42 us against 78, the sum 63
-// against 190).  Where that makes less than two workgroups a unit, a row's
-// columns go to several too (the sum of 8 x 4096 tokens, 400 x 2048 bf16: 98 us
-// against 113, of 8 x 100 tokens, 300 x 2048: 26 against 20).
+// (8 ranks x 4096 tokens, 300 x 400 float32: 43 us against 58, the sum 54
+// against 155).  Where that makes less than two workgroups a unit, a row's
+// columns go to several too (the sum of 8 x 4096 tokens, 400 x 2048 bf16: 75 us
+// against 121, of 8 x 100 tokens, 300 x 2048: 16 against 20).
 unsigned embed_blocks(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
   const uint64_t rows = L.summed ? embed_rows<true>() : embed_rows<false>();
   const uint64_t fill = (uint64_t)(4 * compute_units() / (L.summed ? 1 : L.N));
@@ -376,11 +376,18 @@ hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedGradLaunch& L) {
   const unsigned blocks = embed_blocks(a, L);
   const unsigned z = few_rows(a, L) ? (unsigned)std::min<uint64_t>((a.width - 1) / Cols<DT, B>::STEP + 1, 64) : 1;
   const unsigned need = (L.summed ? L.N : 1) * 2 * rows * 4;
-  // A sum written to more than 4 ranks streams best from one workgroup a
-  // compute unit (32000 x 2048 bf16 to 8 ranks 287 us against 334 uncapped, to
-  // 4 ranks of a fourth of the tokens 110 either way, float32 x 1024 to 2 ranks
-  // 93 against 86).
-  const int blocks_per_cu = L.blocks_per_cu > 0 ? L.blocks_per_cu : L.summed && L.N > 4 ? 1 : 0;
+  // A sum of wide rows written to more than 4 ranks streams best from one
+  // workgroup a compute unit, once its table gives a workgroup two rows or
+  // more (8 ranks x 1000 tokens, 10000 x 2048 bf16: 85 us against 99 uncapped; 4096
+  // tokens, 32000 words 254 against 248; to 4 ranks of a fourth of the tokens
+  // 110 either way, float32 x 1024 to 2 ranks 93 against 86).  Narrow rows and
+  // small tables wait for their loads instead, and need all that fit (8 x 4096
+  // tokens, 32000 x 512: 84 us against 123 with one, 400 x 2048: 75 against
+  // 101; 8 x 100 tokens, 1500 x 2048: 22 against 30).  Rows of two blocks lie
+  // between (10000 x 1024 bf16, 1000 tokens: 5 ranks 38 against 44, 16 ranks 107
+  // against 94).
+  const bool one = L.summed && L.N > 4 && B == 4 && a.vocab >= 2 * (uint64_t)blocks;
+  const int blocks_per_cu = L.blocks_per_cu > 0 ? L.blocks_per_cu : one ? 1 : 0;
   const unsigned cap = lds_for_blocks_per_cu(blocks_per_cu), fixed = sizeof(float) * (2 * Cols<DT, B>::STEP + rows);
   const unsigned lds = std::max(need, cap > fixed ? cap - fixed : 0u);
   if (L.summed) CC_LAUNCH((k_embed_grad<DT, VEC, true, B>), dim3(blocks, 1, z), dim3(kEmbedBlock), lds, L.st, a);

@@ -89,3 +89,19 @@ def test_order_of_the_sums(case, dtype, summed):
     assert other > 0 or dtype == "bf16"
     want = torch.from_numpy(want).to(out.dtype).expand(N, -1, -1)
     assert torch.equal(out.cpu().reshape(N, V, D), want)
+
+
+@pytest.mark.parametrize("table", [(300, 2048), (2100, 2048), (2600, 512), (40, 8)], ids=str)
+def test_order_does_not_depend_on_the_cap(table):
+    """The call's own choice of workgroups per compute unit (one for some sums to more than 4 ranks), one, and none."""
+    (V, D), N, T = table, 5, 1100
+    say("cap", table)
+    g = gen(V)
+    ids = (torch.rand((N, T), generator=g, device=DEV) ** 3 * V).int()
+    grad = torch.randn((N, T * D), generator=g, device=DEV)
+    ws = ccgpu.make_embedding_grad_workspace(N, V, T, D)
+    outs = [torch.full((N, V * D), 5.0, device=DEV) for _ in range(3)]
+    for o, n in zip(outs, (0, 1, 64)):
+        ccgpu.all_reduce_embedding_grad(grad, ids, o, D, workspace=ws, blocks_per_cu=n)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
