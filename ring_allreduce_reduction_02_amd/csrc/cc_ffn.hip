@@ -279,7 +279,7 @@ enum Act { ACT_SILU = 0, ACT_GELU = 1 };
 // steps (2^-24) of their value, also where they are small (with exp2 and the
 // reciprocal as for bf16 the case of 8 x 2048 tokens, top-2 of 16 experts, 768 x
 // 768 takes 847 us against 850 forward, 2092 against 2109 for the gradients, and
-// silu(-60) is off by 60 half steps).
+// silu is off by up to 64 half steps for |g| up to 87).
 // bf16: from the hardware's exp2 and reciprocal (1 ulp each).  log2(e) is off
 // by 0.23 half steps and its product with g by one, so s is off by at most
 // (1.25 |g| + 6) 2^-24 of its value, 2^-17 at |g| = 87, below the 2^-8 that the
@@ -598,8 +598,9 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TM][TN]) {
 
 // Any alignment: tiles staged through registers, the next stage's on their way
 // while this one's products run.  2 x 333 tokens, top-2 of 6 experts, 515 x 331
-// float32: 32 and 20 us, bound by the latency of 17 and 11 stages (the products
-// are 9 us of the matrix units); element by element they took 54 and 35.
+// float32: 32 and 20 us.  Its 506 and 414 waves leave half of the 1024 SIMDs idle,
+// and a wave spends half of its time, 14 of 28 us, in matrix instructions, the
+// rest on the latency of 17 and 11 stages; element by element they took 54 and 35.
 template <int DT, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_any(GemmArgs g) {
   constexpr int NT = 64 * (BM / WM) * (BN / WN);
@@ -758,8 +759,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const RowSide& s, 
 // 2048 x 2048 bf16 (60.7k rows): gate and up 1.04 ms (980 TFLOP/s), down 0.48-0.51
 // (1000-1060), hidden gradient 0.65 (780; it reads and writes 1.5 GB more), row
 // gradient 0.87 (1170), weight gradients 0.54 and 1.10 (930).  The matrix units
-// are busy 58-63% of the cycles, at 1.65-1.8 GHz: the card lowers its clock under
-// this load.  With the loads left out a stage took 1.36 us, with loads that
+// are busy 58, 61, 41, 63 and 50% of the cycles, at 1.64-1.93 GHz: the card lowers
+// its clock under this load.  With the loads left out a stage took 1.36 us, with loads that
 // hit the L2 1.58, as it is 1.95.
 // What else was tried there: four stages of 64-byte lines (twice the cache
 // requests: 10% slower), 128 x 128 tiles two to a unit (10-25% slower), four

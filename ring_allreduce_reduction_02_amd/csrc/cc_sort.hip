@@ -5,9 +5,10 @@
 // Least significant digit first, 8 bits a pass.  A pass is three kernels: the
 // digit counts of every tile, their exclusive prefix in (digit, tile) order,
 // and the scatter, in which a key's place inside its tile is the number of
-// equal digits before it (8 ranks x 32768 keys, one pass: 4 + 3.5 + 5 us): in its wave's earlier rounds, in the lanes below it
+// equal digits before it: in its wave's earlier rounds, in the lanes below it
 // (one ballot per bit), and in the waves before it.  Every place is a count,
-// so nothing depends on the order in which workgroups run.
+// so nothing depends on the order in which workgroups run.  One pass over 8
+// ranks x 32768 keys takes 4, 3.5 and 5 us, bound by latency.
 
 #include <algorithm>
 
