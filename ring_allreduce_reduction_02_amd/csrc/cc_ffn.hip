@@ -10,7 +10,9 @@
 // the first ends in the activation and the product, the third in the
 // activation's derivative.  Products run on the matrix cores and sum in
 // float32; h, dg and du are rounded once to the buffers' type between two
-// products, because the matrix cores read that type.
+// products, because the matrix cores read that type.  bf16 results are so off
+// by 0.0024 of their norm against 64 bits, where float32 between the products
+// would leave 0.0017, the rounding of the results themselves.
 
 #include <algorithm>
 
@@ -759,8 +761,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const RowSide& s, 
 // 2048 x 2048 bf16 (60.7k rows): gate and up 1.04 ms (980 TFLOP/s), down 0.48-0.51
 // (1000-1060), hidden gradient 0.65 (780; it reads and writes 1.5 GB more), row
 // gradient 0.87 (1170), weight gradients 0.54 and 1.10 (930).  The matrix units
-// are busy 58, 61, 41, 63 and 50% of the cycles, at 1.64-1.93 GHz: the card lowers
-// its clock under this load.  With the loads left out a stage took 1.36 us, with loads that
+// are busy 56-58, 59-61, 40, 63 and 50-53% of the cycles, at 1.6-1.9 GHz: the card
+// lowers its clock under this load.  With the loads left out a stage took 1.36 us, with loads that
 // hit the L2 1.58, as it is 1.95.
 // What else was tried there: four stages of 64-byte lines (twice the cache
 // requests: 10% slower), 128 x 128 tiles two to a unit (10-25% slower), four

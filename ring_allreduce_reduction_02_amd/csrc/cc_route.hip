@@ -98,8 +98,8 @@ __device__ __forceinline__ float load_exp(const char* row, int E, int lane, floa
 }
 
 // Both kernels are bound by their vector instructions, 265 and 176 a token of top-8
-// of 64, issued in about 94% of the cycles: 8 x 4096 tokens 16 us and 12 us (4.2 to
-// 17 MB of memory traffic, 1-4 us of it).
+// of 64, which take about 90 and 80% of the cycles: 8 x 4096 tokens 16 us and 12 us
+// (4.2 to 17 MB of memory traffic, 1-4 us of it).
 //
 // One wave a token.  The chosen experts one after the other: the largest bits
 // of the wave, the lowest index that has them, then taken out.
