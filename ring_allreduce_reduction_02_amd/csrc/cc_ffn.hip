@@ -761,8 +761,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const RowSide& s, 
 // 2048 x 2048 bf16 (60.7k rows): gate and up 1.04 ms (980 TFLOP/s), down 0.48-0.51
 // (1000-1060), hidden gradient 0.65 (780; it reads and writes 1.5 GB more), row
 // gradient 0.87 (1170), weight gradients 0.54 and 1.10 (930).  The matrix units
-// are busy 56-58, 59-61, 40, 63 and 50-53% of the cycles, at 1.6-1.9 GHz: the card
-// lowers its clock under this load.  With the loads left out a stage took 1.36 us, with loads that
+// are busy 57, 60, 40, 64 and 49-51% of the cycles, at 1.6, 1.6, 1.9, 1.8 and 1.9
+// GHz: the card lowers its clock under this load.  With the loads left out a stage took 1.36 us, with loads that
 // hit the L2 1.58, as it is 1.95.
 // What else was tried there: four stages of 64-byte lines (twice the cache
 // requests: 10% slower), 128 x 128 tiles two to a unit (10-25% slower), four
