@@ -38,8 +38,9 @@
  *    blocks_per_cu),
  *    CC_ERR_UNSUPPORTED for a schedule the collective does not have,
  *    CC_ERR_NO_DEVICE when no GPU is visible, CC_ERR_HIP for a launch error.
- *    Every enum below spans the whole int range (its *_MAX_ENUM member), so
- *    any int a C caller passes is a value of the type and is validated.
+ *    Every enum below spans the whole int range (its *_MIN_ENUM and
+ *    *_MAX_ENUM members), so any int a C caller passes is a value of the type
+ *    and is validated.
  *    cc_last_error() returns a message for the last failing call on the
  *    calling thread.
  */
@@ -61,14 +62,27 @@ typedef enum {
   CC_ERR_UNSUPPORTED = 2,
   CC_ERR_NO_DEVICE = 3,
   CC_ERR_HIP = 4,
+  CC_STATUS_MIN_ENUM = -0x7fffffff - 1,
   CC_STATUS_MAX_ENUM = 0x7fffffff
 } cc_status_t;
 
-typedef enum { CC_INT32 = 0, CC_FLOAT32 = 1, CC_BFLOAT16 = 2, CC_DTYPE_MAX_ENUM = 0x7fffffff } cc_dtype_t;
+typedef enum {
+  CC_INT32 = 0,
+  CC_FLOAT32 = 1,
+  CC_BFLOAT16 = 2,
+  CC_DTYPE_MIN_ENUM = -0x7fffffff - 1,
+  CC_DTYPE_MAX_ENUM = 0x7fffffff
+} cc_dtype_t;
 
 /* Elementwise operators named by the course lesson "第 3 课：分布式通信原语"
  * (核心概念, item 1: SUM, MAX, PROD). */
-typedef enum { CC_SUM = 0, CC_MAX = 1, CC_PROD = 2, CC_OP_MAX_ENUM = 0x7fffffff } cc_op_t;
+typedef enum {
+  CC_SUM = 0,
+  CC_MAX = 1,
+  CC_PROD = 2,
+  CC_OP_MIN_ENUM = -0x7fffffff - 1,
+  CC_OP_MAX_ENUM = 0x7fffffff
+} cc_op_t;
 
 /* Schedules.  Only CC_ALGO_RING and CC_ALGO_HALVING_DOUBLING (N = 2^k) serve
  * ReduceScatter and AllGather; broadcast takes ring (chain) and
@@ -96,6 +110,7 @@ typedef enum {
   CC_ALGO_TREE = 3,             /* AllReduce only */
   CC_ALGO_DOUBLE_TREE = 4,      /* AllReduce only */
   CC_ALGO_RING_2PORT = 5,       /* AllReduce only */
+  CC_ALGO_MIN_ENUM = -0x7fffffff - 1,
   CC_ALGO_MAX_ENUM = 0x7fffffff
 } cc_algo_t;
 
@@ -105,6 +120,7 @@ typedef enum {
   CC_COLL_ALL_GATHER = 2,
   CC_COLL_BROADCAST = 3,
   CC_COLL_ALL_TO_ALL = 4,
+  CC_COLL_MIN_ENUM = -0x7fffffff - 1,
   CC_COLL_MAX_ENUM = 0x7fffffff
 } cc_coll_t;
 
@@ -480,6 +496,7 @@ typedef enum {
   CC_A2A_MOE_DISPATCH = 1,
   CC_A2A_MOE_COMBINE = 2,
   CC_A2A_HIERARCHICAL = 3,
+  CC_A2A_MIN_ENUM = -0x7fffffff - 1,
   CC_A2A_MAX_ENUM = 0x7fffffff
 } cc_a2a_kind_t;
 typedef struct {
@@ -630,7 +647,11 @@ cc_status_t cc_moe_route_grad(cc_rankbuf_t logits, cc_rankbuf_t experts, cc_rank
  * rounded to dtype between the products.  A dense block is one
  * expert with capacity rows.  SiLU is g / (1 + exp(-g)), GELU the exact one
  * (g times the normal distribution function). */
-typedef enum { CC_ACT_SILU = 0, CC_ACT_GELU = 1, CC_ACT_MAX_ENUM = 0x7fffffff } cc_act_t;
+typedef enum {
+  CC_ACT_SILU = 0, CC_ACT_GELU = 1,
+  CC_ACT_MIN_ENUM = -0x7fffffff - 1,
+  CC_ACT_MAX_ENUM = 0x7fffffff
+} cc_act_t;
 cc_status_t cc_moe_ffn(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t pre, cc_rankbuf_t y,
                        const size_t* counts, int nexperts, size_t capacity, size_t width, size_t hidden, cc_act_t act,
                        cc_dtype_t dtype, int nranks, const cc_config_t* cfg, cc_stream_t stream);
