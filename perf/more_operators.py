@@ -1,0 +1,612 @@
+"""What the operators beside the MoE routing and the experts' feed-forward block
+are measured on: the balance loss of the router with its gradient, products in
+8-bit integers, and the feed-forward block's activation checkpoints in 8 bits.
+
+Each case names one pass with its sizes.  The ranks are the logical ranks of
+the library: rank r's buffers are row r of every tensor.  `run` computes a pass
+in elementary torch operations, or with `own` set through the calls of the
+library; `exact` gives the same values in 64 bits.
+
+Sizes come from this repository's own MoE workload (8 ranks, 4096 tokens,
+top-8 of 64 experts) and its textbook napkin (width 2048), or are generic.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+DEV = "cuda"
+TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
+SIZE = {"f32": 4, "bf16": 2}
+BLOCK = 32     # elements of a checkpoint that share a power of two
+
+
+# ------------------------------------------------------------------ the cases
+
+def listed():
+    return [
+        # the loss of one training step of the MoE workload, over all ranks' tokens
+        dict(name="balance train bf16", op="balance", ranks=8, tokens=4096, experts=64, topk=8, summed=True, dtype="bf16"),
+        # each rank's own loss in a small model of an odd number of experts
+        dict(name="balance odd f32", op="balance", ranks=3, tokens=1023, experts=61, topk=2, summed=False, dtype="f32"),
+        # its gradient, added to the one that the routing weights gave
+        dict(name="balance-grad train f32", op="balance_grad", ranks=8, tokens=4096, experts=64, topk=8, summed=True,
+             accumulate=True, dtype="f32"),
+        # the gradient of a long batch over many experts
+        dict(name="balance-grad large bf16", op="balance_grad", ranks=8, tokens=32768, experts=256, topk=8, summed=True,
+             accumulate=False, dtype="bf16"),
+        # a projection of tokens that arrive in float32, odd sizes: rows start anywhere
+        dict(name="int8 odd f32", op="int8", ranks=2, tokens=333, experts=6, topk=2, width=515, cols=331, factor=5,
+             dtype="f32"),
+        # the experts' first product of a long prompt: rows quantised, then multiplied
+        dict(name="int8 prompt bf16", op="int8", ranks=8, tokens=4096, experts=16, topk=2, width=2048, cols=4096,
+             factor=5, dtype="bf16"),
+        # the whole block of one decoding step: few rows an expert, the weights' bytes count
+        dict(name="int8-ffn decode bf16", op="int8_ffn", ranks=8, tokens=4, experts=64, topk=8, width=2048, hidden=1024,
+             factor=0, act="silu", dtype="bf16"),
+        # the whole block of a prompt
+        dict(name="int8-ffn prompt bf16", op="int8_ffn", ranks=8, tokens=4096, experts=16, topk=2, width=2048,
+             hidden=2048, factor=5, act="silu", dtype="bf16"),
+        # a training step of the block that keeps its activations in 8 bits: forward, then the gradients from them
+        dict(name="ckpt-step train bf16", op="ckpt_step", ranks=8, tokens=4096, experts=16, topk=2, width=2048,
+             hidden=2048, factor=5, act="silu", dtype="bf16"),
+        # the same of a small model of odd sizes, blocks that end inside a row
+        dict(name="ckpt-step odd bf16", op="ckpt_step", ranks=2, tokens=401, experts=6, topk=2, width=515, hidden=331,
+             factor=6, act="gelu", dtype="bf16"),
+        # float32 gradients from a checkpoint, odd sizes
+        dict(name="ckpt-grad odd f32", op="ckpt_grad", ranks=2, tokens=333, experts=6, topk=2, width=515, hidden=331,
+             factor=6, act="gelu", dtype="f32"),
+        # float32 gradients with ragged rows
+        dict(name="ckpt-grad f32", op="ckpt_grad", ranks=4, tokens=509, experts=8, topk=2, width=1024, hidden=1100,
+             factor=5, act="silu", dtype="f32"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _wide(rng, lo, hi):
+    """A row width: a multiple of 16 three times in four, any number otherwise."""
+    v = _log(rng, lo, hi)
+    return v if rng.random() < 0.25 else max(16, v // 16 * 16)
+
+
+def draw(rng):
+    op = rng.choice(["balance", "balance_grad", "int8", "int8", "int8_ffn", "ckpt_step", "ckpt_grad"])
+    c = dict(op=op, ranks=rng.choice([1, 2, 3, 4, 5, 8]), dtype=rng.choice(["f32", "bf16"]))
+    if op.startswith("balance"):
+        c.update(tokens=_log(rng, 1, 32768), experts=_log(rng, 2, 256), summed=rng.random() < 0.75)
+        c["topk"] = rng.randint(1, min(8, c["experts"]))
+        if op == "balance_grad":
+            c["accumulate"] = rng.random() < 0.5
+        return c
+    c["tokens"] = _log(rng, 1, 4096)
+    c["experts"] = c["ranks"] * rng.randint(1, max(1, 32 // c["ranks"]))
+    c["topk"] = rng.randint(1, min(2, c["experts"]))
+    c["factor"] = rng.choice([0, 4, 5, 6])
+    if c["factor"] == 0:
+        c["tokens"] = min(c["tokens"], 512)
+    if op == "int8":
+        return {**c, "width": _wide(rng, 32, 2048), "cols": _wide(rng, 32, 4096)}
+    # a block's hidden rows are quantised after a float32 sum, whose last bits may move one of them over a border
+    # to the next integer: a float32 result would show that, a bf16 one does not
+    if op != "ckpt_grad":
+        c["dtype"] = "bf16"
+    big = 2048 if c["dtype"] == "bf16" else 768
+    return {**c, "act": rng.choice(["silu", "gelu"]), "width": _wide(rng, 32, big), "hidden": _wide(rng, 32, big)}
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+
+def _shares(tokens, experts, topk):
+    """Rows one source rank routes to the experts, most loaded first: shares of
+    (e + 1)^-0.4, at most `tokens` each, tokens * topk in all."""
+    w = np.arange(1, experts + 1, dtype=np.float64) ** -0.4
+    left, out = tokens * topk, np.zeros(experts, dtype=np.int64)
+    for e in range(experts):
+        out[e] = min(tokens, left, int(math.ceil(left * w[e] / w[e:].sum())))
+        left -= out[e]
+    e = 0
+    while left > 0:
+        add = min(left, tokens - int(out[e]))
+        out[e] += add
+        left -= add
+        e += 1
+    return out
+
+
+def _capacity(c):
+    """Rows of one (source, expert) block: factor / 4 times the even share, or
+    room for every row where nothing may be dropped (factor 0)."""
+    if c["factor"] == 0:
+        return max(c["tokens"], 1)
+    return -(-c["tokens"] * c["topk"] * c["factor"] // (4 * c["experts"]))
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def work(c):
+    n, t, s, e = c["ranks"], c["tokens"], SIZE[c["dtype"]], c["experts"]
+    if c["op"] == "balance":
+        return {"bytes": n * (t * e * s + 4 * e + 4 * (2 * e + 2)), "flops": 6 * n * t * e}
+    if c["op"] == "balance_grad":
+        return {"bytes": n * (t * e * s * (3 if c["accumulate"] else 2) + 4 * (e + 2)), "flops": 9 * n * t * e}
+    kept = np.minimum(_shares(t, e, c["topk"]), _capacity(c))
+    rows, live, w = n * int(kept.sum()), int((kept > 0).sum()), c["width"]
+    if c["op"] == "int8":
+        k = c["cols"]
+        return {"bytes": rows * (w + k) * s + live * k * (w + 4), "flops": 2 * rows * w * k}
+    h = c["hidden"]
+    if c["op"] == "int8_ffn":
+        return {"bytes": rows * 2 * w * s + live * (3 * w * h + 4 * (2 * h + w)), "flops": 6 * rows * w * h}
+    keep = rows * (w + 2 * h + _blocks(w) + 2 * _blocks(h))        # the checkpoint
+    grad = {"bytes": keep + s * (rows * 2 * w + (live + e) * 3 * w * h), "flops": 12 * rows * w * h}
+    if c["op"] == "ckpt_grad":
+        return grad
+    return {"bytes": grad["bytes"] + keep + s * (rows * 2 * w + live * 3 * w * h), "flops": 18 * rows * w * h}
+
+
+# ------------------------------------------------------------------ inputs
+
+def _randn(g, shape, dtype, sigma):
+    return torch.randn(shape, generator=g, device=DEV, dtype=torch.float32).mul_(sigma).to(TORCH[dtype])
+
+
+def _plan(c, seed):
+    """The exchange's plan: the counts of every (source, expert), the same
+    experts popular on every source, and each expert's kept rows (their
+    positions in its rank's buffer)."""
+    n, e = c["ranks"], c["experts"]
+    perm = np.random.default_rng([seed, 7]).permutation(e)
+    share = _shares(c["tokens"], e, c["topk"])[np.argsort(perm)]
+    cap, per = _capacity(c), e // n
+    counts = [[int(v) for v in share] for _ in range(n)]
+    rows = []
+    for x in range(e):
+        kept = min(counts[0][x], cap)
+        at = (np.arange(n)[:, None] * per + x % per) * cap + np.arange(kept)[None, :]
+        rows.append(torch.from_numpy(at.reshape(-1)).to(DEV))
+    return counts, cap, rows
+
+
+def _channels(g, shape, sigma):
+    """Weights in 8 bits with a scale for each channel (the last axis is summed)."""
+    w = torch.randn(shape, generator=g, device=DEV) * sigma
+    w *= torch.exp(0.5 * torch.randn(shape[:-1] + (1,), generator=g, device=DEV))     # channels differ in size
+    return _int8_rows(w)
+
+
+def prepare(c, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed * 7919 + 29)
+    n, t, dt, e = c["ranks"], c["tokens"], c["dtype"], c["experts"]
+    st = {"c": c}
+    if own:
+        from ring_allreduce_reduction_02_amd import ccgpu
+        st["cc"] = ccgpu
+    if c["op"].startswith("balance"):
+        lg = torch.randn((n, t, e), generator=g, device=DEV) + torch.randn((1, 1, e), generator=g, device=DEV)
+        lg[torch.rand((n, t, e), generator=g, device=DEV) < 1 / 64] = -math.inf      # experts a token may not use
+        lg[torch.rand((n, t), generator=g, device=DEV) < 1 / 32] = -math.inf         # padding tokens
+        lg = lg.to(TORCH[dt])
+        st["logits"] = lg.view(n, t * e)
+        top, pick = torch.topk(lg.float(), c["topk"], -1)
+        hit = torch.zeros((n, t, e), dtype=torch.int32, device=DEV).scatter_(-1, pick, (top > -math.inf).int())
+        st["counts"] = hit.sum(1).int()
+        if c["op"] == "balance":
+            st["total"] = torch.empty((n, e + 1), dtype=torch.int32, device=DEV)
+            st["prob"] = torch.empty((n, e), dtype=torch.float32, device=DEV)
+            st["loss"] = torch.empty((n, 1), dtype=torch.float32, device=DEV)
+            if own:
+                st["ws"] = st["cc"].make_moe_balance_loss_workspace(n, t, e)
+            return st
+        live = (lg > -math.inf).any(-1).sum(1, keepdim=True)
+        total = torch.cat([st["counts"], live], 1)
+        st["total"] = (total.sum(0, keepdim=True).expand(n, -1) if c["summed"] else total).int().contiguous()
+        st["dloss"] = torch.rand((n, 1), generator=g, device=DEV) * 0.01 + 0.005
+        st["base"] = _randn(g, (n, t * e), dt, 1e-4)
+        st["dlogits"] = torch.empty_like(st["base"])
+        return st
+    w = c["width"]
+    per = e // n
+    counts, cap, rows = _plan(c, seed)
+    st.update(counts=counts, cap=cap, rows=rows)
+    keep = torch.zeros((n, e * cap, 1), dtype=torch.bool, device=DEV)
+    for x in range(e):
+        keep[x // per, rows[x]] = True
+
+    def side(width, sigma):                          # an expert-side buffer: zero rows behind the kept ones
+        b = _randn(g, (n, e * cap, width), dt, sigma)
+        b.masked_fill_(~keep, 0)
+        return b
+    x = side(w, 1.0)
+    if c["op"] == "int8":
+        k = c["cols"]
+        st["x"] = x.view(n, -1)
+        q, s = _channels(g, (e, k, w), 1 / math.sqrt(w))
+        st["w"], st["sw"] = q.view(n, -1), s.view(n, -1)
+        st["y"] = torch.zeros((n, e * cap * k), dtype=TORCH[dt], device=DEV)
+        if own:
+            st["q"] = torch.empty((n, e * cap * w), dtype=torch.int8, device=DEV)
+            st["s"] = torch.empty((n, e * cap), dtype=torch.float32, device=DEV)
+            st["ws"] = st["cc"].make_moe_matmul_int8_workspace(counts, cap, w, k)
+        return st
+    h = c["hidden"]
+    if c["op"] == "int8_ffn":
+        st["x"] = x.view(n, -1)
+        for name, shape, fan in (("in", (e, 2 * h, w), w), ("out", (e, w, h), h)):
+            q, s = _channels(g, shape, 1 / math.sqrt(fan))
+            st["w_" + name], st["s_" + name] = q.view(n, -1), s.view(n, -1)
+        st["y"] = torch.zeros((n, e * cap * w), dtype=TORCH[dt], device=DEV)
+        if own:
+            st["ws"] = st["cc"].make_moe_ffn_int8_workspace(counts, cap, w, h, dt)
+        return st
+    st["w_in"] = _randn(g, (n, per * 2 * h * w), dt, 1 / math.sqrt(w))
+    st["w_out"] = _randn(g, (n, per * w * h), dt, 1 / math.sqrt(h))
+    st["dy"] = side(w, 1e-2).view(n, -1)
+    st["dx"] = torch.zeros((n, e * cap * w), dtype=TORCH[dt], device=DEV)
+    st["dw_in"] = torch.empty_like(st["w_in"])
+    st["dw_out"] = torch.empty_like(st["w_out"])
+    row = _layout(w, h)[-1]
+    st["ckpt"] = torch.zeros((n, e * cap * row), dtype=torch.uint8, device=DEV)
+    if c["op"] == "ckpt_step":
+        st["x"] = x.view(n, -1)
+        st["y"] = torch.zeros((n, e * cap * w), dtype=TORCH[dt], device=DEV)
+        if own:
+            st["ws"] = st["cc"].make_moe_ffn_checkpoint_workspace(counts, cap, w, h, dt)
+    else:
+        # the checkpoint that a forward pass left
+        wi = st["w_in"].view(e, 2 * h, w)
+        for i in range(e):
+            if len(rows[i]):
+                j, xe = i // per, x[i // per, rows[i]].float()
+                gu = xe @ wi[i].float().t()
+                st["ckpt"].view(n, e * cap, row)[j, rows[i]] = _kept(xe, gu[:, :h], gu[:, h:])
+    if own:
+        st["wg"] = st["cc"].make_moe_ffn_checkpoint_workspace(counts, cap, w, h, dt, grad=True)
+    return st
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(st):
+    return (_run_own if own else _PLAIN[st["c"]["op"]])(st)
+
+
+def _run_own(st):
+    c, cc = st["c"], st["cc"]
+    op = c["op"]
+    if op == "balance":
+        cc.moe_balance_loss(st["logits"], st["counts"], st["total"], st["prob"], st["loss"], summed=c["summed"],
+                            workspace=st["ws"])
+        return st["loss"], st["total"], st["prob"]
+    if op == "balance_grad":
+        cc.moe_balance_loss_grad(st["logits"], st["total"], st["dloss"], st["dlogits"],
+                                 base=st["base"] if c["accumulate"] else None)
+        return st["dlogits"]
+    if op == "int8":
+        cc.quantize_rows(st["x"], st["q"], st["s"], c["width"])
+        cc.moe_matmul_int8(st["q"], st["s"], st["w"], st["sw"], st["y"], st["counts"], st["cap"], c["width"],
+                           workspace=st["ws"])
+        return st["y"]
+    if op == "int8_ffn":
+        cc.moe_ffn_int8(st["x"], st["w_in"], st["s_in"], st["w_out"], st["s_out"], st["y"], st["counts"], st["cap"],
+                        c["width"], act=c["act"], workspace=st["ws"])
+        return st["y"]
+    if op == "ckpt_step":
+        cc.moe_ffn_checkpoint(st["x"], st["w_in"], st["w_out"], st["ckpt"], st["y"], st["counts"], st["cap"],
+                              c["width"], act=c["act"], workspace=st["ws"])
+    cc.moe_ffn_checkpoint_grad(st["ckpt"], st["w_in"], st["w_out"], st["dy"], st["dx"], st["dw_in"], st["dw_out"],
+                               st["counts"], st["cap"], c["width"], act=c["act"], workspace=st["wg"])
+    grads = st["dx"], st["dw_in"], st["dw_out"]
+    return (st["y"],) + grads if op == "ckpt_step" else grads
+
+
+# ------------------------------------------------------------------ the plain forms
+
+def _masked_softmax(x):
+    top = x.amax(-1, keepdim=True)
+    ex = torch.exp(x - torch.where(top == -math.inf, 0.0, top))
+    s = ex.sum(-1, keepdim=True)
+    return torch.where(s > 0, ex / s, 0.0)
+
+
+def _balance_plain(st):
+    c = st["c"]
+    n, t, e = c["ranks"], c["tokens"], c["experts"]
+    x = st["logits"].view(n, t, e).float()
+    total = torch.cat([st["counts"].long(), (x > -math.inf).any(-1).sum(1, keepdim=True)], 1)
+    p = _masked_softmax(x).sum(1)
+    if c["summed"]:
+        total, p = total.sum(0, keepdim=True).expand(n, -1), p.sum(0, keepdim=True).expand(n, -1)
+    prob = p / total[:, e:].clamp(min=1)
+    f = total[:, :e].float() / total[:, :e].sum(1, keepdim=True).clamp(min=1)
+    return e * (f * prob).sum(1, keepdim=True), total.int(), prob.contiguous()
+
+
+def _balance_grad_plain(st):
+    c = st["c"]
+    n, t, e = c["ranks"], c["tokens"], c["experts"]
+    total = st["total"].view(n, 1, e + 1)
+    f = total[..., :e].float() / total[..., :e].long().sum(-1, keepdim=True).clamp(min=1)
+    p = _masked_softmax(st["logits"].view(n, t, e).float())
+    d = st["dloss"].view(n, 1, 1) * (e / total[..., e:].clamp(min=1).float()) * p * (f - (f * p).sum(-1, keepdim=True))
+    if c["accumulate"]:
+        d = d + st["base"].view(n, t, e).float()
+    return d.to(TORCH[c["dtype"]]).view(n, t * e)
+
+
+def _int8_rows(x):
+    """Rows in 8 bits: the integers nearest x / s, s = max|x| / 127 in 32 bits
+    (the quotients in 64: which integer is nearest must not hang on their rounding)."""
+    s = x.abs().amax(-1, keepdim=True).float() / 127.0
+    q = torch.where(s > 0, torch.round(x.double() / s.double()), 0.0).clamp(-127, 127)
+    return q.to(torch.int8), s[..., 0].contiguous()
+
+
+def _product(q, s, w, sw):
+    return (q.float() @ w.float().t()) * s[:, None] * sw[None, :]
+
+
+def _int8_plain(st):
+    c = st["c"]
+    n, e, w, k, cap = c["ranks"], c["experts"], c["width"], c["cols"], st["cap"]
+    x, wt, sw = st["x"].view(n, e * cap, w), st["w"].view(e, k, w), st["sw"].view(e, k)
+    y = torch.zeros((n, e * cap, k), dtype=TORCH[c["dtype"]], device=x.device)
+    for i in range(e):
+        j, rows = i * n // e, st["rows"][i]
+        if len(rows):
+            q, s = _int8_rows(x[j, rows].float())
+            y[j, rows] = _product(q, s, wt[i], sw[i]).to(y.dtype)
+    return y.view(n, -1)
+
+
+def _int8_ffn_plain(st):
+    c = st["c"]
+    n, e, w, h, cap = c["ranks"], c["experts"], c["width"], c["hidden"], st["cap"]
+    x, wi, wo = st["x"].view(n, e * cap, w), st["w_in"].view(e, 2 * h, w), st["w_out"].view(e, w, h)
+    si, so = st["s_in"].view(e, 2 * h), st["s_out"].view(e, w)
+    y = torch.zeros((n, e * cap, w), dtype=TORCH[c["dtype"]], device=x.device)
+    for i in range(e):
+        j, rows = i * n // e, st["rows"][i]
+        if len(rows):
+            q, s = _int8_rows(x[j, rows].float())
+            gu = _product(q, s, wi[i], si[i])
+            # the block's definition: the rows that the second product quantises are of the buffers' type
+            q, s = _int8_rows((_act(gu[:, :h], c["act"]) * gu[:, h:]).to(y.dtype).float())
+            y[j, rows] = _product(q, s, wo[i], so[i]).to(y.dtype)
+    return y.view(n, -1)
+
+
+def _act(g, act):
+    if act == "silu":
+        return g / (1 + torch.exp(-g))
+    return 0.5 * g * (1 + torch.erf(g * math.sqrt(0.5)))
+
+
+def _dact(g, act):
+    if act == "silu":
+        s = 1 / (1 + torch.exp(-g))
+        return s * (1 + g * (1 - s))
+    return 0.5 * (1 + torch.erf(g * math.sqrt(0.5))) + g * torch.exp(-0.5 * g * g) * (1 / math.sqrt(2 * math.pi))
+
+
+def _layout(w, h):
+    """Byte offsets of a checkpoint row's parts -- x, gate, up, their blocks' exponents -- and its length."""
+    up = lambda v: -(-v // 16) * 16  # noqa: E731
+    at = [0, up(w), up(w) + up(h), up(w) + 2 * up(h)]
+    at += [at[3] + _blocks(w), at[3] + _blocks(w) + _blocks(h)]
+    return at + [up(at[5] + _blocks(h))]
+
+
+def _pack(v):
+    """Rows of v in 8 bits, a power of two for each 32 elements: integers and exponents + 127."""
+    r, n = v.shape
+    b = torch.zeros((r, _blocks(n), BLOCK), dtype=v.dtype, device=v.device)
+    b.view(r, -1)[:, :n] = v
+    top = b.abs().amax(-1)
+    m, ex = torch.frexp(top)                              # top = m 2^ex, m in [1/2, 1)
+    ex = torch.where(m * 128 >= 127.5, ex + 1, ex) - 7    # the least that rounds to at most 127
+    ex = torch.where(top > 0, ex.clamp(-126, 121), -126)
+    q = torch.round(torch.ldexp(b, -ex[..., None])).clamp(-127, 127)
+    return q.view(r, -1)[:, :n].to(torch.int8), (ex + 127).to(torch.uint8)
+
+
+def _unpack(q, ex, dtype=torch.float32):
+    s = torch.ldexp(torch.ones_like(ex, dtype=dtype), ex.int() - 127)
+    return q.to(dtype) * s.repeat_interleave(BLOCK, -1)[:, :q.shape[1]]
+
+
+def _kept(x, g, u):
+    """The checkpoint rows of x, g and u, as bytes."""
+    at = _layout(x.shape[1], g.shape[1])
+    row = torch.zeros((x.shape[0], at[-1]), dtype=torch.uint8, device=x.device)
+    for k, v in enumerate((x, g, u)):
+        q, ex = _pack(v)
+        row[:, at[k]:at[k] + q.shape[1]] = q.view(torch.uint8)
+        row[:, at[k + 3]:at[k + 3] + ex.shape[1]] = ex
+    return row
+
+
+def _held(row, w, h, dtype=torch.float32):
+    """x, g and u as checkpoint rows hold them."""
+    at, out = _layout(w, h), []
+    for k, n in enumerate((w, h, h)):
+        out.append(_unpack(row[:, at[k]:at[k] + n].contiguous().view(torch.int8), row[:, at[k + 3]:at[k + 3] + _blocks(n)], dtype))
+    return out
+
+
+def _ckpt_forward_plain(st):
+    c = st["c"]
+    n, e, w, h, cap = c["ranks"], c["experts"], c["width"], c["hidden"], st["cap"]
+    x, wi, wo = st["x"].view(n, e * cap, w), st["w_in"].view(e, 2 * h, w), st["w_out"].view(e, w, h)
+    y, ckpt = torch.zeros_like(x), st["ckpt"].view(n, e * cap, -1)
+    for i in range(e):
+        j, rows = i * n // e, st["rows"][i]
+        if len(rows):
+            xe = x[j, rows].float()
+            gu = xe @ wi[i].float().t()
+            ckpt[j, rows] = _kept(xe, gu[:, :h], gu[:, h:])
+            y[j, rows] = ((_act(gu[:, :h], c["act"]) * gu[:, h:]) @ wo[i].float().t()).to(y.dtype)
+    return y.view(n, -1)
+
+
+def _ckpt_grad_plain(st):
+    c = st["c"]
+    n, e, w, h, cap = c["ranks"], c["experts"], c["width"], c["hidden"], st["cap"]
+    dy, ckpt = st["dy"].view(n, e * cap, w), st["ckpt"].view(n, e * cap, -1)
+    wi, wo = st["w_in"].view(e, 2 * h, w), st["w_out"].view(e, w, h)
+    dx, dwi, dwo = torch.zeros_like(dy), torch.zeros_like(wi), torch.zeros_like(wo)
+    for i in range(e):
+        j, rows = i * n // e, st["rows"][i]
+        if len(rows):
+            xe, g, u = _held(ckpt[j, rows], w, h)
+            de, a = dy[j, rows].float(), _act(g, c["act"])
+            dh = de @ wo[i].float()
+            dgu = torch.cat([dh * u * _dact(g, c["act"]), dh * a], 1)
+            dwo[i] = (de.t() @ (a * u)).to(wo.dtype)
+            dwi[i] = (dgu.t() @ xe).to(wi.dtype)
+            dx[j, rows] = (dgu @ wi[i].float()).to(dx.dtype)
+    return dx.view(n, -1), dwi.view(n, -1), dwo.view(n, -1)
+
+
+def _ckpt_step_plain(st):
+    return (_ckpt_forward_plain(st),) + _ckpt_grad_plain(st)
+
+
+_PLAIN = {"balance": _balance_plain, "balance_grad": _balance_grad_plain, "int8": _int8_plain,
+          "int8_ffn": _int8_ffn_plain, "ckpt_step": _ckpt_step_plain, "ckpt_grad": _ckpt_grad_plain}
+
+
+# ------------------------------------------------------------------ the definitions in 64 bits
+
+def _probabilities64(st, c):
+    """Softmax rows of the logits in float64 [n, t, e]; a row of -inf gives zeros."""
+    z = st["logits"].view(c["ranks"], c["tokens"], c["experts"]).double()
+    dead = torch.isneginf(z).all(-1, keepdim=True)
+    return torch.where(dead, 0.0, torch.softmax(torch.where(dead, 0.0, z), -1)), ~dead[..., 0]
+
+
+def _exact_balance(st, c):
+    n, e = c["ranks"], c["experts"]
+    p, live = _probabilities64(st, c)
+    each = [(st["counts"][r].long(), int(live[r].sum()), p[r].sum(0)) for r in range(n)]
+    if c["summed"]:
+        each = [tuple(sum(a[k] for a in each) for k in range(3))] * n
+    loss, total, prob = [], [], []
+    for cnt, tok, s in each:
+        mean = s / max(tok, 1)
+        loss.append(e * (cnt.double() @ mean) / max(int(cnt.sum()), 1))
+        total.append(torch.cat([cnt, cnt.new_tensor([tok])]))
+        prob.append(mean)
+    return torch.stack(loss).view(n, 1), torch.stack(total).int(), torch.stack(prob)
+
+
+def _exact_balance_grad(st, c):
+    n, t, e = c["ranks"], c["tokens"], c["experts"]
+    p, _ = _probabilities64(st, c)
+    out = torch.zeros((n, t, e), dtype=torch.float64, device=DEV)
+    for r in range(n):
+        cnt, tok = st["total"][r, :e].double(), int(st["total"][r, e])
+        f = cnt / max(float(cnt.sum()), 1.0)
+        out[r] = float(st["dloss"][r, 0]) * e / max(tok, 1) * p[r] * (f - torch.mv(p[r], f)[:, None])
+    if c["accumulate"]:
+        out += st["base"].view(n, t, e).double()
+    return out.view(n, -1)
+
+
+def _nearest64(v):
+    """Rows of v (float64) as integers (float64) and their 32-bit scales."""
+    s = (v.abs().max(1).values.float() / 127).double()
+    return torch.round(v / torch.where(s > 0, s, 1.0)[:, None]) * (s > 0)[:, None], s
+
+
+def _exact_int8(st, c):
+    n, e, w, k, cap = c["ranks"], c["experts"], c["width"], c["cols"], st["cap"]
+    y = torch.zeros((n, e * cap, k), dtype=torch.float64, device=DEV)
+    for i in range(e):
+        j, rows = i // (e // n), st["rows"][i]
+        if len(rows):
+            q, s = _nearest64(st["x"][j].view(-1, w).index_select(0, rows).double())
+            wt = st["w"].view(e, k, w)[i].double() * st["sw"].view(e, k, 1)[i].double()
+            y[j, rows] = torch.mm(q * s[:, None], wt.t())
+    return y.view(n, -1)
+
+
+def _gate64(g, act):
+    """The activation and its derivative at g, in float64."""
+    if act == "silu":
+        s = torch.sigmoid(g)
+        return g * s, s + g * s * (1 - s)
+    cdf = 0.5 * torch.special.erfc(-g / math.sqrt(2.0))
+    return g * cdf, cdf + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+
+
+def _exact_int8_ffn(st, c):
+    n, e, w, h, cap = c["ranks"], c["experts"], c["width"], c["hidden"], st["cap"]
+    y = torch.zeros((n, e * cap, w), dtype=torch.float64, device=DEV)
+    for i in range(e):
+        j, rows = i // (e // n), st["rows"][i]
+        if len(rows) == 0:
+            continue
+        q, s = _nearest64(st["x"][j].view(-1, w).index_select(0, rows).double())
+        wi = st["w_in"].view(e, 2, h, w)[i].double() * st["s_in"].view(e, 2, h, 1)[i].double()
+        x = q * s[:, None]
+        a = _gate64(torch.mm(x, wi[0].t()), c["act"])[0] * torch.mm(x, wi[1].t())
+        q, s = _nearest64(a.to(TORCH[c["dtype"]]).double())
+        wo = st["w_out"].view(e, w, h)[i].double() * st["s_out"].view(e, w, 1)[i].double()
+        y[j, rows] = torch.mm(q * s[:, None], wo.t())
+    return y.view(n, -1)
+
+
+def _through64(v):
+    """v [r, n] (float64) as an 8-bit checkpoint holds it."""
+    r, n = v.shape
+    b = torch.nn.functional.pad(v, (0, -n % BLOCK)).view(r, -1, BLOCK)
+    top = b.abs().max(-1, keepdim=True).values
+    ex = torch.floor(torch.log2(top.clamp(min=2.0 ** -120))) - 6
+    ex = torch.where(top >= torch.exp2(ex) * 127.5, ex + 1, ex)
+    step = torch.exp2(ex.clamp(-126, 121))
+    return (torch.round(b / step) * step).view(r, -1)[:, :n]
+
+
+def _exact_ckpt(st, c):
+    n, e, w, h, cap = c["ranks"], c["experts"], c["width"], c["hidden"], st["cap"]
+    step = c["op"] == "ckpt_step"
+    y, dx = (torch.zeros((n, e * cap, w), dtype=torch.float64, device=DEV) for _ in range(2))
+    dwi = torch.zeros((e, 2, h, w), dtype=torch.float64, device=DEV)
+    dwo = torch.zeros((e, w, h), dtype=torch.float64, device=DEV)
+    for i in range(e):
+        j, rows = i // (e // n), st["rows"][i]
+        if len(rows) == 0:
+            continue
+        gate, up = st["w_in"].view(e, 2, h, w)[i].double()
+        wo = st["w_out"].view(e, w, h)[i].double()
+        if step:
+            x = st["x"][j].view(-1, w).index_select(0, rows).double()
+            g, u = torch.mm(x, gate.t()), torch.mm(x, up.t())
+            y[j, rows] = torch.mm(_gate64(g, c["act"])[0] * u, wo.t())
+            x, g, u = _through64(x), _through64(g), _through64(u)
+        else:
+            x, g, u = _held(st["ckpt"][j].view(e * cap, -1).index_select(0, rows), w, h, torch.float64)
+        de = st["dy"][j].view(-1, w).index_select(0, rows).double()
+        a, da = _gate64(g, c["act"])
+        dh = torch.mm(de, wo)
+        dg, du = dh * u * da, dh * a
+        dwo[i] = torch.mm(de.t(), a * u)
+        dwi[i, 0], dwi[i, 1] = torch.mm(dg.t(), x), torch.mm(du.t(), x)
+        dx[j, rows] = torch.mm(dg, gate) + torch.mm(du, up)
+    grads = dx.view(n, -1), dwi.view(n, -1), dwo.view(n, -1)
+    return (y.view(n, -1),) + grads if step else grads
+
+
+def exact(c, seed):
+    st = prepare(c, seed)
+    op = c["op"]
+    if op.startswith("ckpt"):
+        return _exact_ckpt(st, c)
+    return {"balance": _exact_balance, "balance_grad": _exact_balance_grad, "int8": _exact_int8,
+            "int8_ffn": _exact_int8_ffn}[op](st, c)
