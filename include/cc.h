@@ -671,6 +671,114 @@ cc_status_t cc_moe_ffn_grad(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_ou
 cc_status_t cc_moe_ffn_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width, size_t hidden,
                                       cc_dtype_t dtype, int nranks, int grad, size_t* bytes);
 
+/* ---- The loss that keeps the router's experts evenly used.  Over a batch's T
+ * tokens with a logit other than -inf (a token without any is padding), with C_e
+ * the rows that cc_moe_route gave expert e, S their sum (0: f_e = 0) and p_t the
+ * softmax of token t's logits over all experts,
+ *   f_e = C_e / S,  P_e = (1 / T) sum_t p_te,  loss = E sum_e f_e P_e,
+ * 1 where either is even.  A batch is each rank's own tokens, or with `summed` 1
+ * all ranks' (f and P over the whole data-parallel batch: the AllReduce of both
+ * and the loss in one call), whose results every rank gets.
+ *  logits [tokens][nexperts] of dtype, counts [nexperts] int32, as in
+ *    cc_moe_route;
+ *  total [nexperts + 1] int32: the batch's C_e, then T;
+ *  prob [nexperts] float32: P_e (0 where T is 0);
+ *  loss [1] float32.
+ * A logit that is NaN or +inf makes prob and loss of its batch NaN.  Fewer than
+ * 2^24 tokens a rank.  Takes a workspace (cc_moe_balance_loss_workspace_size). */
+cc_status_t cc_moe_balance_loss(cc_rankbuf_t logits, cc_rankbuf_t counts, cc_rankbuf_t total, cc_rankbuf_t prob,
+                                cc_rankbuf_t loss, size_t tokens, int nexperts, int summed, cc_dtype_t dtype,
+                                int nranks, const cc_config_t* cfg, cc_stream_t stream);
+cc_status_t cc_moe_balance_loss_workspace_size(int nranks, size_t tokens, int nexperts, size_t* bytes);
+
+/* Its gradient, with `total` as the call above left it (the counts have none):
+ *   dlogits_te = base_te + dloss (E / T) p_te (f_e - sum_j f_j p_tj),
+ * rounded once to dtype.  dloss [1] float32 of each rank is the gradient of the
+ * loss that the rank holds.  base (dtype, laid out as logits; base.base NULL:
+ * zeros) is the gradient that cc_moe_route_grad gave, say; in place iff
+ * base.base == dlogits.base with equal strides.  A padding token's row is base
+ * (0 without); NaN in a row whose logits hold a NaN or +inf.  Takes no workspace. */
+cc_status_t cc_moe_balance_loss_grad(cc_rankbuf_t logits, cc_rankbuf_t total, cc_rankbuf_t dloss, cc_rankbuf_t base,
+                                     cc_rankbuf_t dlogits, size_t tokens, int nexperts, cc_dtype_t dtype, int nranks,
+                                     const cc_config_t* cfg, cc_stream_t stream);
+
+/* ---- Products of 8-bit integers with a scale for each token and each channel,
+ * for experts that serve.  A row v (a token, or a channel: a row of a weight
+ * matrix) is kept as
+ *   s = max|v| / 127 rounded to float32,  q = the integer nearest v / s (ties to even),
+ * cut to [-127, 127] (only where s is subnormal, and so inexact); s = 0 and q = 0
+ * for a row of zeros, s = NaN and q = 0 for one that holds a NaN or an infinity.
+ * x: `rows` rows of `width` elements of dtype a rank; q [rows][width] int8,
+ * scales [rows] float32.  Quantised before the dispatch, a row is a quarter of
+ * its float32 bytes on the wire: rows of a multiple of 4 elements pass
+ * cc_moe_dispatch_padded as CC_INT32 with width / 4 elements a row, their scales
+ * as CC_FLOAT32 with one.  rows and width below 2^31.  Takes no workspace. */
+cc_status_t cc_quantize_rows(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t scales, size_t rows, size_t width,
+                             cc_dtype_t dtype, int nranks, const cc_config_t* cfg, cc_stream_t stream);
+
+/* The experts' product of quantised rows and weights, on the expert side of
+ * cc_moe_dispatch_padded: for the kept rows x of every expert
+ *   y_c = (sum_k x_k w_ck) sx sw_c,
+ * the sum exact in int32, then float32 with one rounding a step (the sum, times
+ * sx, times sw_c), rounded once to dtype.  x: E * capacity rows of `width` int8 a
+ * rank, sx their float32 scales; rank j's weights w [cols][width] int8 and
+ * scales sw [cols] float32, one local expert after the other; y: E * capacity rows of
+ * `cols` elements of dtype.  counts, nexperts, capacity and the limits on
+ * rows as in cc_moe_ffn; width below 2^17, so that no sum overflows.  Rows behind a
+ * block's kept ones are neither read nor written.  Takes a workspace. */
+cc_status_t cc_moe_matmul_int8(cc_rankbuf_t x, cc_rankbuf_t sx, cc_rankbuf_t w, cc_rankbuf_t sw, cc_rankbuf_t y,
+                               const size_t* counts, int nexperts, size_t capacity, size_t width, size_t cols,
+                               cc_dtype_t dtype, int nranks, const cc_config_t* cfg, cc_stream_t stream);
+cc_status_t cc_moe_matmul_int8_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width,
+                                              size_t cols, int nranks, size_t* bytes);
+
+/* cc_moe_ffn with both products in 8-bit integers: x, y as there (dtype), w_in
+ * [2 * hidden][width] and w_out [width][hidden] int8 with a float32 scale a row,
+ * s_in [2 * hidden] and s_out [width], one local expert after the other.  The kept
+ * rows x are quantised as by cc_quantize_rows, g and u are the float32 products,
+ * h = act(g) * u is rounded to dtype and its rows are quantised likewise.  width
+ * and hidden below 2^17. */
+cc_status_t cc_moe_ffn_int8(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t s_in, cc_rankbuf_t w_out,
+                            cc_rankbuf_t s_out, cc_rankbuf_t y, const size_t* counts, int nexperts, size_t capacity,
+                            size_t width, size_t hidden, cc_act_t act, cc_dtype_t dtype, int nranks,
+                            const cc_config_t* cfg, cc_stream_t stream);
+cc_status_t cc_moe_ffn_int8_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width,
+                                           size_t hidden, cc_dtype_t dtype, int nranks, size_t* bytes);
+
+/* ---- cc_moe_ffn and its gradients with the activations kept in 8 bits: in place
+ * of x and pre, the backward pass reads one checkpoint, 33/32 bytes an element.
+ * Every CC_CKPT_BLOCK consecutive elements of a row's x, g or u (blocks from
+ * element 0, the last one possibly short) share a power of two 2^e, the least for
+ * which the largest of them rounds to at most 127 (e at least -126 and at most 121),
+ * and are kept as the integers nearest v / 2^e, ties to even, cut to [-127, 127].
+ * g and u are taken from the product's float32 sums.  A block that holds a NaN or
+ * an infinity stands for NaN in all its elements.
+ * ckpt: E * capacity rows a rank in x's layout, each of
+ * cc_moe_ffn_checkpoint_row bytes: the int8 values of x, of g and of u, each from
+ * a multiple of 16 bytes, then the blocks' exponents of x, of g and of u, a byte
+ * e + 127 each (255: NaN), back to back.  Base and rank stride are multiples of
+ * 16 bytes.  Rows behind a block's kept ones are neither read nor written, nor are
+ * the bytes between a row's parts.
+ * y, and every other argument, is that of cc_moe_ffn. */
+#define CC_CKPT_BLOCK 32
+cc_status_t cc_moe_ffn_checkpoint(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t ckpt,
+                                  cc_rankbuf_t y, const size_t* counts, int nexperts, size_t capacity, size_t width,
+                                  size_t hidden, cc_act_t act, cc_dtype_t dtype, int nranks, const cc_config_t* cfg,
+                                  cc_stream_t stream);
+
+/* The gradients of cc_moe_ffn (cc_moe_ffn_grad) at the x, g and u that the
+ * checkpoint stands for; h is computed from g and u again. */
+cc_status_t cc_moe_ffn_checkpoint_grad(cc_rankbuf_t ckpt, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t dy,
+                                       cc_rankbuf_t dx, cc_rankbuf_t dw_in, cc_rankbuf_t dw_out, const size_t* counts,
+                                       int nexperts, size_t capacity, size_t width, size_t hidden, cc_act_t act,
+                                       cc_dtype_t dtype, int nranks, const cc_config_t* cfg, cc_stream_t stream);
+
+/* Bytes of a checkpoint row (width and hidden below 2^24), and the workspace of
+ * the two calls (grad 0 and 1). */
+cc_status_t cc_moe_ffn_checkpoint_row(size_t width, size_t hidden, size_t* bytes);
+cc_status_t cc_moe_ffn_checkpoint_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width,
+                                                 size_t hidden, cc_dtype_t dtype, int nranks, int grad, size_t* bytes);
+
 const char* cc_status_string(cc_status_t status);
 const char* cc_last_error(void);
 const char* cc_version(void);

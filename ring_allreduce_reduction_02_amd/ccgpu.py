@@ -138,6 +138,29 @@ EXPORTS = {
                        + [ctypes.c_int] * 3 + [ctypes.POINTER(Config), ctypes.c_void_p],
     "cc_moe_ffn_workspace_size": [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
                                  + [ctypes.c_int] * 3 + [ctypes.POINTER(ctypes.c_size_t)],
+    "cc_moe_balance_loss": [RankBuf] * 5 + [ctypes.c_size_t] + [ctypes.c_int] * 4 + [ctypes.POINTER(Config),
+                                                                                    ctypes.c_void_p],
+    "cc_moe_balance_loss_workspace_size": [ctypes.c_int, ctypes.c_size_t, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
+    "cc_moe_balance_loss_grad": [RankBuf] * 5 + [ctypes.c_size_t] + [ctypes.c_int] * 3 + [ctypes.POINTER(Config),
+                                                                                         ctypes.c_void_p],
+    "cc_quantize_rows": [RankBuf] * 3 + [ctypes.c_size_t] * 2 + [ctypes.c_int] * 2 + [ctypes.POINTER(Config),
+                                                                                     ctypes.c_void_p],
+    "cc_moe_matmul_int8": [RankBuf] * 5 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                          + [ctypes.c_int] * 2 + [ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_moe_matmul_int8_workspace_size": [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                                         + [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
+    "cc_moe_ffn_int8": [RankBuf] * 6 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                       + [ctypes.c_int] * 3 + [ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_moe_ffn_int8_workspace_size": [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                                      + [ctypes.c_int] * 2 + [ctypes.POINTER(ctypes.c_size_t)],
+    "cc_moe_ffn_checkpoint": [RankBuf] * 5 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                             + [ctypes.c_int] * 3 + [ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_moe_ffn_checkpoint_grad": [RankBuf] * 7 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int]
+                                  + [ctypes.c_size_t] * 3 + [ctypes.c_int] * 3 + [ctypes.POINTER(Config),
+                                                                                  ctypes.c_void_p],
+    "cc_moe_ffn_checkpoint_row": [ctypes.c_size_t, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)],
+    "cc_moe_ffn_checkpoint_workspace_size": [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                                            + [ctypes.c_int] * 3 + [ctypes.POINTER(ctypes.c_size_t)],
     "cc_status_string": [ctypes.c_int],
     "cc_last_error": [],
     "cc_version": [],
@@ -756,6 +779,193 @@ def moe_ffn_grad(x, w_in, w_out, pre, dy, dx, dw_in, dw_out, counts: Sequence[Se
             c.operand(dw_out, "dw_out", N, wo, dt))
     _check(load().cc_moe_ffn_grad(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N, c.cfg,
                                   c.stream))
+
+
+def moe_balance_loss_workspace_size(nranks: int, tokens: int, nexperts: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().cc_moe_balance_loss_workspace_size(nranks, tokens, nexperts, ctypes.byref(out)))
+    return out.value
+
+
+def make_moe_balance_loss_workspace(nranks: int, tokens: int, nexperts: int, device="cuda"):
+    """Allocate (with torch) the workspace of moe_balance_loss."""
+    import torch
+    return torch.empty(moe_balance_loss_workspace_size(nranks, tokens, nexperts), dtype=torch.uint8, device=device)
+
+
+def moe_balance_loss(logits, counts, total, prob, loss, summed: bool = True, workspace=None, stream=None) -> None:
+    """loss (f32) [N, 1] of logits [N, T * E] and the router's counts (int32)
+    [N, E], over all ranks' tokens (summed) or each rank's own; total (int32)
+    [N, E + 1]: the counts of the batch and its tokens, prob (f32) [N, E]: its
+    mean probabilities."""
+    import torch
+    N, E = counts.shape
+    T, c = _rows(logits, E, "logits"), _Call(stream, workspace)
+    _check(load().cc_moe_balance_loss(c.operand(logits, "logits", N, T * E),
+                                      c.operand(counts, "counts", N, E, torch.int32),
+                                      c.operand(total, "total", N, E + 1, torch.int32),
+                                      c.operand(prob, "prob", N, E, torch.float32),
+                                      c.operand(loss, "loss", N, 1, torch.float32), T, E, 1 if summed else 0,
+                                      DTYPES[dtype_name(logits)], N, c.cfg, c.stream))
+
+
+def moe_balance_loss_grad(logits, total, dloss, dlogits, base=None, stream=None) -> None:
+    """dlogits [N, T * E] = base (None: 0; may be dlogits) + the gradient from
+    dloss (f32) [N, 1], with total as moe_balance_loss left it."""
+    import torch
+    if total.dim() != 2 or total.shape[1] < 2:
+        raise ValueError("total must be [nranks, nexperts + 1]")
+    N, E = total.shape[0], total.shape[1] - 1
+    T, c = _rows(logits, E, "logits"), _Call(stream)
+    _check(load().cc_moe_balance_loss_grad(c.operand(logits, "logits", N, T * E),
+                                           c.operand(total, "total", N, E + 1, torch.int32),
+                                           c.operand(dloss, "dloss", N, 1, torch.float32),
+                                           RankBuf(None, 0) if base is None
+                                           else c.operand(base, "base", N, T * E, logits.dtype),
+                                           c.operand(dlogits, "dlogits", N, T * E, logits.dtype), T, E,
+                                           DTYPES[dtype_name(logits)], N, c.cfg, c.stream))
+
+
+def quantize_rows(x, q, scales, width: int, stream=None) -> None:
+    """Rows of `width` elements of x [N, R * width] as int8 q [N, R * width] and a
+    scale each (f32) [N, R]: tokens, or the rows (channels) of weights."""
+    import torch
+    N, R, c = x.shape[0], _rows(x, width, "x"), _Call(stream)
+    _check(load().cc_quantize_rows(c.operand(x, "x", N, R * width), c.operand(q, "q", N, R * width, torch.int8),
+                                   c.operand(scales, "scales", N, R, torch.float32), R, width,
+                                   DTYPES[dtype_name(x)], N, c.cfg, c.stream))
+
+
+def _counts(counts):
+    """(N, E, the counts as an array) of a call on the expert side."""
+    N, E = len(counts), len(counts[0]) if len(counts) else 0
+    arr = _sizes(counts, N, E, "counts")
+    if E < N or N < 1 or E % N:
+        raise ValueError(f"{E} experts are not a multiple of {N} ranks")
+    return N, E, arr
+
+
+def moe_matmul_int8_workspace_size(counts: Sequence[Sequence[int]], capacity: int, width: int, cols: int) -> int:
+    N, E, arr = _counts(counts)
+    out = ctypes.c_size_t(0)
+    _check(load().cc_moe_matmul_int8_workspace_size(arr, E, capacity, width, cols, N, ctypes.byref(out)))
+    return out.value
+
+
+def make_moe_matmul_int8_workspace(counts, capacity: int, width: int, cols: int, device="cuda"):
+    """Allocate (with torch) the workspace of moe_matmul_int8."""
+    import torch
+    return torch.empty(moe_matmul_int8_workspace_size(counts, capacity, width, cols), dtype=torch.uint8, device=device)
+
+
+def moe_matmul_int8(x, sx, w, sw, y, counts: Sequence[Sequence[int]], capacity: int, width: int, workspace=None,
+                    stream=None) -> None:
+    """The experts' product in 8-bit integers on the expert side of
+    moe_dispatch_padded: x int8 [N, E * capacity * width] with a scale a row, sx (f32)
+    [N, E * capacity], w int8 [N, E/N * cols * width] with sw (f32) [N, E/N * cols],
+    y [N, E * capacity * cols]."""
+    import torch
+    N, E, arr = _counts(counts)
+    cols, c = _rows(sw, E // N, "sw"), _Call(stream, workspace)
+    _check(load().cc_moe_matmul_int8(c.operand(x, "x", N, E * capacity * width, torch.int8),
+                                     c.operand(sx, "sx", N, E * capacity, torch.float32),
+                                     c.operand(w, "w", N, E // N * cols * width, torch.int8),
+                                     c.operand(sw, "sw", N, E // N * cols, torch.float32),
+                                     c.operand(y, "y", N, E * capacity * cols), arr, E, capacity, width, cols,
+                                     DTYPES[dtype_name(y)], N, c.cfg, c.stream))
+
+
+def moe_ffn_int8_workspace_size(counts: Sequence[Sequence[int]], capacity: int, width: int, hidden: int,
+                                dtype: str) -> int:
+    N, E, arr = _counts(counts)
+    out = ctypes.c_size_t(0)
+    _check(load().cc_moe_ffn_int8_workspace_size(arr, E, capacity, width, hidden, DTYPES[dtype], N, ctypes.byref(out)))
+    return out.value
+
+
+def make_moe_ffn_int8_workspace(counts, capacity: int, width: int, hidden: int, dtype: str, device="cuda"):
+    """Allocate (with torch) the workspace of moe_ffn_int8."""
+    import torch
+    n = moe_ffn_int8_workspace_size(counts, capacity, width, hidden, dtype)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_ffn_int8(x, w_in, s_in, w_out, s_out, y, counts: Sequence[Sequence[int]], capacity: int, width: int,
+                 act: str = "silu", workspace=None, stream=None) -> None:
+    """moe_ffn with both products in 8-bit integers: x, y as there, w_in int8
+    [N, E/N * 2 * hidden * width] with s_in (f32) [N, E/N * 2 * hidden], w_out int8
+    [N, E/N * width * hidden] with s_out (f32) [N, E/N * width]."""
+    import torch
+    N, E, arr = _counts(counts)
+    per = E // N
+    hidden, c, side = _rows(w_out, per * width, "w_out"), _Call(stream, workspace), E * capacity * width
+    args = (c.operand(x, "x", N, side), c.operand(w_in, "w_in", N, per * 2 * hidden * width, torch.int8),
+            c.operand(s_in, "s_in", N, per * 2 * hidden, torch.float32),
+            c.operand(w_out, "w_out", N, per * width * hidden, torch.int8),
+            c.operand(s_out, "s_out", N, per * width, torch.float32), c.operand(y, "y", N, side, x.dtype))
+    _check(load().cc_moe_ffn_int8(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N, c.cfg,
+                                  c.stream))
+
+
+def moe_ffn_checkpoint_row(width: int, hidden: int) -> int:
+    """Bytes of a row of an 8-bit checkpoint."""
+    out = ctypes.c_size_t(0)
+    _check(load().cc_moe_ffn_checkpoint_row(width, hidden, ctypes.byref(out)))
+    return out.value
+
+
+def make_moe_ffn_checkpoint(counts, capacity: int, width: int, hidden: int, device="cuda"):
+    """Allocate (with torch) a checkpoint of moe_ffn_checkpoint."""
+    import torch
+    N, E, _ = _counts(counts)
+    return torch.empty((N, E * capacity * moe_ffn_checkpoint_row(width, hidden)), dtype=torch.uint8, device=device)
+
+
+def moe_ffn_checkpoint_workspace_size(counts: Sequence[Sequence[int]], capacity: int, width: int, hidden: int,
+                                      dtype: str, grad: bool = False) -> int:
+    N, E, arr = _counts(counts)
+    out = ctypes.c_size_t(0)
+    _check(load().cc_moe_ffn_checkpoint_workspace_size(arr, E, capacity, width, hidden, DTYPES[dtype], N,
+                                                       int(bool(grad)), ctypes.byref(out)))
+    return out.value
+
+
+def make_moe_ffn_checkpoint_workspace(counts, capacity: int, width: int, hidden: int, dtype: str, grad: bool = False,
+                                      device="cuda"):
+    """Allocate (with torch) the workspace of moe_ffn_checkpoint (or its gradient)."""
+    import torch
+    n = moe_ffn_checkpoint_workspace_size(counts, capacity, width, hidden, dtype, grad)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_ffn_checkpoint(x, w_in, w_out, ckpt, y, counts: Sequence[Sequence[int]], capacity: int, width: int,
+                       act: str = "silu", workspace=None, stream=None) -> None:
+    """moe_ffn that keeps x and the pre-activations in 8 bits: ckpt uint8
+    [N, E * capacity * moe_ffn_checkpoint_row(width, hidden)]."""
+    import torch
+    N, E, hidden, side, arr = _ffn_operands(x, w_in, w_out, counts, capacity, width)
+    per, dt, c = E // N, x.dtype, _Call(stream, workspace)
+    args = (c.operand(x, "x", N, side), c.operand(w_in, "w_in", N, per * 2 * hidden * width, dt),
+            c.operand(w_out, "w_out", N, per * width * hidden, dt),
+            c.operand(ckpt, "ckpt", N, E * capacity * moe_ffn_checkpoint_row(width, hidden), torch.uint8),
+            c.operand(y, "y", N, side, dt))
+    _check(load().cc_moe_ffn_checkpoint(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N,
+                                        c.cfg, c.stream))
+
+
+def moe_ffn_checkpoint_grad(ckpt, w_in, w_out, dy, dx, dw_in, dw_out, counts: Sequence[Sequence[int]], capacity: int,
+                            width: int, act: str = "silu", workspace=None, stream=None) -> None:
+    """The gradients of moe_ffn from dy, at what moe_ffn_checkpoint kept."""
+    import torch
+    N, E, hidden, side, arr = _ffn_operands(dy, w_in, w_out, counts, capacity, width)
+    per, dt, c = E // N, dy.dtype, _Call(stream, workspace)
+    wi, wo = per * 2 * hidden * width, per * width * hidden
+    args = (c.operand(ckpt, "ckpt", N, E * capacity * moe_ffn_checkpoint_row(width, hidden), torch.uint8),
+            c.operand(w_in, "w_in", N, wi, dt), c.operand(w_out, "w_out", N, wo, dt), c.operand(dy, "dy", N, side, dt),
+            c.operand(dx, "dx", N, side, dt), c.operand(dw_in, "dw_in", N, wi, dt),
+            c.operand(dw_out, "dw_out", N, wo, dt))
+    _check(load().cc_moe_ffn_checkpoint_grad(*args, arr, E, capacity, width, hidden, ACTS[act],
+                                             DTYPES[dtype_name(dy)], N, c.cfg, c.stream))
 
 
 def raw(fn: str, *args):

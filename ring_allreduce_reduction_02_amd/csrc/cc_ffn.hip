@@ -162,28 +162,28 @@ __global__ __launch_bounds__(256) void k_ffn_copy(CopyArgs a) {
   }
 }
 
-hipError_t plan(const FfnLaunch& L) {
+hipError_t plan(const FfnShape& s, const FfnWs& o, char* ws, const uint32_t* kept, hipStream_t st) {
   PlanArgs a;
-  const int n = L.s.N * L.s.E;
+  const int n = s.N * s.E;
   a.kept = nullptr;
   if (n <= kPlanCounts) {
-    for (int i = 0; i < n; ++i) a.v[i] = L.kept[i];
+    for (int i = 0; i < n; ++i) a.v[i] = kept[i];
   } else {
-    uint32_t* to = (uint32_t*)(L.ws + L.o.kept);
+    uint32_t* to = (uint32_t*)(ws + o.kept);
     for (int i = 0; i < n; i += kPlanCounts) {
       PutArgs p;
       p.n = n - i < kPlanCounts ? n - i : kPlanCounts;
-      for (int k = 0; k < p.n; ++k) p.v[k] = L.kept[i + k];
+      for (int k = 0; k < p.n; ++k) p.v[k] = kept[i + k];
       p.to = to + i;
-      CC_LAUNCH(k_ffn_put, dim3(1), dim3(256), 0, L.st, p);
+      CC_LAUNCH(k_ffn_put, dim3(1), dim3(256), 0, st, p);
     }
     a.kept = to;
   }
-  a.N = L.s.N; a.E = L.s.E; a.cap = L.s.cap;
-  a.start = (int*)(L.ws + L.o.start);
-  for (int k = 0; k < kFfnTiles; ++k) a.mtab[k] = (int2*)(L.ws + L.o.mtab[k]);
-  a.rowmap = (int*)(L.ws + L.o.rowmap);
-  CC_LAUNCH(k_ffn_plan, dim3((unsigned)L.s.E), dim3(256), 0, L.st, a);
+  a.N = s.N; a.E = s.E; a.cap = s.cap;
+  a.start = (int*)(ws + o.start);
+  for (int k = 0; k < kFfnTiles; ++k) a.mtab[k] = (int2*)(ws + o.mtab[k]);
+  a.rowmap = (int*)(ws + o.rowmap);
+  CC_LAUNCH(k_ffn_plan, dim3((unsigned)s.E), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -221,6 +221,15 @@ WtSide wts_in(const FfnLaunch& L, const Side& s, uint64_t copy, uint64_t r, uint
   return WtSide{L.ws + copy, (uint64_t)(L.s.E / L.s.N) * r * p, r * p, p};
 }
 
+CkArgs ckpt_args(const FfnLaunch& L, const GemmArgs& g) {
+  CkArgs a;
+  (GemmArgs&)a = g;
+  a.at = ckpt_row(L.s.W, L.s.F);
+  const uint64_t pitch = (uint64_t)a.at.pitch;
+  a.ck = RowSide{L.ckpt.base, L.ckpt.stride, pitch, (const int*)(L.ws + L.o.rowmap), (uint64_t)L.s.E * L.s.cap * pitch};
+  return a;
+}
+
 hipError_t copy_operands(const FfnLaunch& L, int grad) {
   const uint64_t W = L.s.W, F = L.s.F, n = L.s.E, tiles = L.s.mtiles[kFfnTiles - 1];
   CopyArgs a = {};
@@ -228,7 +237,8 @@ hipError_t copy_operands(const FfnLaunch& L, int grad) {
   a.mtab = (const int2*)(L.ws + L.o.mtab[kFfnTiles - 1]);
   a.map = (const int*)(L.ws + L.o.rowmap);
   a.per = L.s.E / L.s.N;
-  a.job[0] = {L.x.base, L.x.stride, tiles, 0, L.ws + L.o.x, W, line_pitch(L.s, W)};
+  // rows x that a checkpoint holds are unpacked there (ckpt_unpack_x)
+  a.job[0] = {L.x.base, L.x.stride, grad && L.ckpt.base ? 0 : tiles, 0, L.ws + L.o.x, W, line_pitch(L.s, W)};
   a.job[1] = {L.w_in.base, L.w_in.stride, n * 2 * F, 2 * F, L.ws + L.o.w_in, W, line_pitch(L.s, W)};
   a.job[2] = {L.w_out.base, L.w_out.stride, n * W, W, L.ws + L.o.w_out, F, line_pitch(L.s, F)};
   if (grad) a.job[3] = {L.dy.base, L.dy.stride, tiles, 0, L.ws + L.o.dy, W, line_pitch(L.s, W)};
@@ -245,13 +255,13 @@ hipError_t copy_operands(const FfnLaunch& L, int grad) {
 }
 
 hipError_t prepare(const FfnLaunch& L, int grad) {
-  const hipError_t e = plan(L);
+  const hipError_t e = plan(L.s, L.o, L.ws, L.kept, L.st);
   return e == hipSuccess && L.o.copied ? copy_operands(L, grad) : e;
 }
 
 }  // namespace
 
-FfnWs ffn_ws(const FfnShape& s, int grad) {
+FfnWs ffn_ws(const FfnShape& s, int grad, int ckpt) {
   FfnWs o;
   const uint64_t es = elem_size(s.dt);
   uint64_t at = 0;
@@ -276,9 +286,14 @@ FfnWs ffn_ws(const FfnShape& s, int grad) {
   } else {
     o.h = take(s.rows * s.F * es);
     o.dgu = grad ? take(s.rows * 2 * s.F * es) : 0;
+    if (grad && ckpt) o.x = take(s.rows * s.W * es);
   }
   o.bytes = at;
   return o;
+}
+
+hipError_t launch_ffn_plan(const FfnShape& s, const FfnWs& o, char* ws, const uint32_t* kept, hipStream_t st) {
+  return plan(s, o, ws, kept, st);
 }
 
 hipError_t launch_ffn(const FfnLaunch& L) {
@@ -291,8 +306,12 @@ hipError_t launch_ffn(const FfnLaunch& L) {
   g.a = rows_in(L, L.x, L.o.x);
   g.b = wts_in(L, L.w_in, L.o.w_in, 2 * F, W);
   g.out = compact(L, L.o.h, F);
-  g.pre = rows_of(L, L.pre, 2 * F);
-  if ((e = pick_gemm<K_GATEUP>(g, L)) != hipSuccess) return e;
+  if (L.ckpt.base) {
+    if ((e = ckpt_pack_x(L)) != hipSuccess || (e = ckpt_gateup(ckpt_args(L, g), L)) != hipSuccess) return e;
+  } else {
+    g.pre = rows_of(L, L.pre, 2 * F);
+    if ((e = pick_gemm<K_GATEUP>(g, L)) != hipSuccess) return e;
+  }
   g = gemm_args(L);
   g.K = (int)F;
   g.N = (int)W;
@@ -313,8 +332,12 @@ hipError_t launch_ffn_grad(const FfnLaunch& L) {
   g.b = wts_in(L, L.w_out, L.o.w_out, W, F);
   g.out = compact(L, L.o.dgu, 2 * F);
   g.h = compact(L, L.o.h, F);
-  g.pre = rows_of(L, L.pre, 2 * F);
-  if ((e = pick_gemm<K_DHID>(g, L)) != hipSuccess) return e;
+  if (L.ckpt.base) {
+    if ((e = ckpt_unpack_x(L)) != hipSuccess || (e = ckpt_dhid(ckpt_args(L, g), L)) != hipSuccess) return e;
+  } else {
+    g.pre = rows_of(L, L.pre, 2 * F);
+    if ((e = pick_gemm<K_DHID>(g, L)) != hipSuccess) return e;
+  }
   g = gemm_args(L);
   g.K = (int)(2 * F);
   g.N = (int)W;
@@ -333,7 +356,7 @@ hipError_t launch_ffn_grad(const FfnLaunch& L) {
   g.M = (int)(2 * F);
   g.N = (int)W;
   g.a = compact(L, L.o.dgu, 2 * F);
-  g.b_rows = rows_in(L, L.x, L.o.x);
+  g.b_rows = L.ckpt.base ? compact(L, L.o.x, W) : rows_in(L, L.x, L.o.x);
   g.wout = wts(L, L.dw_in, 2 * F, W);
   return pick_gemm<K_DW>(g, L);
 }

@@ -4,10 +4,28 @@
 // kernels and how their results leave.
 #pragma once
 
+#include "cc_ckpt.h"
 #include "cc_device.h"
 #include "cc_llm.h"
 
 namespace cc {
+
+// Further kinds and types of the products: gate and up keeping an 8-bit
+// checkpoint, the hidden gradient from one, and 8-bit integers (summed in
+// int32; the rows of W or F bytes of cc_ffn_rule.h's element size 1).
+constexpr int K_GATEUP_CK = 5, K_DHID_CK = 6;
+constexpr bool is_gateup(int kind) { return kind == K_GATEUP || kind == K_GATEUP_CK; }
+constexpr bool is_dhid(int kind) { return kind == K_DHID || kind == K_DHID_CK; }
+constexpr int base_kind(int kind) { return is_gateup(kind) ? K_GATEUP : is_dhid(kind) ? K_DHID : kind; }
+constexpr int DT_I8 = 3;
+namespace {
+template <>
+struct Ty<DT_I8> {
+  typedef int32_t A;
+  static constexpr int V = 16;
+  static constexpr int SZ = 1;
+};
+}  // namespace
 
 // ------------------------------------------------------------------ operands
 
@@ -44,9 +62,39 @@ struct GemmArgs {
   const int* map;        // compact rows' places in their rank's buffer
   WtSide wout;           // K_DW
 };
+struct CkArgs : GemmArgs {
+  RowSide ck;            // checkpoint rows, in the ranks' buffers
+  CkptRow at;
+};
+struct I8Args : GemmArgs {
+  const char* sx;        // a scale for each row: of the compact rows, or (sx_map) in the ranks' buffers
+  uint64_t sx_stride;
+  const int* sx_map;
+  const char* sw;        // and for each weight row, M an expert
+  uint64_t sw_stride;
+};
 namespace {
 
+template <int DT, int KIND>
+struct ArgsOf {
+  typedef GemmArgs T;
+};
+template <int DT>
+struct ArgsOf<DT, K_GATEUP_CK> {
+  typedef CkArgs T;
+};
+template <int DT>
+struct ArgsOf<DT, K_DHID_CK> {
+  typedef CkArgs T;
+};
+template <int KIND>
+struct ArgsOf<DT_I8, KIND> {
+  typedef I8Args T;
+};
+
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -154,18 +202,23 @@ __device__ __forceinline__ u32x4 pack_row(const float* v) {
 // repeated past the end), elements [k0, K).  Column tiles: lp[k] is summed line
 // k0 + k (NULL past the end: zeros), columns [c0, C).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 
 template <int DT, bool COL, int R, int NT>
 struct Chunks {
   static constexpr int SZ = Ty<DT>::SZ, V = Ty<DT>::V, Q = R * kKBytes / 16 / NT;
   static constexpr int PER = COL ? R * SZ / 16 : kKBytes / 16;   // chunks per line
   u32x4 v[Q];
+  __device__ __forceinline__ static u32x4 load_any(const char* p) {
+    if constexpr (DT == DT_I8) return *(const u32x4_byte*)p;
+    else return *(const u32x4_any*)p;
+  }
   __device__ __forceinline__ void load(const char* const* lp, int64_t k0, int64_t K, int64_t c0, int64_t C) {
     if (k0 + kKBytes / SZ <= K && (!COL || c0 + R <= C)) {   // whole chunks only
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int e = threadIdx.x + q * NT;
-        v[q] = *(const u32x4_any*)(lp[e / PER] + ((COL ? c0 : k0) + (int64_t)(e % PER) * V) * SZ);
+        v[q] = load_any(lp[e / PER] + ((COL ? c0 : k0) + (int64_t)(e % PER) * V) * SZ);
       }
       return;
     }
@@ -176,7 +229,10 @@ struct Chunks {
       const char* p = lp[e / PER];
       v[q] = u32x4{0u, 0u, 0u, 0u};
       if (p && left >= V) {
-        v[q] = *(const u32x4_any*)(p + at * SZ);
+        v[q] = load_any(p + at * SZ);
+      } else if constexpr (DT == DT_I8) {
+        if (p)
+          for (int i = 0; i < left; ++i) v[q][i >> 2] |= (uint32_t)(uint8_t)p[at + i] << (8 * (i & 3));
       } else if (p && left > 0) {
         float x[V] = {};
 #pragma unroll
@@ -194,6 +250,24 @@ struct Chunks {
     }
   }
 };
+
+// a tile's sums
+template <int DT>
+struct Acc {
+  typedef f32x16 T;
+};
+template <>
+struct Acc<DT_I8> {
+  typedef i32x16 T;
+};
+__device__ __forceinline__ i32x16 mma_i8(u32x4 a, u32x4 b, i32x16 c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+template <int DT>
+__device__ __forceinline__ typename Acc<DT>::T mma_of(u32x4 a, u32x4 b, typename Acc<DT>::T c) {
+  if constexpr (DT == DT_I8) return mma_i8(a, b, c);
+  else return mma<DT>(a, b, c);
+}
 
 // ------------------------------------------------------------------ activations
 
@@ -304,7 +378,7 @@ __device__ __forceinline__ u32x4 load_n(const char* p, int n) {
 // lane holds both.
 template <int KIND, int BN>
 constexpr int tile_cols() {
-  return KIND == K_GATEUP ? BN / 2 : BN;
+  return is_gateup(KIND) ? BN / 2 : BN;
 }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -369,7 +443,7 @@ __device__ __forceinline__ Part tile_of(const GemmArgs& g) {
 // The weight row of line r of a row tile of weights, or -1.
 template <int KIND>
 __device__ __forceinline__ int64_t weight_line(const GemmArgs& g, const Part& t, int r) {
-  if constexpr (KIND == K_GATEUP) {
+  if constexpr (is_gateup(KIND)) {
     const int f = t.n0 + (r >> 6) * 32 + (r & 31);
     return f < g.F ? (int64_t)((r >> 5) & 1) * g.F + f : -1;
   } else {
@@ -388,18 +462,19 @@ constexpr int finish_bytes() {
   return 32 * (WN * 4 + 16);
 }
 
-template <int DT, int KIND, bool VEC, int TM, int TN>
-__device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f32x16 (&acc)[TM][TN], int mw, int nw,
+template <int DT, int KIND, bool VEC, int TM, int TN, class G>
+__device__ __forceinline__ void finish(const G& g, const Part& t, const f32x16 (&acc)[TM][TN], int mw, int nw,
                                        int lane, char* lds) {
   constexpr int SZ = Ty<DT>::SZ, V = Ty<DT>::V, WN = 32 * TN, PITCH = WN * 4 + 16;
-  constexpr int COLS = KIND == K_GATEUP ? WN / 2 : WN;   // result columns of the wave
+  constexpr bool GU = is_gateup(KIND), CK = KIND != base_kind(KIND);
+  constexpr int COLS = GU ? WN / 2 : WN;                 // result columns of the wave
   constexpr int LPR = COLS / V, RPP = 64 / LPR;          // lanes per row, rows per pass
   constexpr int PASSES = 32 / RPP;
   const int cl = (lane % LPR) * V;
   // K_GATEUP: columns alternate 32 gate and 32 up
-  const int at = KIND == K_GATEUP ? (cl / 32) * 64 + cl % 32 : cl;
-  const int n = t.n0 + (KIND == K_GATEUP ? nw / 2 : nw) + cl;
-  const int left = (KIND == K_GATEUP ? g.F : g.N) - n;
+  const int at = GU ? (cl / 32) * 64 + cl % 32 : cl;
+  const int n = t.n0 + (GU ? nw / 2 : nw) + cl;
+  const int left = (GU ? g.F : g.N) - n;
   const int rows = KIND == K_DW ? g.M - t.m0 : t.p1 - t.p0;
   // the rows' places in the rank's buffer, 64 rows of the wave a register
   constexpr bool MAPPED = KIND != K_DW;
@@ -408,7 +483,7 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
 #pragma unroll
     for (int k = 0; k < (TM + 1) / 2; ++k) {
       const int m = mw + 64 * k + lane;
-      place[k] = KIND == K_GATEUP && !g.pre.base ? 0 : m < rows ? g.map[t.p0 + m] : 0;
+      place[k] = GU && !CK && !g.pre.base ? 0 : m < rows ? g.map[t.p0 + m] : 0;
     }
   }
   auto place_of = [&](int i, int row) { return __shfl(place[i / 2], (i & 1) * 32 + row); };
@@ -417,9 +492,19 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
   };
   auto packed = [&](const RowSide& s, int m) { return s.base + (uint64_t)(t.p0 + m) * s.pitch + (int64_t)n * SZ; };
   // K_DHID: the pre-activations, loaded 32 rows ahead (bf16; of float32 they
-  // would fill the registers)
+  // would fill the registers, in 8 bits they do not)
   constexpr bool AHEAD = KIND == K_DHID && PASSES <= 4;
   u32x4 fg[2][PASSES], fu[2][PASSES];
+  Kept<V> kg[2][PASSES], ku[2][PASSES];
+  auto kept = [&](int m, int place, Kept<V>& gt, Kept<V>& up) {
+    if constexpr (KIND == K_DHID_CK) {
+      const char* ck = g.ck.base + (uint64_t)t.rank * g.ck.rank_stride + (uint64_t)(uint32_t)place * g.ck.pitch;
+      if (m < rows && left > 0) {
+        gt = kept_load<V>(ck + g.at.g + n, ck + g.at.ge + n / kCkptBlock);
+        up = kept_load<V>(ck + g.at.u + n, ck + g.at.ue + n / kCkptBlock);
+      }
+    }
+  };
   auto ahead = [&](int i) {
     if constexpr (AHEAD) {
 #pragma unroll
@@ -429,6 +514,12 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
         const int n = mw + 32 * i + row < rows ? left : 0;
         fg[i & 1][r] = load_n<DT, VEC>(pre, n);
         fu[i & 1][r] = load_n<DT, VEC>(pre + (int64_t)g.F * SZ, n);
+      }
+    } else if constexpr (KIND == K_DHID_CK) {
+#pragma unroll
+      for (int r = 0; r < PASSES; ++r) {
+        const int row = r * RPP + lane / LPR;
+        kept(mw + 32 * i + row, place_of(i, row), kg[i & 1][r], ku[i & 1][r]);
       }
     }
   };
@@ -456,19 +547,28 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
                             left);
       } else if constexpr (KIND == K_DOWN || KIND == K_DX) {
         store_n<DT, VEC, V>(mapped(g.out, at_row), v, left);
-      } else if constexpr (KIND == K_GATEUP) {
+      } else if constexpr (GU) {
         float up[V], h[V];
         read_row<V>(lds + row * PITCH + (at + 32) * 4, up);
         gate<DT, V>(v, up, g.act, h);
         store_n<DT, VEC, V>(packed(g.out, m), h, left);
-        if (g.pre.base) {
+        if constexpr (CK) {
+          // the wave's 32 columns are a block; a row's lanes hold the block's columns
+          static_assert(COLS == kCkptBlock, "a block a row");
+          char* ck = g.ck.base + (uint64_t)t.rank * g.ck.rank_stride + (uint64_t)(uint32_t)at_row * g.ck.pitch;
+          kept_store<V, LPR>(v, left, lane, ck + g.at.g + n, ck + g.at.ge + n / kCkptBlock);
+          kept_store<V, LPR>(up, left, lane, ck + g.at.u + n, ck + g.at.ue + n / kCkptBlock);
+        } else if (g.pre.base) {
           char* pre = mapped(g.pre, at_row);
           store_n<DT, VEC, V>(pre, v, left);
           store_n<DT, VEC, V>(pre + (int64_t)g.F * SZ, up, left);
         }
       } else {   // K_DHID
         float gt[V], up[V], dg[V], du[V], h[V];
-        if constexpr (AHEAD) {
+        if constexpr (CK) {
+          kept_unpack<V>(kg[i & 1][r], gt);
+          kept_unpack<V>(ku[i & 1][r], up);
+        } else if constexpr (AHEAD) {
           unpack<DT>(fg[i & 1][r], gt);
           unpack<DT>(fu[i & 1][r], up);
         } else {
@@ -487,11 +587,79 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const Part& t, const f
   }
 }
 
+// The same of 8-bit integer products (K_GATEUP, K_DOWN): sums times the row's and
+// the column's scale, in float32.  The int32 sum is rounded once to float32, and
+// each scale's product once.
+template <int OT, int KIND, bool VEC, int TM, int TN>
+__device__ __forceinline__ void finish_i8(const I8Args& g, const Part& t, const i32x16 (&acc)[TM][TN], int mw, int nw,
+                                          int lane, char* lds) {
+  constexpr int SZ = Ty<OT>::SZ, V = Ty<OT>::V, WN = 32 * TN, PITCH = WN * 4 + 16;
+  constexpr bool GU = KIND == K_GATEUP;
+  constexpr int COLS = GU ? WN / 2 : WN, LPR = COLS / V, RPP = 64 / LPR, PASSES = 32 / RPP;
+  const int cl = (lane % LPR) * V;
+  const int at = GU ? (cl / 32) * 64 + cl % 32 : cl;
+  const int n = t.n0 + (GU ? nw / 2 : nw) + cl;
+  const int left = (GU ? g.F : g.N) - n;
+  const int rows = t.p1 - t.p0;
+  float sc[V], su[V];   // the columns' scales
+  const float* sw = (const float*)(g.sw + (uint64_t)t.rank * g.sw_stride) + (uint64_t)t.local * (uint32_t)g.M + n;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    sc[i] = i < left ? sw[i] : 0.0f;
+    if constexpr (GU) su[i] = i < left ? sw[i + g.F] : 0.0f;
+  }
+  // the rows' places and scales, 64 rows of the wave a register
+  int place[(TM + 1) / 2];
+  float sr[(TM + 1) / 2];
+#pragma unroll
+  for (int k = 0; k < (TM + 1) / 2; ++k) {
+    const int m = mw + 64 * k + lane;
+    place[k] = !GU && m < rows ? g.map[t.p0 + m] : 0;
+    const int p = g.sx_map ? place[k] : t.p0 + m;
+    sr[k] = m < rows ? *(const float*)(g.sx + (uint64_t)t.rank * g.sx_stride + (uint64_t)(uint32_t)p * 4) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(f32x4*)(lds + (lane & 31) * PITCH + (32 * j + 8 * q + 4 * (lane >> 5)) * 4) =
+            f32x4{(float)acc[i][j][4 * q], (float)acc[i][j][4 * q + 1], (float)acc[i][j][4 * q + 2],
+                  (float)acc[i][j][4 * q + 3]};
+    wave_lds_sync();
+#pragma unroll
+    for (int r = 0; r < PASSES; ++r) {
+      const int row = r * RPP + lane / LPR, m = mw + 32 * i + row;
+      const float s = __shfl(sr[i / 2], (i & 1) * 32 + row);
+      int at_row = 0;
+      if constexpr (!GU) at_row = __shfl(place[i / 2], (i & 1) * 32 + row);
+      if (m >= rows) continue;
+      float v[V];
+      read_row<V>(lds + row * PITCH + at * 4, v);
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[c] = v[c] * s * sc[c];
+      if constexpr (GU) {
+        float up[V], h[V];
+        read_row<V>(lds + row * PITCH + (at + 32) * 4, up);
+#pragma unroll
+        for (int c = 0; c < V; ++c) up[c] = up[c] * s * su[c];
+        gate<OT, V>(v, up, g.act, h);
+        store_n<OT, VEC, V>(g.out.base + (uint64_t)(t.p0 + m) * g.out.pitch + (int64_t)n * SZ, h, left);
+      } else {
+        store_n<OT, VEC, V>(g.out.base + (uint64_t)t.rank * g.out.rank_stride +
+                                (uint64_t)(uint32_t)at_row * g.out.pitch + (int64_t)n * SZ, v, left);
+      }
+    }
+    wave_lds_sync();
+  }
+}
+
 // One stage's products of a wave: the next unit's fragments are read while the
 // matrix instructions of the last ones run.
 template <int DT, bool ACOL, bool BCOL, int BM, int BN, int TM, int TN>
-__device__ __forceinline__ void multiply(const char* ta, const char* tb, f32x16 (&acc)[TM][TN], int mw, int nw,
-                                         int lane) {
+__device__ __forceinline__ void multiply(const char* ta, const char* tb, typename Acc<DT>::T (&acc)[TM][TN], int mw,
+                                         int nw, int lane) {
   u32x4 fa[2][TM], fb[2][TN];
   auto read = [&](int u) {
 #pragma unroll
@@ -506,19 +674,19 @@ __device__ __forceinline__ void multiply(const char* ta, const char* tb, f32x16 
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma_of<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
     __builtin_amdgcn_sched_barrier(0);   // keeps at most two units' fragments in registers
   }
 }
 
-template <int TM, int TN>
-__device__ __forceinline__ void clear(f32x16 (&acc)[TM][TN]) {
+template <class A, int TM, int TN>
+__device__ __forceinline__ void clear(A (&acc)[TM][TN]) {
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
 }
 
 // Any alignment: tiles staged through registers, the next stage's on their way
@@ -526,12 +694,12 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TM][TN]) {
 // float32: 32 and 20 us.  Its 506 and 414 waves leave half of the 1024 SIMDs idle,
 // and a wave spends half of its time, 14 of 28 us, in matrix instructions, the
 // rest on the latency of 17 and 11 stages; element by element they took 54 and 35.
-template <int DT, int KIND, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_any(GemmArgs g) {
+template <int DT, int KIND, int BM, int BN, int WM, int WN, int OT = DT>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_any(typename ArgsOf<DT, KIND>::T g) {
   constexpr int NT = 64 * (BM / WM) * (BN / WN);
   constexpr int BK = kKBytes / Ty<DT>::SZ;
   constexpr int TM = WM / 32, TN = WN / 32;
-  constexpr bool ACOL = KIND == K_DW, BCOL = KIND == K_DHID || KIND == K_DX || KIND == K_DW;
+  constexpr bool ACOL = KIND == K_DW, BCOL = is_dhid(KIND) || KIND == K_DX || KIND == K_DW;
   __shared__ __attribute__((aligned(16))) char ta[BM * kKBytes];
   __shared__ __attribute__((aligned(16))) char tb[BN * kKBytes];
   __shared__ __attribute__((aligned(16))) char fin[(NT / 64) * finish_bytes<WN>()];
@@ -562,7 +730,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_any(GemmArgs
   };
   Chunks<DT, ACOL, BM, NT> ea;
   Chunks<DT, BCOL, BN, NT> eb;
-  f32x16 acc[TM][TN];
+  typename Acc<DT>::T acc[TM][TN];
   clear(acc);
   summed_lines(0);
   __syncthreads();
@@ -582,7 +750,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_any(GemmArgs
     }
     multiply<DT, ACOL, BCOL, BM, BN>(ta, tb, acc, mw, nw, lane);
   }
-  finish<DT, KIND, false>(g, t, acc, mw, nw, lane, fin + wave * finish_bytes<WN>());
+  if constexpr (DT == DT_I8) finish_i8<OT, KIND, false>(g, t, acc, mw, nw, lane, fin + wave * finish_bytes<WN>());
+  else finish<DT, KIND, false>(g, t, acc, mw, nw, lane, fin + wave * finish_bytes<WN>());
 }
 
 // ---- aligned rows: tiles come by direct loads to LDS, 16 bytes a lane.  Buffer
@@ -692,12 +861,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const RowSide& s, 
 // waves of 128 x 128 (faster per stage, slower results), loads of later
 // stages' lines into the L2 ahead (within 2%), row groups of 8 and 16 (0-5%
 // slower).
-template <int DT, int KIND, bool VEC, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArgs g) {
+template <int DT, int KIND, bool VEC, int BM, int BN, int WM, int WN, int OT = DT>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(typename ArgsOf<DT, KIND>::T g) {
   constexpr int NW = (BM / WM) * (BN / WN);
   constexpr int SZ = Ty<DT>::SZ, BK = kKBytes / SZ;
   constexpr int TM = WM / 32, TN = WN / 32;
-  constexpr bool ACOL = KIND == K_DW, BCOL = KIND == K_DHID || KIND == K_DX || KIND == K_DW;
+  constexpr bool ACOL = KIND == K_DW, BCOL = is_dhid(KIND) || KIND == K_DX || KIND == K_DW;
   // separate arrays: the compiler then knows which of them a load to LDS fills,
   // and waits for no other
   __shared__ __attribute__((aligned(16))) char t0[(BM + BN) * kKBytes], t1[(BM + BN) * kKBytes];
@@ -743,7 +912,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
     }
   }
 
-  f32x16 acc[TM][TN];
+  typename Acc<DT>::T acc[TM][TN];
   clear(acc);
   const int S = (K + 2 * BK - 1) / (2 * BK) * 2;                // an odd last stage is zeros
   const int s_end = (K + BK - 1) / BK - 1;                      // the last stage with elements
@@ -780,7 +949,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
       fa[(u + 1) & 1][i] = frag<DT, ACOL, BM>(rd, ru, mw + 32 * i, lane);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = mma<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma_of<DT>(fb[u & 1][j], fa[u & 1][i], acc[i][j]);
       between(i);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -838,25 +1007,27 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(GemmArg
   constexpr int PER = (BM + BN) * kKBytes / finish_bytes<WN>();   // waves that one stage's LDS serves
   static_assert(NW <= 2 * PER, "every wave has its piece");
   char* fin = wave < PER ? t0 : t1;
-  finish<DT, KIND, VEC>(g, t, acc, mw, nw, lane, fin + (wave % PER) * finish_bytes<WN>());
+  char* piece = fin + (wave % PER) * finish_bytes<WN>();
+  if constexpr (DT == DT_I8) finish_i8<OT, KIND, VEC>(g, t, acc, mw, nw, lane, piece);
+  else finish<DT, KIND, VEC>(g, t, acc, mw, nw, lane, piece);
 }
 
 // ------------------------------------------------------------------ launches
 
-template <int DT, int KIND, bool VEC>
-hipError_t launch_tile(const GemmArgs& g, int k, dim3 grid, hipStream_t st) {
-  if (k == 0) CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 256, 256, 128, 64>), grid, dim3(512), 0, st, g);
-  else if (k == 1) CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 128, 128, 64, 64>), grid, dim3(256), 0, st, g);
-  else CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 64, 64, 32, 64>), grid, dim3(128), 0, st, g);
+template <int DT, int KIND, bool VEC, int OT = DT>
+hipError_t launch_tile(const typename ArgsOf<DT, KIND>::T& g, int k, dim3 grid, hipStream_t st) {
+  if (k == 0) CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 256, 256, 128, 64, OT>), grid, dim3(512), 0, st, g);
+  else if (k == 1) CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 128, 128, 64, 64, OT>), grid, dim3(256), 0, st, g);
+  else CC_LAUNCH((k_ffn_tile<DT, KIND, VEC, 64, 64, 32, 64, OT>), grid, dim3(128), 0, st, g);
   return hipGetLastError();
 }
 
 template <int DT, int KIND>
-hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
+hipError_t run_gemm(typename ArgsOf<DT, KIND>::T g, const FfnLaunch& L) {
   const bool fast = ffn_tiled(L.s, L.o.copied, L.vec_ok);
-  const int cus = dev_info().cus > 0 ? dev_info().cus : 256, cols = KIND == K_GATEUP ? g.F : g.N;
-  const int k = ffn_pick_tile(L.s, KIND, g.M, cols, fast, cus);
-  const FfnGrid tiles = ffn_grid(L.s, KIND, g.M, cols, k);
+  const int cus = dev_info().cus > 0 ? dev_info().cus : 256, cols = is_gateup(KIND) ? g.F : g.N;
+  const int k = ffn_pick_tile(L.s, base_kind(KIND), g.M, cols, fast, cus);
+  const FfnGrid tiles = ffn_grid(L.s, base_kind(KIND), g.M, cols, k);
   const uint64_t blocks = tiles.blocks;
   if (blocks == 0) return hipSuccess;
   g.mtiles = (int)tiles.mt;
@@ -871,7 +1042,7 @@ hipError_t run_gemm(GemmArgs g, const FfnLaunch& L) {
 }
 
 template <int KIND>
-hipError_t pick_gemm(const GemmArgs& g, const FfnLaunch& L) {
+hipError_t pick_gemm(const typename ArgsOf<DT_F32, KIND>::T& g, const FfnLaunch& L) {
   return L.s.dt == DT_F32 ? run_gemm<DT_F32, KIND>(g, L) : run_gemm<DT_BF16, KIND>(g, L);
 }
 

@@ -1,6 +1,7 @@
 // Internal interface between the C ABI of the model-side operators
 // (cc_model.cpp) and their kernels (cc_sort.hip, cc_embed.hip, cc_route.hip,
-// cc_ffn.hip).  Host-side only; not installed.
+// cc_balance.hip, cc_ffn.hip, cc_ffn_ckpt.hip, cc_int8.hip).  Host-side only; not
+// installed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -97,6 +98,53 @@ struct RouteLaunch {
 hipError_t launch_route(const RouteLaunch& L);
 hipError_t launch_route_grad(const RouteLaunch& L);
 
+// ---- balance loss of the routing
+constexpr int kBalanceBlock = 256;
+struct BalanceLaunch {
+  const char* logits;
+  uint64_t logits_stride;
+  const char* counts;    // int32 [nexperts]
+  uint64_t counts_stride;
+  char* total;           // int32 [nexperts + 1]; the gradient's input
+  uint64_t total_stride;
+  char* prob;            // float32 [nexperts]
+  uint64_t prob_stride;
+  char* loss;            // float32; dloss of the gradient
+  uint64_t loss_stride;
+  const char* base;      // the gradient's addend, or NULL
+  uint64_t base_stride;
+  char* dlogits;
+  uint64_t dlogits_stride;
+  char* ws;
+  uint64_t tokens;
+  int nexperts, summed;
+  int N, dt;
+  hipStream_t st;
+};
+uint64_t balance_ws(int N, uint64_t tokens, int nexperts);
+hipError_t launch_balance(const BalanceLaunch& L);
+hipError_t launch_balance_grad(const BalanceLaunch& L);
+
+// ---- a checkpoint row: x, gate and up integers, each part on a multiple of 16
+// bytes, then the exponents of their blocks
+constexpr int kCkptBlock = 32;
+struct CkptRow {
+  int x, g, u, xe, ge, ue, pitch;
+};
+inline CkptRow ckpt_row(uint64_t W, uint64_t F) {
+  auto up = [](uint64_t v) { return (int)((v + 15) / 16 * 16); };
+  auto blocks = [](uint64_t v) { return (int)((v + kCkptBlock - 1) / kCkptBlock); };
+  CkptRow r;
+  r.x = 0;
+  r.g = up(W);
+  r.u = r.g + up(F);
+  r.xe = r.u + up(F);
+  r.ge = r.xe + blocks(W);
+  r.ue = r.ge + blocks(F);
+  r.pitch = up((uint64_t)r.ue + blocks(F));
+  return r;
+}
+
 // ---- gated feed-forward block of the experts.  Compact rows: the kept rows
 // of all experts back to back, expert by expert, source by source.
 // Workspace: row starts [E + 1], row tiles of each size (expert, first row), row
@@ -109,7 +157,8 @@ struct FfnWs {
   int copied;
   uint64_t x, dy, w_in, w_out;
 };
-FfnWs ffn_ws(const FfnShape& s, int grad);
+// `ckpt`: the gradient's rows x come from checkpoints, unpacked into the workspace
+FfnWs ffn_ws(const FfnShape& s, int grad, int ckpt = 0);
 struct FfnLaunch {
   FfnShape s;
   FfnWs o;
@@ -117,10 +166,60 @@ struct FfnLaunch {
   const uint32_t* kept;  // host, [E][N]: kept rows of expert e from source i
   Side x, w_in, w_out, pre, y;      // pre.base may be NULL (forward)
   Side dy, dx, dw_in, dw_out;       // gradient
+  Side ckpt;                        // checkpoint rows in x's layout (base NULL: none)
   int vec_ok;
   hipStream_t st;
 };
 hipError_t launch_ffn(const FfnLaunch& L);
 hipError_t launch_ffn_grad(const FfnLaunch& L);
+// the plan alone: o.kept, o.start, o.mtab and o.rowmap
+hipError_t launch_ffn_plan(const FfnShape& s, const FfnWs& o, char* ws, const uint32_t* kept, hipStream_t st);
+
+// the parts of the block that keep or read a checkpoint (cc_ffn_ckpt.hip)
+struct CkArgs;
+hipError_t ckpt_gateup(const CkArgs& g, const FfnLaunch& L);
+hipError_t ckpt_dhid(const CkArgs& g, const FfnLaunch& L);
+hipError_t ckpt_pack_x(const FfnLaunch& L);
+hipError_t ckpt_unpack_x(const FfnLaunch& L);
+
+// ---- 8-bit integers: rows and their scales, grouped products
+struct Int8Rows {
+  const char* x;         // rows of `width` elements: rank-strided, or (tiles) the experts' rows
+  uint64_t x_stride;
+  char* q;               // rows of q_pitch bytes, zeros past the width
+  uint64_t q_stride, q_pitch;
+  char* s;               // a float32 a row
+  uint64_t s_stride;
+  uint64_t rows, width;
+  // the experts' kept rows, compact rows out: the plan's row starts, tiles of 64 rows and map (NULL: plain rows)
+  const int* start;
+  const int2* mtab;
+  const int* map;
+  uint64_t tiles;
+  int per;               // experts a rank
+  int N, dt;
+  hipStream_t st;
+};
+hipError_t launch_int8_rows(const Int8Rows& L);
+struct Int8Ws {
+  FfnWs plan;
+  uint64_t xq, xs, h, hq, hs, bytes;
+  uint64_t xq_pitch, hq_pitch;
+};
+Int8Ws int8_ws(const FfnShape& s, int block, int out_es);
+struct Int8Launch {
+  FfnShape s;            // element size 1; W summed, F the product's columns, or the block's hidden size
+  Int8Ws o;
+  char* ws;
+  const uint32_t* kept;
+  Side x, xs;            // the product: 8-bit rows and scales; the block: rows of type dt
+  Side w_in, s_in, w_out, s_out, y;
+  int w_in_ok, w_out_ok, x_ok, y_ok;   // whole 16-byte vectors
+  int dt;                // of the results
+  hipStream_t st;
+};
+hipError_t launch_int8(const Int8Launch& L);
+hipError_t launch_int8_ffn(const Int8Launch& L);
+
 
 }  // namespace cc

@@ -1,5 +1,7 @@
 // C ABI of the model-side operators: embedding and its gradients, MoE routing
-// and its gradient, the experts' gated feed-forward block and its gradients.
+// and its gradient, the routing's balance loss and its gradient, the experts' gated
+// feed-forward block and its gradients, with 8-bit checkpoints too, and the
+// experts' products in 8-bit integers.
 // Declared in include/cc.h.
 
 #include <algorithm>
@@ -203,6 +205,8 @@ cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uin
 
 struct FfnBufs {
   cc_rankbuf_t x, w_in, w_out, pre, y, dy, dx, dw_in, dw_out;
+  cc_rankbuf_t ckpt;   // in place of pre, and for the gradients of x
+  bool kept8;
 };
 
 Side side(const cc_rankbuf_t& b) { return Side{(char*)b.base, (uint64_t)b.rank_stride_bytes}; }
@@ -218,13 +222,14 @@ cc_status_t run_ffn(const FfnBufs& f, const size_t* counts, int E, uint64_t cap,
   if ((s = ffn_shape(counts, E, cap, W, F, dtype, N, &L.s, &kept))) return s;
   const int es = elem_size((int)dtype);
   L.s.act = (int)act;
-  L.o = ffn_ws(L.s, grad);
+  L.o = ffn_ws(L.s, grad, f.kept8);
   const u128 side_n = (u128)E * cap * W * es, pre_n = (u128)E * cap * 2 * F * es;
   const u128 wi_n = (u128)(E / N) * 2 * F * W * es, wo_n = (u128)(E / N) * W * F * es;
-  const bool keep = grad || f.pre.base != nullptr;
-  std::vector<Buf> b = {{&f.x, side_n, "x", false, N},
-                        {&f.w_in, wi_n, "w_in", false, N},
-                        {&f.w_out, wo_n, "w_out", false, N}};
+  const u128 ckpt_n = (u128)E * cap * (unsigned)ckpt_row(W, F).pitch;
+  const bool keep = !f.kept8 && (grad || f.pre.base != nullptr);
+  std::vector<Buf> b = {{&f.w_in, wi_n, "w_in", false, N}, {&f.w_out, wo_n, "w_out", false, N}};
+  if (!grad || !f.kept8) b.push_back({&f.x, side_n, "x", false, N});
+  if (f.kept8) b.push_back({&f.ckpt, ckpt_n, "ckpt", !grad, N});
   if (keep) b.push_back({&f.pre, pre_n, "pre", !grad, N});
   if (grad) {
     b.push_back({&f.dy, side_n, "dy", false, N});
@@ -234,10 +239,14 @@ cc_status_t run_ffn(const FfnBufs& f, const size_t* counts, int E, uint64_t cap,
   } else {
     b.push_back({&f.y, side_n, "y", true, N});
   }
-  if ((s = check_bufs(b.data(), (int)b.size(), cfg, L.o.bytes, "cc_moe_ffn_workspace_size"))) return s;
+  if ((s = check_bufs(b.data(), (int)b.size(), cfg, L.o.bytes,
+                      f.kept8 ? "cc_moe_ffn_checkpoint_workspace_size" : "cc_moe_ffn_workspace_size")))
+    return s;
+  if (f.kept8 && ckpt_n != 0 && !al(f.ckpt))
+    return fail(CC_ERR_INVALID_ARG, "ckpt must start on a multiple of 16 bytes on every rank");
   L.vec_ok = al16(W * es) && al16(F * es);
   for (const Buf& x : b) {
-    if (x.n == 0) continue;   // no rows: never touched
+    if (x.n == 0 || x.b == &f.ckpt) continue;   // no rows: never touched
     if ((s = check_elems(*x.b, es, x.name))) return s;
     L.vec_ok = L.vec_ok && al(*x.b);
   }
@@ -248,9 +257,82 @@ cc_status_t run_ffn(const FfnBufs& f, const size_t* counts, int E, uint64_t cap,
   L.x = side(f.x); L.w_in = side(f.w_in); L.w_out = side(f.w_out);
   L.pre = keep ? side(f.pre) : Side{nullptr, 0};
   L.y = side(f.y);
+  L.ckpt = f.kept8 ? side(f.ckpt) : Side{nullptr, 0};
   L.dy = side(f.dy); L.dx = side(f.dx); L.dw_in = side(f.dw_in); L.dw_out = side(f.dw_out);
   L.st = st;
   return hip_status(grad ? launch_ffn_grad(L) : launch_ffn(L), grad ? "expert feed-forward gradient" : "expert feed-forward");
+}
+
+// ------------------------------------------------------------------ balance loss
+
+cc_status_t balance_sizes(int nranks, uint64_t tokens, int nexperts) {
+  return route_sizes(nranks, tokens, nexperts, 1, 0);
+}
+
+// ------------------------------------------------------------------ 8-bit integers
+
+constexpr uint64_t kMaxInt8Sum = 1ull << 17;   // 2^14 a product: sums below 2^31
+
+// The shape of a product (cols, block 0) or of the block (hidden, block 1).
+cc_status_t int8_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uint64_t F, int N, bool block,
+                       FfnShape* sh, std::vector<uint32_t>* kept) {
+  if (W >= kMaxInt8Sum || (block && F >= kMaxInt8Sum))
+    return fail(CC_ERR_INVALID_ARG, "a summed axis must be shorter than %llu", (unsigned long long)kMaxInt8Sum);
+  cc_status_t s = ffn_shape(counts, E, cap, W, F, CC_BFLOAT16, N, sh, kept);
+  sh->es = 1;
+  return s;
+}
+
+bool rows16(const cc_rankbuf_t& b, uint64_t row_bytes) { return al(b) && al16(row_bytes); }
+
+struct Int8Bufs {
+  cc_rankbuf_t x, xs, w_in, s_in, w_out, s_out, y;
+};
+
+cc_status_t run_int8(const Int8Bufs& f, const size_t* counts, int E, uint64_t cap, uint64_t W, uint64_t F, int act,
+                     cc_dtype_t dtype, int N, const cc_config_t& cfg, bool block, hipStream_t st) {
+  cc_status_t s = model_checks(N, dtype, cfg);
+  if (s) return s;
+  if (act != CC_ACT_SILU && act != CC_ACT_GELU) return fail(CC_ERR_INVALID_ARG, "unknown activation %d", act);
+  Int8Launch L = {};
+  std::vector<uint32_t> kept;
+  if ((s = int8_shape(counts, E, cap, W, F, N, block, &L.s, &kept))) return s;
+  const int es = elem_size((int)dtype);
+  L.s.act = act;
+  L.o = int8_ws(L.s, block, es);
+  const u128 side_n = (u128)E * cap, per = (unsigned)(E / N), lines = block ? 2 * F : F;
+  const uint64_t ycols = block ? W : F;
+  std::vector<Buf> b = {{&f.x, side_n * W * (block ? es : 1), "x", false, N},
+                        {&f.w_in, per * lines * W, block ? "w_in" : "w", false, N},
+                        {&f.s_in, per * lines * 4, block ? "s_in" : "sw", false, N},
+                        {&f.y, side_n * ycols * es, "y", true, N}};
+  const int elems[] = {block ? es : 1, 1, 4, es, block ? 1 : 4, 4};
+  if (block) {
+    b.push_back({&f.w_out, per * W * F, "w_out", false, N});
+    b.push_back({&f.s_out, per * W * 4, "s_out", false, N});
+  } else {
+    b.push_back({&f.xs, side_n * 4, "sx", false, N});
+  }
+  if ((s = check_bufs(b.data(), (int)b.size(), cfg, L.o.bytes,
+                      block ? "cc_moe_ffn_int8_workspace_size" : "cc_moe_matmul_int8_workspace_size")))
+    return s;
+  for (size_t i = 0; i < b.size(); ++i)
+    if (b[i].n && (s = check_elems(*b[i].b, elems[i], b[i].name))) return s;
+  if (L.s.rows == 0) return ok();
+  if ((s = device_ready())) return s;
+  L.ws = (char*)cfg.workspace;
+  L.kept = kept.data();
+  L.x = side(f.x); L.xs = side(f.xs);
+  L.w_in = side(f.w_in); L.s_in = side(f.s_in); L.w_out = side(f.w_out); L.s_out = side(f.s_out);
+  L.y = side(f.y);
+  L.x_ok = rows16(f.x, W);
+  L.w_in_ok = rows16(f.w_in, W);
+  L.w_out_ok = block && rows16(f.w_out, F);
+  L.y_ok = rows16(f.y, ycols * es);
+  L.dt = (int)dtype;
+  L.st = st;
+  return hip_status(block ? launch_int8_ffn(L) : launch_int8(L),
+                    block ? "expert feed-forward in 8-bit integers" : "product in 8-bit integers");
 }
 
 }  // namespace
@@ -381,7 +463,7 @@ cc_status_t cc_moe_ffn(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc
                        cc_dtype_t dtype, int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
   return guarded([&] {
     const cc_rankbuf_t none{nullptr, 0};
-    return run_ffn(FfnBufs{x, w_in, w_out, pre, y, none, none, none, none}, counts, nexperts, capacity, width, hidden,
+    return run_ffn(FfnBufs{x, w_in, w_out, pre, y, none, none, none, none, none, false}, counts, nexperts, capacity, width, hidden,
                    act, dtype, nranks, cfgp ? *cfgp : kDefaultCfg, false, (hipStream_t)stream);
   });
 }
@@ -392,7 +474,7 @@ cc_status_t cc_moe_ffn_grad(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_ou
                             int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
   return guarded([&] {
     const cc_rankbuf_t none{nullptr, 0};
-    return run_ffn(FfnBufs{x, w_in, w_out, pre, none, dy, dx, dw_in, dw_out}, counts, nexperts, capacity, width, hidden,
+    return run_ffn(FfnBufs{x, w_in, w_out, pre, none, dy, dx, dw_in, dw_out, none, false}, counts, nexperts, capacity, width, hidden,
                    act, dtype, nranks, cfgp ? *cfgp : kDefaultCfg, true, (hipStream_t)stream);
   });
 }
@@ -407,6 +489,188 @@ cc_status_t cc_moe_ffn_workspace_size(const size_t* counts, int nexperts, size_t
     if (grad != 0 && grad != 1) return fail(CC_ERR_INVALID_ARG, "grad=%d is neither 0 nor 1", grad);
     if (!bytes) return fail(CC_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = (size_t)ffn_ws(sh, grad).bytes;
+    return ok();
+  });
+}
+
+cc_status_t cc_moe_balance_loss(cc_rankbuf_t logits, cc_rankbuf_t counts, cc_rankbuf_t total, cc_rankbuf_t prob,
+                                cc_rankbuf_t loss, size_t tokens, int nexperts, int summed, cc_dtype_t dtype,
+                                int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
+  const cc_config_t& cfg = cfgp ? *cfgp : kDefaultCfg;
+  cc_status_t s = model_checks(nranks, dtype, cfg);
+  if (s || (s = balance_sizes(nranks, tokens, nexperts))) return s;
+  if (summed != 0 && summed != 1) return fail(CC_ERR_INVALID_ARG, "summed=%d is neither 0 nor 1", summed);
+  const int N = nranks, es = elem_size((int)dtype);
+  const u128 E = (unsigned)nexperts;
+  const Buf b[] = {{&logits, (u128)tokens * E * es, "logits", false, N},
+                   {&counts, E * 4, "counts", false, N},
+                   {&total, (E + 1) * 4, "total", true, N},
+                   {&prob, E * 4, "prob", true, N},
+                   {&loss, 4, "loss", true, N}};
+  if ((s = check_bufs(b, 5, cfg, balance_ws(N, tokens, nexperts), "cc_moe_balance_loss_workspace_size"))) return s;
+  for (int i = 0; i < 5; ++i)
+    if (b[i].n && (s = check_elems(*b[i].b, i ? 4 : es, b[i].name))) return s;
+  if ((s = device_ready())) return s;
+  BalanceLaunch L = {};
+  L.logits = (const char*)logits.base; L.logits_stride = logits.rank_stride_bytes;
+  L.counts = (const char*)counts.base; L.counts_stride = counts.rank_stride_bytes;
+  L.total = (char*)total.base; L.total_stride = total.rank_stride_bytes;
+  L.prob = (char*)prob.base; L.prob_stride = prob.rank_stride_bytes;
+  L.loss = (char*)loss.base; L.loss_stride = loss.rank_stride_bytes;
+  L.ws = (char*)cfg.workspace;
+  L.tokens = tokens; L.nexperts = nexperts; L.summed = summed;
+  L.N = N; L.dt = (int)dtype; L.st = (hipStream_t)stream;
+  return hip_status(launch_balance(L), "balance loss");
+}
+
+cc_status_t cc_moe_balance_loss_workspace_size(int nranks, size_t tokens, int nexperts, size_t* bytes) {
+  cc_status_t s = balance_sizes(nranks, tokens, nexperts);
+  if (s) return s;
+  if (!bytes) return fail(CC_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = (size_t)balance_ws(nranks, tokens, nexperts);
+  return ok();
+}
+
+cc_status_t cc_moe_balance_loss_grad(cc_rankbuf_t logits, cc_rankbuf_t total, cc_rankbuf_t dloss, cc_rankbuf_t base,
+                                     cc_rankbuf_t dlogits, size_t tokens, int nexperts, cc_dtype_t dtype, int nranks,
+                                     const cc_config_t* cfgp, cc_stream_t stream) {
+  const cc_config_t& cfg = cfgp ? *cfgp : kDefaultCfg;
+  cc_status_t s = model_checks(nranks, dtype, cfg);
+  if (s || (s = balance_sizes(nranks, tokens, nexperts))) return s;
+  if (tokens == 0) return ok();
+  const int N = nranks, es = elem_size((int)dtype);
+  const u128 E = (unsigned)nexperts, lg = (u128)tokens * E * es;
+  std::vector<Buf> b = {{&logits, lg, "logits", false, N},
+                        {&total, (E + 1) * 4, "total", false, N},
+                        {&dloss, 4, "dloss", false, N},
+                        {&dlogits, lg, "dlogits", true, N}};
+  // in place: one buffer, read and written element by element
+  if (base.base && !same_side(base, dlogits)) b.push_back({&base, lg, "base", false, N});
+  if ((s = check_bufs(b.data(), (int)b.size(), cfg, 0, ""))) return s;
+  for (const Buf& x : b)
+    if ((s = check_elems(*x.b, x.b == &total || x.b == &dloss ? 4 : es, x.name))) return s;
+  if ((s = device_ready())) return s;
+  BalanceLaunch L = {};
+  L.logits = (const char*)logits.base; L.logits_stride = logits.rank_stride_bytes;
+  L.total = (char*)total.base; L.total_stride = total.rank_stride_bytes;
+  L.loss = (char*)dloss.base; L.loss_stride = dloss.rank_stride_bytes;
+  L.base = (const char*)base.base; L.base_stride = base.rank_stride_bytes;
+  L.dlogits = (char*)dlogits.base; L.dlogits_stride = dlogits.rank_stride_bytes;
+  L.tokens = tokens; L.nexperts = nexperts;
+  L.N = N; L.dt = (int)dtype; L.st = (hipStream_t)stream;
+  return hip_status(launch_balance_grad(L), "balance loss gradient");
+}
+
+cc_status_t cc_quantize_rows(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t scales, size_t rows, size_t width,
+                             cc_dtype_t dtype, int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
+  const cc_config_t& cfg = cfgp ? *cfgp : kDefaultCfg;
+  cc_status_t s = model_checks(nranks, dtype, cfg);
+  if (s) return s;
+  if (width == 0) return fail(CC_ERR_INVALID_ARG, "width must be positive");
+  if (width >= (1ull << 31) || rows >= (1ull << 31)) return fail(CC_ERR_INVALID_ARG, "width or rows too large");
+  if (rows == 0) return ok();
+  const int N = nranks, es = elem_size((int)dtype);
+  const Buf b[] = {{&x, (u128)rows * width * es, "x", false, N},
+                   {&q, (u128)rows * width, "q", true, N},
+                   {&scales, (u128)rows * 4, "scales", true, N}};
+  if ((s = check_bufs(b, 3, cfg, 0, "")) || (s = check_elems(x, es, "x")) || (s = check_elems(scales, 4, "scales")))
+    return s;
+  if ((s = device_ready())) return s;
+  Int8Rows L = {};
+  L.x = (const char*)x.base; L.x_stride = x.rank_stride_bytes;
+  L.q = (char*)q.base; L.q_stride = q.rank_stride_bytes; L.q_pitch = width;
+  L.s = (char*)scales.base; L.s_stride = scales.rank_stride_bytes;
+  L.rows = rows; L.width = width; L.N = N; L.dt = (int)dtype; L.st = (hipStream_t)stream;
+  return hip_status(launch_int8_rows(L), "quantisation of rows");
+}
+
+cc_status_t cc_moe_matmul_int8(cc_rankbuf_t x, cc_rankbuf_t sx, cc_rankbuf_t w, cc_rankbuf_t sw, cc_rankbuf_t y,
+                               const size_t* counts, int nexperts, size_t capacity, size_t width, size_t cols,
+                               cc_dtype_t dtype, int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
+  return guarded([&] {
+    const cc_rankbuf_t none{nullptr, 0};
+    return run_int8(Int8Bufs{x, sx, w, sw, none, none, y}, counts, nexperts, capacity, width, cols, CC_ACT_SILU, dtype,
+                    nranks, cfgp ? *cfgp : kDefaultCfg, false, (hipStream_t)stream);
+  });
+}
+
+cc_status_t cc_moe_ffn_int8(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t s_in, cc_rankbuf_t w_out,
+                            cc_rankbuf_t s_out, cc_rankbuf_t y, const size_t* counts, int nexperts, size_t capacity,
+                            size_t width, size_t hidden, cc_act_t act, cc_dtype_t dtype, int nranks,
+                            const cc_config_t* cfgp, cc_stream_t stream) {
+  return guarded([&] {
+    const cc_rankbuf_t none{nullptr, 0};
+    return run_int8(Int8Bufs{x, none, w_in, s_in, w_out, s_out, y}, counts, nexperts, capacity, width, hidden, (int)act,
+                    dtype, nranks, cfgp ? *cfgp : kDefaultCfg, true, (hipStream_t)stream);
+  });
+}
+
+cc_status_t cc_moe_matmul_int8_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width,
+                                              size_t cols, int nranks, size_t* bytes) {
+  return guarded([&] {
+    FfnShape sh;
+    std::vector<uint32_t> kept;
+    cc_status_t s = int8_shape(counts, nexperts, capacity, width, cols, nranks, false, &sh, &kept);
+    if (s) return s;
+    if (!bytes) return fail(CC_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = (size_t)int8_ws(sh, 0, 0).bytes;
+    return ok();
+  });
+}
+
+cc_status_t cc_moe_ffn_int8_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width,
+                                           size_t hidden, cc_dtype_t dtype, int nranks, size_t* bytes) {
+  return guarded([&] {
+    FfnShape sh;
+    std::vector<uint32_t> kept;
+    cc_status_t s = model_checks(nranks, dtype, kDefaultCfg);
+    if (s || (s = int8_shape(counts, nexperts, capacity, width, hidden, nranks, true, &sh, &kept))) return s;
+    if (!bytes) return fail(CC_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = (size_t)int8_ws(sh, 1, elem_size((int)dtype)).bytes;
+    return ok();
+  });
+}
+
+cc_status_t cc_moe_ffn_checkpoint(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t ckpt,
+                                  cc_rankbuf_t y, const size_t* counts, int nexperts, size_t capacity, size_t width,
+                                  size_t hidden, cc_act_t act, cc_dtype_t dtype, int nranks, const cc_config_t* cfgp,
+                                  cc_stream_t stream) {
+  return guarded([&] {
+    const cc_rankbuf_t none{nullptr, 0};
+    return run_ffn(FfnBufs{x, w_in, w_out, none, y, none, none, none, none, ckpt, true}, counts, nexperts, capacity,
+                   width, hidden, act, dtype, nranks, cfgp ? *cfgp : kDefaultCfg, false, (hipStream_t)stream);
+  });
+}
+
+cc_status_t cc_moe_ffn_checkpoint_grad(cc_rankbuf_t ckpt, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t dy,
+                                       cc_rankbuf_t dx, cc_rankbuf_t dw_in, cc_rankbuf_t dw_out, const size_t* counts,
+                                       int nexperts, size_t capacity, size_t width, size_t hidden, cc_act_t act,
+                                       cc_dtype_t dtype, int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
+  return guarded([&] {
+    const cc_rankbuf_t none{nullptr, 0};
+    return run_ffn(FfnBufs{none, w_in, w_out, none, none, dy, dx, dw_in, dw_out, ckpt, true}, counts, nexperts,
+                   capacity, width, hidden, act, dtype, nranks, cfgp ? *cfgp : kDefaultCfg, true, (hipStream_t)stream);
+  });
+}
+
+cc_status_t cc_moe_ffn_checkpoint_row(size_t width, size_t hidden, size_t* bytes) {
+  if (width == 0 || hidden == 0 || width >= (1ull << 24) || hidden >= (1ull << 24))
+    return fail(CC_ERR_INVALID_ARG, "width or hidden outside [1, 2^24)");
+  if (!bytes) return fail(CC_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = (size_t)ckpt_row(width, hidden).pitch;
+  return ok();
+}
+
+cc_status_t cc_moe_ffn_checkpoint_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width,
+                                                 size_t hidden, cc_dtype_t dtype, int nranks, int grad, size_t* bytes) {
+  return guarded([&] {
+    FfnShape sh;
+    std::vector<uint32_t> kept;
+    cc_status_t s = model_checks(nranks, dtype, kDefaultCfg);
+    if (s || (s = ffn_shape(counts, nexperts, capacity, width, hidden, dtype, nranks, &sh, &kept))) return s;
+    if (grad != 0 && grad != 1) return fail(CC_ERR_INVALID_ARG, "grad=%d is neither 0 nor 1", grad);
+    if (!bytes) return fail(CC_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = (size_t)ffn_ws(sh, grad, 1).bytes;
     return ok();
   });
 }

@@ -1,0 +1,299 @@
+"""The feed-forward block with 8-bit activation checkpoints on the GPU: what is
+kept against the definition, the gradients against 64-bit ones at the kept
+values (the bounds of the block's own tests)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV
+from model_tiles import CASES
+from ring_allreduce_reduction_02_amd import ccgpu
+from test_gpu_model import FFNS, U, Ffn, act64, gen, say, spread
+
+pytestmark = pytest.mark.gpu
+B = 32
+
+
+def blocks(n):
+    return -(-n // B)
+
+
+def layout(W, F):
+    up = lambda v: -(-v // 16) * 16  # noqa: E731
+    at = [0, up(W), up(W) + up(F), up(W) + 2 * up(F)]
+    return at + [at[3] + blocks(W), at[3] + blocks(W) + blocks(F)]
+
+
+def power(e):
+    """2^e, exact (torch's own powers need not be), e from -127 to 128."""
+    return torch.tensor([2.0 ** k for k in range(-127, 129)], dtype=torch.float64, device=DEV)[e.long() + 127]
+
+
+def kept(rows, W, F):
+    """x, g and u (float64) of checkpoint rows [r, bytes], and their blocks' steps."""
+    at, out = layout(W, F), []
+    for k, n in enumerate((W, F, F)):
+        q = rows[:, at[k]:at[k] + n].contiguous().view(torch.int8).double()
+        ex = rows[:, at[k + 3]:at[k + 3] + blocks(n)].int()
+        step = torch.where(ex == 255, math.nan, power(ex - 127))
+        step = step.repeat_interleave(B, -1)[:, :n]
+        out.append((q * step, step))
+    return out
+
+
+def packed(v):
+    """The values that rows v (float64, finite) are kept as, by the definition."""
+    r, n = v.shape
+    b = torch.zeros((r, blocks(n) * B), dtype=torch.float64, device=DEV)
+    b[:, :n] = v
+    top = b.view(r, -1, B).abs().amax(-1)
+    e = torch.full_like(top, -126.0)
+    for k in range(-126, 121):                       # the least e for which top / 2^e rounds to at most 127
+        e = torch.where(torch.round(top * 2.0 ** -k) > 127, k + 1.0, e)
+    step = power(e).repeat_interleave(B, -1)[:, :n]
+    return torch.round(v / step).clamp(-127, 127) * step
+
+
+class Ckpt(Ffn):
+    def __init__(self, *a, **kw):
+        super().__init__(*a, **kw)
+        pad = kw.get("pad", 0)
+        n = self.E * self.cap * ccgpu.moe_ffn_checkpoint_row(self.W, self.F)
+        self.ckpt = torch.full((self.N, n + 16 * pad), 0x5A, dtype=torch.uint8, device=DEV)[:, :n]
+
+    def forward(self, act, stream=None, ws=None):
+        if ws is None:
+            ws = ccgpu.make_moe_ffn_checkpoint_workspace(self.counts, self.cap, self.W, self.F, self.dtype)
+            ws.fill_(0xA5)
+        ccgpu.moe_ffn_checkpoint(self.x, self.w_in, self.w_out, self.ckpt, self.y, self.counts, self.cap, self.W, act=act,
+                                 workspace=ws, stream=stream)
+
+    def backward(self, act, stream=None, ws=None):
+        if ws is None:
+            ws = ccgpu.make_moe_ffn_checkpoint_workspace(self.counts, self.cap, self.W, self.F, self.dtype, grad=True)
+            ws.fill_(0xA5)
+        ccgpu.moe_ffn_checkpoint_grad(self.ckpt, self.w_in, self.w_out, self.dy, self.dx, self.dw_in, self.dw_out, self.counts,
+                                      self.cap, self.W, act=act, workspace=ws, stream=stream)
+
+    def check_kept(self):
+        """x kept as defined; g and u within half their block's step of the float32 sums, whose error is that of W
+        additions, and no block's step larger than its largest value asks for."""
+        W, F, per = self.W, self.F, self.per
+        rows = self.ckpt.reshape(self.N, self.E * self.cap, -1) if self.ckpt.numel() else None
+        for e in range(self.E):
+            j, l, at = self.expert(e)
+            if len(at) == 0:
+                continue
+            (x, _), *gu = kept(rows[j][at], W, F)
+            assert not (x != packed(self.rows(self.x, j, at))).any(), f"x of expert {e}"
+            wi = self.w_in[j].reshape(per, 2, F, W)[l].double()
+            xe = self.rows(self.x, j, at)
+            for k, (v, step) in enumerate(gu):
+                want, s = xe @ wi[k].t(), (W + 1) * U * (xe.abs() @ wi[k].abs().t())
+                assert ((v - want).abs() <= step / 2 + s).all(), f"{'gu'[k]} of expert {e}"
+                pad = torch.zeros((len(at), blocks(F) * B), dtype=torch.float64, device=DEV)
+                pad[:, :F] = want.abs() + s
+                top = pad.view(len(at), -1, B).amax(-1).repeat_interleave(B, -1)[:, :F]
+                assert ((step == 2.0 ** -126) | (top >= 63.75 * step)).all(), f"a step of {'gu'[k]}, expert {e}"
+        if rows is not None:
+            assert (rows[~self.keep] == 0x5A).all(), "a row behind the kept ones was written"
+
+    def at_kept(self):
+        """The block at the kept values, whose gradients the checkpoint's are."""
+        W, F = self.W, self.F
+        self.x = torch.zeros((self.N, self.E * self.cap * W), dtype=torch.float64, device=DEV)
+        self.pre = torch.full((self.N, self.E * self.cap * 2 * F), 7.0, dtype=torch.float64, device=DEV)
+        if not self.ckpt.numel():
+            return
+        for j in range(self.N):
+            at = self.keep[j].nonzero().view(-1)
+            (x, _), (g, _), (u, _) = kept(self.ckpt[j].reshape(self.E * self.cap, -1)[at], W, F)
+            self.x[j].view(-1, W)[at] = x
+            self.pre[j].view(-1, 2 * F)[at] = torch.cat([g, u], 1)
+
+    def check(self, act):
+        self.check_forward(act, keep_pre=False)
+        self.check_kept()
+        self.at_kept()
+        self.check_backward(act)
+        self.check_untouched()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", FFNS, ids=[f"{c[:5]}-{i}" for i, c in enumerate(FFNS)])
+def test_checkpoint_and_gradients(case, dtype, act):
+    say("ckpt", case, dtype, act)
+    f = Ckpt(*case, dtype, 51)
+    f.forward(act)
+    torch.cuda.synchronize()
+    say("ckpt grad", case, dtype, act)
+    f.backward(act)
+    torch.cuda.synchronize()
+    f.check(act)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", CASES)
+def test_checkpoint_tiles(name, dtype):
+    """Every tile size and form; and the y of the block that keeps no checkpoint."""
+    case, offset = CASES[name]
+    say("ckpt tiles", name, dtype)
+    f = Ckpt(*case, dtype, 52, offset=offset)
+    Ffn.forward(f, "silu", keep_pre=False)
+    y = f.y.clone()
+    f.y.fill_(7.0)
+    f.forward("silu")
+    f.backward("silu")
+    torch.cuda.synchronize()
+    assert torch.equal(y, f.y)
+    outs = [t.clone() for t in (f.ckpt, f.dx, f.dw_in, f.dw_out)]
+    f.forward("silu")
+    f.backward("silu")
+    torch.cuda.synchronize()
+    for t, was in zip((f.ckpt, f.dx, f.dw_in, f.dw_out), outs):
+        assert torch.equal(t, was)
+    f.check("silu")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (3, 0), (0, 1)], ids=str)
+def test_checkpoint_strides(dtype, pad, offset):
+    say("ckpt strides", dtype, pad, offset)
+    f = Ckpt(2, 4, 37, 96, 80, spread(2, 4, 37, 8, 50), dtype, 53, pad=pad, offset=offset)
+    f.forward("silu")
+    f.backward("silu")
+    torch.cuda.synchronize()
+    f.check("silu")
+
+
+def kept_x(v, dtype):
+    """What the rows v [r, W] are kept as by the call."""
+    r, W = v.shape
+    f = Ckpt(1, 1, r, W, 8, [[r]], dtype, 54)
+    f.x.copy_(v.reshape(1, -1))
+    f.forward("silu")
+    torch.cuda.synchronize()
+    rows = f.ckpt.view(r, -1)
+    return f, kept(rows, W, 8)[0]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_kept_values_at_the_ends_of_the_range(dtype):
+    """Zeros, the smallest and the largest numbers, ties, and tops on both sides of 127.5 steps."""
+    t = torch.float32 if dtype == "f32" else torch.bfloat16
+    big, tiny = torch.finfo(t).max, torch.finfo(t).tiny
+    g = gen(55)
+    v = torch.randn((12, 80), generator=g, device=DEV)
+    v[0] = 0.0
+    v[1] *= tiny
+    v[2] = v[2] / v[2].abs().amax() * big
+    v[3] = torch.randint(-255, 256, (80,), generator=g, device=DEV) * 0.5       # ties of the step 1
+    v[3, ::B] = 127.0
+    v[4, ::B], v[5, ::B] = 127.0, 127.5
+    v[4], v[5] = v[4].clamp(-127, 127), v[5].clamp(-127.5, 127.5)
+    v[6] = -0.0
+    v[7] = tiny * 2.0 ** -6
+    v[8] *= 2.0 ** -119
+    v[9] = big
+    v[10] = -big
+    v = v.to(t).float()
+    f, (x, step) = kept_x(v, dtype)
+    assert not (x != packed(v.double())).any()
+    fine = torch.ones_like(x, dtype=torch.bool)
+    fine[[2, 9, 10]] = False                              # cut at 127 2^121
+    assert ((x - v.double()).abs() <= step / 2)[fine].all()
+    assert ((x - v.double()).abs() <= step)[~fine].all()
+    assert torch.isfinite(x.to(t)).all() and torch.equal(x.to(t).double(), x)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf], ids=str)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_blocks_that_are_not_finite_stand_for_nan(dtype, bad):
+    v = torch.randn((40, 80), generator=gen(56), device=DEV)
+    v[5, 37] = bad
+    f, (x, _) = kept_x(v, dtype)
+    nan = torch.isnan(x)
+    assert nan[5, 32:64].all() and int(nan.sum()) == 32
+    at = layout(80, 8)
+    assert not f.ckpt.view(40, -1)[5, 32:64].any()                      # q = 0
+    f.backward("silu")
+    torch.cuda.synchronize()
+    ok = torch.ones(40, dtype=torch.bool, device=DEV)
+    ok[5] = False
+    assert torch.isnan(f.dx.view(40, 80)[5]).all() and not torch.isnan(f.dx.view(40, 80)[ok]).any()
+    assert at[1] == 80
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_against_differences(act):
+    """The gradients at the kept values against central differences of the 64-bit block there."""
+    f = Ckpt(1, 2, 3, 5, 4, [[3, 2]], "f32", 57)
+    f.forward(act)
+    f.backward(act)
+    torch.cuda.synchronize()
+    W, F = f.W, f.F
+    f.at_kept()
+    h = 1e-4
+    for e in range(2):
+        j, l, at = f.expert(e)
+        x, pre, dy = f.x[0].view(-1, W)[at], f.pre[0].view(-1, 2 * F)[at], f.rows(f.dy, j, at)
+        wi, wo = f.w_in[0].view(2, 2 * F, W)[l].double(), f.w_out[0].view(2, W, F)[l].double()
+
+        def loss(x_, wi_, wo_):
+            # moves of x and w_in move the kept g and u as the product would
+            gu = pre + (x_ @ wi_.t() - x @ wi.t())
+            return float((((act64(gu[:, :F], act)[0] * gu[:, F:]) @ wo_.t()) * dy).sum())
+        args = [x, wi, wo]
+        grads = [f.dx[0].view(-1, W)[at], f.dw_in[0].view(2, 2 * F, W)[l], f.dw_out[0].view(2, W, F)[l]]
+        for k, got in enumerate(grads):
+            for i in np.ndindex(*args[k].shape):
+                v = []
+                for s in (h, -h):
+                    y = [a.clone() for a in args]
+                    y[k][i] += s
+                    v.append(loss(*y))
+                # h^2 / 6 of a third derivative below 100
+                assert abs((v[0] - v[1]) / (2 * h) - float(got[i])) < 1e-5, (k, i)
+
+
+def test_many_ranks_and_experts():
+    f = Ckpt(32, 64, 2, 16, 8, spread(32, 64, 2, 10, 2), "bf16", 58)
+    f.forward("silu")
+    f.backward("silu")
+    torch.cuda.synchronize()
+    f.check("silu")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_checkpoint_past_4_gib(dtype):
+    """An expert whose rows lie behind byte 2^32 of its rank's checkpoint."""
+    W, F = 256, 64
+    row = ccgpu.moe_ffn_checkpoint_row(W, F)
+    cap = int(1.5 * (1 << 32)) // (4 * row)
+    f = object.__new__(Ckpt)
+    f.N, f.E, f.cap, f.W, f.F, f.dtype, f.per = 1, 4, cap, W, F, dtype, 4
+    f.counts = [[3, 0, 0, 70]]
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    f.keep = torch.zeros(1, 4 * cap, dtype=torch.bool, device=DEV)
+    f.keep[0, :3] = f.keep[0, 3 * cap:3 * cap + 70] = True
+    at = f.keep[0].nonzero().view(-1)
+    g = gen(59)
+    f.x, f.dy, f.y, f.dx = (torch.empty(1, 4 * cap * W, dtype=dt, device=DEV) for _ in range(4))
+    for t in (f.x, f.dy):
+        t.view(4 * cap, W)[at] = torch.randn(len(at), W, generator=g, device=DEV).to(dt)
+    f.w_in = (torch.randn(1, 4 * 2 * F * W, generator=g, device=DEV) / math.sqrt(W)).to(dt)
+    f.w_out = (torch.randn(1, 4 * W * F, generator=g, device=DEV) / math.sqrt(F)).to(dt)
+    f.dw_in, f.dw_out = torch.empty_like(f.w_in), torch.empty_like(f.w_out)
+    f.ckpt = torch.full((1, 4 * cap * row), 0x5A, dtype=torch.uint8, device=DEV)
+    f.pre = None
+    say("ckpt past 4 GiB", dtype)
+    f.forward("silu")
+    f.backward("silu")
+    torch.cuda.synchronize()
+    f.check_forward("silu", keep_pre=False)
+    f.check_kept()
+    f.at_kept()
+    f.check_backward("silu")

@@ -1,0 +1,353 @@
+"""8-bit rows, the experts' product of them and the gated block in 8-bit integers
+on the GPU.  Integers and scales are compared exactly; results within bounds
+that count float32 half steps (U) and the one rounding of results."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV, TORCH_DT
+from model_tiles import CASES
+from ring_allreduce_reduction_02_amd import ccgpu
+from test_gpu_model import FFNS, HALF, U, Ffn, act64, gen, near, ranks, say, spread
+
+pytestmark = pytest.mark.gpu
+
+
+def bytes_of(N, L, pad=0, offset=0, fill=55):
+    """An int8 [N, L] view, rows L + pad apart, `offset` bytes into an allocation."""
+    b = torch.full((N * (L + pad) + offset + 16,), fill, dtype=torch.int8, device=DEV)
+    return b[offset:offset + N * (L + pad)].view(N, L + pad)[:, :L]
+
+
+def scale(top):
+    return top / torch.full_like(top, 127.0)      # a division (by a Python number torch multiplies by 1 / 127)
+
+
+def quantized(v):
+    """Integers (float64) and float32 scales of rows v (float32 or float64 values, no NaN), by the definition."""
+    s = scale(v.abs().amax(-1).float())
+    q = torch.where(s[..., None] > 0, torch.round(v.double() / s.double()[..., None]), 0.0).clamp(-127, 127)
+    return q, s
+
+
+# ------------------------------------------------------------------ rows
+
+# (ranks, rows, width, pad, offset)
+ROWS = [(1, 1, 1, 0, 0), (2, 3, 5, 0, 0), (3, 7, 515, 3, 1), (8, 4, 2048, 16, 0), (1, 257, 64, 0, 3), (2, 9, 4096, 0, 0), (2, 3, 4097, 0, 0),
+        (1, 2, 20001, 1, 2), (64, 5, 24, 0, 0), (2, 0, 9, 0, 0), (1, 1000, 33, 0, 0), (1, 3, 70000, 0, 0), (2, 33, 2049, 5, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", ROWS, ids=str)
+def test_quantize_rows(case, dtype):
+    N, R, W, pad, off = case
+    say("quantize_rows", case, dtype)
+    g = gen(R + W)
+    v = torch.randn((N, R, W), generator=g, device=DEV) * torch.exp(3 * torch.randn((N, R, 1), generator=g, device=DEV))
+    v[:, 1::5] = 0.0
+    v[:, 2::7] = torch.round(v[:, 2::7] * 3) * 0.5            # ties
+    if R > 6:
+        v[:, 3] *= 1e-39                                      # subnormal rows
+        v[:, 4] = v[:, 4] / v[:, 4].abs().amax(-1, keepdim=True) * 3e38
+        v[:, 6, 0] = 127.0                                    # the scale 1: halves are ties
+        v[:, 6, 1:] = torch.randint(-200, 201, (N, W - 1), generator=g, device=DEV) * 0.5
+    x = ranks(N, R * W, dtype, pad, off, v) if R else torch.empty(N, 0, dtype=TORCH_DT[dtype], device=DEV)
+    q, s = bytes_of(N, R * W, pad, off), ranks(N, R, "f32", 2)
+    ccgpu.quantize_rows(x, q, s, W)
+    torch.cuda.synchronize()
+    wq, ws = quantized(x.reshape(N, R, W).float())
+    assert torch.equal(s, ws.reshape(N, R))
+    assert torch.equal(q.reshape(N, R, W).double(), wq + 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_rows_next_to_the_borders(dtype):
+    """Values one step of their type on either side of every half-integer of the scale, and on it where there is one."""
+    N, R, W = 1, 40, 1024
+    g = gen(3)
+    top = (torch.rand((R, 1), generator=g, device=DEV) + 0.5).to(TORCH_DT[dtype]).float()
+    s = scale(top)
+    k = torch.randint(-127, 127, (R, W), generator=g, device=DEV) + 0.5
+    v = (k.double() * s.double()).to(TORCH_DT[dtype])
+    step = torch.randint(-1, 2, (R, W), generator=g, device=DEV)
+    bits = v.view(torch.int16 if dtype == "bf16" else torch.int32)
+    v = (bits + step.to(bits.dtype)).view(TORCH_DT[dtype])
+    v[:, :1] = top.to(TORCH_DT[dtype])
+    v = torch.where(v.float().abs() > top, top.to(TORCH_DT[dtype]), v)
+    x = v.reshape(N, R * W).contiguous()
+    q, sc = bytes_of(N, R * W), ranks(N, R, "f32")
+    ccgpu.quantize_rows(x, q, sc, W)
+    torch.cuda.synchronize()
+    wq, ws = quantized(x.reshape(N, R, W).float())
+    assert torch.equal(sc, ws) and torch.equal(q.reshape(N, R, W).double(), wq)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf], ids=str)
+@pytest.mark.parametrize("W", [7, 700, 9000])
+def test_quantize_rows_marks_rows_that_are_not_finite(W, bad):
+    x = torch.randn(1, 5 * W, generator=gen(4), device=DEV)
+    x[0, 2 * W + W // 2] = bad
+    q, s = bytes_of(1, 5 * W), ranks(1, 5, "f32")
+    ccgpu.quantize_rows(x, q, s, W)
+    torch.cuda.synchronize()
+    assert torch.isnan(s[0]).tolist() == [False, False, True, False, False]
+    assert not q[0, 2 * W:3 * W].any() and q[0, 3 * W:].any()
+
+
+# ------------------------------------------------------------------ the product
+
+class Product:
+    """The buffers of one case; scales of rows behind the kept ones are NaN."""
+
+    def __init__(self, N, E, cap, W, C, counts, dtype, seed, pad=0, offset=0, full=False):
+        self.N, self.E, self.cap, self.W, self.C, self.counts, self.dtype, self.per = N, E, cap, W, C, counts, dtype, E // N
+        g = gen(seed)
+        f = object.__new__(Ffn)
+        f.N, f.E, f.cap, f.per, f.counts = N, E, cap, E // N, counts
+        f.keep = torch.zeros((N, N, self.per, cap), dtype=torch.bool, device=DEV)
+        for i in range(N):
+            for e in range(E):
+                f.keep[e // self.per, i, e % self.per, :min(counts[i][e], cap)] = True
+        f.keep = f.keep.reshape(N, E * cap)
+        self.f = f
+
+        def ints8(n):
+            t = bytes_of(N, n, pad * 4, offset)
+            t.copy_(torch.full((N, n), 127, device=DEV, dtype=torch.int8) if full else
+                    torch.randint(-127, 128, (N, n), generator=g, device=DEV, dtype=torch.int8))
+            return t
+        self.x, self.w = ints8(E * cap * W), ints8(self.per * C * W)
+        sx = torch.rand((N, E * cap), generator=g, device=DEV) * 0.1
+        sx[~f.keep] = math.nan
+        self.sx = ranks(N, E * cap, "f32", pad, offset, sx)
+        self.sw = ranks(N, self.per * C, "f32", pad, offset, torch.rand((N, self.per * C), generator=g, device=DEV) * 0.1)
+        self.y = ranks(N, E * cap * C, dtype, pad, offset)
+        self.y.fill_(7.0)
+
+    def run(self):
+        ws = ccgpu.make_moe_matmul_int8_workspace(self.counts, self.cap, self.W, self.C)
+        ws.fill_(0xA5)
+        ccgpu.moe_matmul_int8(self.x, self.sx, self.w, self.sw, self.y, self.counts, self.cap, self.W, workspace=ws)
+
+    def check(self):
+        N, E, cap, W, C, r = self.N, self.E, self.cap, self.W, self.C, HALF[self.dtype]
+        for e in range(E):
+            j, l, at = self.f.expert(e)
+            x = self.x[j].reshape(E * cap, W)[at].double()
+            w = self.w[j].reshape(self.per, C, W)[l].double()
+            y = (x @ w.t()) * self.sx[j][at].double()[:, None] * self.sw[j].reshape(self.per, C)[l].double()
+            # the sum and two products rounded to float32, one rounding to the result's type
+            near(self.y[j].reshape(E * cap, C)[at], y, (3.01 * U + r * 1.01) * y.abs() + 1e-38, f"y of expert {e}")
+        if self.y.numel():
+            assert (self.y.reshape(N, E * cap, C)[~self.f.keep] == 7.0).all(), "a row behind the kept ones was written"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", FFNS, ids=[f"{c[:5]}-{i}" for i, c in enumerate(FFNS)])
+def test_moe_matmul_int8(case, dtype):
+    say("moe_matmul_int8", case, dtype)
+    p = Product(*case, dtype, 21)
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", CASES)
+def test_moe_matmul_int8_tiles(name, dtype):
+    """Tiles of every size, by direct loads and through registers."""
+    case, offset = CASES[name]
+    say("moe_matmul_int8 tiles", name, dtype)
+    p = Product(*case, dtype, 22, offset=offset)
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+    y = p.y.clone()
+    p.y.fill_(7.0)
+    p.run()
+    torch.cuda.synchronize()
+    assert torch.equal(y, p.y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,offset", [(4, 0), (4, 16), (3, 0), (0, 1), (0, 4), (5, 7)], ids=str)
+def test_moe_matmul_int8_strides(dtype, pad, offset):
+    say("moe_matmul_int8 strides", dtype, pad, offset)
+    p = Product(2, 4, 37, 96, 80, spread(2, 4, 37, 8, 50), dtype, 23, pad, offset)
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+
+
+def test_moe_matmul_int8_longest_sum():
+    """Every product 127 * 127 over the longest summed axis: 2.1e9, inside int32, and one of -128 * -128 by hand."""
+    W = (1 << 17) - 1
+    p = Product(1, 1, 2, W, 5, [[2]], "f32", 24, full=True)
+    p.run()
+    torch.cuda.synchronize()
+    p.check()
+    p.x.fill_(-128), p.w.fill_(-128), p.sx.fill_(1.0), p.sw.fill_(1.0)
+    p.run()
+    torch.cuda.synchronize()
+    assert (p.y == float(np.float32(128 * 128 * W))).all()
+
+
+def test_moe_matmul_int8_marked_rows():
+    """A row or channel whose scale is NaN gives NaN there and nowhere else."""
+    p = Product(1, 1, 70, 64, 32, [[70]], "bf16", 25)
+    p.sx[0, 3], p.sw[0, 9] = math.nan, math.nan
+    p.run()
+    torch.cuda.synchronize()
+    nan = torch.isnan(p.y.view(70, 32))
+    assert nan[3].all() and nan[:, 9].all() and int(nan.sum()) == 32 + 70 - 1
+
+
+def test_rows_quantised_before_the_dispatch():
+    """Token rows quantised on the token side, dispatched as int32 words beside their scales, multiplied on the
+    expert side and combined: what the product of the rows themselves gives, sent as bf16."""
+    N, E, cap, W, C = 2, 4, 24, 96, 64
+    counts = spread(N, E, cap, 31, 30)
+    rows = max(sum(r) for r in counts)
+    g = gen(32)
+    x = torch.randn(N, rows * W, generator=g, device=DEV).bfloat16()
+    q, s = torch.empty(N, rows * W, dtype=torch.int8, device=DEV), torch.empty(N, rows, device=DEV)
+    ccgpu.quantize_rows(x, q, s, W)
+    w = torch.randn(N, E // N * C * W, generator=g, device=DEV)
+    wq, sw = torch.empty(N, E // N * C * W, dtype=torch.int8, device=DEV), torch.empty(N, E // N * C, device=DEV)
+    ccgpu.quantize_rows(w, wq, sw, W)
+    eq = torch.zeros(N, E * cap * W // 4, dtype=torch.int32, device=DEV)
+    es = torch.zeros(N, E * cap, device=DEV)
+    ccgpu.moe_dispatch_padded(q.view(torch.int32), eq, counts, cap, W // 4)
+    ccgpu.moe_dispatch_padded(s, es, counts, cap, 1)
+    y = torch.zeros(N, E * cap * C, dtype=torch.bfloat16, device=DEV)
+    ccgpu.moe_matmul_int8(eq.view(torch.int8), es, wq, sw, y, counts, cap, W, workspace=ccgpu.make_moe_matmul_int8_workspace(counts, cap, W, C))
+    back = torch.zeros(N, rows * C, dtype=torch.bfloat16, device=DEV)
+    ccgpu.moe_combine_padded(y, back, counts, cap, C)
+    torch.cuda.synchronize()
+    qx, sx = quantized(x.view(N, rows, W).float())
+    qw, tw = quantized(w.view(E, C, W))
+    for r in range(N):
+        at = 0
+        for e in range(E):
+            n = min(counts[r][e], cap)
+            want = (qx[r, at:at + n] @ qw[e].t()) * sx[r, at:at + n].double()[:, None] * tw[e].double()
+            near(back[r].view(rows, C)[at:at + n], want, (3.01 * U + 2.0 ** -8 * 1.01) * want.abs(), f"rank {r}, expert {e}")
+            at += counts[r][e]
+
+
+# ------------------------------------------------------------------ the block
+
+class Block(Ffn):
+    """The feed-forward block with quantised weights."""
+
+    def __init__(self, *a, **kw):
+        super().__init__(*a, **kw)
+        N, per, W, F = self.N, self.per, self.W, self.F
+        pad, off = kw.get("pad", 0), kw.get("offset", 0)
+        self.q_in, self.q_out = bytes_of(N, per * 2 * F * W, 4 * pad, off), bytes_of(N, per * W * F, 4 * pad, off)
+        self.s_in, self.s_out = ranks(N, per * 2 * F, "f32", pad, off), ranks(N, per * W, "f32", pad, off)
+        ccgpu.quantize_rows(self.w_in, self.q_in, self.s_in, W)
+        ccgpu.quantize_rows(self.w_out, self.q_out, self.s_out, F)
+
+    def forward8(self, act, stream=None, ws=None):
+        if ws is None:
+            ws = ccgpu.make_moe_ffn_int8_workspace(self.counts, self.cap, self.W, self.F, self.dtype)
+            ws.fill_(0xA5)
+        ccgpu.moe_ffn_int8(self.x, self.q_in, self.s_in, self.q_out, self.s_out, self.y, self.counts, self.cap, self.W,
+                           act=act, workspace=ws, stream=stream)
+
+    def check8(self, act):
+        W, F, r, per = self.W, self.F, HALF[self.dtype], self.per
+        dt = TORCH_DT[self.dtype]
+        for e in range(self.E):
+            j, l, at = self.expert(e)
+            if len(at) == 0:
+                continue
+            qx, sx = quantized(self.rows(self.x, j, at).float())
+            wi = self.q_in[j].reshape(per, 2 * F, W)[l].double() * self.s_in[j].reshape(per, 2 * F, 1)[l].double()
+            gu = (qx * sx.double()[:, None]) @ wi.t()
+            g, u = gu[:, :F], gu[:, F:]
+            sg, su = 3.01 * U * g.abs(), 3.01 * U * u.abs()
+            a, _ = act64(g, act)
+            h = a * u
+            # the activation's slope is below 1.13; its own error is below 16 U of |g| (and 4 U)
+            dh = (1.13 * sg + (16 * g.abs() + 4) * U) * (u.abs() + su) + a.abs() * su + 2 * U * (h.abs()) + 1e-40
+            # rounding is monotone, so the rows that are quantised lie between these
+            lo, hi = (h - dh).float().to(dt).double(), (h + dh).float().to(dt).double()
+            least = scale(torch.where(lo * hi > 0, torch.minimum(lo.abs(), hi.abs()), 0.0).amax(-1).float())
+            most = scale(torch.maximum(lo.abs(), hi.abs()).amax(-1).float())
+            ends = []
+            for s in (least.double()[:, None], most.double()[:, None]):
+                for v in (lo, hi):
+                    q = torch.where(s > 0, torch.round(v / torch.where(s > 0, s, 1.0)), 0.0).clamp(-127, 127)
+                    ends += [q * least.double()[:, None], q * most.double()[:, None]]
+            ends = torch.stack(ends)
+            lo, hi = ends.amin(0), ends.amax(0)
+            c, rad = (lo + hi) / 2, (hi - lo) / 2
+            wo = self.q_out[j].reshape(per, W, F)[l].double() * self.s_out[j].reshape(per, W, 1)[l].double()
+            y = c @ wo.t()
+            # where the integers cancel, the 64-bit sum keeps the rounding of its F products and additions
+            err = rad @ wo.abs().t() + (F + 4) * 2.0 ** -53 * (c.abs() @ wo.abs().t())
+            err = err + 3.01 * U * (y.abs() + err)
+            near(self.rows(self.y, j, at), y, err + r * 1.01 * (y.abs() + err) + 1e-38, f"y of expert {e}")
+        assert (self.y.reshape(self.N, self.E * self.cap, -1)[~self.keep] == 7.0).all() if self.y.numel() else True
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", FFNS, ids=[f"{c[:5]}-{i}" for i, c in enumerate(FFNS)])
+def test_moe_ffn_int8(case, dtype, act):
+    say("moe_ffn_int8", case, dtype, act)
+    f = Block(*case, dtype, 26)
+    f.forward8(act)
+    torch.cuda.synchronize()
+    f.check8(act)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", CASES)
+def test_moe_ffn_int8_tiles(name, dtype):
+    case, offset = CASES[name]
+    say("moe_ffn_int8 tiles", name, dtype)
+    f = Block(*case, dtype, 27, offset=offset)
+    f.forward8("silu")
+    torch.cuda.synchronize()
+    f.check8("silu")
+    y = f.y.clone()
+    f.y.fill_(7.0)
+    f.forward8("silu")
+    torch.cuda.synchronize()
+    assert torch.equal(y, f.y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,offset", [(4, 0), (8, 16), (3, 0), (0, 1)], ids=str)
+def test_moe_ffn_int8_strides(dtype, pad, offset):
+    say("moe_ffn_int8 strides", dtype, pad, offset)
+    f = Block(2, 4, 37, 96, 80, spread(2, 4, 37, 8, 50), dtype, 28, pad=pad, offset=offset)
+    f.forward8("gelu")
+    torch.cuda.synchronize()
+    f.check8("gelu")
+
+
+def test_moe_ffn_int8_wide_rows():
+    """Rows longer than a wave keeps in registers."""
+    f = Block(1, 2, 9, 9000, 4104, [[9, 3]], "bf16", 29)
+    f.forward8("silu")
+    torch.cuda.synchronize()
+    f.check8("silu")
+
+
+def test_moe_ffn_int8_keeps_infinities_in_their_rows():
+    f = Block(1, 1, 70, 64, 32, [[70]], "bf16", 30)
+    f.forward8("silu")
+    y = f.y.clone().view(70, 64)
+    x = f.x.view(70, 64)
+    x[3], x[40, 5] = math.nan, math.inf
+    f.forward8("silu")
+    torch.cuda.synchronize()
+    ok = torch.ones(70, dtype=torch.bool, device=DEV)
+    ok[[3, 40]] = False
+    assert torch.equal(f.y.view(70, 64)[ok], y[ok]) and torch.isnan(f.y.view(70, 64)[~ok]).all()
