@@ -15,6 +15,7 @@
 
 #include "cc_device.h"
 #include "cc_llm.h"
+#include "cc_wave.h"
 
 namespace cc {
 namespace {
@@ -45,38 +46,39 @@ struct BalArgs {
 
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// Sums and maxima over the L = 2^k consecutive lanes of a token, on all of them,
-// in a fixed order.
-template <int L, class T, class F>
-__device__ __forceinline__ T over_lanes(T x, F f) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) x = f(x, __shfl_xor(x, d));
-  return x;
-}
-
-// Lane l of a token holds the 16-byte chunks q L + l of its row.
+// Lane l of the L that hold a token has the 16-byte chunks q L + l of its row.
 template <int DT, int L>
 struct Row {
   static constexpr int CH = Ty<DT>::V, Q = kV / CH, SZ = Ty<DT>::SZ;
+  u32x4 w[Q];
   __device__ __forceinline__ static int expert(int l, int q) { return (q * L + l) * CH; }
-  __device__ __forceinline__ static void load(const char* row, int E, int l, float none, float* x) {
+  // elements past E: -inf (PAD_LOW) or 0
+  template <bool PAD_LOW>
+  __device__ __forceinline__ void load(const char* row, int E, int l) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int e = expert(l, q);
       if (e + CH <= E) {
-        unpack<DT>(*(const u32x4_any*)(row + (uint64_t)e * SZ), x + q * CH);
+        w[q] = *(const u32x4_any*)(row + (uint64_t)e * SZ);
       } else {
+        float x[CH];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) x[q * CH + i] = e + i < E ? ld1<DT>(row + (uint64_t)(e + i) * SZ) : none;
+        for (int i = 0; i < CH; ++i)
+          x[i] = e + i < E ? ld1<DT>(row + (uint64_t)(e + i) * SZ) : PAD_LOW ? -INFINITY : 0.0f;
+        w[q] = pack_row<DT>(x);   // widened and packed again: the same bits
       }
     }
+  }
+  __device__ __forceinline__ void values(float* x) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) unpack<DT>(w[q], x + q * CH);
   }
   __device__ __forceinline__ static void store(char* row, int E, int l, const float* x) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int e = expert(l, q);
       if (e + CH <= E) {
-        *(u32x4_any*)(row + (uint64_t)e * SZ) = pack<DT>(x + q * CH);
+        *(u32x4_any*)(row + (uint64_t)e * SZ) = pack_row<DT>(x + q * CH);
       } else {
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -88,159 +90,212 @@ struct Row {
 
 // exp(l - max l) in place of the logits, and their sum: NaN if a logit is NaN or
 // the maximum +inf, 0 if every logit is -inf.
-template <int L>
+// bf16: the hardware's exp2 (1 ulp) of the difference d times log2(e), whose
+// rounding and the constant's make (1.25 |d| + 2) 2^-24 of the value, the size of
+// what d's own rounding makes of float32 logits; expf on them.
+template <int DT, int L>
 __device__ __forceinline__ float exps(float* x) {
-  float top = -INFINITY;
+  float top = x[0];
 #pragma unroll
-  for (int i = 0; i < kV; ++i) top = fmaxf(top, x[i]);
-  top = over_lanes<L>(top, [](float a, float b) { return fmaxf(a, b); });
-  const float m = top == -INFINITY ? 0.0f : top;
+  for (int i = 1; i < kV; ++i) top = fmaxf(top, x[i]);
+  top = group_max<L>(top);
+  const float m = top > -INFINITY ? top : 0.0f;   // (NaN, where every logit is one: they stay NaN)
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
-    x[i] = expf(x[i] - m);
+    if constexpr (DT == DT_BF16) x[i] = __builtin_amdgcn_exp2f((x[i] - m) * 1.44269504088896341f);
+    else x[i] = expf(x[i] - m);
     s += x[i];
   }
-  return over_lanes<L>(s, [](float a, float b) { return a + b; });
+  return group_sum<L>(s);
 }
 
 // Workgroup b of a rank sums the probabilities of every blocks-th group of
-// tokens and counts those that have any.
+// tokens and counts those that have any; the next group's logits are under way
+// meanwhile.
 template <int DT, int L>
 __global__ __launch_bounds__(kBalanceBlock) void k_balance(BalArgs a) {
-  constexpr int PER = kBalanceBlock / L;    // tokens at a time
+  constexpr int G = kBalanceBlock / L, C = L * kV;      // tokens at a time, columns
+  constexpr int P = C < kBalanceBlock ? kBalanceBlock / C : 1;   // parts of a column's sum
   typedef Row<DT, L> R;
-  __shared__ float red[kBalanceBlock / 64][L * kV];
+  __shared__ __attribute__((aligned(16))) float red[G][C];
+  __shared__ float part[P][C];
   __shared__ uint32_t red_live[kBalanceBlock / 64];
-  const int tid = threadIdx.x, l = tid % L, lane = tid & 63, wave = tid >> 6;
-  const uint64_t r = blockIdx.y;
+  const int tid = threadIdx.x, l = tid % L;
+  const uint64_t r = blockIdx.y, step = (uint64_t)a.blocks * G, pitch = (uint64_t)a.E * R::SZ;
+  const char* logits = a.logits + r * a.ls;
   float sum[kV] = {};
   uint32_t live = 0;
-  for (uint64_t t = (uint64_t)blockIdx.x * PER + tid / L; t < a.tokens; t += (uint64_t)a.blocks * PER) {
+  R now, next;
+  uint64_t t = (uint64_t)blockIdx.x * G + tid / L;
+  if (t < a.tokens) next.template load<true>(logits + t * pitch, a.E, l);
+  for (; t < a.tokens; t += step) {
+    now = next;
+    if (t + step < a.tokens) next.template load<true>(logits + (t + step) * pitch, a.E, l);
     float x[kV];
-    R::load(a.logits + r * a.ls + t * a.E * R::SZ, a.E, l, -INFINITY, x);
-    const float s = exps<L>(x);
+    now.values(x);
+    const float s = exps<DT, L>(x);
     const float inv = s == 0.0f ? 0.0f : 1.0f / s;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) sum[i] += x[i] * inv;
+    for (int i = 0; i < kV; ++i) sum[i] = __builtin_fmaf(x[i], inv, sum[i]);
     live += l == 0 && s != 0.0f ? 1 : 0;
   }
+  live = group_usum<64>(live);
+  if ((tid & 63) == 0) red_live[tid >> 6] = live;
 #pragma unroll
-  for (int d = L; d < 64; d <<= 1) {
-#pragma unroll
-    for (int i = 0; i < kV; ++i) sum[i] += __shfl_xor(sum[i], d);
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) live += __shfl_xor(live, d);
-  if (lane < L) {
-#pragma unroll
-    for (int i = 0; i < kV; ++i) red[wave][R::expert(l, i / R::CH) + i % R::CH] = sum[i];
-  }
-  if (lane == 0) red_live[wave] = live;
+  for (int i = 0; i < kV; ++i) red[tid / L][R::expert(l, i / R::CH) + i % R::CH] = sum[i];
   __syncthreads();
   const uint64_t at = r * a.blocks + blockIdx.x;
-  for (int e = tid; e < a.E; e += kBalanceBlock)
-    a.part[at * a.E + e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+  for (int e = tid % C; e < C; e += kBalanceBlock) {
+    float s = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G / P; ++g) s += red[tid / C * (G / P) + g][e];
+    if constexpr (P > 1) part[tid / C][e] = s;
+    else if (e < a.E) a.part[at * a.E + e] = s;
+  }
+  if constexpr (P > 1) {
+    __syncthreads();
+    if (tid < a.E) {
+      float s = 0.0f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) s += part[p][tid];
+      a.part[at * a.E + tid] = s;
+    }
+  }
   if (tid == 0) a.live[at] = red_live[0] + red_live[1] + red_live[2] + red_live[3];
 }
 
 // The sums of a rank's workgroups (or of all ranks'), a workgroup: its threads
-// are C = 64 .. 1024 columns times 1024 / C parts of the rows.
+// are C = 64 .. 1024 columns times 1024 / C parts of the rows.  One column's sums,
+// counts and loss then lie in the threads below C, whose waves are joined.
 constexpr int kJoin = 1024;
 __global__ __launch_bounds__(kJoin) void k_balance_join(BalArgs a) {
   __shared__ float sum[kJoin];
-  __shared__ long long num[kJoin];
-  const int tid = threadIdx.x, E = a.E;
+  __shared__ uint32_t num[2][kJoin / 64];
+  __shared__ float lsum[kJoin / 64];
+  const int tid = threadIdx.x, wave = tid >> 6, E = a.E;
   int C = 64;
   while (C < E) C *= 2;
   const int parts = kJoin / C, e = tid % C, part = tid / C;
   const uint32_t first = a.summed ? 0 : blockIdx.x, ranks = a.summed ? a.N : 1;
-  const uint64_t row0 = (uint64_t)first * a.blocks, rows = (uint64_t)ranks * a.blocks;
+  const uint64_t row0 = (uint64_t)first * a.blocks;
+  const uint32_t rows = ranks * a.blocks;
   float s = 0.0f;
-  if (e < E)
-    for (uint64_t k = part; k < rows; k += parts) s += a.part[(row0 + k) * E + e];
-  long long n = 0;
-  for (uint64_t k = tid; k < rows; k += kJoin) n += a.live[row0 + k];
-  sum[tid] = s;
-  num[tid] = n;
-  __syncthreads();
-  for (int d = kJoin / 2; d; d >>= 1) {
-    if (tid < d) {
-      num[tid] += num[tid + d];
-      if (d >= C) sum[tid] += sum[tid + d];
+  if (e < E) {
+    const float* p = a.part + row0 * E + e;
+    uint32_t k = part;
+    for (; k + 7 * parts < rows; k += 8 * parts) {   // eight loads under way
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p[(uint64_t)(k + i * parts) * E];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
     }
-    __syncthreads();
+    for (; k < rows; k += parts) s += p[(uint64_t)k * E];
   }
-  const long long T = num[0];
-  const float p = e < E && part == 0 && T ? sum[tid] / (float)T : 0.0f;
+  uint32_t n = 0;
+  for (uint32_t k = tid; k < rows; k += kJoin) n += a.live[row0 + k];
   long long c = 0;
-  if (e < E && part == 0)
-    for (uint32_t r = 0; r < ranks; ++r) c += ((const int*)(a.counts + (uint64_t)(first + r) * a.cs))[e];
-  __syncthreads();
-  num[tid] = c;
-  __syncthreads();
-  for (int d = kJoin / 2; d; d >>= 1) {
-    if (tid < d) num[tid] += num[tid + d];
-    __syncthreads();
+  if (tid < E)
+    for (uint32_t r = 0; r < ranks; ++r) c += ((const int*)(a.counts + (uint64_t)(first + r) * a.cs))[tid];
+  sum[tid] = s;
+  n = group_usum<64>(n);
+  // 64-bit sums in two halves (ranks times int32: the upper ones below 2^21)
+  const uint32_t lo = group_usum<64>((uint32_t)(c & 0xffff)), hi = group_usum<64>((uint32_t)(c >> 16));
+  __shared__ uint32_t live[kJoin / 64];
+  if ((tid & 63) == 0) {
+    live[wave] = n;
+    num[0][wave] = lo;
+    num[1][wave] = hi;
   }
-  const long long S = num[0];
-  sum[tid] = S ? ((float)c / (float)S) * p : 0.0f;
   __syncthreads();
-  for (int d = kJoin / 2; d; d >>= 1) {
-    if (tid < d) sum[tid] += sum[tid + d];
-    __syncthreads();
+  uint32_t T = 0;
+  long long S = 0;
+#pragma unroll
+  for (int w = 0; w < kJoin / 64; ++w) {
+    T += live[w];
+    S += (long long)num[0][w] + ((long long)(int)num[1][w] << 16);
   }
+  float p = 0.0f, v = 0.0f;
+  if (tid < E) {
+    for (int k = 0; k < parts; ++k) p += sum[k * C + tid];
+    p = T ? p / (float)T : 0.0f;
+    v = S ? ((float)c / (float)S) * p : 0.0f;
+  }
+  v = group_sum<64>(v);
+  if ((tid & 63) == 0) lsum[wave] = v;
+  __syncthreads();
+  float loss = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoin / 64; ++w) loss += lsum[w];
   for (uint32_t r = first; r < first + ranks; ++r) {
-    if (e < E && part == 0) {
-      ((int*)(a.total + (uint64_t)r * a.ts))[e] = (int)c;
-      ((float*)(a.prob + (uint64_t)r * a.ps))[e] = p;
+    int* total = (int*)(a.total + (uint64_t)r * a.ts);
+    if (tid < E) {
+      total[tid] = (int)c;
+      ((float*)(a.prob + (uint64_t)r * a.ps))[tid] = p;
     }
     if (tid == 0) {
-      ((int*)(a.total + (uint64_t)r * a.ts))[E] = (int)T;
-      *(float*)(a.loss + (uint64_t)r * a.os) = (float)E * sum[0];
+      total[E] = (int)T;
+      *(float*)(a.loss + (uint64_t)r * a.os) = (float)E * loss;
     }
   }
 }
 
-template <int DT, int L>
+template <int DT, int L, bool BASE>
 __global__ __launch_bounds__(kBalanceBlock) void k_balance_grad(BalArgs a) {
-  constexpr int PER = kBalanceBlock / L;
+  constexpr int G = kBalanceBlock / L;
   typedef Row<DT, L> R;
   const int tid = threadIdx.x, l = tid % L, E = a.E;
-  const uint64_t r = blockIdx.y;
+  const uint64_t r = blockIdx.y, step = (uint64_t)a.blocks * G, pitch = (uint64_t)E * R::SZ;
+  const char* logits = a.logits + r * a.ls;
+  const char* base = a.base + r * a.bs;
+  char* out = a.dlogits + r * a.ds;
+  uint64_t t = (uint64_t)blockIdx.x * G + tid / L;
+  R now, next, add, next_add;
+  if (t < a.tokens) {
+    next.template load<true>(logits + t * pitch, E, l);
+    if constexpr (BASE) next_add.template load<false>(base + t * pitch, E, l);
+  }
   const int* total = (const int*)(a.total + r * a.ts);
   float f[kV];
-  long long S = 0;
+  uint32_t lo = 0, hi = 0;   // the counts' sum, of at most 1024 below 2^31, in two halves
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
     const int e = R::expert(l, i / R::CH) + i % R::CH, c = e < E ? total[e] : 0;
-    S += c;
+    lo += (uint32_t)(c & 0xffff);
+    hi += (uint32_t)(c >> 16);
     f[i] = (float)c;
   }
-  S = over_lanes<L>(S, [](long long x, long long y) { return x + y; });
+  const long long S = (long long)group_usum<L>(lo) + ((long long)(int)group_usum<L>(hi) << 16);
 #pragma unroll
   for (int i = 0; i < kV; ++i) f[i] = S ? f[i] / (float)S : 0.0f;
   const int T = total[E];
   const float scale = T > 0 ? *(const float*)(a.loss + r * a.os) * ((float)E / (float)T) : 0.0f;
-  for (uint64_t t = (uint64_t)blockIdx.x * PER + tid / L; t < a.tokens; t += (uint64_t)a.blocks * PER) {
+  for (; t < a.tokens; t += step) {
+    now = next;
+    add = next_add;
+    if (t + step < a.tokens) {
+      next.template load<true>(logits + (t + step) * pitch, E, l);
+      if constexpr (BASE) next_add.template load<false>(base + (t + step) * pitch, E, l);
+    }
     float x[kV], b[kV];
-    R::load(a.logits + r * a.ls + t * E * R::SZ, E, l, -INFINITY, x);
-    if (a.base) R::load(a.base + r * a.bs + t * E * R::SZ, E, l, 0.0f, b);
-    const float s = exps<L>(x);
+    now.values(x);
+    if constexpr (BASE) add.values(b);
+    const float s = exps<DT, L>(x);
     const float inv = s == 0.0f ? 0.0f : 1.0f / s;
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       x[i] *= inv;
-      dot += x[i] * f[i];
+      dot = __builtin_fmaf(x[i], f[i], dot);
     }
-    dot = over_lanes<L>(dot, [](float u, float v) { return u + v; });
+    dot = group_sum<L>(dot);
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-      x[i] = scale * x[i] * (f[i] - dot);
-      if (a.base) x[i] += b[i];
+      x[i] *= scale;
+      x[i] = BASE ? __builtin_fmaf(x[i], f[i] - dot, b[i]) : x[i] * (f[i] - dot);
     }
-    R::store(a.dlogits + r * a.ds + t * E * R::SZ, E, l, x);
+    R::store(out + t * pitch, E, l, x);
   }
 }
 
@@ -258,7 +313,7 @@ uint32_t blocks_of(int N, uint64_t tokens, int E, uint32_t rounds, uint32_t most
   const uint64_t each = std::max<uint64_t>(1, most / N);
   return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(each, (groups + rounds - 1) / rounds));
 }
-constexpr uint32_t kSumRounds = 4, kSumMost = 512, kGradRounds = 2, kGradMost = 2048;
+constexpr uint32_t kSumRounds = 2, kSumMost = 512, kGradRounds = 2, kGradMost = 2048;
 
 BalArgs balance_args(const BalanceLaunch& L) {
   BalArgs a = {};
@@ -277,8 +332,9 @@ BalArgs balance_args(const BalanceLaunch& L) {
 template <bool GRAD, int DT, int LN>
 hipError_t run_balance(const BalArgs& a, hipStream_t st) {
   const dim3 grid(a.blocks, (unsigned)a.N), blk(kBalanceBlock);
-  if constexpr (GRAD) CC_LAUNCH((k_balance_grad<DT, LN>), grid, blk, 0, st, a);
-  else CC_LAUNCH((k_balance<DT, LN>), grid, blk, 0, st, a);
+  if constexpr (!GRAD) CC_LAUNCH((k_balance<DT, LN>), grid, blk, 0, st, a);
+  else if (a.base) CC_LAUNCH((k_balance_grad<DT, LN, true>), grid, blk, 0, st, a);
+  else CC_LAUNCH((k_balance_grad<DT, LN, false>), grid, blk, 0, st, a);
   return hipGetLastError();
 }
 template <bool GRAD, int DT>

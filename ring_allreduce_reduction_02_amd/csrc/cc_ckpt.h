@@ -10,6 +10,7 @@
 
 #include "cc_device.h"
 #include "cc_llm.h"
+#include "cc_wave.h"
 
 namespace cc {
 namespace {
@@ -44,12 +45,6 @@ __device__ __forceinline__ void kept_unpack(const Kept<V>& k, float* v) {
   for (int i = 0; i < V; ++i) v[i] = (float)((int)(k.w[i / 4] << (24 - 8 * (i & 3))) >> 24) * s;
 }
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t x) {
-  const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, false);
-  return x > o ? x : o;
-}
-
 // A block of 32 that LANES consecutive lanes hold, V each, `left` of this lane's
 // inside the row: integers to p (zeros for those outside), the exponent to pe.
 template <int V, int LANES>
@@ -61,9 +56,7 @@ __device__ __forceinline__ void kept_store(const float* v, int left, int lane, c
     const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
     top = i < left && b > top ? b : top;
   }
-  top = max_dpp<0xB1>(top);                               // quad_perm [1,0,3,2]
-  top = max_dpp<0x4E>(top);                               // quad_perm [2,3,0,1]
-  if constexpr (LANES == 8) top = max_dpp<0x141>(top);    // row_half_mirror
+  top = group_umax<LANES>(top);
   const uint32_t ex = kept_exponent(top);
   const float inv = __uint_as_float((254u - ex) << 23);   // 2^-e (unused where ex is 255)
   uint32_t w[V / 4];

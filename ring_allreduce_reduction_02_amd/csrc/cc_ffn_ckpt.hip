@@ -23,15 +23,15 @@ struct XArgs {
   uint64_t F, h_pitch, dgu_pitch;
 };
 
-constexpr int kXRows = 16;   // of a tile's 64 rows a workgroup
+constexpr int kXParts = 16, kXRows = kFfnTile[kFfnTiles - 1] / kXParts;   // workgroups of a tile of 64 rows
 
-// The compact rows of a workgroup (four a tile), a wave each; false: none.
+// The compact rows of a workgroup, a wave each.
 struct XRows {
   int first, end, rank;
 };
 __device__ __forceinline__ XRows rows_of_block(const XArgs& a) {
-  const int2 at = a.mtab[blockIdx.x / 4];
-  const int stop = a.start[at.x + 1], first = at.y + (int)(blockIdx.x % 4) * kXRows;
+  const int2 at = a.mtab[blockIdx.x / kXParts];
+  const int stop = a.start[at.x + 1], first = at.y + (int)(blockIdx.x % kXParts) * kXRows;
   return XRows{first, first + kXRows < stop ? first + kXRows : stop, at.x / a.per};
 }
 
@@ -99,7 +99,6 @@ XArgs x_args(const FfnLaunch& L, const Side& x) {
   a.W = L.s.W;
   return a;
 }
-static_assert(kFfnTile[kFfnTiles - 1] == 4 * kXRows, "four workgroups a tile");
 
 }  // namespace
 
@@ -110,7 +109,7 @@ hipError_t ckpt_pack_x(const FfnLaunch& L) {
   const uint64_t tiles = L.s.mtiles[kFfnTiles - 1];
   if (tiles == 0) return hipSuccess;
   const XArgs a = x_args(L, L.x);
-  const dim3 grid((unsigned)(4 * tiles)), blk(256);
+  const dim3 grid((unsigned)(kXParts * tiles)), blk(256);
   if (L.s.dt == DT_F32) CC_LAUNCH(k_ckpt_pack<DT_F32>, grid, blk, 0, L.st, a);
   else CC_LAUNCH(k_ckpt_pack<DT_BF16>, grid, blk, 0, L.st, a);
   return hipGetLastError();
@@ -128,7 +127,7 @@ hipError_t ckpt_unpack_x(const FfnLaunch& L) {
     a.h_pitch = line_pitch(L.s, L.s.F);
     a.dgu_pitch = line_pitch(L.s, 2 * L.s.F);
   }
-  const dim3 grid((unsigned)(4 * tiles)), blk(256);
+  const dim3 grid((unsigned)(kXParts * tiles)), blk(256);
   if (L.s.dt == DT_F32) CC_LAUNCH(k_ckpt_unpack<DT_F32>, grid, blk, 0, L.st, a);
   else CC_LAUNCH(k_ckpt_unpack<DT_BF16>, grid, blk, 0, L.st, a);
   return hipGetLastError();

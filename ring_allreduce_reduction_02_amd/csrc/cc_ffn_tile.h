@@ -179,23 +179,6 @@ __device__ __forceinline__ u32x4 frag(const char* t, int u, int i0, int lane) {
   }
 }
 
-// V floats in one 16-byte vector; bf16 by the hardware's conversion (nearest,
-// ties to even), one instruction for two elements
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-template <int DT>
-__device__ __forceinline__ u32x4 pack_row(const float* v) {
-  if constexpr (DT == DT_BF16) {
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[2 * i], v[2 * i + 1]}), bf16x2));
-    return w;
-  } else {
-    return pack<DT>(v);
-  }
-}
-
 // Staging of a tile of lines that start anywhere, through registers: 16-byte
 // chunks (global memory takes whole vectors at any element), a line's last
 // one by elements.  Row tiles: lp[r] is line r's first byte (the last line

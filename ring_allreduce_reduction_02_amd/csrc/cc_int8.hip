@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "cc_ffn_tile.h"
+#include "cc_wave.h"
 
 namespace cc {
 namespace {
@@ -29,76 +30,116 @@ struct RowsArgs {
   int per;
 };
 
-// The integer nearest u / s, ties to even.  u times the hardware reciprocal of s
-// is within 2.5e-5 of the quotient (127 at most, off by the reciprocal's 2^-23 and
-// the product's 2^-24 of it); where that lies closer to a half-integer, and for
-// scales whose reciprocal is not normal, the quotient in float64 decides.  That
-// is exact: u and (k + 1/2) s are multiples of s 2^-26 unless equal, and float64 is
-// off by 2^-46.
-__device__ __forceinline__ float nearest(float u, float s, float inv) {
-  const float est = u * inv;
-  float r = __builtin_rintf(est);
-  if (__builtin_expect(!(fabsf(fabsf(est - r) - 0.5f) > 4e-5f), 0)) r = (float)__builtin_rint((double)u / (double)s);
-  return __builtin_amdgcn_fmed3f(r, -127.0f, 127.0f);
+// The integer nearest |u| / s, ties to even, for s of 2^-100 and more: k or k + 1,
+// by the sign of |u| - (k + 1/2) s, which one rounding of a fused multiply-add
+// keeps (the difference is 0 or a multiple of 2^-26 s).  `est` lies within 1/4 of
+// the quotient.
+__device__ __forceinline__ float nearest(float u, float s, float est) {
+  const float k = __builtin_truncf(est), rem = __builtin_fmaf(-(k + 0.5f), s, u);
+  const bool odd = (int)k & 1;
+  return rem > 0.0f || (rem == 0.0f && odd) ? k + 1.0f : k;
 }
 
 typedef uint32_t u32_byte __attribute__((aligned(1)));
+typedef uint32_t u32x2_byte __attribute__((ext_vector_type(2), aligned(1)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-template <int V>
-__device__ __forceinline__ void put_bytes(char* p, const float* q, int n, int room) {
-  uint32_t w[V / 4];
+// the largest magnitude's bits so far, of a type's own width
+template <int DT>
+struct Top;
+template <>
+struct Top<DT_F32> {
+  uint32_t m = 0;
+  __device__ __forceinline__ void take(u32x4 w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = w[i] & 0x7fffffffu;
+      m = b > m ? b : m;
+    }
+  }
+  __device__ __forceinline__ uint32_t bits() const { return m; }
+};
+template <>
+struct Top<DT_BF16> {
+  u16x2 m = {0, 0};
+  __device__ __forceinline__ void take(u32x4 w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+  }
+  __device__ __forceinline__ uint32_t bits() const { return (uint32_t)(m.x > m.y ? m.x : m.y) << 16; }
+};
+
+// V quantised values, in V / 4 words.  u times the hardware reciprocal of s is within
+// 2.3e-5 of the quotient (127 at most; the reciprocal is off by 2^-23 and the product
+// by 2^-24 of it), so that both round to the same integer unless the product
+// lies closer than that to a half-integer: those are decided by `nearest`.
+// The product plus 1.5 2^23 is that integer, in its lowest bits.
+template <int DT, int V>
+__device__ __forceinline__ void quantized(u32x4 in, float s, float inv, uint32_t* w) {
+  constexpr float kMagic = 12582912.0f;
+  float v[V], far = 0.0f;
+  uint32_t b[V];
+  unpack<DT>(in, v);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float est = v[i] * inv, t = est + kMagic;
+    far = fmaxf(far, fabsf(est - (t - kMagic)));
+    b[i] = __float_as_uint(t);
+  }
+  if (__builtin_expect(far > 0.499975f, 0)) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float q = nearest(fabsf(v[i]), s, fabsf(v[i] * inv));
+      b[i] = __float_as_uint((v[i] < 0.0f ? -q : q) + kMagic);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i)
+    w[i] = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u) |
+           __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x04000c0cu);
+}
+// The same for scales below 2^-100, whose reciprocal need not be a number: by the
+// quotient in float64, which is exact enough (off by 2^-46, and not closer than
+// 2^-26 to a half-integer it does not equal).
+template <int DT, int V>
+__device__ __forceinline__ void quantized_small(u32x4 in, float s, uint32_t* w) {
+  float v[V];
+  unpack<DT>(in, v);
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
     w[i] = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[i] |= 4 * i + j < n ? ((uint32_t)(int)q[4 * i + j] & 0xffu) << (8 * j) : 0u;
-  }
-  if (room >= V) {
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) ((u32_byte*)p)[i] = w[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < room) p[i] = (char)(w[i / 4] >> (8 * (i & 3)));
+    for (int j = 0; j < 4; ++j) {
+      const double q = __builtin_rint((double)v[4 * i + j] / (double)s);
+      w[i] |= ((uint32_t)(int)(q > 127.0 ? 127.0 : q < -127.0 ? -127.0 : q) & 0xffu) << (8 * j);
+    }
   }
 }
 
-// A row by WPR waves (1 or 4), R vectors a lane in registers; longer rows are
-// read twice.
-constexpr int kHeld = 8;
-template <int DT, int WPR>
+// A row by WPR waves (1 or 4), R vectors a lane in registers; longer rows (WPR 4)
+// are read twice.  Bound by memory: 81920 rows of 2048 bf16, 503 MB in and out, 79 us,
+// 6.4 TB/s; 60.7k kept rows 61 us.  (With a branch to the float64 quotient behind
+// every element 150 and 168.)
+template <int DT, int WPR, int R>
 __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char* q, uint64_t pitch, float* scale,
                                              uint32_t* red) {
   constexpr int V = Ty<DT>::V, SZ = Ty<DT>::SZ;
   const int tid = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
   constexpr uint64_t STEP = (uint64_t)64 * WPR * V;
-  u32x4 held[kHeld];
-  uint32_t top = 0;
+  u32x4 held[R];
+  Top<DT> best;
   auto load = [&](uint64_t c) {
-    const int64_t left = (int64_t)width - (int64_t)c;
-    return load_n<DT, false>(x + c * SZ, left < V ? (int)(left > 0 ? left : 0) : V);
-  };
-  auto larger = [&](u32x4 w) {
-    float v[V];
-    unpack<DT>(w, v);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-      top = b > top ? b : top;
-    }
+    if (c + V <= width) return (u32x4) * (const u32x4_any*)(x + c * SZ);
+    if (c < width) return load_n<DT, false>(x + c * SZ, (int)(width - c));
+    return u32x4{0u, 0u, 0u, 0u};
   };
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    held[k] = load(k * STEP + (uint64_t)tid * V);
-    larger(held[k]);
-  }
-  for (uint64_t c = kHeld * STEP + (uint64_t)tid * V; c < width; c += STEP) larger(load(c));
+  for (int k = 0; k < R; ++k) held[k] = load(k * STEP + (uint64_t)tid * V);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)top, d);
-    top = o > top ? o : top;
-  }
+  for (int k = 0; k < R; ++k) best.take(held[k]);
+  if constexpr (WPR > 1)
+    for (uint64_t c = R * STEP + (uint64_t)tid * V; c < width; c += STEP) best.take(load(c));
+  uint32_t top = wave_umax(best.bits());
   if constexpr (WPR > 1) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
     __syncthreads();
@@ -107,61 +148,89 @@ __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char
   }
   const bool nan = top >= 0x7f800000u;
   const float s = nan ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
-  // a scale whose reciprocal is not normal: an estimate of infinity or NaN, which float64 decides
-  const float inv = s >= 0x1p-100f ? __builtin_amdgcn_rcpf(s) : __uint_as_float(0x7fc00000u);
-  auto put = [&](uint64_t c, u32x4 w) {
-    float v[V], r[V];
-    unpack<DT>(w, v);
+  const float inv = __builtin_amdgcn_rcpf(s);
+  auto put = [&](uint64_t c, u32x4 in) {
+    if (c >= pitch) return;
+    uint32_t w[V / 4];
+    if (s >= 0x1p-100f) {
+      quantized<DT, V>(in, s, inv, w);
+    } else if (s > 0.0f) {
+      quantized_small<DT, V>(in, s, w);
+    } else {   // zeros, or (NaN) marked
 #pragma unroll
-    for (int i = 0; i < V; ++i) r[i] = nan || s == 0.0f ? 0.0f : nearest(v[i], s, inv);
-    const int64_t left = (int64_t)width - (int64_t)c, room = (int64_t)pitch - (int64_t)c;
-    if (room > 0) put_bytes<V>(q + c, r, (int)(left < V ? left : V), (int)(room < V ? room : V));
+      for (int i = 0; i < V / 4; ++i) w[i] = 0;
+    }
+    char* o = q + c;
+    if (c + V <= pitch) {
+      if constexpr (V == 8) *(u32x2_byte*)o = u32x2_byte{w[0], w[1]};
+      else *(u32_byte*)o = w[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c + i < pitch) o[i] = (char)(w[i / 4] >> (8 * (i & 3)));
+    }
   };
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) put(k * STEP + (uint64_t)tid * V, held[k]);
-  for (uint64_t c = kHeld * STEP + (uint64_t)tid * V; c < pitch; c += STEP) put(c, load(c));
+  for (int k = 0; k < R; ++k) put(k * STEP + (uint64_t)tid * V, held[k]);
+  if constexpr (WPR > 1)
+    for (uint64_t c = R * STEP + (uint64_t)tid * V; c < pitch; c += STEP) put(c, load(c));
   if (tid == 0) *scale = s;
 }
 
 // Plain rows: blockIdx.y the rank, 4 / WPR rows a workgroup.
-template <int DT, int WPR>
+template <int DT, int WPR, int R>
 __global__ __launch_bounds__(256) void k_int8_rows(RowsArgs a) {
   __shared__ uint32_t red[4];
   const uint64_t r = blockIdx.y, row = (uint64_t)blockIdx.x * (4 / WPR) + (WPR == 1 ? threadIdx.x >> 6 : 0);
   if (row >= a.rows) return;   // a whole wave, or (WPR 4) the workgroup
-  quantize_row<DT, WPR>(a.x + r * a.x_stride + row * a.width * Ty<DT>::SZ, a.width, a.q + r * a.q_stride + row * a.q_pitch,
-                        a.q_pitch, (float*)(a.s + r * a.s_stride) + row, red);
+  quantize_row<DT, WPR, R>(a.x + r * a.x_stride + row * a.width * Ty<DT>::SZ, a.width,
+                           a.q + r * a.q_stride + row * a.q_pitch, a.q_pitch, (float*)(a.s + r * a.s_stride) + row, red);
 }
 
-// The experts' kept rows: four workgroups a tile of 64 rows.
-constexpr int kTileRows = 16;
-template <int DT, int WPR>
+// The experts' kept rows: kParts workgroups a tile of 64 rows, 4 rows each.
+constexpr int kParts = 16, kPartRows = kFfnTile[kFfnTiles - 1] / kParts;
+static_assert(kPartRows == 4, "a row a wave");
+template <int DT, int WPR, int R>
 __global__ __launch_bounds__(256) void k_int8_kept(RowsArgs a) {
   __shared__ uint32_t red[4];
-  const int2 at = a.mtab[blockIdx.x / 4];
-  const int stop = a.start[at.x + 1], first = at.y + (int)(blockIdx.x % 4) * kTileRows;
-  const int end = first + kTileRows < stop ? first + kTileRows : stop;
+  const int2 at = a.mtab[blockIdx.x / kParts];
+  const int stop = a.start[at.x + 1], first = at.y + (int)(blockIdx.x % kParts) * kPartRows;
+  const int end = first + kPartRows < stop ? first + kPartRows : stop;
   const char* x = a.x + (uint64_t)(at.x / a.per) * a.x_stride;
-  for (int l = first + (WPR == 1 ? threadIdx.x >> 6 : 0); l < end; l += 4 / WPR) {
-    quantize_row<DT, WPR>(x + (uint64_t)(uint32_t)a.map[l] * a.width * Ty<DT>::SZ, a.width,
-                          a.q + (uint64_t)l * a.q_pitch, a.q_pitch, (float*)a.s + l, red);
-    if constexpr (WPR > 1) __syncthreads();   // `red` is read
+  auto row = [&](int l) {
+    quantize_row<DT, WPR, R>(x + (uint64_t)(uint32_t)a.map[l] * a.width * Ty<DT>::SZ, a.width,
+                             a.q + (uint64_t)l * a.q_pitch, a.q_pitch, (float*)a.s + l, red);
+  };
+  if constexpr (WPR == 1) {
+    const int l = first + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (l < end) row(l);
+  } else {
+    for (int l = first; l < end; ++l) {
+      row(l);
+      __syncthreads();   // `red` is read
+    }
   }
 }
 
-template <int DT, int WPR>
+template <int DT, int WPR, int R>
 hipError_t run_rows(const RowsArgs& a, const Int8Rows& L) {
   if (L.map) {
-    CC_LAUNCH((k_int8_kept<DT, WPR>), dim3((unsigned)(4 * L.tiles)), dim3(256), 0, L.st, a);
+    CC_LAUNCH((k_int8_kept<DT, WPR, R>), dim3((unsigned)(kParts * L.tiles)), dim3(256), 0, L.st, a);
   } else {
     const uint64_t per = 4 / WPR;
-    CC_LAUNCH((k_int8_rows<DT, WPR>), dim3((unsigned)((L.rows + per - 1) / per), (unsigned)L.N), dim3(256), 0, L.st, a);
+    CC_LAUNCH((k_int8_rows<DT, WPR, R>), dim3((unsigned)((L.rows + per - 1) / per), (unsigned)L.N), dim3(256), 0, L.st, a);
   }
   return hipGetLastError();
 }
+// the least registers that hold a row
 template <int DT>
 hipError_t pick_rows(const RowsArgs& a, const Int8Rows& L) {
-  return L.width <= (uint64_t)64 * Ty<DT>::V * kHeld ? run_rows<DT, 1>(a, L) : run_rows<DT, 4>(a, L);
+  const uint64_t one = (uint64_t)64 * Ty<DT>::V;
+  if (L.width <= one) return run_rows<DT, 1, 1>(a, L);
+  if (L.width <= 2 * one) return run_rows<DT, 1, 2>(a, L);
+  if (L.width <= 4 * one) return run_rows<DT, 1, 4>(a, L);
+  if (L.width <= 8 * one) return run_rows<DT, 1, 8>(a, L);
+  return run_rows<DT, 4, 8>(a, L);
 }
 
 // ------------------------------------------------------------------ products
