@@ -1,16 +1,13 @@
 // The experts' feed-forward block with its activations kept in 8 bits
 // (cc_ckpt.h): the products that write and read them, and the rows x.
 
+#include "cc_ffn_plan.h"
 #include "cc_ffn_tile.h"
 
 namespace cc {
 namespace {
 
-struct XArgs {
-  const int* start;
-  const int2* mtab;      // row tiles of 64
-  const int* map;
-  int per;
+struct XRows {
   char* ck;
   uint64_t ck_stride;
   CkptRow at;
@@ -21,82 +18,133 @@ struct XArgs {
   char* h;
   char* dgu;
   uint64_t F, h_pitch, dgu_pitch;
+  int per;               // experts a rank
+  // where the tables are written
+  const int* start;
+  const int2* mtab;
+  const int* map;
 };
 
-constexpr int kXParts = 16, kXRows = kFfnTile[kFfnTiles - 1] / kXParts;   // workgroups of a tile of 64 rows
-
-// The compact rows of a workgroup, a wave each.
-struct XRows {
-  int first, end, rank;
-};
-__device__ __forceinline__ XRows rows_of_block(const XArgs& a) {
-  const int2 at = a.mtab[blockIdx.x / kXParts];
-  const int stop = a.start[at.x + 1], first = at.y + (int)(blockIdx.x % kXParts) * kXRows;
-  return XRows{first, first + kXRows < stop ? first + kXRows : stop, at.x / a.per};
-}
-
-// A lane takes V consecutive elements, so that 32 / V lanes hold a block.
+// A kept row x into the checkpoint, by a wave.  A lane takes V consecutive
+// elements, so that 32 / V lanes hold a block.
 template <int DT>
-__global__ __launch_bounds__(256) void k_ckpt_pack(XArgs a) {
+__device__ __forceinline__ void pack_x(const XRows& a, uint64_t rank, uint32_t row) {
   constexpr int V = Ty<DT>::V, SZ = Ty<DT>::SZ;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const XRows b = rows_of_block(a);
-  for (int l = b.first + wave; l < b.end; l += 4) {
-    const uint64_t row = (uint64_t)(uint32_t)a.map[l];
-    const char* x = a.x + (uint64_t)b.rank * a.x_stride + row * a.W * SZ;
-    char* ck = a.ck + (uint64_t)b.rank * a.ck_stride + row * (uint64_t)a.at.pitch;
-    for (uint64_t c0 = 0; c0 < a.W; c0 += 64 * V) {
-      const uint64_t c = c0 + (uint64_t)lane * V;
-      const int left = (int)((int64_t)a.W - (int64_t)c < V ? (int64_t)a.W - (int64_t)c : V);
+  const int lane = threadIdx.x & 63;
+  const char* x = a.x + rank * a.x_stride + (uint64_t)row * a.W * SZ;
+  char* ck = a.ck + rank * a.ck_stride + (uint64_t)row * (uint64_t)a.at.pitch;
+  for (uint64_t c0 = 0; c0 < a.W; c0 += 4 * 64 * V) {   // four loads under way
+    u32x4 w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + (uint64_t)(q * 64 + lane) * V;
+      const int64_t left = (int64_t)a.W - (int64_t)c;
+      w[q] = u32x4{0u, 0u, 0u, 0u};
+      if (left > 0) w[q] = load_n<DT, false>(x + c * SZ, (int)(left < V ? left : V));
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + (uint64_t)(q * 64 + lane) * V;
+      const int64_t left = (int64_t)a.W - (int64_t)c;
       float v[V];
-      unpack<DT>(load_n<DT, false>(x + c * SZ, left), v);
-      kept_store<V, kCkptBlock / V>(v, left, lane, ck + a.at.x + c, ck + a.at.xe + c / kCkptBlock);
+      unpack<DT>(w[q], v);
+      if (c0 + q * 64 * V < a.W)   // the same on all lanes
+        kept_store<V, kCkptBlock / V>(v, (int)(left < V ? left : V), lane, ck + a.at.x + c, ck + a.at.xe + c / kCkptBlock);
     }
   }
 }
 
-// The kept values as rows of the matrix products' type, exact in either (7
+// A row's kept values as one of the matrix products' type, exact in either (7
 // significant bits, no exponent below -126); zeros up to the pitch.
 template <int DT>
-__global__ __launch_bounds__(256) void k_ckpt_unpack(XArgs a) {
+__device__ __forceinline__ void unpack_x(const XRows& a, uint64_t rank, uint32_t row, uint64_t to) {
   constexpr int V = Ty<DT>::V, SZ = Ty<DT>::SZ;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const XRows b = rows_of_block(a);
-  for (int l = b.first + wave; l < b.end; l += 4) {
-    const uint64_t row = (uint64_t)(uint32_t)a.map[l];
-    const char* ck = a.ck + (uint64_t)b.rank * a.ck_stride + row * (uint64_t)a.at.pitch;
-    char* x = a.x + (uint64_t)l * a.pitch;
-    for (uint64_t c = (uint64_t)lane * V; c * SZ < a.pitch; c += 64 * V) {
-      const int64_t left = (int64_t)a.W - (int64_t)c;
+  const int lane = threadIdx.x & 63;
+  const char* ck = a.ck + rank * a.ck_stride + (uint64_t)row * (uint64_t)a.at.pitch;
+  char* x = a.x + to * a.pitch;
+  for (uint64_t c0 = (uint64_t)lane * V; c0 * SZ < a.pitch; c0 += 4 * 64 * V) {   // four loads under way
+    Kept<V> k[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + q * 64 * V;
+      if (c < a.W) k[q] = kept_load<V>(ck + a.at.x + c, ck + a.at.xe + c / kCkptBlock);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + q * 64 * V;
+      const int64_t left = (int64_t)a.W - (int64_t)c, room = (int64_t)(a.pitch / SZ) - (int64_t)c;
       float v[V] = {};
       if (left > 0) {
-        kept_unpack<V>(kept_load<V>(ck + a.at.x + c, ck + a.at.xe + c / kCkptBlock), v);
+        kept_unpack<V>(k[q], v);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = i < left ? v[i] : 0.0f;
       }
-      const int64_t room = (int64_t)(a.pitch / SZ) - (int64_t)c;
-      store_n<DT, false, V>(x + c * SZ, v, (int)(room < V ? room : V));
+      if (room > 0) store_n<DT, false, V>(x + c * SZ, v, (int)(room < V ? room : V));
     }
-    if (a.h) {
-      for (uint64_t c = a.F * SZ + lane * SZ; c < a.h_pitch; c += 64 * SZ) st1<DT>(a.h + l * a.h_pitch + c, 0.0f);
-      for (uint64_t c = 2 * a.F * SZ + lane * SZ; c < a.dgu_pitch; c += 64 * SZ)
-        st1<DT>(a.dgu + l * a.dgu_pitch + c, 0.0f);
-    }
+  }
+  if (a.h) {
+    for (uint64_t c = a.F * SZ + lane * SZ; c < a.h_pitch; c += 64 * SZ) st1<DT>(a.h + to * a.h_pitch + c, 0.0f);
+    for (uint64_t c = 2 * a.F * SZ + lane * SZ; c < a.dgu_pitch; c += 64 * SZ)
+      st1<DT>(a.dgu + to * a.dgu_pitch + c, 0.0f);
   }
 }
 
-XArgs x_args(const FfnLaunch& L, const Side& x) {
-  XArgs a = {};
-  a.start = (const int*)(L.ws + L.o.start);
-  a.mtab = (const int2*)(L.ws + L.o.mtab[kFfnTiles - 1]);
-  a.map = (const int*)(L.ws + L.o.rowmap);
-  a.per = L.s.E / L.s.N;
+// Both are bound by memory: 60.7k rows of 2048 bf16 67 and 63 us, 5.6 and 5.9 TB/s.
+
+// The plan of expert blockIdx.x, and its kept rows.
+struct PlanXArgs {
+  PlanArgs plan;
+  XRows r;
+};
+static_assert(sizeof(PlanXArgs) <= 4096, "a launch's arguments");
+template <int DT, bool UNPACK>
+__global__ __launch_bounds__(kPlanBlock) void k_ckpt_plan_x(PlanXArgs a) {
+  const int e = blockIdx.x;
+  if (blockIdx.y == 0) plan_tables(a.plan, e);
+  const uint32_t first = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  plan_rows(a.plan, e, first, gridDim.y * 4, [&](uint32_t l, uint32_t row) {
+    if ((threadIdx.x & 63) == 0) a.plan.rowmap[l] = (int)row;
+    if constexpr (UNPACK) unpack_x<DT>(a.r, (uint64_t)(e / a.r.per), row, l);
+    else pack_x<DT>(a.r, (uint64_t)(e / a.r.per), row);
+  });
+}
+// The kept rows, where the tables are written.
+template <int DT, bool UNPACK>
+__global__ __launch_bounds__(256) void k_ckpt_x(XRows a) {
+  table_rows(a.start, a.mtab, a.map, [&](uint32_t l, uint32_t row, int e) {
+    if constexpr (UNPACK) unpack_x<DT>(a, (uint64_t)(e / a.per), row, l);
+    else pack_x<DT>(a, (uint64_t)(e / a.per), row);
+  });
+}
+
+template <int DT, bool UNPACK>
+hipError_t run_x(const XRows& r, const FfnLaunch& L) {
+  if (const unsigned parts = plan_parts(L.s)) {
+    PlanXArgs a = {};
+    a.r = r;
+    const hipError_t e = ffn_plan_args(L.s, L.o, L.ws, L.kept, L.st, &a.plan);
+    if (e != hipSuccess) return e;
+    CC_LAUNCH((k_ckpt_plan_x<DT, UNPACK>), dim3((unsigned)L.s.E, parts), dim3(kPlanBlock), 0, L.st, a);
+    return hipGetLastError();
+  }
+  const hipError_t e = launch_ffn_plan(L.s, L.o, L.ws, L.kept, L.st);
+  if (e != hipSuccess) return e;
+  CC_LAUNCH((k_ckpt_x<DT, UNPACK>), dim3((unsigned)L.s.mtiles[kFfnTiles - 1], kTileParts), dim3(256), 0, L.st, r);
+  return hipGetLastError();
+}
+
+XRows x_rows(const FfnLaunch& L, const Side& x) {
+  XRows a = {};
   a.ck = L.ckpt.base;
   a.ck_stride = L.ckpt.stride;
   a.at = ckpt_row(L.s.W, L.s.F);
   a.x = x.base;
   a.x_stride = x.stride;
   a.W = L.s.W;
+  a.per = L.s.E / L.s.N;
+  a.start = (const int*)(L.ws + L.o.start);
+  a.mtab = (const int2*)(L.ws + L.o.mtab[kFfnTiles - 1]);
+  a.map = (const int*)(L.ws + L.o.rowmap);
   return a;
 }
 
@@ -105,20 +153,13 @@ XArgs x_args(const FfnLaunch& L, const Side& x) {
 hipError_t ckpt_gateup(const CkArgs& g, const FfnLaunch& L) { return pick_gemm<K_GATEUP_CK>(g, L); }
 hipError_t ckpt_dhid(const CkArgs& g, const FfnLaunch& L) { return pick_gemm<K_DHID_CK>(g, L); }
 
-hipError_t ckpt_pack_x(const FfnLaunch& L) {
-  const uint64_t tiles = L.s.mtiles[kFfnTiles - 1];
-  if (tiles == 0) return hipSuccess;
-  const XArgs a = x_args(L, L.x);
-  const dim3 grid((unsigned)(kXParts * tiles)), blk(256);
-  if (L.s.dt == DT_F32) CC_LAUNCH(k_ckpt_pack<DT_F32>, grid, blk, 0, L.st, a);
-  else CC_LAUNCH(k_ckpt_pack<DT_BF16>, grid, blk, 0, L.st, a);
-  return hipGetLastError();
+hipError_t ckpt_plan_pack(const FfnLaunch& L) {
+  const XRows a = x_rows(L, L.x);
+  return L.s.dt == DT_F32 ? run_x<DT_F32, false>(a, L) : run_x<DT_BF16, false>(a, L);
 }
 
-hipError_t ckpt_unpack_x(const FfnLaunch& L) {
-  const uint64_t tiles = L.s.mtiles[kFfnTiles - 1];
-  if (tiles == 0) return hipSuccess;
-  XArgs a = x_args(L, Side{L.ws + L.o.x, 0});
+hipError_t ckpt_plan_unpack(const FfnLaunch& L) {
+  XRows a = x_rows(L, Side{L.ws + L.o.x, 0});
   a.pitch = L.o.copied ? line_pitch(L.s, L.s.W) : L.s.W * elem_size(L.s.dt);
   if (L.o.copied) {
     a.h = L.ws + L.o.h;
@@ -127,10 +168,7 @@ hipError_t ckpt_unpack_x(const FfnLaunch& L) {
     a.h_pitch = line_pitch(L.s, L.s.F);
     a.dgu_pitch = line_pitch(L.s, 2 * L.s.F);
   }
-  const dim3 grid((unsigned)(kXParts * tiles)), blk(256);
-  if (L.s.dt == DT_F32) CC_LAUNCH(k_ckpt_unpack<DT_F32>, grid, blk, 0, L.st, a);
-  else CC_LAUNCH(k_ckpt_unpack<DT_BF16>, grid, blk, 0, L.st, a);
-  return hipGetLastError();
+  return L.s.dt == DT_F32 ? run_x<DT_F32, true>(a, L) : run_x<DT_BF16, true>(a, L);
 }
 
 }  // namespace cc

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 
+#include "cc_ffn_plan.h"
 #include "cc_ffn_tile.h"
 #include "cc_wave.h"
 
@@ -24,10 +25,6 @@ struct RowsArgs {
   char* s;
   uint64_t s_stride;
   uint64_t rows, width;
-  const int* start;
-  const int2* mtab;
-  const int* map;
-  int per;
 };
 
 // The integer nearest |u| / s, ties to even, for s of 2^-100 and more: k or k + 1,
@@ -177,60 +174,111 @@ __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char
   if (tid == 0) *scale = s;
 }
 
-// Plain rows: blockIdx.y the rank, 4 / WPR rows a workgroup.
+// Plain rows: blockIdx.y the rank, 4 / WPR rows a workgroup at a time.
+constexpr uint64_t kRowsGrid = 1u << 22;   // workgroups of 256 threads whose work-items fit 32 bits
 template <int DT, int WPR, int R>
 __global__ __launch_bounds__(256) void k_int8_rows(RowsArgs a) {
   __shared__ uint32_t red[4];
-  const uint64_t r = blockIdx.y, row = (uint64_t)blockIdx.x * (4 / WPR) + (WPR == 1 ? threadIdx.x >> 6 : 0);
-  if (row >= a.rows) return;   // a whole wave, or (WPR 4) the workgroup
-  quantize_row<DT, WPR, R>(a.x + r * a.x_stride + row * a.width * Ty<DT>::SZ, a.width,
-                           a.q + r * a.q_stride + row * a.q_pitch, a.q_pitch, (float*)(a.s + r * a.s_stride) + row, red);
+  const uint64_t r = blockIdx.y;
+  const char* x = a.x + r * a.x_stride;
+  char* q = a.q + r * a.q_stride;
+  float* s = (float*)(a.s + r * a.s_stride);
+  const int wave = WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  for (uint64_t row = (uint64_t)blockIdx.x * (4 / WPR) + wave; row < a.rows; row += (uint64_t)gridDim.x * (4 / WPR)) {
+    quantize_row<DT, WPR, R>(x + row * a.width * Ty<DT>::SZ, a.width, q + row * a.q_pitch, a.q_pitch, s + row, red);
+    if constexpr (WPR > 1) __syncthreads();   // `red` is read
+  }
 }
 
-// The experts' kept rows: kParts workgroups a tile of 64 rows, 4 rows each.
-constexpr int kParts = 16, kPartRows = kFfnTile[kFfnTiles - 1] / kParts;
-static_assert(kPartRows == 4, "a row a wave");
+// The plan of expert blockIdx.x, and its kept rows, compact.
+struct KeptArgs {
+  PlanArgs plan;
+  RowsArgs r;
+};
+static_assert(sizeof(KeptArgs) <= 4096, "a launch's arguments");
 template <int DT, int WPR, int R>
-__global__ __launch_bounds__(256) void k_int8_kept(RowsArgs a) {
+__global__ __launch_bounds__(kPlanBlock) void k_int8_kept(KeptArgs a) {
   __shared__ uint32_t red[4];
-  const int2 at = a.mtab[blockIdx.x / kParts];
-  const int stop = a.start[at.x + 1], first = at.y + (int)(blockIdx.x % kParts) * kPartRows;
-  const int end = first + kPartRows < stop ? first + kPartRows : stop;
-  const char* x = a.x + (uint64_t)(at.x / a.per) * a.x_stride;
-  auto row = [&](int l) {
-    quantize_row<DT, WPR, R>(x + (uint64_t)(uint32_t)a.map[l] * a.width * Ty<DT>::SZ, a.width,
-                             a.q + (uint64_t)l * a.q_pitch, a.q_pitch, (float*)a.s + l, red);
+  const int e = blockIdx.x, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (blockIdx.y == 0) plan_tables(a.plan, e);
+  const char* x = a.r.x + (uint64_t)(e / (a.plan.E / a.plan.N)) * a.r.x_stride;
+  const uint32_t first = WPR == 1 ? blockIdx.y * 4 + wave : blockIdx.y, step = WPR == 1 ? gridDim.y * 4 : gridDim.y;
+  plan_rows(a.plan, e, first, step, [&](uint32_t l, uint32_t row) {
+    if (threadIdx.x % (64 * WPR) == 0) a.plan.rowmap[l] = (int)row;
+    quantize_row<DT, WPR, R>(x + (uint64_t)row * a.r.width * Ty<DT>::SZ, a.r.width, a.r.q + (uint64_t)l * a.r.q_pitch,
+                             a.r.q_pitch, (float*)a.r.s + l, red);
+    if constexpr (WPR > 1) __syncthreads();   // `red` is read
+  });
+}
+
+// The kept rows, where the tables are written.
+struct TileArgs {
+  RowsArgs r;
+  const int* start;
+  const int2* mtab;
+  const int* map;
+  int per;
+};
+template <int DT, int WPR, int R>
+__global__ __launch_bounds__(256) void k_int8_tiles(TileArgs a) {
+  __shared__ uint32_t red[4];
+  auto row = [&](uint32_t l, uint32_t place, int e) {
+    quantize_row<DT, WPR, R>(a.r.x + (uint64_t)(e / a.per) * a.r.x_stride + (uint64_t)place * a.r.width * Ty<DT>::SZ,
+                             a.r.width, a.r.q + (uint64_t)l * a.r.q_pitch, a.r.q_pitch, (float*)a.r.s + l, red);
   };
   if constexpr (WPR == 1) {
-    const int l = first + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (l < end) row(l);
+    table_rows(a.start, a.mtab, a.map, row);
   } else {
-    for (int l = first; l < end; ++l) {
-      row(l);
-      __syncthreads();   // `red` is read
+    const int2 at = a.mtab[blockIdx.x];
+    const int stop = a.start[at.x + 1];
+    for (int k = 0; k < 4; ++k) {
+      const int l = at.y + (int)blockIdx.y * 4 + k;
+      if (l < stop) row((uint32_t)l, (uint32_t)a.map[l], at.x);   // the same on the whole workgroup
+      __syncthreads();                                            // `red` is read
     }
   }
 }
 
-template <int DT, int WPR, int R>
-hipError_t run_rows(const RowsArgs& a, const Int8Rows& L) {
-  if (L.map) {
-    CC_LAUNCH((k_int8_kept<DT, WPR, R>), dim3((unsigned)(kParts * L.tiles)), dim3(256), 0, L.st, a);
-  } else {
-    const uint64_t per = 4 / WPR;
-    CC_LAUNCH((k_int8_rows<DT, WPR, R>), dim3((unsigned)((L.rows + per - 1) / per), (unsigned)L.N), dim3(256), 0, L.st, a);
+struct Plain {
+  RowsArgs a;
+  unsigned ranks;
+  hipStream_t st;
+  template <int DT, int WPR, int R>
+  hipError_t run() const {
+    const uint64_t per = 4 / WPR, blocks = std::min((a.rows + per - 1) / per, kRowsGrid);
+    CC_LAUNCH((k_int8_rows<DT, WPR, R>), dim3((unsigned)blocks, ranks), dim3(256), 0, st, a);
+    return hipGetLastError();
   }
-  return hipGetLastError();
-}
+};
+struct Planned {
+  KeptArgs a;
+  dim3 grid;
+  hipStream_t st;
+  template <int DT, int WPR, int R>
+  hipError_t run() const {
+    CC_LAUNCH((k_int8_kept<DT, WPR, R>), grid, dim3(kPlanBlock), 0, st, a);
+    return hipGetLastError();
+  }
+};
+struct Tiled {
+  TileArgs a;
+  dim3 grid;
+  hipStream_t st;
+  template <int DT, int WPR, int R>
+  hipError_t run() const {
+    CC_LAUNCH((k_int8_tiles<DT, WPR, R>), grid, dim3(256), 0, st, a);
+    return hipGetLastError();
+  }
+};
 // the least registers that hold a row
-template <int DT>
-hipError_t pick_rows(const RowsArgs& a, const Int8Rows& L) {
+template <int DT, class L>
+hipError_t pick_rows(uint64_t width, const L& launch) {
   const uint64_t one = (uint64_t)64 * Ty<DT>::V;
-  if (L.width <= one) return run_rows<DT, 1, 1>(a, L);
-  if (L.width <= 2 * one) return run_rows<DT, 1, 2>(a, L);
-  if (L.width <= 4 * one) return run_rows<DT, 1, 4>(a, L);
-  if (L.width <= 8 * one) return run_rows<DT, 1, 8>(a, L);
-  return run_rows<DT, 4, 8>(a, L);
+  if (width <= one) return launch.template run<DT, 1, 1>();
+  if (width <= 2 * one) return launch.template run<DT, 1, 2>();
+  if (width <= 4 * one) return launch.template run<DT, 1, 4>();
+  if (width <= 8 * one) return launch.template run<DT, 1, 8>();
+  return launch.template run<DT, 4, 8>();
 }
 
 // ------------------------------------------------------------------ products
@@ -269,6 +317,26 @@ I8Args int8_args(const Int8Launch& L) {
   return g;
 }
 
+// the plan, and the kept rows quantised
+hipError_t planned_rows(const Int8Launch& L, const RowsArgs& r) {
+  if (const unsigned parts = plan_parts(L.s)) {
+    Planned p = {};
+    p.a.r = r;
+    p.grid = dim3((unsigned)L.s.E, parts);
+    p.st = L.st;
+    const hipError_t e = ffn_plan_args(L.s, L.o.plan, L.ws, L.kept, L.st, &p.a.plan);
+    if (e != hipSuccess) return e;
+    return L.dt == DT_F32 ? pick_rows<DT_F32>(r.width, p) : pick_rows<DT_BF16>(r.width, p);
+  }
+  const hipError_t e = launch_ffn_plan(L.s, L.o.plan, L.ws, L.kept, L.st);
+  if (e != hipSuccess) return e;
+  const int last = kFfnTiles - 1;
+  const Tiled t{{r, (const int*)(L.ws + L.o.plan.start), (const int2*)(L.ws + L.o.plan.mtab[last]),
+                 (const int*)(L.ws + L.o.plan.rowmap), L.s.E / L.s.N},
+                dim3((unsigned)L.s.mtiles[last], kTileParts), L.st};
+  return L.dt == DT_F32 ? pick_rows<DT_F32>(r.width, t) : pick_rows<DT_BF16>(r.width, t);
+}
+
 // `lines` rows of `cols` weights an expert
 void weights_of(I8Args* g, const Side& w, const Side& s, uint64_t lines, uint64_t cols) {
   g->b = WtSide{w.base, w.stride, lines * cols, cols};
@@ -281,9 +349,8 @@ void weights_of(I8Args* g, const Side& w, const Side& s, uint64_t lines, uint64_
 
 hipError_t launch_int8_rows(const Int8Rows& L) {
   if (L.rows == 0) return hipSuccess;
-  const RowsArgs a{L.x, L.x_stride, L.q, L.q_stride, L.q_pitch, L.s, L.s_stride, L.rows, L.width,
-                   L.start, L.mtab, L.map, L.per};
-  return L.dt == DT_F32 ? pick_rows<DT_F32>(a, L) : pick_rows<DT_BF16>(a, L);
+  const Plain p{{L.x, L.x_stride, L.q, L.q_stride, L.q_pitch, L.s, L.s_stride, L.rows, L.width}, (unsigned)L.N, L.st};
+  return L.dt == DT_F32 ? pick_rows<DT_F32>(L.width, p) : pick_rows<DT_BF16>(L.width, p);
 }
 
 Int8Ws int8_ws(const FfnShape& s, int block, int out_es) {
@@ -294,7 +361,7 @@ Int8Ws int8_ws(const FfnShape& s, int block, int out_es) {
     at += up256(bytes);
     return p;
   };
-  o.plan.kept = take((uint64_t)s.N * s.E * 4);
+  o.plan.kept = take(plan_words(s) * 4);
   o.plan.start = take(((uint64_t)s.E + 1) * 4);
   for (int k = 0; k < kFfnTiles; ++k) o.plan.mtab[k] = take(s.mtiles[k] * 8);
   o.plan.rowmap = take(s.rows * 4);
@@ -330,32 +397,25 @@ hipError_t launch_int8(const Int8Launch& L) {
 
 hipError_t launch_int8_ffn(const Int8Launch& L) {
   const uint64_t W = L.s.W, F = L.s.F, es = elem_size(L.dt);
-  hipError_t e = launch_ffn_plan(L.s, L.o.plan, L.ws, L.kept, L.st);
+  const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, L.ws + L.o.xs, 0, L.s.rows, W};
+  hipError_t e = planned_rows(L, r);
   if (e != hipSuccess) return e;
   I8Args g = int8_args(L);
-  Int8Rows q = {};
-  q.x = L.x.base; q.x_stride = L.x.stride;
-  q.q = L.ws + L.o.xq; q.q_pitch = L.o.xq_pitch;
-  q.s = L.ws + L.o.xs;
-  q.rows = L.s.rows; q.width = W;
-  q.start = g.start; q.mtab = (const int2*)(L.ws + L.o.plan.mtab[kFfnTiles - 1]); q.map = g.map;
-  q.tiles = L.s.mtiles[kFfnTiles - 1]; q.per = g.per;
-  q.N = 1; q.dt = L.dt; q.st = L.st;
-  if ((e = launch_int8_rows(q)) != hipSuccess) return e;
   g.K = (int)W;
   g.N = (int)(2 * F);
-  g.a = RowSide{q.q, 0, L.o.xq_pitch, nullptr, L.s.most * L.o.xq_pitch};
+  g.a = RowSide{r.q, 0, L.o.xq_pitch, nullptr, L.s.most * L.o.xq_pitch};
   weights_of(&g, L.w_in, L.s_in, 2 * F, W);
-  g.sx = q.s;
+  g.sx = r.s;
   g.out = RowSide{L.ws + L.o.h, 0, F * es, nullptr, L.s.most * F * es};
   const bool rows_fit = L.s.most * std::max(L.o.xq_pitch, L.o.hq_pitch) <= kMaxSpan;
   if ((e = pick_int8<K_GATEUP>(g, L, L.w_in_ok && rows_fit && 2 * F * W <= kMaxSpan, F * es % 16 == 0)) != hipSuccess)
     return e;
-  q.x = L.ws + L.o.h; q.x_stride = 0;
+  Int8Rows q = {};
+  q.x = L.ws + L.o.h;
   q.q = L.ws + L.o.hq; q.q_pitch = L.o.hq_pitch;
   q.s = L.ws + L.o.hs;
-  q.width = F;
-  q.map = nullptr;
+  q.rows = L.s.rows; q.width = F;
+  q.N = 1; q.dt = L.dt; q.st = L.st;
   if ((e = launch_int8_rows(q)) != hipSuccess) return e;
   g.K = (int)F;
   g.N = (int)W;
