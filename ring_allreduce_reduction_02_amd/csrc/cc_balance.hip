@@ -59,7 +59,7 @@ struct Row {
     for (int q = 0; q < Q; ++q) {
       const int e = expert(l, q);
       if (e + CH <= E) {
-        w[q] = *(const u32x4_any*)(row + (uint64_t)e * SZ);
+        w[q] = __builtin_nontemporal_load((const u32x4_any*)(row + (uint64_t)e * SZ));
       } else {
         float x[CH];
 #pragma unroll
@@ -78,7 +78,7 @@ struct Row {
     for (int q = 0; q < Q; ++q) {
       const int e = expert(l, q);
       if (e + CH <= E) {
-        *(u32x4_any*)(row + (uint64_t)e * SZ) = pack_row<DT>(x + q * CH);
+        __builtin_nontemporal_store((u32x4_any)pack_row<DT>(x + q * CH), (u32x4_any*)(row + (uint64_t)e * SZ));
       } else {
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -267,8 +267,9 @@ __global__ __launch_bounds__(kBalanceBlock) void k_balance_grad(BalArgs a) {
     f[i] = (float)c;
   }
   const long long S = (long long)group_usum<L>(lo) + ((long long)(int)group_usum<L>(hi) << 16);
+  const float one = S ? 1.0f / (float)S : 0.0f;
 #pragma unroll
-  for (int i = 0; i < kV; ++i) f[i] = S ? f[i] / (float)S : 0.0f;
+  for (int i = 0; i < kV; ++i) f[i] *= one;
   const int T = total[E];
   const float scale = T > 0 ? *(const float*)(a.loss + r * a.os) * ((float)E / (float)T) : 0.0f;
   for (; t < a.tokens; t += step) {
@@ -283,16 +284,14 @@ __global__ __launch_bounds__(kBalanceBlock) void k_balance_grad(BalArgs a) {
     if constexpr (BASE) add.values(b);
     const float s = exps<DT, L>(x);
     const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-    float dot = 0.0f;
+    float dot = 0.0f;   // of f and the exponentials
+#pragma unroll
+    for (int i = 0; i < kV; ++i) dot = __builtin_fmaf(x[i], f[i], dot);
+    dot = group_sum<L>(dot) * inv;
+    const float k = scale * inv;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-      x[i] *= inv;
-      dot = __builtin_fmaf(x[i], f[i], dot);
-    }
-    dot = group_sum<L>(dot);
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      x[i] *= scale;
+      x[i] *= k;
       x[i] = BASE ? __builtin_fmaf(x[i], f[i] - dot, b[i]) : x[i] * (f[i] - dot);
     }
     R::store(out + t * pitch, E, l, x);
