@@ -540,15 +540,17 @@ cc_status_t cc_moe_balance_loss_grad(cc_rankbuf_t logits, cc_rankbuf_t total, cc
   if (tokens == 0) return ok();
   const int N = nranks, es = elem_size((int)dtype);
   const u128 E = (unsigned)nexperts, lg = (u128)tokens * E * es;
-  std::vector<Buf> b = {{&logits, lg, "logits", false, N},
-                        {&total, (E + 1) * 4, "total", false, N},
-                        {&dloss, 4, "dloss", false, N},
-                        {&dlogits, lg, "dlogits", true, N}};
   // in place: one buffer, read and written element by element
-  if (base.base && !same_side(base, dlogits)) b.push_back({&base, lg, "base", false, N});
-  if ((s = check_bufs(b.data(), (int)b.size(), cfg, 0, ""))) return s;
-  for (const Buf& x : b)
-    if ((s = check_elems(*x.b, x.b == &total || x.b == &dloss ? 4 : es, x.name))) return s;
+  const bool apart = base.base && !same_side(base, dlogits);
+  const Buf b[] = {{&logits, lg, "logits", false, N},
+                   {&total, (E + 1) * 4, "total", false, N},
+                   {&dloss, 4, "dloss", false, N},
+                   {&dlogits, lg, "dlogits", true, N},
+                   {&base, lg, "base", false, N}};
+  const int n = apart ? 5 : 4;
+  if ((s = check_bufs(b, n, cfg, 0, ""))) return s;
+  for (int i = 0; i < n; ++i)
+    if ((s = check_elems(*b[i].b, i == 1 || i == 2 ? 4 : es, b[i].name))) return s;
   if ((s = device_ready())) return s;
   BalanceLaunch L = {};
   L.logits = (const char*)logits.base; L.logits_stride = logits.rank_stride_bytes;

@@ -181,6 +181,24 @@ def test_moe_matmul_int8_strides(dtype, pad, offset):
     p.check()
 
 
+# whole vectors in, results that start anywhere: tiles of every size
+ODD_OUT = {"256": (2, 4, 3450, 2048, 2033, [[3450, 200, 255, 0], [3450, 57, 0, 0]]),
+           "128": (1, 5, 4232, 1024, 1031, [[4232, 255, 256, 257, 0]]), "64": (2, 4, 300, 256, 37, [[255, 1, 64, 65], [300, 0, 128, 2]])}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ODD_OUT)
+def test_odd_results_of_aligned_rows(name, dtype):
+    say("int8 odd results", name, dtype)
+    p = Product(*ODD_OUT[name], dtype, 33)
+    f = Block(*ODD_OUT[name], dtype, 34)
+    p.run()
+    f.forward8("silu")
+    torch.cuda.synchronize()
+    p.check()
+    f.check8("silu")
+
+
 def test_moe_matmul_int8_longest_sum():
     """Every product 127 * 127 over the longest summed axis: 2.1e9, inside int32, and one of -128 * -128 by hand."""
     W = (1 << 17) - 1
