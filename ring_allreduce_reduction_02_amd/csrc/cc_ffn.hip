@@ -16,7 +16,6 @@
 
 #include <algorithm>
 
-#include "cc_ffn_plan.h"
 #include "cc_ffn_tile.h"
 
 namespace cc {
@@ -24,8 +23,9 @@ namespace {
 
 // ------------------------------------------------------------------ plan
 
+constexpr int kPlanCounts = 896;   // counts that fit a launch's arguments
 struct PutArgs {
-  uint32_t v[kPlanWords];
+  uint32_t v[kPlanCounts];
   uint32_t* to;
   int n;
 };
@@ -33,16 +33,56 @@ __global__ __launch_bounds__(256) void k_ffn_put(PutArgs a) {
   for (int i = threadIdx.x; i < a.n; i += 256) a.to[i] = a.v[i];
 }
 
-// Workgroup e writes expert e's tables.
-__global__ __launch_bounds__(kPlanBlock) void k_ffn_plan(PlanArgs a) {
-  const int e = blockIdx.x, per = a.E / a.N;
-  plan_tables(a, e);
-  const uint32_t* w = plan_of(a, e);
-  uint32_t at = w[0];
-  for (int i = 0; i < a.N; ++i) {
-    const uint32_t n = w[kPlanHead + i], src = (uint32_t)(((uint64_t)i * per + e % per) * a.cap);
-    for (uint32_t s = threadIdx.x; s < n; s += kPlanBlock) a.rowmap[at + s] = (int)(src + s);
+struct PlanArgs {
+  uint32_t v[kPlanCounts];
+  const uint32_t* kept;   // in memory, or NULL: v
+  int N, E;
+  uint64_t cap;
+  int* start;
+  int2* mtab[kFfnTiles];
+  int* rowmap;
+};
+
+// Workgroup e writes expert e's first compact row, its row tiles and its rows'
+// places in the rank's buffer.
+__global__ __launch_bounds__(256) void k_ffn_plan(PlanArgs a) {
+  __shared__ uint32_t red[1 + kFfnTiles][256];
+  const int e = blockIdx.x, tid = threadIdx.x, N = a.N;
+  const uint32_t* kept = a.kept ? a.kept : a.v;
+  uint32_t sum[1 + kFfnTiles] = {};
+  for (int x = tid; x < e; x += 256) {
+    uint32_t n = 0;
+    for (int i = 0; i < N; ++i) n += kept[x * N + i];
+    sum[0] += n;
+#pragma unroll
+    for (int k = 0; k < kFfnTiles; ++k) sum[1 + k] += (n + kFfnTile[k] - 1) / kFfnTile[k];
+  }
+#pragma unroll
+  for (int k = 0; k <= kFfnTiles; ++k) red[k][tid] = sum[k];
+  __syncthreads();
+  for (int d = 128; d; d >>= 1) {
+    if (tid < d)
+#pragma unroll
+      for (int k = 0; k <= kFfnTiles; ++k) red[k][tid] += red[k][tid + d];
+    __syncthreads();
+  }
+  const uint32_t r0 = red[0][0];
+  const int per = a.E / N, l = e % per;
+  uint32_t at = r0;
+  for (int i = 0; i < N; ++i) {
+    const uint32_t n = kept[e * N + i];
+    const uint32_t src = (uint32_t)(((uint64_t)i * per + l) * a.cap);
+    for (uint32_t s = tid; s < n; s += 256) a.rowmap[at + s] = (int)(src + s);
     at += n;
+  }
+#pragma unroll
+  for (int k = 0; k < kFfnTiles; ++k) {
+    const uint32_t nt = (at - r0 + kFfnTile[k] - 1) / kFfnTile[k], t0 = red[1 + k][0];
+    for (uint32_t t = tid; t < nt; t += 256) a.mtab[k][t0 + t] = make_int2(e, (int)(r0 + t * kFfnTile[k]));
+  }
+  if (tid == 0) {
+    a.start[e] = (int)r0;
+    if (e == a.E - 1) a.start[a.E] = (int)at;
   }
 }
 
@@ -69,7 +109,10 @@ struct CopyArgs {
 
 constexpr int kCopyLines = kFfnTile[kFfnTiles - 1], kCopyParts = 4;
 
-// Workgroup (x, y, z) copies part z of 64 lines of job y, @@COPY@@
+// Workgroup (x, y, z) copies part z of 64 lines of job y.  Bound by memory: the
+// weights of 16 experts of 2047 x 2047 bf16 and 60.7k rows, 1.3 GB in and out, 271 us,
+// 4.8 TB/s (all 64 lines a workgroup 300, and with one load of a lane under way 350;
+// 6 experts of 515 x 331 and 1.4k rows 12 us and 31).
 template <int DT>
 __global__ __launch_bounds__(256) void k_ffn_copy(CopyArgs a) {
   constexpr int V = Ty<DT>::V, SZ = Ty<DT>::SZ;
@@ -123,6 +166,31 @@ __global__ __launch_bounds__(256) void k_ffn_copy(CopyArgs a) {
   }
 }
 
+hipError_t plan(const FfnShape& s, const FfnWs& o, char* ws, const uint32_t* kept, hipStream_t st) {
+  PlanArgs a;
+  const int n = s.N * s.E;
+  a.kept = nullptr;
+  if (n <= kPlanCounts) {
+    for (int i = 0; i < n; ++i) a.v[i] = kept[i];
+  } else {
+    uint32_t* to = (uint32_t*)(ws + o.kept);
+    for (int i = 0; i < n; i += kPlanCounts) {
+      PutArgs p;
+      p.n = n - i < kPlanCounts ? n - i : kPlanCounts;
+      for (int k = 0; k < p.n; ++k) p.v[k] = kept[i + k];
+      p.to = to + i;
+      CC_LAUNCH(k_ffn_put, dim3(1), dim3(256), 0, st, p);
+    }
+    a.kept = to;
+  }
+  a.N = s.N; a.E = s.E; a.cap = s.cap;
+  a.start = (int*)(ws + o.start);
+  for (int k = 0; k < kFfnTiles; ++k) a.mtab[k] = (int2*)(ws + o.mtab[k]);
+  a.rowmap = (int*)(ws + o.rowmap);
+  CC_LAUNCH(k_ffn_plan, dim3((unsigned)s.E), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
 GemmArgs gemm_args(const FfnLaunch& L) {
   GemmArgs g = {};
   g.start = (const int*)(L.ws + L.o.start);
@@ -173,7 +241,7 @@ hipError_t copy_operands(const FfnLaunch& L, int grad) {
   a.mtab = (const int2*)(L.ws + L.o.mtab[kFfnTiles - 1]);
   a.map = (const int*)(L.ws + L.o.rowmap);
   a.per = L.s.E / L.s.N;
-  // rows x that a checkpoint holds are unpacked there (ckpt_plan_unpack)
+  // rows x that a checkpoint holds are unpacked there (ckpt_unpack_x)
   a.job[0] = {L.x.base, L.x.stride, grad && L.ckpt.base ? 0 : tiles, 0, L.ws + L.o.x, W, line_pitch(L.s, W)};
   a.job[1] = {L.w_in.base, L.w_in.stride, n * 2 * F, 2 * F, L.ws + L.o.w_in, W, line_pitch(L.s, W)};
   a.job[2] = {L.w_out.base, L.w_out.stride, n * W, W, L.ws + L.o.w_out, F, line_pitch(L.s, F)};
@@ -191,9 +259,7 @@ hipError_t copy_operands(const FfnLaunch& L, int grad) {
 }
 
 hipError_t prepare(const FfnLaunch& L, int grad) {
-  hipError_t e;
-  if (L.ckpt.base) e = grad ? ckpt_plan_unpack(L) : ckpt_plan_pack(L);
-  else e = launch_ffn_plan(L.s, L.o, L.ws, L.kept, L.st);
+  const hipError_t e = plan(L.s, L.o, L.ws, L.kept, L.st);
   return e == hipSuccess && L.o.copied ? copy_operands(L, grad) : e;
 }
 
@@ -208,7 +274,7 @@ FfnWs ffn_ws(const FfnShape& s, int grad, int ckpt) {
     at += up256(bytes);
     return p;
   };
-  o.kept = take(plan_words(s) * 4);
+  o.kept = take((uint64_t)s.N * s.E * 4);
   o.start = take(((uint64_t)s.E + 1) * 4);
   for (int k = 0; k < kFfnTiles; ++k) o.mtab[k] = take(s.mtiles[k] * 8);
   o.rowmap = take(s.rows * 4);
@@ -230,54 +296,8 @@ FfnWs ffn_ws(const FfnShape& s, int grad, int ckpt) {
   return o;
 }
 
-// the experts' words, in the launch's arguments or (many) in memory
-hipError_t ffn_plan_args(const FfnShape& s, const FfnWs& o, char* ws, const uint32_t* kept, hipStream_t st,
-                         PlanArgs* out) {
-  PlanArgs& a = *out;
-  const uint64_t n = plan_words(s);
-  uint32_t at[kPlanHead] = {};   // of the next expert
-  a.w = nullptr;
-  PutArgs p;
-  uint32_t* const memory = (uint32_t*)(ws + o.kept);
-  uint64_t done = 0;             // words put into memory
-  int here = 0;
-  uint32_t* to = n <= kPlanWords ? a.v : p.v;
-  auto put = [&](uint32_t v) -> hipError_t {
-    to[here++] = v;
-    if (n <= kPlanWords || (here < kPlanWords && done + here < n)) return hipSuccess;
-    p.to = memory + done;
-    p.n = here;
-    CC_LAUNCH(k_ffn_put, dim3(1), dim3(256), 0, st, p);
-    done += here;
-    here = 0;
-    return hipGetLastError();
-  };
-  hipError_t e = hipSuccess;
-  for (int x = 0; x < s.E && e == hipSuccess; ++x) {
-    uint32_t rows = 0;
-    for (int k = 0; k < kPlanHead && e == hipSuccess; ++k) e = put(at[k]);
-    for (int i = 0; i < s.N && e == hipSuccess; ++i) {
-      e = put(kept[(uint64_t)x * s.N + i]);
-      rows += kept[(uint64_t)x * s.N + i];
-    }
-    at[0] += rows;
-    for (int k = 0; k < kFfnTiles; ++k) at[1 + k] += (rows + kFfnTile[k] - 1) / kFfnTile[k];
-  }
-  if (e != hipSuccess) return e;
-  if (n > kPlanWords) a.w = memory;
-  a.N = s.N; a.E = s.E; a.cap = s.cap;
-  a.start = (int*)(ws + o.start);
-  for (int k = 0; k < kFfnTiles; ++k) a.mtab[k] = (int2*)(ws + o.mtab[k]);
-  a.rowmap = (int*)(ws + o.rowmap);
-  return hipGetLastError();
-}
-
 hipError_t launch_ffn_plan(const FfnShape& s, const FfnWs& o, char* ws, const uint32_t* kept, hipStream_t st) {
-  PlanArgs a;
-  const hipError_t e = ffn_plan_args(s, o, ws, kept, st, &a);
-  if (e != hipSuccess) return e;
-  CC_LAUNCH(k_ffn_plan, dim3((unsigned)s.E), dim3(kPlanBlock), 0, st, a);
-  return hipGetLastError();
+  return plan(s, o, ws, kept, st);
 }
 
 hipError_t launch_ffn(const FfnLaunch& L) {
@@ -291,7 +311,7 @@ hipError_t launch_ffn(const FfnLaunch& L) {
   g.b = wts_in(L, L.w_in, L.o.w_in, 2 * F, W);
   g.out = compact(L, L.o.h, F);
   if (L.ckpt.base) {
-    if ((e = ckpt_gateup(ckpt_args(L, g), L)) != hipSuccess) return e;
+    if ((e = ckpt_pack_x(L)) != hipSuccess || (e = ckpt_gateup(ckpt_args(L, g), L)) != hipSuccess) return e;
   } else {
     g.pre = rows_of(L, L.pre, 2 * F);
     if ((e = pick_gemm<K_GATEUP>(g, L)) != hipSuccess) return e;
@@ -317,7 +337,7 @@ hipError_t launch_ffn_grad(const FfnLaunch& L) {
   g.out = compact(L, L.o.dgu, 2 * F);
   g.h = compact(L, L.o.h, F);
   if (L.ckpt.base) {
-    if ((e = ckpt_dhid(ckpt_args(L, g), L)) != hipSuccess) return e;
+    if ((e = ckpt_unpack_x(L)) != hipSuccess || (e = ckpt_dhid(ckpt_args(L, g), L)) != hipSuccess) return e;
   } else {
     g.pre = rows_of(L, L.pre, 2 * F);
     if ((e = pick_gemm<K_DHID>(g, L)) != hipSuccess) return e;

@@ -1,7 +1,6 @@
 // The experts' feed-forward block with its activations kept in 8 bits
 // (cc_ckpt.h): the products that write and read them, and the rows x.
 
-#include "cc_ffn_plan.h"
 #include "cc_ffn_tile.h"
 
 namespace cc {
@@ -19,7 +18,6 @@ struct XRows {
   char* dgu;
   uint64_t F, h_pitch, dgu_pitch;
   int per;               // experts a rank
-  // where the tables are written
   const int* start;
   const int2* mtab;
   const int* map;
@@ -90,25 +88,8 @@ __device__ __forceinline__ void unpack_x(const XRows& a, uint64_t rank, uint32_t
 }
 
 // Both are bound by memory: 60.7k rows of 2048 bf16 67 and 63 us, 5.6 and 5.9 TB/s.
-
-// The plan of expert blockIdx.x, and its kept rows.
-struct PlanXArgs {
-  PlanArgs plan;
-  XRows r;
-};
-static_assert(sizeof(PlanXArgs) <= 4096, "a launch's arguments");
-template <int DT, bool UNPACK>
-__global__ __launch_bounds__(kPlanBlock) void k_ckpt_plan_x(PlanXArgs a) {
-  const int e = blockIdx.x;
-  if (blockIdx.y == 0) plan_tables(a.plan, e);
-  const uint32_t first = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  plan_rows(a.plan, e, first, gridDim.y * 4, [&](uint32_t l, uint32_t row) {
-    if ((threadIdx.x & 63) == 0) a.plan.rowmap[l] = (int)row;
-    if constexpr (UNPACK) unpack_x<DT>(a.r, (uint64_t)(e / a.r.per), row, l);
-    else pack_x<DT>(a.r, (uint64_t)(e / a.r.per), row);
-  });
-}
-// The kept rows, where the tables are written.
+// (In one kernel with the plan, whose counts lie in the host's memory, the whole
+// step of 64 to 32768 rows took 0-4% less where few rows, 0-2% more where many.)
 template <int DT, bool UNPACK>
 __global__ __launch_bounds__(256) void k_ckpt_x(XRows a) {
   table_rows(a.start, a.mtab, a.map, [&](uint32_t l, uint32_t row, int e) {
@@ -117,19 +98,13 @@ __global__ __launch_bounds__(256) void k_ckpt_x(XRows a) {
   });
 }
 
-template <int DT, bool UNPACK>
-hipError_t run_x(const XRows& r, const FfnLaunch& L) {
-  if (const unsigned parts = plan_parts(L.s)) {
-    PlanXArgs a = {};
-    a.r = r;
-    const hipError_t e = ffn_plan_args(L.s, L.o, L.ws, L.kept, L.st, &a.plan);
-    if (e != hipSuccess) return e;
-    CC_LAUNCH((k_ckpt_plan_x<DT, UNPACK>), dim3((unsigned)L.s.E, parts), dim3(kPlanBlock), 0, L.st, a);
-    return hipGetLastError();
-  }
-  const hipError_t e = launch_ffn_plan(L.s, L.o, L.ws, L.kept, L.st);
-  if (e != hipSuccess) return e;
-  CC_LAUNCH((k_ckpt_x<DT, UNPACK>), dim3((unsigned)L.s.mtiles[kFfnTiles - 1], kTileParts), dim3(256), 0, L.st, r);
+template <bool UNPACK>
+hipError_t run_x(const XRows& a, const FfnLaunch& L) {
+  const uint64_t tiles = L.s.mtiles[kFfnTiles - 1];
+  if (tiles == 0) return hipSuccess;
+  const dim3 grid((unsigned)tiles, kTileParts), blk(256);
+  if (L.s.dt == DT_F32) CC_LAUNCH((k_ckpt_x<DT_F32, UNPACK>), grid, blk, 0, L.st, a);
+  else CC_LAUNCH((k_ckpt_x<DT_BF16, UNPACK>), grid, blk, 0, L.st, a);
   return hipGetLastError();
 }
 
@@ -153,12 +128,9 @@ XRows x_rows(const FfnLaunch& L, const Side& x) {
 hipError_t ckpt_gateup(const CkArgs& g, const FfnLaunch& L) { return pick_gemm<K_GATEUP_CK>(g, L); }
 hipError_t ckpt_dhid(const CkArgs& g, const FfnLaunch& L) { return pick_gemm<K_DHID_CK>(g, L); }
 
-hipError_t ckpt_plan_pack(const FfnLaunch& L) {
-  const XRows a = x_rows(L, L.x);
-  return L.s.dt == DT_F32 ? run_x<DT_F32, false>(a, L) : run_x<DT_BF16, false>(a, L);
-}
+hipError_t ckpt_pack_x(const FfnLaunch& L) { return run_x<false>(x_rows(L, L.x), L); }
 
-hipError_t ckpt_plan_unpack(const FfnLaunch& L) {
+hipError_t ckpt_unpack_x(const FfnLaunch& L) {
   XRows a = x_rows(L, Side{L.ws + L.o.x, 0});
   a.pitch = L.o.copied ? line_pitch(L.s, L.s.W) : L.s.W * elem_size(L.s.dt);
   if (L.o.copied) {
@@ -168,7 +140,7 @@ hipError_t ckpt_plan_unpack(const FfnLaunch& L) {
     a.h_pitch = line_pitch(L.s, L.s.F);
     a.dgu_pitch = line_pitch(L.s, 2 * L.s.F);
   }
-  return L.s.dt == DT_F32 ? run_x<DT_F32, true>(a, L) : run_x<DT_BF16, true>(a, L);
+  return run_x<true>(a, L);
 }
 
 }  // namespace cc

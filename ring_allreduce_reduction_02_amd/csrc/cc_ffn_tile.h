@@ -995,6 +995,18 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_ffn_tile(typenam
   else finish<DT, KIND, VEC>(g, t, acc, mw, nw, lane, piece);
 }
 
+// ------------------------------------------------------------------ rows
+
+// f(compact row, place in the rank's buffer, expert) for the experts' kept rows, a
+// wave each: workgroup (tile of 64 rows, part of it).
+constexpr int kTileParts = kFfnTile[kFfnTiles - 1] / 4;
+template <class F>
+__device__ __forceinline__ void table_rows(const int* start, const int2* mtab, const int* map, F f) {
+  const int2 at = mtab[blockIdx.x];
+  const int l = at.y + (int)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (l < start[at.x + 1]) f((uint32_t)l, (uint32_t)map[l], at.x);
+}
+
 // ------------------------------------------------------------------ launches
 
 template <int DT, int KIND, bool VEC, int OT = DT>

@@ -8,7 +8,6 @@
 
 #include <algorithm>
 
-#include "cc_ffn_plan.h"
 #include "cc_ffn_tile.h"
 #include "cc_wave.h"
 
@@ -190,28 +189,7 @@ __global__ __launch_bounds__(256) void k_int8_rows(RowsArgs a) {
   }
 }
 
-// The plan of expert blockIdx.x, and its kept rows, compact.
-struct KeptArgs {
-  PlanArgs plan;
-  RowsArgs r;
-};
-static_assert(sizeof(KeptArgs) <= 4096, "a launch's arguments");
-template <int DT, int WPR, int R>
-__global__ __launch_bounds__(kPlanBlock) void k_int8_kept(KeptArgs a) {
-  __shared__ uint32_t red[4];
-  const int e = blockIdx.x, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (blockIdx.y == 0) plan_tables(a.plan, e);
-  const char* x = a.r.x + (uint64_t)(e / (a.plan.E / a.plan.N)) * a.r.x_stride;
-  const uint32_t first = WPR == 1 ? blockIdx.y * 4 + wave : blockIdx.y, step = WPR == 1 ? gridDim.y * 4 : gridDim.y;
-  plan_rows(a.plan, e, first, step, [&](uint32_t l, uint32_t row) {
-    if (threadIdx.x % (64 * WPR) == 0) a.plan.rowmap[l] = (int)row;
-    quantize_row<DT, WPR, R>(x + (uint64_t)row * a.r.width * Ty<DT>::SZ, a.r.width, a.r.q + (uint64_t)l * a.r.q_pitch,
-                             a.r.q_pitch, (float*)a.r.s + l, red);
-    if constexpr (WPR > 1) __syncthreads();   // `red` is read
-  });
-}
-
-// The kept rows, where the tables are written.
+// The experts' kept rows, compact.
 struct TileArgs {
   RowsArgs r;
   const int* start;
@@ -250,16 +228,6 @@ struct Plain {
     return hipGetLastError();
   }
 };
-struct Planned {
-  KeptArgs a;
-  dim3 grid;
-  hipStream_t st;
-  template <int DT, int WPR, int R>
-  hipError_t run() const {
-    CC_LAUNCH((k_int8_kept<DT, WPR, R>), grid, dim3(kPlanBlock), 0, st, a);
-    return hipGetLastError();
-  }
-};
 struct Tiled {
   TileArgs a;
   dim3 grid;
@@ -279,6 +247,61 @@ hipError_t pick_rows(uint64_t width, const L& launch) {
   if (width <= 4 * one) return launch.template run<DT, 1, 4>();
   if (width <= 8 * one) return launch.template run<DT, 1, 8>();
   return launch.template run<DT, 4, 8>();
+}
+
+// ------------------------------------------------------------------ copies
+
+// Lines that start at any byte into lines of whole 16-byte chunks, zeros past
+// their end, by a wave, four loads under way.
+__device__ __forceinline__ void copy_line(const char* from, uint64_t cols, char* to, uint64_t pitch) {
+  const int lane = threadIdx.x & 63;
+  for (uint64_t c0 = (uint64_t)lane * 16; c0 < pitch; c0 += 4 * 1024) {
+    u32x4 w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + q * 1024;
+      w[q] = u32x4{0u, 0u, 0u, 0u};
+      if (c + 16 <= cols) {
+        w[q] = *(const u32x4_byte*)(from + c);
+      } else if (c < cols) {
+        for (uint64_t i = 0; c + i < cols; ++i) w[q][i >> 2] |= (uint32_t)(uint8_t)from[c + i] << (8 * (i & 3));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (c0 + q * 1024 < pitch) *(u32x4*)(to + c0 + q * 1024) = w[q];
+  }
+}
+
+// The experts' weights, 16 lines a workgroup; y: which of them.
+struct WeightCopy {
+  const int* start;
+  int per;
+  struct {
+    const char* from;
+    uint64_t rank_stride;
+    uint64_t lines, each, cols;   // lines in all and of an expert
+    char* to;
+    uint64_t pitch;
+  } job[2];
+};
+constexpr int kCopyLines = 16;
+__global__ __launch_bounds__(256) void k_int8_copy_weights(WeightCopy a) {
+  const auto& j = a.job[blockIdx.y];
+  const uint64_t first = (uint64_t)blockIdx.x * kCopyLines + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (uint64_t l = first; l < first + kCopyLines && l < j.lines; l += 4) {
+    const uint64_t e = l / j.each, r = e / a.per;
+    if (a.start[e] == a.start[e + 1]) continue;   // no rows: never read
+    copy_line(j.from + r * j.rank_stride + (l - r * a.per * j.each) * j.cols, j.cols, j.to + l * j.pitch, j.pitch);
+  }
+}
+
+// The kept rows of a product, compact.
+__global__ __launch_bounds__(256) void k_int8_copy_rows(TileArgs a) {
+  table_rows(a.start, a.mtab, a.map, [&](uint32_t l, uint32_t place, int e) {
+    copy_line(a.r.x + (uint64_t)(e / a.per) * a.r.x_stride + (uint64_t)place * a.r.width, a.r.width,
+              a.r.q + (uint64_t)l * a.r.q_pitch, a.r.q_pitch);
+  });
 }
 
 // ------------------------------------------------------------------ products
@@ -317,29 +340,44 @@ I8Args int8_args(const Int8Launch& L) {
   return g;
 }
 
+hipError_t copy_weights(const Int8Launch& L, bool block) {
+  const uint64_t W = L.s.W, F = L.s.F, n = L.s.E, in = block ? 2 * F : F;
+  WeightCopy a = {};
+  a.start = (const int*)(L.ws + L.o.plan.start);
+  a.per = L.s.E / L.s.N;
+  int jobs = 0;
+  uint64_t lines = 0;
+  auto add = [&](const Side& w, uint64_t each, uint64_t cols, uint64_t to) {
+    a.job[jobs++] = {w.base, w.stride, n * each, each, cols, L.ws + to, line_pitch(L.s, cols)};
+    lines = std::max(lines, n * each);
+  };
+  if (L.o.copied_in) add(L.w_in, in, W, L.o.w_in);
+  if (L.o.copied_out) add(L.w_out, W, F, L.o.w_out);
+  if (jobs == 0) return hipSuccess;
+  const dim3 grid((unsigned)((lines + kCopyLines - 1) / kCopyLines), (unsigned)jobs);
+  CC_LAUNCH(k_int8_copy_weights, grid, dim3(256), 0, L.st, a);
+  return hipGetLastError();
+}
+
+TileArgs tile_args(const Int8Launch& L, const RowsArgs& r) {
+  return TileArgs{r, (const int*)(L.ws + L.o.plan.start), (const int2*)(L.ws + L.o.plan.mtab[kFfnTiles - 1]),
+                  (const int*)(L.ws + L.o.plan.rowmap), L.s.E / L.s.N};
+}
+
 // the plan, and the kept rows quantised
 hipError_t planned_rows(const Int8Launch& L, const RowsArgs& r) {
-  if (const unsigned parts = plan_parts(L.s)) {
-    Planned p = {};
-    p.a.r = r;
-    p.grid = dim3((unsigned)L.s.E, parts);
-    p.st = L.st;
-    const hipError_t e = ffn_plan_args(L.s, L.o.plan, L.ws, L.kept, L.st, &p.a.plan);
-    if (e != hipSuccess) return e;
-    return L.dt == DT_F32 ? pick_rows<DT_F32>(r.width, p) : pick_rows<DT_BF16>(r.width, p);
-  }
   const hipError_t e = launch_ffn_plan(L.s, L.o.plan, L.ws, L.kept, L.st);
   if (e != hipSuccess) return e;
-  const int last = kFfnTiles - 1;
-  const Tiled t{{r, (const int*)(L.ws + L.o.plan.start), (const int2*)(L.ws + L.o.plan.mtab[last]),
-                 (const int*)(L.ws + L.o.plan.rowmap), L.s.E / L.s.N},
-                dim3((unsigned)L.s.mtiles[last], kTileParts), L.st};
+  const Tiled t{tile_args(L, r), dim3((unsigned)L.s.mtiles[kFfnTiles - 1], kTileParts), L.st};
   return L.dt == DT_F32 ? pick_rows<DT_F32>(r.width, t) : pick_rows<DT_BF16>(r.width, t);
 }
 
-// `lines` rows of `cols` weights an expert
-void weights_of(I8Args* g, const Side& w, const Side& s, uint64_t lines, uint64_t cols) {
-  g->b = WtSide{w.base, w.stride, lines * cols, cols};
+// `lines` rows of `cols` weights an expert, the caller's or their copies
+void weights_of(I8Args* g, const Int8Launch& L, const Side& w, const Side& s, uint64_t lines, uint64_t cols, int copied,
+                uint64_t copy) {
+  const uint64_t p = copied ? line_pitch(L.s, cols) : cols;
+  g->b = copied ? WtSide{L.ws + copy, (uint64_t)g->per * lines * p, lines * p, p}
+                : WtSide{w.base, w.stride, lines * p, p};
   g->sw = s.base;
   g->sw_stride = s.stride;
   g->M = (int)lines;
@@ -353,6 +391,21 @@ hipError_t launch_int8_rows(const Int8Rows& L) {
   return L.dt == DT_F32 ? pick_rows<DT_F32>(L.width, p) : pick_rows<DT_BF16>(L.width, p);
 }
 
+// Whether weights of rows that are no whole 16-byte vectors are copied into lines
+// that direct loads take, so that the same tiles run on them.  The block's rows x
+// and h lie in such lines anyway; a product on its own copies its rows too.
+// Measured on 16 experts, bf16, through registers and copied: block 2047 x 2047
+// 256 rows an expert 255 us and 276, 512 377 and 340, 4096 2175 and 1153; 201 x 333 512
+// rows 59 and 54, 4096 219 and 163; product 2047 x 2047 512 rows 165 and 150, 1001 x 733
+// 1024 rows 73 and 78, 4096 230 and 195, 517 x 300 4096 rows 118 and 139.
+constexpr uint64_t kCopyBlockRows = 512, kCopyBlockCols = 192, kCopyProductRows = 1024, kCopyProductCols = 512;
+static int int8_copied(const FfnShape& s, bool block, uint64_t lines, uint64_t cols) {
+  const uint64_t p = line_pitch(s, cols);
+  return cols % 16 != 0 && s.rows >= (block ? kCopyBlockRows : kCopyProductRows) * s.E &&
+         std::min(lines, cols) >= (block ? kCopyBlockCols : kCopyProductCols) && s.most * p <= kMaxSpan &&
+         lines * p <= kMaxSpan;
+}
+
 Int8Ws int8_ws(const FfnShape& s, int block, int out_es) {
   Int8Ws o = {};
   uint64_t at = 0;
@@ -361,19 +414,23 @@ Int8Ws int8_ws(const FfnShape& s, int block, int out_es) {
     at += up256(bytes);
     return p;
   };
-  o.plan.kept = take(plan_words(s) * 4);
+  o.plan.kept = take((uint64_t)s.N * s.E * 4);
   o.plan.start = take(((uint64_t)s.E + 1) * 4);
   for (int k = 0; k < kFfnTiles; ++k) o.plan.mtab[k] = take(s.mtiles[k] * 8);
   o.plan.rowmap = take(s.rows * 4);
+  o.xq_pitch = line_pitch(s, s.W);
+  o.hq_pitch = line_pitch(s, s.F);
+  o.copied_in = int8_copied(s, block, block ? 2 * s.F : s.F, s.W);
+  o.copied_out = block && int8_copied(s, true, s.W, s.F);
+  if (block || o.copied_in) o.xq = take(s.rows * o.xq_pitch);
   if (block) {
-    o.xq_pitch = line_pitch(s, s.W);
-    o.hq_pitch = line_pitch(s, s.F);
-    o.xq = take(s.rows * o.xq_pitch);
     o.xs = take(s.rows * 4);
     o.h = take(s.rows * s.F * out_es);
     o.hq = take(s.rows * o.hq_pitch);
     o.hs = take(s.rows * 4);
   }
+  if (o.copied_in) o.w_in = take((uint64_t)s.E * (block ? 2 : 1) * s.F * o.xq_pitch);
+  if (o.copied_out) o.w_out = take((uint64_t)s.E * s.W * o.hq_pitch);
   o.bytes = at;
   return o;
 }
@@ -385,13 +442,20 @@ hipError_t launch_int8(const Int8Launch& L) {
   I8Args g = int8_args(L);
   g.K = (int)W;
   g.N = (int)C;
+  bool fast = L.x_ok && L.w_in_ok && side * W <= kMaxSpan && C * W <= kMaxSpan;
   g.a = RowSide{L.x.base, L.x.stride, W, g.map, side * W};
-  weights_of(&g, L.w_in, L.s_in, C, W);
+  if (L.o.copied_in) {
+    const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, nullptr, 0, L.s.rows, W};
+    CC_LAUNCH(k_int8_copy_rows, dim3((unsigned)L.s.mtiles[kFfnTiles - 1], kTileParts), dim3(256), 0, L.st, tile_args(L, r));
+    if ((e = hipGetLastError()) != hipSuccess || (e = copy_weights(L, false)) != hipSuccess) return e;
+    g.a = RowSide{r.q, 0, r.q_pitch, nullptr, L.s.most * r.q_pitch};
+    fast = true;
+  }
+  weights_of(&g, L, L.w_in, L.s_in, C, W, L.o.copied_in, L.o.w_in);
   g.sx = L.xs.base;
   g.sx_stride = L.xs.stride;
   g.sx_map = g.map;
   g.out = RowSide{L.y.base, L.y.stride, C * es, g.map, side * C * es};
-  const bool fast = L.x_ok && L.w_in_ok && side * W <= kMaxSpan && C * W <= kMaxSpan;
   return pick_int8<K_DOWN>(g, L, fast, L.y_ok);
 }
 
@@ -399,16 +463,17 @@ hipError_t launch_int8_ffn(const Int8Launch& L) {
   const uint64_t W = L.s.W, F = L.s.F, es = elem_size(L.dt);
   const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, L.ws + L.o.xs, 0, L.s.rows, W};
   hipError_t e = planned_rows(L, r);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || (e = copy_weights(L, true)) != hipSuccess) return e;
   I8Args g = int8_args(L);
   g.K = (int)W;
   g.N = (int)(2 * F);
   g.a = RowSide{r.q, 0, L.o.xq_pitch, nullptr, L.s.most * L.o.xq_pitch};
-  weights_of(&g, L.w_in, L.s_in, 2 * F, W);
+  weights_of(&g, L, L.w_in, L.s_in, 2 * F, W, L.o.copied_in, L.o.w_in);
   g.sx = r.s;
   g.out = RowSide{L.ws + L.o.h, 0, F * es, nullptr, L.s.most * F * es};
   const bool rows_fit = L.s.most * std::max(L.o.xq_pitch, L.o.hq_pitch) <= kMaxSpan;
-  if ((e = pick_int8<K_GATEUP>(g, L, L.w_in_ok && rows_fit && 2 * F * W <= kMaxSpan, F * es % 16 == 0)) != hipSuccess)
+  if ((e = pick_int8<K_GATEUP>(g, L, L.o.copied_in || (L.w_in_ok && rows_fit && 2 * F * W <= kMaxSpan),
+                                F * es % 16 == 0)) != hipSuccess)
     return e;
   Int8Rows q = {};
   q.x = L.ws + L.o.h;
@@ -420,10 +485,10 @@ hipError_t launch_int8_ffn(const Int8Launch& L) {
   g.K = (int)F;
   g.N = (int)W;
   g.a = RowSide{q.q, 0, L.o.hq_pitch, nullptr, L.s.most * L.o.hq_pitch};
-  weights_of(&g, L.w_out, L.s_out, W, F);
+  weights_of(&g, L, L.w_out, L.s_out, W, F, L.o.copied_out, L.o.w_out);
   g.sx = q.s;
   g.out = RowSide{L.y.base, L.y.stride, W * es, g.map, (uint64_t)L.s.E * L.s.cap * W * es};
-  return pick_int8<K_DOWN>(g, L, L.w_out_ok && rows_fit && F * W <= kMaxSpan, L.y_ok);
+  return pick_int8<K_DOWN>(g, L, L.o.copied_out || (L.w_out_ok && rows_fit && F * W <= kMaxSpan), L.y_ok);
 }
 
 }  // namespace cc

@@ -148,7 +148,7 @@ inline CkptRow ckpt_row(uint64_t W, uint64_t F) {
 // ---- gated feed-forward block of the experts.  Compact rows: the kept rows
 // of all experts back to back, expert by expert, source by source.
 // Workspace: row starts [E + 1], row tiles of each size (expert, first row), row
-// map [rows] (row in the rank's buffer), the plan's words, h [rows][F],
+// map [rows] (row in the rank's buffer), kept counts [N * E], h [rows][F],
 // and for the gradient d(gate | up) [rows][2F].  Where rows are no whole
 // 16-byte vectors it may hold aligned copies, lines padded with zeros to 128
 // bytes (h and d(gate | up) then too): x and dy by compact rows, the weights.
@@ -172,8 +172,6 @@ struct FfnLaunch {
 };
 hipError_t launch_ffn(const FfnLaunch& L);
 hipError_t launch_ffn_grad(const FfnLaunch& L);
-// words that the plan's launches take, of every expert its first row and tiles and its kept rows from each source
-inline uint64_t plan_words(const FfnShape& s) { return (uint64_t)s.E * (1 + kFfnTiles + s.N); }
 // the plan alone: o.kept, o.start, o.mtab and o.rowmap
 hipError_t launch_ffn_plan(const FfnShape& s, const FfnWs& o, char* ws, const uint32_t* kept, hipStream_t st);
 
@@ -181,8 +179,8 @@ hipError_t launch_ffn_plan(const FfnShape& s, const FfnWs& o, char* ws, const ui
 struct CkArgs;
 hipError_t ckpt_gateup(const CkArgs& g, const FfnLaunch& L);
 hipError_t ckpt_dhid(const CkArgs& g, const FfnLaunch& L);
-hipError_t ckpt_plan_pack(const FfnLaunch& L);     // the plan, and x into the checkpoint
-hipError_t ckpt_plan_unpack(const FfnLaunch& L);   // and out of it, into the workspace
+hipError_t ckpt_pack_x(const FfnLaunch& L);
+hipError_t ckpt_unpack_x(const FfnLaunch& L);   // into the workspace
 
 // ---- 8-bit integers: rows and their scales, grouped products
 struct Int8Rows {
@@ -197,10 +195,16 @@ struct Int8Rows {
   hipStream_t st;
 };
 hipError_t launch_int8_rows(const Int8Rows& L);
+// Workspace: the plan's tables; of the block the rows x and h in 8 bits (lines
+// padded with zeros to 128 bytes), their scales and h; and where a product's rows
+// are no whole 16-byte vectors it may hold copies in such lines: of the weights,
+// and of the product's rows.
 struct Int8Ws {
   FfnWs plan;
   uint64_t xq, xs, h, hq, hs, bytes;
   uint64_t xq_pitch, hq_pitch;
+  int copied_in, copied_out;
+  uint64_t w_in, w_out;
 };
 Int8Ws int8_ws(const FfnShape& s, int block, int out_es);
 struct Int8Launch {
