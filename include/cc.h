@@ -757,8 +757,8 @@ cc_status_t cc_moe_ffn_int8_workspace_size(const size_t* counts, int nexperts, s
  * cc_moe_ffn_checkpoint_row bytes: the int8 values of x, of g and of u, each from
  * a multiple of 16 bytes, then the blocks' exponents of x, of g and of u, a byte
  * e + 127 each (255: NaN), back to back.  Base and rank stride are multiples of
- * 16 bytes.  Rows behind a block's kept ones are neither read nor written, nor are
- * the bytes between a row's parts.
+ * 16 bytes.  Rows behind a block's kept ones are neither read nor written; the
+ * bytes between a row's parts mean nothing.
  * y, and every other argument, is that of cc_moe_ffn. */
 #define CC_CKPT_BLOCK 32
 cc_status_t cc_moe_ffn_checkpoint(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t ckpt,

@@ -187,6 +187,14 @@ __device__ __forceinline__ u32x4 frag(const char* t, int u, int i0, int lane) {
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 
+// The last n (1 to 15) bytes of a line of at least 16 whose end is `end`, zeros
+// behind them: its last 16 bytes, shifted (byte by byte each load would wait for
+// the one before).
+__device__ __forceinline__ u32x4 line_tail(const char* end, int n) {
+  typedef unsigned __int128 u128;
+  return __builtin_bit_cast(u32x4, __builtin_bit_cast(u128, (u32x4) * (const u32x4_byte*)(end - 16)) >> (8 * (16 - n)));
+}
+
 template <int DT, bool COL, int R, int NT>
 struct Chunks {
   static constexpr int SZ = Ty<DT>::SZ, V = Ty<DT>::V, Q = R * kKBytes / 16 / NT;
@@ -214,8 +222,12 @@ struct Chunks {
       if (p && left >= V) {
         v[q] = load_any(p + at * SZ);
       } else if constexpr (DT == DT_I8) {
-        if (p)
-          for (int i = 0; i < left; ++i) v[q][i >> 2] |= (uint32_t)(uint8_t)p[at + i] << (8 * (i & 3));
+        static_assert(!COL, "rows end at K");
+        if (left > 0) {
+          if (K >= V) v[q] = line_tail(p + K, (int)left);
+          else
+            for (int i = 0; i < left; ++i) v[q][i >> 2] |= (uint32_t)(uint8_t)p[at + i] << (8 * (i & 3));
+        }
       } else if (p && left > 0) {
         float x[V] = {};
 #pragma unroll

@@ -251,36 +251,24 @@ hipError_t pick_rows(uint64_t width, const L& launch) {
 
 // ------------------------------------------------------------------ copies
 
-// Lines that start at any byte into lines of whole 16-byte chunks, zeros past
-// their end, by a wave, four loads under way.
-__device__ __forceinline__ void copy_line(const char* from, uint64_t cols, char* to, uint64_t pitch) {
-  const int lane = threadIdx.x & 63;
-  for (uint64_t c0 = (uint64_t)lane * 16; c0 < pitch; c0 += 4 * 1024) {
-    u32x4 w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint64_t c = c0 + q * 1024;
-      w[q] = u32x4{0u, 0u, 0u, 0u};
-      if (c + 16 <= cols) {
-        w[q] = *(const u32x4_byte*)(from + c);
-      } else if (c < cols) {
-        for (uint64_t i = 0; c + i < cols; ++i) w[q][i >> 2] |= (uint32_t)(uint8_t)from[c + i] << (8 * (i & 3));
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (c0 + q * 1024 < pitch) *(u32x4*)(to + c0 + q * 1024) = w[q];
-  }
+// Lines of at least 16 bytes that start at any byte into lines of whole 16-byte
+// chunks, zeros past their end.
+__device__ __forceinline__ u32x4 line_chunk(const char* from, uint64_t cols, uint64_t c) {
+  if (c + 16 <= cols) return *(const u32x4_byte*)(from + c);
+  if (c < cols) return line_tail(from + cols, (int)(cols - c));
+  return u32x4{0u, 0u, 0u, 0u};
 }
 
-// The experts' weights, 16 lines a workgroup; y: which of them.
+// An expert's weights (z), 16 lines a workgroup, 4 a wave at a time; y: which of
+// them.  Bound by memory: 16 experts of 2047 x 2047 30 us, 4.5 TB/s (53 with the last
+// bytes of a line loaded one by one).
 struct WeightCopy {
   const int* start;
   int per;
   struct {
     const char* from;
     uint64_t rank_stride;
-    uint64_t lines, each, cols;   // lines in all and of an expert
+    uint64_t each, cols;   // lines of an expert
     char* to;
     uint64_t pitch;
   } job[2];
@@ -288,19 +276,35 @@ struct WeightCopy {
 constexpr int kCopyLines = 16;
 __global__ __launch_bounds__(256) void k_int8_copy_weights(WeightCopy a) {
   const auto& j = a.job[blockIdx.y];
-  const uint64_t first = (uint64_t)blockIdx.x * kCopyLines + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (uint64_t l = first; l < first + kCopyLines && l < j.lines; l += 4) {
-    const uint64_t e = l / j.each, r = e / a.per;
-    if (a.start[e] == a.start[e + 1]) continue;   // no rows: never read
-    copy_line(j.from + r * j.rank_stride + (l - r * a.per * j.each) * j.cols, j.cols, j.to + l * j.pitch, j.pitch);
+  const int lane = threadIdx.x & 63, e = blockIdx.z, r = e / a.per;
+  if (a.start[e] == a.start[e + 1]) return;   // no rows: never read
+  const uint64_t first = (uint64_t)blockIdx.x * kCopyLines + 4 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const char* from = j.from + (uint64_t)r * j.rank_stride + ((uint64_t)(e - r * a.per) * j.each + first) * j.cols;
+  char* to = j.to + ((uint64_t)e * j.each + first) * j.pitch;
+  for (uint64_t c = (uint64_t)lane * 16; c < j.pitch; c += 1024) {
+    u32x4 w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (first + k < j.each) w[k] = line_chunk(from + k * j.cols, j.cols, c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (first + k < j.each) *(u32x4*)(to + k * j.pitch + c) = w[k];
   }
 }
 
 // The kept rows of a product, compact.
 __global__ __launch_bounds__(256) void k_int8_copy_rows(TileArgs a) {
   table_rows(a.start, a.mtab, a.map, [&](uint32_t l, uint32_t place, int e) {
-    copy_line(a.r.x + (uint64_t)(e / a.per) * a.r.x_stride + (uint64_t)place * a.r.width, a.r.width,
-              a.r.q + (uint64_t)l * a.r.q_pitch, a.r.q_pitch);
+    const char* from = a.r.x + (uint64_t)(e / a.per) * a.r.x_stride + (uint64_t)place * a.r.width;
+    char* to = a.r.q + (uint64_t)l * a.r.q_pitch;
+    for (uint64_t c0 = (uint64_t)(threadIdx.x & 63) * 16; c0 < a.r.q_pitch; c0 += 4 * 1024) {   // four loads under way
+      u32x4 w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = line_chunk(from, a.r.width, c0 + q * 1024);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c0 + q * 1024 < a.r.q_pitch) *(u32x4*)(to + c0 + q * 1024) = w[q];
+    }
   });
 }
 
@@ -341,20 +345,20 @@ I8Args int8_args(const Int8Launch& L) {
 }
 
 hipError_t copy_weights(const Int8Launch& L, bool block) {
-  const uint64_t W = L.s.W, F = L.s.F, n = L.s.E, in = block ? 2 * F : F;
+  const uint64_t W = L.s.W, F = L.s.F, in = block ? 2 * F : F;
   WeightCopy a = {};
   a.start = (const int*)(L.ws + L.o.plan.start);
   a.per = L.s.E / L.s.N;
   int jobs = 0;
   uint64_t lines = 0;
   auto add = [&](const Side& w, uint64_t each, uint64_t cols, uint64_t to) {
-    a.job[jobs++] = {w.base, w.stride, n * each, each, cols, L.ws + to, line_pitch(L.s, cols)};
-    lines = std::max(lines, n * each);
+    a.job[jobs++] = {w.base, w.stride, each, cols, L.ws + to, line_pitch(L.s, cols)};
+    lines = std::max(lines, each);
   };
   if (L.o.copied_in) add(L.w_in, in, W, L.o.w_in);
   if (L.o.copied_out) add(L.w_out, W, F, L.o.w_out);
   if (jobs == 0) return hipSuccess;
-  const dim3 grid((unsigned)((lines + kCopyLines - 1) / kCopyLines), (unsigned)jobs);
+  const dim3 grid((unsigned)((lines + kCopyLines - 1) / kCopyLines), (unsigned)jobs, (unsigned)L.s.E);
   CC_LAUNCH(k_int8_copy_weights, grid, dim3(256), 0, L.st, a);
   return hipGetLastError();
 }
@@ -394,14 +398,15 @@ hipError_t launch_int8_rows(const Int8Rows& L) {
 // Whether weights of rows that are no whole 16-byte vectors are copied into lines
 // that direct loads take, so that the same tiles run on them.  The block's rows x
 // and h lie in such lines anyway; a product on its own copies its rows too.
-// Measured on 16 experts, bf16, through registers and copied: block 2047 x 2047
-// 256 rows an expert 255 us and 276, 512 377 and 340, 4096 2175 and 1153; 201 x 333 512
-// rows 59 and 54, 4096 219 and 163; product 2047 x 2047 512 rows 165 and 150, 1001 x 733
-// 1024 rows 73 and 78, 4096 230 and 195, 517 x 300 4096 rows 118 and 139.
-constexpr uint64_t kCopyBlockRows = 512, kCopyBlockCols = 192, kCopyProductRows = 1024, kCopyProductCols = 512;
+// Measured on 16 experts, bf16, through registers and copied: block 2047 x 2047 512
+// rows an expert 273 us and 289, 1024 418 and 397, 4096 1505 and 1059; 201 x 333 512 rows
+// 42 and 45, 1024 62 and 60, 4096 161 and 140; product 2047 x 2047 1024 rows 188 and
+// 161, 4096 679 and 486, 1001 x 733 1024 rows 61 and 61, 517 x 300 4096 rows 108 and 119.
+constexpr uint64_t kCopyRows = 1024, kCopyBlockCols = 192, kCopyProductCols = 512;
+static_assert(kCopyBlockCols >= 16 && kCopyProductCols >= 16, "line_chunk's lines");
 static int int8_copied(const FfnShape& s, bool block, uint64_t lines, uint64_t cols) {
   const uint64_t p = line_pitch(s, cols);
-  return cols % 16 != 0 && s.rows >= (block ? kCopyBlockRows : kCopyProductRows) * s.E &&
+  return cols % 16 != 0 && s.rows >= kCopyRows * s.E &&
          std::min(lines, cols) >= (block ? kCopyBlockCols : kCopyProductCols) && s.most * p <= kMaxSpan &&
          lines * p <= kMaxSpan;
 }

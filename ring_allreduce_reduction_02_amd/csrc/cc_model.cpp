@@ -227,8 +227,10 @@ cc_status_t run_ffn(const FfnBufs& f, const size_t* counts, int E, uint64_t cap,
   const u128 wi_n = (u128)(E / N) * 2 * F * W * es, wo_n = (u128)(E / N) * W * F * es;
   const u128 ckpt_n = (u128)E * cap * (unsigned)ckpt_row(W, F).pitch;
   const bool keep = !f.kept8 && (grad || f.pre.base != nullptr);
-  std::vector<Buf> b = {{&f.w_in, wi_n, "w_in", false, N}, {&f.w_out, wo_n, "w_out", false, N}};
+  std::vector<Buf> b;
   if (!grad || !f.kept8) b.push_back({&f.x, side_n, "x", false, N});
+  b.push_back({&f.w_in, wi_n, "w_in", false, N});
+  b.push_back({&f.w_out, wo_n, "w_out", false, N});
   if (f.kept8) b.push_back({&f.ckpt, ckpt_n, "ckpt", !grad, N});
   if (keep) b.push_back({&f.pre, pre_n, "pre", !grad, N});
   if (grad) {
