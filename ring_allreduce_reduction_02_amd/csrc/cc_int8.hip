@@ -402,12 +402,12 @@ hipError_t launch_int8_rows(const Int8Rows& L) {
 // rows an expert 273 us and 289, 1024 418 and 397, 4096 1505 and 1059; 201 x 333 512 rows
 // 42 and 45, 1024 62 and 60, 4096 161 and 140; product 2047 x 2047 1024 rows 188 and
 // 161, 4096 679 and 486, 1001 x 733 1024 rows 61 and 61, 517 x 300 4096 rows 108 and 119.
-constexpr uint64_t kCopyRows = 1024, kCopyBlockCols = 192, kCopyProductCols = 512;
-static_assert(kCopyBlockCols >= 16 && kCopyProductCols >= 16, "line_chunk's lines");
+constexpr uint64_t kCopyInt8Rows = 1024, kCopyInt8BlockCols = 192, kCopyInt8ProductCols = 512;
+static_assert(kCopyInt8BlockCols >= 16 && kCopyInt8ProductCols >= 16, "line_chunk's lines");
 static int int8_copied(const FfnShape& s, bool block, uint64_t lines, uint64_t cols) {
   const uint64_t p = line_pitch(s, cols);
-  return cols % 16 != 0 && s.rows >= kCopyRows * s.E &&
-         std::min(lines, cols) >= (block ? kCopyBlockCols : kCopyProductCols) && s.most * p <= kMaxSpan &&
+  return cols % 16 != 0 && s.rows >= kCopyInt8Rows * s.E &&
+         std::min(lines, cols) >= (block ? kCopyInt8BlockCols : kCopyInt8ProductCols) && s.most * p <= kMaxSpan &&
          lines * p <= kMaxSpan;
 }
 
