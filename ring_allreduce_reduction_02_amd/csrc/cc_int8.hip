@@ -24,6 +24,7 @@ struct RowsArgs {
   char* s;
   uint64_t s_stride;
   uint64_t rows, width;
+  uint64_t row0;         // of a launch
 };
 
 // The integer nearest |u| / s, ties to even, for s of 2^-100 and more: k or k + 1,
@@ -32,8 +33,8 @@ struct RowsArgs {
 // the quotient.
 __device__ __forceinline__ float nearest(float u, float s, float est) {
   const float k = __builtin_truncf(est), rem = __builtin_fmaf(-(k + 0.5f), s, u);
-  const bool odd = (int)k & 1;
-  return rem > 0.0f || (rem == 0.0f && odd) ? k + 1.0f : k;
+  const int up = (int)(rem > 0.0f) | ((int)(rem == 0.0f) & (int)k & 1);
+  return k + (float)up;
 }
 
 typedef uint32_t u32_byte __attribute__((aligned(1)));
@@ -113,9 +114,9 @@ __device__ __forceinline__ void quantized_small(u32x4 in, float s, uint32_t* w) 
 }
 
 // A row by WPR waves (1 or 4), R vectors a lane in registers; longer rows (WPR 4)
-// are read twice.  Bound by memory: 81920 rows of 2048 bf16, 503 MB in and out, 79 us,
-// 6.4 TB/s; 60.7k kept rows 61 us.  (With a branch to the float64 quotient behind
-// every element 150 and 168.)
+// are read twice.  Bound by memory: 81920 rows of 2048 bf16, 503 MB in and out, 82 us,
+// 6.1 TB/s; 60.7k kept rows 67 us, as many compact ones 57.  (With a branch to the
+// float64 quotient behind every element 150 and 168.)
 template <int DT, int WPR, int R>
 __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char* q, uint64_t pitch, float* scale,
                                              uint32_t* red) {
@@ -124,40 +125,36 @@ __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char
   constexpr uint64_t STEP = (uint64_t)64 * WPR * V;
   u32x4 held[R];
   Top<DT> best;
-  auto load = [&](uint64_t c) {
-    if (c + V <= width) return (u32x4) * (const u32x4_any*)(x + c * SZ);
-    if (c < width) return load_n<DT, false>(x + c * SZ, (int)(width - c));
+  // this lane's vector of the STEP elements from b on; whether all of them are inside is the same on all lanes
+  auto load = [&](uint64_t b) {
+    const uint64_t c = b + (uint64_t)tid * V;
+    if (b + STEP <= width) return (u32x4) * (const u32x4_any*)(x + c * SZ);
+    if (b < width) {
+      const int64_t left = (int64_t)width - (int64_t)c;
+      return load_n<DT, false>(x + c * SZ, (int)(left < V ? left > 0 ? left : 0 : V));
+    }
     return u32x4{0u, 0u, 0u, 0u};
   };
 #pragma unroll
-  for (int k = 0; k < R; ++k) held[k] = load(k * STEP + (uint64_t)tid * V);
+  for (int k = 0; k < R; ++k) held[k] = load(k * STEP);
 #pragma unroll
   for (int k = 0; k < R; ++k) best.take(held[k]);
   if constexpr (WPR > 1)
-    for (uint64_t c = R * STEP + (uint64_t)tid * V; c < width; c += STEP) best.take(load(c));
+    for (uint64_t b = R * STEP; b < width; b += STEP) best.take(load(b));
   uint32_t top = wave_umax(best.bits());
   if constexpr (WPR > 1) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < WPR; ++k) top = red[k] > top ? red[k] : top;
+    top = (uint32_t)__builtin_amdgcn_readfirstlane((int)top);
   }
   const bool nan = top >= 0x7f800000u;
   const float s = nan ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
-  const float inv = __builtin_amdgcn_rcpf(s);
-  auto put = [&](uint64_t c, u32x4 in) {
-    if (c >= pitch) return;
-    uint32_t w[V / 4];
-    if (s >= 0x1p-100f) {
-      quantized<DT, V>(in, s, inv, w);
-    } else if (s > 0.0f) {
-      quantized_small<DT, V>(in, s, w);
-    } else {   // zeros, or (NaN) marked
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) w[i] = 0;
-    }
+  auto put = [&](uint64_t b, const uint32_t* w) {
+    const uint64_t c = b + (uint64_t)tid * V;
     char* o = q + c;
-    if (c + V <= pitch) {
+    if (b + STEP <= pitch || c + V <= pitch) {
       if constexpr (V == 8) *(u32x2_byte*)o = u32x2_byte{w[0], w[1]};
       else *(u32_byte*)o = w[0];
     } else {
@@ -166,27 +163,47 @@ __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char
         if (c + i < pitch) o[i] = (char)(w[i / 4] >> (8 * (i & 3)));
     }
   };
+  uint32_t w[V / 4];
+  if (s >= 0x1p-100f) {
+    const float inv = __builtin_amdgcn_rcpf(s);
 #pragma unroll
-  for (int k = 0; k < R; ++k) put(k * STEP + (uint64_t)tid * V, held[k]);
-  if constexpr (WPR > 1)
-    for (uint64_t c = R * STEP + (uint64_t)tid * V; c < pitch; c += STEP) put(c, load(c));
+    for (int k = 0; k < R; ++k)
+      if (k * STEP < pitch) {
+        quantized<DT, V>(held[k], s, inv, w);
+        put(k * STEP, w);
+      }
+    if constexpr (WPR > 1)
+      for (uint64_t b = R * STEP; b < pitch; b += STEP) {
+        quantized<DT, V>(load(b), s, inv, w);
+        put(b, w);
+      }
+  } else {   // a small scale, zeros, or (NaN) a marked row
+#pragma unroll 1
+    for (uint64_t b = 0; b < pitch; b += STEP) {
+      if (s > 0.0f) {
+        quantized_small<DT, V>(load(b), s, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) w[i] = 0;
+      }
+      put(b, w);
+    }
+  }
   if (tid == 0) *scale = s;
 }
 
-// Plain rows: blockIdx.y the rank, 4 / WPR rows a workgroup at a time.
+// Plain rows: blockIdx.y the rank, 4 / WPR rows a workgroup.  (One row a wave: in a
+// loop over rows the compiler keeps the masks of a row's end for the next one.)
 constexpr uint64_t kRowsGrid = 1u << 22;   // workgroups of 256 threads whose work-items fit 32 bits
 template <int DT, int WPR, int R>
 __global__ __launch_bounds__(256) void k_int8_rows(RowsArgs a) {
   __shared__ uint32_t red[4];
   const uint64_t r = blockIdx.y;
-  const char* x = a.x + r * a.x_stride;
-  char* q = a.q + r * a.q_stride;
-  float* s = (float*)(a.s + r * a.s_stride);
   const int wave = WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-  for (uint64_t row = (uint64_t)blockIdx.x * (4 / WPR) + wave; row < a.rows; row += (uint64_t)gridDim.x * (4 / WPR)) {
-    quantize_row<DT, WPR, R>(x + row * a.width * Ty<DT>::SZ, a.width, q + row * a.q_pitch, a.q_pitch, s + row, red);
-    if constexpr (WPR > 1) __syncthreads();   // `red` is read
-  }
+  const uint64_t row = a.row0 + (uint64_t)blockIdx.x * (4 / WPR) + wave;
+  if (row < a.rows)   // the same on the wave, or (WPR 4) the workgroup
+    quantize_row<DT, WPR, R>(a.x + r * a.x_stride + row * a.width * Ty<DT>::SZ, a.width,
+                             a.q + r * a.q_stride + row * a.q_pitch, a.q_pitch, (float*)(a.s + r * a.s_stride) + row, red);
 }
 
 // The experts' kept rows, compact.
@@ -206,14 +223,10 @@ __global__ __launch_bounds__(256) void k_int8_tiles(TileArgs a) {
   };
   if constexpr (WPR == 1) {
     table_rows(a.start, a.mtab, a.map, row);
-  } else {
+  } else {   // a row of the tile's a workgroup
     const int2 at = a.mtab[blockIdx.x];
-    const int stop = a.start[at.x + 1];
-    for (int k = 0; k < 4; ++k) {
-      const int l = at.y + (int)blockIdx.y * 4 + k;
-      if (l < stop) row((uint32_t)l, (uint32_t)a.map[l], at.x);   // the same on the whole workgroup
-      __syncthreads();                                            // `red` is read
-    }
+    const int l = at.y + (int)blockIdx.y;
+    if (l < a.start[at.x + 1]) row((uint32_t)l, (uint32_t)a.map[l], at.x);
   }
 }
 
@@ -223,17 +236,22 @@ struct Plain {
   hipStream_t st;
   template <int DT, int WPR, int R>
   hipError_t run() const {
-    const uint64_t per = 4 / WPR, blocks = std::min((a.rows + per - 1) / per, kRowsGrid);
-    CC_LAUNCH((k_int8_rows<DT, WPR, R>), dim3((unsigned)blocks, ranks), dim3(256), 0, st, a);
+    const uint64_t per = 4 / WPR;
+    RowsArgs b = a;
+    for (b.row0 = 0; b.row0 < a.rows; b.row0 += kRowsGrid * per) {
+      const uint64_t blocks = std::min((a.rows - b.row0 + per - 1) / per, kRowsGrid);
+      CC_LAUNCH((k_int8_rows<DT, WPR, R>), dim3((unsigned)blocks, ranks), dim3(256), 0, st, b);
+    }
     return hipGetLastError();
   }
 };
 struct Tiled {
   TileArgs a;
-  dim3 grid;
+  unsigned tiles;
   hipStream_t st;
   template <int DT, int WPR, int R>
   hipError_t run() const {
+    const dim3 grid(tiles, WPR == 1 ? kTileParts : kFfnTile[kFfnTiles - 1]);
     CC_LAUNCH((k_int8_tiles<DT, WPR, R>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
   }
@@ -372,7 +390,7 @@ TileArgs tile_args(const Int8Launch& L, const RowsArgs& r) {
 hipError_t planned_rows(const Int8Launch& L, const RowsArgs& r) {
   const hipError_t e = launch_ffn_plan(L.s, L.o.plan, L.ws, L.kept, L.st);
   if (e != hipSuccess) return e;
-  const Tiled t{tile_args(L, r), dim3((unsigned)L.s.mtiles[kFfnTiles - 1], kTileParts), L.st};
+  const Tiled t{tile_args(L, r), (unsigned)L.s.mtiles[kFfnTiles - 1], L.st};
   return L.dt == DT_F32 ? pick_rows<DT_F32>(r.width, t) : pick_rows<DT_BF16>(r.width, t);
 }
 
@@ -391,7 +409,7 @@ void weights_of(I8Args* g, const Int8Launch& L, const Side& w, const Side& s, ui
 
 hipError_t launch_int8_rows(const Int8Rows& L) {
   if (L.rows == 0) return hipSuccess;
-  const Plain p{{L.x, L.x_stride, L.q, L.q_stride, L.q_pitch, L.s, L.s_stride, L.rows, L.width}, (unsigned)L.N, L.st};
+  const Plain p{{L.x, L.x_stride, L.q, L.q_stride, L.q_pitch, L.s, L.s_stride, L.rows, L.width, 0}, (unsigned)L.N, L.st};
   return L.dt == DT_F32 ? pick_rows<DT_F32>(L.width, p) : pick_rows<DT_BF16>(L.width, p);
 }
 
@@ -450,7 +468,7 @@ hipError_t launch_int8(const Int8Launch& L) {
   bool fast = L.x_ok && L.w_in_ok && side * W <= kMaxSpan && C * W <= kMaxSpan;
   g.a = RowSide{L.x.base, L.x.stride, W, g.map, side * W};
   if (L.o.copied_in) {
-    const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, nullptr, 0, L.s.rows, W};
+    const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, nullptr, 0, L.s.rows, W, 0};
     CC_LAUNCH(k_int8_copy_rows, dim3((unsigned)L.s.mtiles[kFfnTiles - 1], kTileParts), dim3(256), 0, L.st, tile_args(L, r));
     if ((e = hipGetLastError()) != hipSuccess || (e = copy_weights(L, false)) != hipSuccess) return e;
     g.a = RowSide{r.q, 0, r.q_pitch, nullptr, L.s.most * r.q_pitch};
@@ -466,7 +484,7 @@ hipError_t launch_int8(const Int8Launch& L) {
 
 hipError_t launch_int8_ffn(const Int8Launch& L) {
   const uint64_t W = L.s.W, F = L.s.F, es = elem_size(L.dt);
-  const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, L.ws + L.o.xs, 0, L.s.rows, W};
+  const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, L.ws + L.o.xs, 0, L.s.rows, W, 0};
   hipError_t e = planned_rows(L, r);
   if (e != hipSuccess || (e = copy_weights(L, true)) != hipSuccess) return e;
   I8Args g = int8_args(L);
