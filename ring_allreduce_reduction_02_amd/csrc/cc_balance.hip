@@ -112,7 +112,11 @@ __device__ __forceinline__ float exps(float* x) {
 
 // Workgroup b of a rank sums the probabilities of every blocks-th group of
 // tokens and counts those that have any; the next group's logits are under way
-// meanwhile.
+// meanwhile.  16 experts a lane: of 64, 4 lanes hold a token and each sum over
+// them takes 2 moves where a wave a token takes 6 (with 8-byte chunks and moves
+// through LDS 8.0 us where this takes 4.1).  Bound by the latency of a group's
+// loads and exponentials: 8 x 4096 tokens of 64 bf16 4.1 us, 1.0 TB/s; 3 x 1023 of
+// 61 float32 4.7.
 template <int DT, int L>
 __global__ __launch_bounds__(kBalanceBlock) void k_balance(BalArgs a) {
   constexpr int G = kBalanceBlock / L, C = L * kV;      // tokens at a time, columns
@@ -167,7 +171,9 @@ __global__ __launch_bounds__(kBalanceBlock) void k_balance(BalArgs a) {
 
 // The sums of a rank's workgroups (or of all ranks'), a workgroup: its threads
 // are C = 64 .. 1024 columns times 1024 / C parts of the rows.  One column's sums,
-// counts and loss then lie in the threads below C, whose waves are joined.
+// counts and loss then lie in the threads below C, whose waves are joined.  Bound by
+// the latency of a launch and of two rounds of loads: 4.7 us after 8 x 4096 tokens of
+// 64, 3.3 after 3 x 1023 of 61.
 constexpr int kJoin = 1024;
 __global__ __launch_bounds__(kJoin) void k_balance_join(BalArgs a) {
   __shared__ float sum[kJoin];
@@ -241,6 +247,10 @@ __global__ __launch_bounds__(kJoin) void k_balance_join(BalArgs a) {
   }
 }
 
+// A group of tokens at a time as in the sums; f from the counts, once a workgroup.
+// Bound by memory from some megabytes on: 8 x 32768 tokens of 256 bf16, 268 MB in and
+// out, 53.6 us, 5.0 TB/s, its vector instructions 51% of the cycles; below that by
+// latency: 8 x 4096 of 64 float32 added to another gradient 7.1 us, 3.5 TB/s.
 template <int DT, int L, bool BASE>
 __global__ __launch_bounds__(kBalanceBlock) void k_balance_grad(BalArgs a) {
   constexpr int G = kBalanceBlock / L;

@@ -110,8 +110,8 @@ struct CopyArgs {
 constexpr int kCopyLines = kFfnTile[kFfnTiles - 1], kCopyParts = 4;
 
 // Workgroup (x, y, z) copies part z of 64 lines of job y.  Bound by memory: the
-// weights of 16 experts of 2047 x 2047 bf16 and 60.7k rows, 1.3 GB in and out, 271 us,
-// 4.8 TB/s (all 64 lines a workgroup 300, and with one load of a lane under way 350;
+// weights of 16 experts of 2047 x 2047 bf16 and 60.7k rows, 1.3 GB in and out, 260 us,
+// 5.0 TB/s (all 64 lines a workgroup 300, and with one load of a lane under way 350;
 // 6 experts of 515 x 331 and 1.4k rows 12 us and 31).
 template <int DT>
 __global__ __launch_bounds__(256) void k_ffn_copy(CopyArgs a) {

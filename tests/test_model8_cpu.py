@@ -164,6 +164,24 @@ def test_int8_ffn_workspace_grows_with_the_kept_rows():
     assert a >= 64 * (128 + 256 + 200 * 2) and b >= 256 * (128 + 256 + 200 * 2) > a
 
 
+def test_odd_widths_are_copied_from_1024_rows_an_expert():
+    """Weights (and a product's rows) whose rows are no whole 16-byte vectors: copies in the workspace where they pay."""
+    def block(rows, W, F):
+        return ccgpu.moe_ffn_int8_workspace_size([[rows, rows]], rows, W, F, "bf16")
+
+    def product(rows, W, C):
+        return ccgpu.moe_matmul_int8_workspace_size([[rows, rows]], rows, W, C)
+    line = lambda v: -(-v // 128) * 128  # noqa: E731
+    for W, F in ((2047, 1001), (201, 333)):
+        rest = 2048 * (line(W) + line(F) + 2 * F + 12) + (64 << 10)
+        weights = 2 * (2 * F * line(W) + W * line(F))
+        assert block(1023, W, F) < rest and weights <= block(1024, W, F) < rest + weights
+    assert block(1024, 2048, 1008) < 2048 * (2048 + 1024 + 2016 + 12) + (64 << 10)              # whole vectors
+    assert product(1023, 2047, 515) < 64 << 10 and product(1024, 2048, 515) < 64 << 10
+    assert 2048 * 2048 + 2 * 515 * 2048 <= product(1024, 2047, 515) < 2048 * 2048 + 2 * 515 * 2048 + (64 << 10)
+    assert product(1024, 2047, 511) < 64 << 10                                                  # too few columns
+
+
 # ------------------------------------------------------------------ checkpoints
 
 def test_checkpoint_row():
