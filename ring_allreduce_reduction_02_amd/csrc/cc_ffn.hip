@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void k_ffn_put(PutArgs a) {
 
 struct PlanArgs {
   uint32_t v[kPlanCounts];
-  const uint32_t* kept;   // in memory, or NULL: v
+  const uint32_t* kept;   // in memory (ARGS: v)
   int N, E;
   uint64_t cap;
   int* start;
@@ -44,40 +44,53 @@ struct PlanArgs {
 };
 
 // Workgroup e writes expert e's first compact row, its row tiles and its rows'
-// places in the rank's buffer.
+// places in the rank's buffer.  ARGS: the counts are the launch's arguments, which lie in
+// the host's memory: read once, side by side (8 ranks' of 64 experts 4.2 us, one after
+// another 5.6).
+template <bool ARGS>
 __global__ __launch_bounds__(256) void k_ffn_plan(PlanArgs a) {
-  __shared__ uint32_t red[1 + kFfnTiles][256];
+  __shared__ uint32_t red[1 + kFfnTiles][4];
+  __shared__ uint32_t counts[ARGS ? kPlanCounts : 1];
   const int e = blockIdx.x, tid = threadIdx.x, N = a.N;
-  const uint32_t* kept = a.kept ? a.kept : a.v;
+  if constexpr (ARGS) {
+    constexpr int Q = (kPlanCounts + 255) / 256;
+    const int n = (e + 1) * N;
+    uint32_t v[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) v[q] = tid + q * 256 < n ? a.v[tid + q * 256] : 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (tid + q * 256 < n) counts[tid + q * 256] = v[q];
+    __syncthreads();
+  }
+  auto kept = [&](int i) { return ARGS ? counts[i] : a.kept[i]; };
   uint32_t sum[1 + kFfnTiles] = {};
   for (int x = tid; x < e; x += 256) {
     uint32_t n = 0;
-    for (int i = 0; i < N; ++i) n += kept[x * N + i];
+    for (int i = 0; i < N; ++i) n += kept(x * N + i);
     sum[0] += n;
 #pragma unroll
     for (int k = 0; k < kFfnTiles; ++k) sum[1 + k] += (n + kFfnTile[k] - 1) / kFfnTile[k];
   }
 #pragma unroll
-  for (int k = 0; k <= kFfnTiles; ++k) red[k][tid] = sum[k];
-  __syncthreads();
-  for (int d = 128; d; d >>= 1) {
-    if (tid < d)
-#pragma unroll
-      for (int k = 0; k <= kFfnTiles; ++k) red[k][tid] += red[k][tid + d];
-    __syncthreads();
+  for (int k = 0; k <= kFfnTiles; ++k) {
+    const uint32_t s = group_usum<64>(sum[k]);
+    if ((tid & 63) == 0) red[k][tid >> 6] = s;
   }
-  const uint32_t r0 = red[0][0];
+  __syncthreads();
+  auto before = [&](int k) { return red[k][0] + red[k][1] + red[k][2] + red[k][3]; };
+  const uint32_t r0 = before(0);
   const int per = a.E / N, l = e % per;
   uint32_t at = r0;
   for (int i = 0; i < N; ++i) {
-    const uint32_t n = kept[e * N + i];
+    const uint32_t n = kept(e * N + i);
     const uint32_t src = (uint32_t)(((uint64_t)i * per + l) * a.cap);
     for (uint32_t s = tid; s < n; s += 256) a.rowmap[at + s] = (int)(src + s);
     at += n;
   }
 #pragma unroll
   for (int k = 0; k < kFfnTiles; ++k) {
-    const uint32_t nt = (at - r0 + kFfnTile[k] - 1) / kFfnTile[k], t0 = red[1 + k][0];
+    const uint32_t nt = (at - r0 + kFfnTile[k] - 1) / kFfnTile[k], t0 = before(1 + k);
     for (uint32_t t = tid; t < nt; t += 256) a.mtab[k][t0 + t] = make_int2(e, (int)(r0 + t * kFfnTile[k]));
   }
   if (tid == 0) {
@@ -150,8 +163,7 @@ __global__ __launch_bounds__(256) void k_ffn_copy(CopyArgs a) {
       u32x4 w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t left = (int64_t)j.cols - (int64_t)(c + q * 64 * V);
-        w[q] = load_n<DT, false>(p + (c + q * 64 * V) * SZ, left < V ? (int)(left > 0 ? left : 0) : V);
+        w[q] = load_line<DT>(p, j.cols, c + q * 64 * V);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -187,7 +199,8 @@ hipError_t plan(const FfnShape& s, const FfnWs& o, char* ws, const uint32_t* kep
   a.start = (int*)(ws + o.start);
   for (int k = 0; k < kFfnTiles; ++k) a.mtab[k] = (int2*)(ws + o.mtab[k]);
   a.rowmap = (int*)(ws + o.rowmap);
-  CC_LAUNCH(k_ffn_plan, dim3((unsigned)s.E), dim3(256), 0, st, a);
+  if (a.kept) CC_LAUNCH(k_ffn_plan<false>, dim3((unsigned)s.E), dim3(256), 0, st, a);
+  else CC_LAUNCH(k_ffn_plan<true>, dim3((unsigned)s.E), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

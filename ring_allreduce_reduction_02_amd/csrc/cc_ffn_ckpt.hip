@@ -36,9 +36,7 @@ __device__ __forceinline__ void pack_x(const XRows& a, uint64_t rank, uint32_t r
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint64_t c = c0 + (uint64_t)(q * 64 + lane) * V;
-      const int64_t left = (int64_t)a.W - (int64_t)c;
-      w[q] = u32x4{0u, 0u, 0u, 0u};
-      if (left > 0) w[q] = load_n<DT, false>(x + c * SZ, (int)(left < V ? left : V));
+      w[q] = load_line<DT>(x, a.W, c);
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {

@@ -189,12 +189,19 @@ __device__ __forceinline__ u32x4 frag(const char* t, int u, int i0, int lane) {
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 
+// An address that is in memory, not in LDS: of one that came out of LDS the
+// compiler does not know, and waits for such a load before it uses LDS again.
+template <class T>
+__device__ __forceinline__ const __attribute__((address_space(1))) T* in_memory(const char* p) {
+  return (const __attribute__((address_space(1))) T*)p;
+}
+
 // The last n (1 to 15) bytes of a line of at least 16 whose end is `end`, zeros
 // behind them: its last 16 bytes, shifted (byte by byte each load would wait for
 // the one before).
 __device__ __forceinline__ u32x4 line_tail(const char* end, int n) {
   typedef unsigned __int128 u128;
-  return __builtin_bit_cast(u32x4, __builtin_bit_cast(u128, (u32x4) * (const u32x4_byte*)(end - 16)) >> (8 * (16 - n)));
+  return __builtin_bit_cast(u32x4, __builtin_bit_cast(u128, (u32x4) * in_memory<u32x4_byte>(end - 16)) >> (8 * (16 - n)));
 }
 
 template <int DT, bool COL, int R, int NT>
@@ -203,8 +210,8 @@ struct Chunks {
   static constexpr int PER = COL ? R * SZ / 16 : kKBytes / 16;   // chunks per line
   u32x4 v[Q];
   __device__ __forceinline__ static u32x4 load_any(const char* p) {
-    if constexpr (DT == DT_I8) return *(const u32x4_byte*)p;
-    else return *(const u32x4_any*)p;
+    if constexpr (DT == DT_I8) return *in_memory<u32x4_byte>(p);
+    else return *in_memory<u32x4_any>(p);
   }
   __device__ __forceinline__ void load(const char* const* lp, int64_t k0, int64_t K, int64_t c0, int64_t C) {
     if (k0 + kKBytes / SZ <= K && (!COL || c0 + R <= C)) {   // whole chunks only
@@ -223,19 +230,10 @@ struct Chunks {
       v[q] = u32x4{0u, 0u, 0u, 0u};
       if (p && left >= V) {
         v[q] = load_any(p + at * SZ);
-      } else if constexpr (DT == DT_I8) {
-        static_assert(!COL, "rows end at K");
-        if (left > 0) {
-          if (K >= V) v[q] = line_tail(p + K, (int)left);
-          else
-            for (int i = 0; i < left; ++i) v[q][i >> 2] |= (uint32_t)(uint8_t)p[at + i] << (8 * (i & 3));
-        }
       } else if (p && left > 0) {
-        float x[V] = {};
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i < left) x[i] = ld1<DT>(p + (at + i) * SZ);
-        v[q] = pack_row<DT>(x);   // widened and packed again: the same bits
+        if ((COL ? C : K) >= V) v[q] = line_tail(p + (at + left) * SZ, (int)left * SZ);
+        else
+          for (int i = 0; i < left * SZ; ++i) v[q][i >> 2] |= (uint32_t)*in_memory<uint8_t>(p + at * SZ + i) << (8 * (i & 3));
       }
     }
   }
@@ -295,8 +293,32 @@ __device__ __forceinline__ void sigmoid(float g, float& s, float& c) {
 // a small value takes g^2 times (erfc(x) falls by 2 x^2 of its value a step).
 __device__ __forceinline__ float normal_cdf(float g) { return 0.5f * erfcf(-g * 0.70710678118654752f); }
 
-// h = act(g) u
-template <int DT, int V>
+// The same, and e = exp(-g^2 / 2), for results in bf16: 0.5 erfc(x / sqrt 2) = e P(t)
+// with t = 1 / (1 + 0.3 x), P the polynomial of degree 8 whose largest relative
+// error over x = 0 .. 14.5 is least (5.9e-8; by reweighted least squares on 2000
+// points); exp2 and the reciprocal are the hardware's.  Off by at most 10 half steps
+// of 1; below 0 by (1.5 g^2 + 16) 2^-24 of its value, 2^-15 at g = -13, below the
+// 2^-8 that the result is rounded by; below 2^-126 it may be 0.  (erfcf has two
+// branches, and a wave takes both: the 8-bit block of 16 experts of 2047 x 2047, 60.7k
+// rows, 1199 us with it, 1103 so; the checkpoint step of 2048 x 2048 4850 and 4640.)
+__device__ __forceinline__ float normal_cdf_bf16(float g, float& e) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, fabsf(g), 1.0f));
+  e = __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f);
+  float r = 0.0384070873f;
+  r = __builtin_fmaf(r, t, -0.169306159f);
+  r = __builtin_fmaf(r, t, 0.228949443f);
+  r = __builtin_fmaf(r, t, -0.0768373683f);
+  r = __builtin_fmaf(r, t, 0.142763928f);
+  r = __builtin_fmaf(r, t, 0.0945863351f);
+  r = __builtin_fmaf(r, t, 0.121945165f);
+  r = __builtin_fmaf(r, t, 0.119484216f);
+  r = __builtin_fmaf(r, t, 7.37187929e-06f);
+  r *= e;
+  return g < 0.0f ? r : 1.0f - r;
+}
+
+// h = act(g) u.  HW: the normal distribution function as for bf16
+template <int DT, int V, bool HW = false>
 __device__ __forceinline__ void gate(const float* g, const float* u, int act, float* h) {
   if (act == ACT_SILU) {
 #pragma unroll
@@ -307,11 +329,16 @@ __device__ __forceinline__ void gate(const float* g, const float* u, int act, fl
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = g[i] * normal_cdf(g[i]) * u[i];
+    for (int i = 0; i < V; ++i) {
+      float c, e;
+      if constexpr (HW) c = normal_cdf_bf16(g[i], e);
+      else c = normal_cdf(g[i]);
+      h[i] = g[i] * c * u[i];
+    }
   }
 }
 // dh -> dg, du and h
-template <int DT, int V>
+template <int DT, int V, bool HW = false>
 __device__ __forceinline__ void gate_grad(const float* g, const float* u, int act, const float* dh, float* dg,
                                           float* du, float* h) {
   if (act == ACT_SILU) {
@@ -327,7 +354,14 @@ __device__ __forceinline__ void gate_grad(const float* g, const float* u, int ac
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float c = normal_cdf(g[i]), a = g[i] * c, d = c + g[i] * expf(-0.5f * g[i] * g[i]) * 0.39894228040143268f;
+      float c, e;
+      if constexpr (HW) {
+        c = normal_cdf_bf16(g[i], e);
+      } else {
+        c = normal_cdf(g[i]);
+        e = expf(-0.5f * g[i] * g[i]);
+      }
+      const float a = g[i] * c, d = c + g[i] * e * 0.39894228040143268f;
       dg[i] = dh[i] * u[i] * d;
       du[i] = dh[i] * a;
       h[i] = a * u[i];
@@ -363,6 +397,16 @@ __device__ __forceinline__ u32x4 load_n(const char* p, int n) {
     for (int i = 0; i < V; ++i) x[i] = i < n ? ld1<DT>(p + i * Ty<DT>::SZ) : 0.0f;
     return pack_row<DT>(x);   // widened and packed again: the same bits
   }
+}
+
+// The V elements from c on of a line of `cols`, zeros past its end.
+template <int DT>
+__device__ __forceinline__ u32x4 load_line(const char* line, uint64_t cols, uint64_t c) {
+  constexpr int V = Ty<DT>::V, SZ = Ty<DT>::SZ;
+  if (c + V <= cols) return *(const u32x4_any*)(line + c * SZ);
+  if (c >= cols) return u32x4{0u, 0u, 0u, 0u};
+  if (cols >= V) return line_tail(line + cols * SZ, (int)(cols - c) * SZ);
+  return load_n<DT, false>(line + c * SZ, (int)(cols - c));
 }
 
 // ------------------------------------------------------------------ the products
@@ -547,7 +591,7 @@ __device__ __forceinline__ void finish(const G& g, const Part& t, const f32x16 (
       } else if constexpr (GU) {
         float up[V], h[V];
         read_row<V>(lds + row * PITCH + (at + 32) * 4, up);
-        gate<DT, V>(v, up, g.act, h);
+        gate<DT, V, CK && DT == DT_BF16>(v, up, g.act, h);
         store_n<DT, VEC, V>(packed(g.out, m), h, left);
         if constexpr (CK) {
           // the wave's 32 columns are a block; a row's lanes hold the block's columns
@@ -573,7 +617,7 @@ __device__ __forceinline__ void finish(const G& g, const Part& t, const f32x16 (
           unpack<DT>(load_n<DT, VEC>(pre, left), gt);
           unpack<DT>(load_n<DT, VEC>(pre + (int64_t)g.F * SZ, left), up);
         }
-        gate_grad<DT, V>(gt, up, g.act, v, dg, du, h);
+        gate_grad<DT, V, CK && DT == DT_BF16>(gt, up, g.act, v, dg, du, h);
         char* o = packed(g.out, m);
         store_n<DT, VEC, V>(o, dg, left);
         store_n<DT, VEC, V>(o + (int64_t)g.F * SZ, du, left);
@@ -646,7 +690,7 @@ __device__ __forceinline__ void finish_i8(const I8Args& g, const Part& t, const 
         read_row<V>(lds + row * PITCH + (at + 32) * 4, up);
 #pragma unroll
         for (int c = 0; c < V; ++c) up[c] = up[c] * s * su[c];
-        gate<OT, V>(v, up, g.act, h);
+        gate<OT, V, OT == DT_BF16>(v, up, g.act, h);
         store_n<OT, VEC, V>(g.out.base + (uint64_t)(t.p0 + m) * g.out.pitch + (int64_t)n * SZ, h, left);
       } else {
         store_n<OT, VEC, V>(g.out.base + (uint64_t)t.rank * g.out.rank_stride +

@@ -259,6 +259,52 @@ def test_gradients_against_differences(act):
                 assert abs((v[0] - v[1]) / (2 * h) - float(got[i])) < 1e-5, (k, i)
 
 
+@pytest.mark.parametrize("width", [2, 16], ids=["any rows", "whole vectors"])
+def test_gelu_bf16(width):
+    """gelu and its derivative element by element over [-12.75, 12.75]: x = [g, 1, 0 ..], gate rows [1, 0 ..], up rows
+    [0, 1, 0 ..] and an identity behind them make every product exact, and g of 7 significant bits is kept as it is.
+
+    U half a step of float32.  e = exp(-g^2 / 2): the square, its product and the constant U each of an exponent g^2 / 2,
+    one step (2 U) of exp2: (1.5 g^2 + 2) U.  t = 1 / (1 + 0.3 x): U, U and a step, 4 U, and P(t) grows by no more than
+    its argument does; P's terms are together at most 2 P, 8 of them summed from the smallest power's side: 6 U; the fit
+    U, the product with e U: (1.5 g^2 + 14) U, and above 0 half of 16 U, U of the difference: 10 U.  Then a product of
+    three, U each, and one rounding to bf16, 2^-8."""
+    say("gelu", width)
+    m = torch.arange(64, 128, dtype=torch.float64)
+    g = torch.cat([m * 2.0 ** (k - 6) for k in range(-20, 4)])
+    g = g[g <= 12.75]
+    g = torch.cat([g, -g, torch.zeros(1, dtype=torch.float64)]).to(DEV)
+    R, W, F = len(g), width, width // 2
+    bf = torch.bfloat16
+    x = torch.zeros(R, W, device=DEV, dtype=bf)
+    x[:, 0], x[:, 1] = g.to(bf), 1.0
+    w_in = torch.zeros(2 * F, W, device=DEV, dtype=bf)
+    w_in[:F, 0], w_in[F:, 1] = 1.0, 1.0
+    w_out = torch.eye(W, F, device=DEV, dtype=bf)
+    dy = torch.zeros(R, W, device=DEV, dtype=bf)
+    dy[:, 0] = 1.0
+    x, dy, w_in, w_out = (v.reshape(1, -1) for v in (x, dy, w_in, w_out))
+    y, dx, counts = torch.empty_like(x), torch.empty_like(x), [[R]]
+    ckpt = ccgpu.make_moe_ffn_checkpoint(counts, R, W, F)
+    ccgpu.moe_ffn_checkpoint(x, w_in, w_out, ckpt, y, counts, R, W, act="gelu",
+                             workspace=ccgpu.make_moe_ffn_checkpoint_workspace(counts, R, W, F, "bf16"))
+    ccgpu.moe_ffn_checkpoint_grad(ckpt, w_in, w_out, dy, dx, torch.empty_like(w_in), torch.empty_like(w_out), counts, R, W,
+                                  act="gelu", workspace=ccgpu.make_moe_ffn_checkpoint_workspace(counts, R, W, F, "bf16",
+                                                                                                grad=True))
+    torch.cuda.synchronize()
+    c, e = torch.erfc(-g / math.sqrt(2)) / 2, torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+    a, d = g * c, c + g * e
+    off = (1.5 * g * g + 16) * c.clamp(max=0.5) + 10 * (g > 0)           # of c, in U
+    half = 2.0 ** -8
+    for got, what in ((y, "gelu"), (dx, "gelu of the gradient")):
+        got = got.view(R, W)[:, 0 if what == "gelu" else 1].double()
+        bound = U * (off * g.abs() + 3 * a.abs())
+        assert ((got - a).abs() <= half * a.abs() + 1.01 * bound).all(), what
+    bound = U * (off + (1.5 * g * g + 6) * (g * e).abs() + 3 * d.abs())
+    got = dx.view(R, W)[:, 0].double()
+    assert ((got - d).abs() <= half * d.abs() + 1.01 * bound).all()
+
+
 def test_many_ranks_and_experts():
     f = Ckpt(32, 64, 2, 16, 8, spread(32, 64, 2, 10, 2), "bf16", 58)
     f.forward("silu")
