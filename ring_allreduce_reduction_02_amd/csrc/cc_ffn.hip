@@ -45,7 +45,7 @@ struct PlanArgs {
 
 // Workgroup e writes expert e's first compact row, its row tiles and its rows'
 // places in the rank's buffer.  ARGS: the counts are the launch's arguments, which lie in
-// the host's memory: read once, side by side (8 ranks' of 64 experts 4.2 us, one after
+// the host's memory: read once, side by side (8 ranks' of 64 experts 4.8 us, one after
 // another 5.6).
 template <bool ARGS>
 __global__ __launch_bounds__(256) void k_ffn_plan(PlanArgs a) {
@@ -123,9 +123,9 @@ struct CopyArgs {
 constexpr int kCopyLines = kFfnTile[kFfnTiles - 1], kCopyParts = 4;
 
 // Workgroup (x, y, z) copies part z of 64 lines of job y.  Bound by memory: the
-// weights of 16 experts of 2047 x 2047 bf16 and 60.7k rows, 1.3 GB in and out, 260 us,
-// 5.0 TB/s (all 64 lines a workgroup 300, and with one load of a lane under way 350;
-// 6 experts of 515 x 331 and 1.4k rows 12 us and 31).
+// weights of 16 experts of 2047 x 2047 bf16 and 60.7k rows, 1.3 GB in and out, 248 us,
+// 5.2 TB/s (all 64 lines a workgroup 300, and with one load of a lane under way 350;
+// 6 experts of 515 x 331 and 1.4k rows 11 us and 31).
 template <int DT>
 __global__ __launch_bounds__(256) void k_ffn_copy(CopyArgs a) {
   constexpr int V = Ty<DT>::V, SZ = Ty<DT>::SZ;

@@ -14,7 +14,7 @@ namespace cc {
 // checkpoint, the hidden gradient from one, and 8-bit integers (summed in
 // int32; the rows of W or F bytes of cc_ffn_rule.h's element size 1).
 // The checkpoint's cost little beside the products: 16 experts of 2048 x 2048 bf16,
-// 60.7k rows, gate and up 1037 us (1026 that keep bf16), the hidden gradient 676 (653).
+// 60.7k rows, gate and up 1037 us (1028 that keep bf16), the hidden gradient 675 (639).
 constexpr int K_GATEUP_CK = 5, K_DHID_CK = 6;
 constexpr bool is_gateup(int kind) { return kind == K_GATEUP || kind == K_GATEUP_CK; }
 constexpr bool is_dhid(int kind) { return kind == K_DHID || kind == K_DHID_CK; }
@@ -632,7 +632,7 @@ __device__ __forceinline__ void finish(const G& g, const Part& t, const f32x16 (
 // the column's scale, in float32.  The int32 sum is rounded once to float32, and
 // each scale's product once.
 // Gate and up of 16 experts of 2048 x 2048 (or a product of 4096 columns) for 60.7k
-// rows: 256 x 256 tiles 529-536 us, 1.9 POP/s, the matrix units 50% of the cycles, of
+// rows: 256 x 256 tiles 521-526 us, 1.9 POP/s, the matrix units 51% of the cycles, of
 // which this takes about a fifth: 429 us with the sums dropped, 503 with all but the
 // stores.  (128 x 128 tiles, two a unit at a time, 16% slower, 192 x 128 6%; scales
 // loaded before the products, stores through the caches: nothing gained.)
@@ -737,7 +737,7 @@ __device__ __forceinline__ void clear(A (&acc)[TM][TN]) {
 
 // Any alignment: tiles staged through registers, the next stage's on their way
 // while this one's products run.  2 x 333 tokens, top-2 of 6 experts, 515 x 331
-// float32: 32 and 20 us.  Its 506 and 414 waves leave half of the 1024 SIMDs idle,
+// float32: 31 and 19.5 us.  Its 506 and 414 waves leave half of the 1024 SIMDs idle,
 // and a wave spends half of its time, 14 of 28 us, in matrix instructions, the
 // rest on the latency of 17 and 11 stages; element by element they took 54 and 35.
 template <int DT, int KIND, int BM, int BN, int WM, int WN, int OT = DT>
