@@ -342,8 +342,7 @@ def _balance_grad_plain(st):
 def _int8_rows(x):
     """Rows in 8 bits: the integers nearest x / s, s = max|x| / 127 in 32 bits
     (the quotients in 64: which integer is nearest must not hang on their rounding)."""
-    top = x.abs().amax(-1, keepdim=True).float()
-    s = top / torch.full_like(top, 127.0)      # a quotient: by a plain number it would be a product with 1 / 127
+    s = x.abs().amax(-1, keepdim=True).float() / 127.0
     q = torch.where(s > 0, torch.round(x.double() / s.double()), 0.0).clamp(-127, 127)
     return q.to(torch.int8), s[..., 0].contiguous()
 
@@ -521,7 +520,7 @@ def _exact_balance_grad(st, c):
 
 def _nearest64(v):
     """Rows of v (float64) as integers (float64) and their 32-bit scales."""
-    s = (v.abs().max(1).values / 127).float().double()
+    s = (v.abs().max(1).values.float() / 127).double()
     return torch.round(v / torch.where(s > 0, s, 1.0)[:, None]) * (s > 0)[:, None], s
 
 
