@@ -716,6 +716,22 @@ cc_status_t cc_moe_balance_loss_grad(cc_rankbuf_t logits, cc_rankbuf_t total, cc
 cc_status_t cc_quantize_rows(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t scales, size_t rows, size_t width,
                              cc_dtype_t dtype, int nranks, const cc_config_t* cfg, cc_stream_t stream);
 
+/* The same with the scale's arithmetic chosen: CC_SCALE_QUOTIENT is max|v| / 127,
+ * rounded once (the call above); CC_SCALE_PRODUCT is max|v| times float32(1 / 127),
+ * rounded once, what torch makes of `x.abs().amax(-1) / 127.0` on a GPU, so
+ * that rows kept by either are the same integers.  The two scales differ in their
+ * last bit in about 5% of rows, which takes an integer next to a border to the
+ * other side of it. */
+typedef enum {
+  CC_SCALE_QUOTIENT = 0,
+  CC_SCALE_PRODUCT = 1,
+  CC_SCALE_MIN_ENUM = -0x7fffffff - 1,
+  CC_SCALE_MAX_ENUM = 0x7fffffff
+} cc_scale_t;
+cc_status_t cc_quantize_rows_scaled(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t scales, size_t rows, size_t width,
+                                    cc_scale_t scale, cc_dtype_t dtype, int nranks, const cc_config_t* cfg,
+                                    cc_stream_t stream);
+
 /* The experts' product of quantised rows and weights, on the expert side of
  * cc_moe_dispatch_padded: for the kept rows x of every expert
  *   y_c = (sum_k x_k w_ck) sx sw_c,
@@ -742,6 +758,11 @@ cc_status_t cc_moe_ffn_int8(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t s_in
                             cc_rankbuf_t s_out, cc_rankbuf_t y, const size_t* counts, int nexperts, size_t capacity,
                             size_t width, size_t hidden, cc_act_t act, cc_dtype_t dtype, int nranks,
                             const cc_config_t* cfg, cc_stream_t stream);
+/* The same with the scales of x's and h's rows as in cc_quantize_rows_scaled. */
+cc_status_t cc_moe_ffn_int8_scaled(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t s_in, cc_rankbuf_t w_out,
+                                   cc_rankbuf_t s_out, cc_rankbuf_t y, const size_t* counts, int nexperts,
+                                   size_t capacity, size_t width, size_t hidden, cc_act_t act, cc_scale_t scale,
+                                   cc_dtype_t dtype, int nranks, const cc_config_t* cfg, cc_stream_t stream);
 cc_status_t cc_moe_ffn_int8_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width,
                                            size_t hidden, cc_dtype_t dtype, int nranks, size_t* bytes);
 

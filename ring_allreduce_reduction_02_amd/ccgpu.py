@@ -147,12 +147,16 @@ EXPORTS = {
                                                                                          ctypes.c_void_p],
     "cc_quantize_rows": [RankBuf] * 3 + [ctypes.c_size_t] * 2 + [ctypes.c_int] * 2 + [ctypes.POINTER(Config),
                                                                                      ctypes.c_void_p],
+    "cc_quantize_rows_scaled": [RankBuf] * 3 + [ctypes.c_size_t] * 2 + [ctypes.c_int] * 3 + [ctypes.POINTER(Config),
+                                                                                            ctypes.c_void_p],
     "cc_moe_matmul_int8": [RankBuf] * 5 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
                           + [ctypes.c_int] * 2 + [ctypes.POINTER(Config), ctypes.c_void_p],
     "cc_moe_matmul_int8_workspace_size": [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
                                          + [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
     "cc_moe_ffn_int8": [RankBuf] * 6 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
                        + [ctypes.c_int] * 3 + [ctypes.POINTER(Config), ctypes.c_void_p],
+    "cc_moe_ffn_int8_scaled": [RankBuf] * 6 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
+                              + [ctypes.c_int] * 4 + [ctypes.POINTER(Config), ctypes.c_void_p],
     "cc_moe_ffn_int8_workspace_size": [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
                                       + [ctypes.c_int] * 2 + [ctypes.POINTER(ctypes.c_size_t)],
     "cc_moe_ffn_checkpoint": [RankBuf] * 5 + [ctypes.POINTER(ctypes.c_size_t), ctypes.c_int] + [ctypes.c_size_t] * 3
@@ -593,6 +597,7 @@ def int8_message_bytes(count: int) -> int:
 # ---- the model's side of the exchanges: embedding, routing, expert feed-forward
 
 ACTS = {"silu": 0, "gelu": 1}
+SCALES = {"quotient": 0, "product": 1}
 
 
 def _current_stream(dev: int) -> int:
@@ -841,14 +846,16 @@ def moe_balance_loss_grad(logits, total, dloss, dlogits, base=None, stream=None)
                                            DTYPES[dtype_name(logits)], N, c.cfg, c.stream))
 
 
-def quantize_rows(x, q, scales, width: int, stream=None) -> None:
+def quantize_rows(x, q, scales, width: int, stream=None, scale: str = "quotient") -> None:
     """Rows of `width` elements of x [N, R * width] as int8 q [N, R * width] and a
-    scale each (f32) [N, R]: tokens, or the rows (channels) of weights."""
+    scale each (f32) [N, R]: tokens, or the rows (channels) of weights.  A scale
+    is max|x| / 127, or with "product" max|x| times float32(1 / 127), as torch
+    computes x.abs().amax(-1) / 127.0 on a GPU."""
     import torch
     N, R, c = x.shape[0], _rows(x, width, "x"), _Call(stream)
-    _check(load().cc_quantize_rows(c.operand(x, "x", N, R * width), c.operand(q, "q", N, R * width, torch.int8),
-                                   c.operand(scales, "scales", N, R, torch.float32), R, width,
-                                   DTYPES[dtype_name(x)], N, c.cfg, c.stream))
+    _check(load().cc_quantize_rows_scaled(c.operand(x, "x", N, R * width), c.operand(q, "q", N, R * width, torch.int8),
+                                          c.operand(scales, "scales", N, R, torch.float32), R, width, SCALES[scale],
+                                          DTYPES[dtype_name(x)], N, c.cfg, c.stream))
 
 
 def _counts(counts):
@@ -906,10 +913,11 @@ def make_moe_ffn_int8_workspace(counts, capacity: int, width: int, hidden: int, 
 
 
 def moe_ffn_int8(x, w_in, s_in, w_out, s_out, y, counts: Sequence[Sequence[int]], capacity: int, width: int,
-                 act: str = "silu", workspace=None, stream=None) -> None:
+                 act: str = "silu", workspace=None, stream=None, scale: str = "quotient") -> None:
     """moe_ffn with both products in 8-bit integers: x, y as there, w_in int8
     [N, E/N * 2 * hidden * width] with s_in (f32) [N, E/N * 2 * hidden], w_out int8
-    [N, E/N * width * hidden] with s_out (f32) [N, E/N * width]."""
+    [N, E/N * width * hidden] with s_out (f32) [N, E/N * width]; the scales of x's
+    and h's rows as in quantize_rows."""
     import torch
     N, E, arr = _counts(counts)
     per = E // N
@@ -918,8 +926,8 @@ def moe_ffn_int8(x, w_in, s_in, w_out, s_out, y, counts: Sequence[Sequence[int]]
             c.operand(s_in, "s_in", N, per * 2 * hidden, torch.float32),
             c.operand(w_out, "w_out", N, per * width * hidden, torch.int8),
             c.operand(s_out, "s_out", N, per * width, torch.float32), c.operand(y, "y", N, side, x.dtype))
-    _check(load().cc_moe_ffn_int8(*args, arr, E, capacity, width, hidden, ACTS[act], DTYPES[dtype_name(x)], N, c.cfg,
-                                  c.stream))
+    _check(load().cc_moe_ffn_int8_scaled(*args, arr, E, capacity, width, hidden, ACTS[act], SCALES[scale],
+                                         DTYPES[dtype_name(x)], N, c.cfg, c.stream))
 
 
 def moe_ffn_checkpoint_row(width: int, hidden: int) -> int:

@@ -2,8 +2,9 @@
 // (channel), grouped by experts.
 //
 // A row v becomes the integers q nearest v / s (ties to even) with s = max|v| / 127
-// rounded to float32, cut to [-127, 127]; q = 0 where s = 0, and s = NaN, q = 0
-// where the row holds a NaN or an infinity.  A product's sums of q's are exact
+// rounded to float32 (or the product with float32(1 / 127), where the caller wants
+// the rows that such code keeps), cut to [-127, 127]; q = 0 where s = 0, and s = NaN,
+// q = 0 where the row holds a NaN or an infinity.  A product's sums of q's are exact
 // in int32; float32 takes a sum, its row's scale and its column's.
 
 #include <algorithm>
@@ -25,6 +26,7 @@ struct RowsArgs {
   uint64_t s_stride;
   uint64_t rows, width;
   uint64_t row0;         // of a launch
+  int product;           // the scale is a product
 };
 
 // The integer nearest |u| / s, ties to even, for s of 2^-100 and more: k or k + 1,
@@ -119,7 +121,7 @@ __device__ __forceinline__ void quantized_small(u32x4 in, float s, uint32_t* w) 
 // float64 quotient behind every element 150 and 168.)
 template <int DT, int WPR, int R>
 __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char* q, uint64_t pitch, float* scale,
-                                             uint32_t* red) {
+                                             int product, uint32_t* red) {
   constexpr int V = Ty<DT>::V, SZ = Ty<DT>::SZ;
   const int tid = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
   constexpr uint64_t STEP = (uint64_t)64 * WPR * V;
@@ -150,7 +152,8 @@ __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char
     top = (uint32_t)__builtin_amdgcn_readfirstlane((int)top);
   }
   const bool nan = top >= 0x7f800000u;
-  const float s = nan ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
+  const float most = __uint_as_float(top);
+  const float s = nan ? __uint_as_float(0x7fc00000u) : product ? most * (1.0f / 127.0f) : most / 127.0f;
   auto put = [&](uint64_t b, const uint32_t* w) {
     const uint64_t c = b + (uint64_t)tid * V;
     char* o = q + c;
@@ -203,7 +206,8 @@ __global__ __launch_bounds__(256) void k_int8_rows(RowsArgs a) {
   const uint64_t row = a.row0 + (uint64_t)blockIdx.x * (4 / WPR) + wave;
   if (row < a.rows)   // the same on the wave, or (WPR 4) the workgroup
     quantize_row<DT, WPR, R>(a.x + r * a.x_stride + row * a.width * Ty<DT>::SZ, a.width,
-                             a.q + r * a.q_stride + row * a.q_pitch, a.q_pitch, (float*)(a.s + r * a.s_stride) + row, red);
+                             a.q + r * a.q_stride + row * a.q_pitch, a.q_pitch, (float*)(a.s + r * a.s_stride) + row,
+                             a.product, red);
 }
 
 // The experts' kept rows, compact.
@@ -219,7 +223,7 @@ __global__ __launch_bounds__(256) void k_int8_tiles(TileArgs a) {
   __shared__ uint32_t red[4];
   auto row = [&](uint32_t l, uint32_t place, int e) {
     quantize_row<DT, WPR, R>(a.r.x + (uint64_t)(e / a.per) * a.r.x_stride + (uint64_t)place * a.r.width * Ty<DT>::SZ,
-                             a.r.width, a.r.q + (uint64_t)l * a.r.q_pitch, a.r.q_pitch, (float*)a.r.s + l, red);
+                             a.r.width, a.r.q + (uint64_t)l * a.r.q_pitch, a.r.q_pitch, (float*)a.r.s + l, a.r.product, red);
   };
   if constexpr (WPR == 1) {
     table_rows(a.start, a.mtab, a.map, row);
@@ -409,7 +413,8 @@ void weights_of(I8Args* g, const Int8Launch& L, const Side& w, const Side& s, ui
 
 hipError_t launch_int8_rows(const Int8Rows& L) {
   if (L.rows == 0) return hipSuccess;
-  const Plain p{{L.x, L.x_stride, L.q, L.q_stride, L.q_pitch, L.s, L.s_stride, L.rows, L.width, 0}, (unsigned)L.N, L.st};
+  const Plain p{{L.x, L.x_stride, L.q, L.q_stride, L.q_pitch, L.s, L.s_stride, L.rows, L.width, 0, L.product},
+                (unsigned)L.N, L.st};
   return L.dt == DT_F32 ? pick_rows<DT_F32>(L.width, p) : pick_rows<DT_BF16>(L.width, p);
 }
 
@@ -468,7 +473,7 @@ hipError_t launch_int8(const Int8Launch& L) {
   bool fast = L.x_ok && L.w_in_ok && side * W <= kMaxSpan && C * W <= kMaxSpan;
   g.a = RowSide{L.x.base, L.x.stride, W, g.map, side * W};
   if (L.o.copied_in) {
-    const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, nullptr, 0, L.s.rows, W, 0};
+    const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, nullptr, 0, L.s.rows, W, 0, 0};
     CC_LAUNCH(k_int8_copy_rows, dim3((unsigned)L.s.mtiles[kFfnTiles - 1], kTileParts), dim3(256), 0, L.st, tile_args(L, r));
     if ((e = hipGetLastError()) != hipSuccess || (e = copy_weights(L, false)) != hipSuccess) return e;
     g.a = RowSide{r.q, 0, r.q_pitch, nullptr, L.s.most * r.q_pitch};
@@ -484,7 +489,8 @@ hipError_t launch_int8(const Int8Launch& L) {
 
 hipError_t launch_int8_ffn(const Int8Launch& L) {
   const uint64_t W = L.s.W, F = L.s.F, es = elem_size(L.dt);
-  const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, L.ws + L.o.xs, 0, L.s.rows, W, 0};
+  const RowsArgs r{L.x.base, L.x.stride, L.ws + L.o.xq, 0, L.o.xq_pitch, L.ws + L.o.xs, 0, L.s.rows, W, 0,
+                   L.product};
   hipError_t e = planned_rows(L, r);
   if (e != hipSuccess || (e = copy_weights(L, true)) != hipSuccess) return e;
   I8Args g = int8_args(L);
@@ -503,7 +509,7 @@ hipError_t launch_int8_ffn(const Int8Launch& L) {
   q.q = L.ws + L.o.hq; q.q_pitch = L.o.hq_pitch;
   q.s = L.ws + L.o.hs;
   q.rows = L.s.rows; q.width = F;
-  q.N = 1; q.dt = L.dt; q.st = L.st;
+  q.N = 1; q.dt = L.dt; q.product = L.product; q.st = L.st;
   if ((e = launch_int8_rows(q)) != hipSuccess) return e;
   g.K = (int)F;
   g.N = (int)W;

@@ -192,6 +192,7 @@ struct Int8Rows {
   uint64_t s_stride;
   uint64_t rows, width;
   int N, dt;
+  int product;           // the scale: max|x| times 1 / 127 (1), or max|x| / 127 (0)
   hipStream_t st;
 };
 hipError_t launch_int8_rows(const Int8Rows& L);
@@ -216,6 +217,7 @@ struct Int8Launch {
   Side w_in, s_in, w_out, s_out, y;
   int w_in_ok, w_out_ok, x_ok, y_ok;   // whole 16-byte vectors
   int dt;                // of the results
+  int product;           // the block's rows, as in Int8Rows
   hipStream_t st;
 };
 hipError_t launch_int8(const Int8Launch& L);

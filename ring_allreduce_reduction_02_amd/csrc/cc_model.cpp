@@ -291,11 +291,17 @@ struct Int8Bufs {
   cc_rankbuf_t x, xs, w_in, s_in, w_out, s_out, y;
 };
 
+cc_status_t check_scale(int scale) {
+  return scale == CC_SCALE_QUOTIENT || scale == CC_SCALE_PRODUCT ? CC_OK
+                                                                 : fail(CC_ERR_INVALID_ARG, "unknown scale %d", scale);
+}
+
 cc_status_t run_int8(const Int8Bufs& f, const size_t* counts, int E, uint64_t cap, uint64_t W, uint64_t F, int act,
-                     cc_dtype_t dtype, int N, const cc_config_t& cfg, bool block, hipStream_t st) {
+                     int scale, cc_dtype_t dtype, int N, const cc_config_t& cfg, bool block, hipStream_t st) {
   cc_status_t s = model_checks(N, dtype, cfg);
   if (s) return s;
   if (act != CC_ACT_SILU && act != CC_ACT_GELU) return fail(CC_ERR_INVALID_ARG, "unknown activation %d", act);
+  if ((s = check_scale(scale))) return s;
   Int8Launch L = {};
   std::vector<uint32_t> kept;
   if ((s = int8_shape(counts, E, cap, W, F, N, block, &L.s, &kept))) return s;
@@ -332,6 +338,7 @@ cc_status_t run_int8(const Int8Bufs& f, const size_t* counts, int E, uint64_t ca
   L.w_out_ok = block && rows16(f.w_out, F);
   L.y_ok = rows16(f.y, ycols * es);
   L.dt = (int)dtype;
+  L.product = scale == CC_SCALE_PRODUCT;
   L.st = st;
   return hip_status(block ? launch_int8_ffn(L) : launch_int8(L),
                     block ? "expert feed-forward in 8-bit integers" : "product in 8-bit integers");
@@ -565,11 +572,12 @@ cc_status_t cc_moe_balance_loss_grad(cc_rankbuf_t logits, cc_rankbuf_t total, cc
   return hip_status(launch_balance_grad(L), "balance loss gradient");
 }
 
-cc_status_t cc_quantize_rows(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t scales, size_t rows, size_t width,
-                             cc_dtype_t dtype, int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
+cc_status_t cc_quantize_rows_scaled(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t scales, size_t rows, size_t width,
+                                    cc_scale_t scale, cc_dtype_t dtype, int nranks, const cc_config_t* cfgp,
+                                    cc_stream_t stream) {
   const cc_config_t& cfg = cfgp ? *cfgp : kDefaultCfg;
   cc_status_t s = model_checks(nranks, dtype, cfg);
-  if (s) return s;
+  if (s || (s = check_scale((int)scale))) return s;
   if (width == 0) return fail(CC_ERR_INVALID_ARG, "width must be positive");
   if (width >= (1ull << 31) || rows >= (1ull << 31)) return fail(CC_ERR_INVALID_ARG, "width or rows too large");
   if (rows == 0) return ok();
@@ -584,8 +592,14 @@ cc_status_t cc_quantize_rows(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t scales
   L.x = (const char*)x.base; L.x_stride = x.rank_stride_bytes;
   L.q = (char*)q.base; L.q_stride = q.rank_stride_bytes; L.q_pitch = width;
   L.s = (char*)scales.base; L.s_stride = scales.rank_stride_bytes;
-  L.rows = rows; L.width = width; L.N = N; L.dt = (int)dtype; L.st = (hipStream_t)stream;
+  L.rows = rows; L.width = width; L.N = N; L.dt = (int)dtype; L.product = scale == CC_SCALE_PRODUCT;
+  L.st = (hipStream_t)stream;
   return hip_status(launch_int8_rows(L), "quantisation of rows");
+}
+
+cc_status_t cc_quantize_rows(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t scales, size_t rows, size_t width,
+                             cc_dtype_t dtype, int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
+  return cc_quantize_rows_scaled(x, q, scales, rows, width, CC_SCALE_QUOTIENT, dtype, nranks, cfgp, stream);
 }
 
 cc_status_t cc_moe_matmul_int8(cc_rankbuf_t x, cc_rankbuf_t sx, cc_rankbuf_t w, cc_rankbuf_t sw, cc_rankbuf_t y,
@@ -593,8 +607,19 @@ cc_status_t cc_moe_matmul_int8(cc_rankbuf_t x, cc_rankbuf_t sx, cc_rankbuf_t w, 
                                cc_dtype_t dtype, int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
   return guarded([&] {
     const cc_rankbuf_t none{nullptr, 0};
-    return run_int8(Int8Bufs{x, sx, w, sw, none, none, y}, counts, nexperts, capacity, width, cols, CC_ACT_SILU, dtype,
-                    nranks, cfgp ? *cfgp : kDefaultCfg, false, (hipStream_t)stream);
+    return run_int8(Int8Bufs{x, sx, w, sw, none, none, y}, counts, nexperts, capacity, width, cols, CC_ACT_SILU,
+                    CC_SCALE_QUOTIENT, dtype, nranks, cfgp ? *cfgp : kDefaultCfg, false, (hipStream_t)stream);
+  });
+}
+
+cc_status_t cc_moe_ffn_int8_scaled(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t s_in, cc_rankbuf_t w_out,
+                                   cc_rankbuf_t s_out, cc_rankbuf_t y, const size_t* counts, int nexperts,
+                                   size_t capacity, size_t width, size_t hidden, cc_act_t act, cc_scale_t scale,
+                                   cc_dtype_t dtype, int nranks, const cc_config_t* cfgp, cc_stream_t stream) {
+  return guarded([&] {
+    const cc_rankbuf_t none{nullptr, 0};
+    return run_int8(Int8Bufs{x, none, w_in, s_in, w_out, s_out, y}, counts, nexperts, capacity, width, hidden, (int)act,
+                    (int)scale, dtype, nranks, cfgp ? *cfgp : kDefaultCfg, true, (hipStream_t)stream);
   });
 }
 
@@ -602,11 +627,8 @@ cc_status_t cc_moe_ffn_int8(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t s_in
                             cc_rankbuf_t s_out, cc_rankbuf_t y, const size_t* counts, int nexperts, size_t capacity,
                             size_t width, size_t hidden, cc_act_t act, cc_dtype_t dtype, int nranks,
                             const cc_config_t* cfgp, cc_stream_t stream) {
-  return guarded([&] {
-    const cc_rankbuf_t none{nullptr, 0};
-    return run_int8(Int8Bufs{x, none, w_in, s_in, w_out, s_out, y}, counts, nexperts, capacity, width, hidden, (int)act,
-                    dtype, nranks, cfgp ? *cfgp : kDefaultCfg, true, (hipStream_t)stream);
-  });
+  return cc_moe_ffn_int8_scaled(x, w_in, s_in, w_out, s_out, y, counts, nexperts, capacity, width, hidden, act,
+                                CC_SCALE_QUOTIENT, dtype, nranks, cfgp, stream);
 }
 
 cc_status_t cc_moe_matmul_int8_workspace_size(const size_t* counts, int nexperts, size_t capacity, size_t width,
