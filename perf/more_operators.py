@@ -288,13 +288,14 @@ def _run_own(st):
                                  base=st["base"] if c["accumulate"] else None)
         return st["dlogits"]
     if op == "int8":
-        cc.quantize_rows(st["x"], st["q"], st["s"], c["width"])
+        # the scale of `_int8_rows`: torch divides by a number as a product with its reciprocal
+        cc.quantize_rows(st["x"], st["q"], st["s"], c["width"], scale="product")
         cc.moe_matmul_int8(st["q"], st["s"], st["w"], st["sw"], st["y"], st["counts"], st["cap"], c["width"],
                            workspace=st["ws"])
         return st["y"]
     if op == "int8_ffn":
         cc.moe_ffn_int8(st["x"], st["w_in"], st["s_in"], st["w_out"], st["s_out"], st["y"], st["counts"], st["cap"],
-                        c["width"], act=c["act"], workspace=st["ws"])
+                        c["width"], act=c["act"], workspace=st["ws"], scale="product")
         return st["y"]
     if op == "ckpt_step":
         cc.moe_ffn_checkpoint(st["x"], st["w_in"], st["w_out"], st["ckpt"], st["y"], st["counts"], st["cap"],
