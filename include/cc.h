@@ -697,7 +697,8 @@ cc_status_t cc_moe_balance_loss_workspace_size(int nranks, size_t tokens, int ne
  * loss that the rank holds.  base (dtype, laid out as logits; base.base NULL:
  * zeros) is the gradient that cc_moe_route_grad gave, say; in place iff
  * base.base == dlogits.base with equal strides.  A padding token's row is base
- * (0 without); NaN in a row whose logits hold a NaN or +inf.  Takes no workspace. */
+ * (0 without), also where dloss is not finite; NaN in a row whose logits hold a
+ * NaN or +inf.  Takes no workspace. */
 cc_status_t cc_moe_balance_loss_grad(cc_rankbuf_t logits, cc_rankbuf_t total, cc_rankbuf_t dloss, cc_rankbuf_t base,
                                      cc_rankbuf_t dlogits, size_t tokens, int nexperts, cc_dtype_t dtype, int nranks,
                                      const cc_config_t* cfg, cc_stream_t stream);

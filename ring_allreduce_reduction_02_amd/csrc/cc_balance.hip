@@ -298,7 +298,7 @@ __global__ __launch_bounds__(kBalanceBlock) void k_balance_grad(BalArgs a) {
 #pragma unroll
     for (int i = 0; i < kV; ++i) dot = __builtin_fmaf(x[i], f[i], dot);
     dot = group_sum<L>(dot) * inv;
-    const float k = scale * inv;
+    const float k = s == 0.0f ? 0.0f : scale * inv;   // a padding token's row is 0 for any dloss
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       x[i] *= k;
