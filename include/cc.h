@@ -741,7 +741,8 @@ cc_status_t cc_quantize_rows_scaled(cc_rankbuf_t x, cc_rankbuf_t q, cc_rankbuf_t
  * rank, sx their float32 scales; rank j's weights w [cols][width] int8 and
  * scales sw [cols] float32, one local expert after the other; y: E * capacity rows of
  * `cols` elements of dtype.  counts, nexperts, capacity and the limits on
- * rows as in cc_moe_ffn; width below 2^17, so that no sum overflows.  Rows behind a
+ * rows as in cc_moe_ffn; width below 2^17, so that no sum overflows, cols below 2^24,
+ * and tiles of 64 kept rows times tiles of 64 columns below 2^24.  Rows behind a
  * block's kept ones are neither read nor written.  Takes a workspace. */
 cc_status_t cc_moe_matmul_int8(cc_rankbuf_t x, cc_rankbuf_t sx, cc_rankbuf_t w, cc_rankbuf_t sw, cc_rankbuf_t y,
                                const size_t* counts, int nexperts, size_t capacity, size_t width, size_t cols,

@@ -169,10 +169,14 @@ cc_status_t route_sizes(int nranks, uint64_t tokens, int nexperts, int topk, int
 
 constexpr int kMaxFfnExperts = 8192;   // the plan's workgroups each sum the counts of the experts before theirs
 
+// What a call launches: the block's products and its weights' gradients, the
+// block's products alone, or one product of F columns.
+enum Launches { BLOCK_AND_GRADIENTS, BLOCK, PRODUCT };
+
 // Counts [N][E] as the caller gives them -> kept rows [E][N], totals and
 // limits.  Row numbers are int32 on the device.
 cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uint64_t F, cc_dtype_t dtype, int N,
-                      FfnShape* sh, std::vector<uint32_t>* kept) {
+                      FfnShape* sh, std::vector<uint32_t>* kept, Launches what = BLOCK_AND_GRADIENTS) {
   if (N < 1 || N > CC_MAX_RANKS) return fail(CC_ERR_INVALID_ARG, "nranks=%d outside [1, %d]", N, CC_MAX_RANKS);
   if (!counts) return fail(CC_ERR_INVALID_ARG, "counts is NULL");
   if (E < N || E % N) return fail(CC_ERR_INVALID_ARG, "nexperts=%d must be a positive multiple of nranks=%d", E, N);
@@ -196,8 +200,10 @@ cc_status_t ffn_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, uin
     for (int k = 0; k < kFfnTiles; ++k) tiles[k] += (n + kFfnTile[k] - 1) / kFfnTile[k];
     if (rows >= (1ull << 31)) return fail(CC_ERR_INVALID_ARG, "2^31 rows or more in one call");
   }
-  const uint64_t wt = (2 * F + 63) / 64, wn = (W + 63) / 64;   // the smallest tile's
-  if ((u128)tiles[kFfnTiles - 1] * std::max(wt, wn) >= kMaxBlocks || (u128)E * wt * wn >= kMaxBlocks)
+  // columns of the smallest tiles
+  const uint64_t wt = ((what == PRODUCT ? F : 2 * F) + 63) / 64, wn = what == PRODUCT ? 0 : (W + 63) / 64;
+  if ((u128)tiles[kFfnTiles - 1] * std::max(wt, wn) >= kMaxBlocks ||
+      (what == BLOCK_AND_GRADIENTS && (u128)E * wt * wn >= kMaxBlocks))
     return fail(CC_ERR_INVALID_ARG, "too many tiles for one launch");
   *sh = FfnShape{N, E, cap, W, F, rows, most, {tiles[0], tiles[1], tiles[2]}, (int)dtype, elem_size((int)dtype), 0};
   return CC_OK;
@@ -280,7 +286,7 @@ cc_status_t int8_shape(const size_t* counts, int E, uint64_t cap, uint64_t W, ui
                        FfnShape* sh, std::vector<uint32_t>* kept) {
   if (W >= kMaxInt8Sum || (block && F >= kMaxInt8Sum))
     return fail(CC_ERR_INVALID_ARG, "a summed axis must be shorter than %llu", (unsigned long long)kMaxInt8Sum);
-  cc_status_t s = ffn_shape(counts, E, cap, W, F, CC_BFLOAT16, N, sh, kept);
+  cc_status_t s = ffn_shape(counts, E, cap, W, F, CC_BFLOAT16, N, sh, kept, block ? BLOCK : PRODUCT);
   sh->es = 1;
   return s;
 }
