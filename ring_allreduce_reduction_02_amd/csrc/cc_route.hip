@@ -12,6 +12,7 @@
 
 #include "cc_device.h"
 #include "cc_llm.h"
+#include "cc_wave.h"
 
 namespace cc {
 namespace {
@@ -38,40 +39,6 @@ __device__ __forceinline__ uint32_t rank_bits(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);
   if ((u & 0x7fffffffu) > 0x7f800000u || u == 0xff800000u) return 0u;
   return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// Reductions over a wave by data-parallel moves (within 16 lanes, then across
-// rows), the result on every lane: a tenth of the latency of shuffles through
-// LDS.  The order is fixed.
-template <int CTRL>
-__device__ __forceinline__ uint32_t moved(uint32_t x, uint32_t none) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, CTRL, 0xf, 0xf, false);
-}
-template <class F>
-__device__ __forceinline__ uint32_t wave_reduce(uint32_t x, uint32_t none, F f) {
-  x = f(x, moved<0x111>(x, none));   // row_shr 1, 2, 4, 8
-  x = f(x, moved<0x112>(x, none));
-  x = f(x, moved<0x114>(x, none));
-  x = f(x, moved<0x118>(x, none));
-  x = f(x, moved<0x142>(x, none));   // row_bcast 15, 31
-  x = f(x, moved<0x143>(x, none));
-  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
-}
-__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
-  return wave_reduce(x, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-}
-__device__ __forceinline__ uint32_t wave_umin(uint32_t x) {
-  return wave_reduce(x, 0xffffffffu, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-}
-__device__ __forceinline__ float wave_max(float x) {
-  return __uint_as_float(wave_reduce(__float_as_uint(x), 0xff800000u, [](uint32_t a, uint32_t b) {
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  }));
-}
-__device__ __forceinline__ float wave_sum(float x) {
-  return __uint_as_float(wave_reduce(__float_as_uint(x), 0u, [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
 }
 
 // A token's logits over a wave, V a lane: lane l holds experts q * 64 + l.
