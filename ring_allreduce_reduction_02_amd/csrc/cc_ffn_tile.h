@@ -294,13 +294,15 @@ __device__ __forceinline__ void sigmoid(float g, float& s, float& c) {
 __device__ __forceinline__ float normal_cdf(float g) { return 0.5f * erfcf(-g * 0.70710678118654752f); }
 
 // The same, and e = exp(-g^2 / 2), for results in bf16: 0.5 erfc(x / sqrt 2) = e P(t)
-// with t = 1 / (1 + 0.3 x), P the polynomial of degree 8 whose largest relative
-// error over x = 0 .. 14.5 is least (5.9e-8; by reweighted least squares on 2000
-// points); exp2 and the reciprocal are the hardware's.  Off by at most 10 half steps
-// of 1; below 0 by (1.5 g^2 + 16) 2^-24 of its value, 2^-15 at g = -13, below the
-// 2^-8 that the result is rounded by; below 2^-126 it may be 0.  (erfcf has two
-// branches, and a wave takes both: the 8-bit block of 16 experts of 2047 x 2047, 60.7k
-// rows, 1199 us with it, 1103 so; the checkpoint step of 2048 x 2048 4850 and 4640.)
+// with t = 1 / (1 + p x), the form of Hastings (Approximations for Digital Computers,
+// 1955).  P has degree 8, fitted here for p = 0.3 over x = 0 .. 14.5 by reweighted least
+// squares on 2000 points; with p and its coefficients in float32 it is off by at most
+// 1.2e-7 (2 half steps) of the value there.  exp2 and the reciprocal are the
+// hardware's.  Off by at most 10 half steps of 1; below 0 by (1.5 g^2 + 16) 2^-24 of its
+// value, 2^-15 at g = -13, below the 2^-8 that the result is rounded by; below 2^-126
+// it may be 0.  (erfcf has two branches, and a wave takes both: the 8-bit block of 16
+// experts of 2047 x 2047, 60.7k rows, 1199 us with it, 1103 so; the checkpoint step of
+// 2048 x 2048 4850 and 4640.)
 __device__ __forceinline__ float normal_cdf_bf16(float g, float& e) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, fabsf(g), 1.0f));
   e = __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f);
