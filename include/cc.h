@@ -754,8 +754,8 @@ cc_status_t cc_moe_matmul_int8_workspace_size(const size_t* counts, int nexperts
  * [2 * hidden][width] and w_out [width][hidden] int8 with a float32 scale a row,
  * s_in [2 * hidden] and s_out [width], one local expert after the other.  The kept
  * rows x are quantised as by cc_quantize_rows, g and u are the float32 products,
- * h = act(g) * u is rounded to dtype and its rows are quantised likewise.  width
- * and hidden below 2^17. */
+ * h = act(g) * u is rounded to dtype and its rows are quantised likewise (for bf16
+ * act is first computed to 2^-15 of its value, to 0 below 2^-126).  width and hidden below 2^17. */
 cc_status_t cc_moe_ffn_int8(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t s_in, cc_rankbuf_t w_out,
                             cc_rankbuf_t s_out, cc_rankbuf_t y, const size_t* counts, int nexperts, size_t capacity,
                             size_t width, size_t hidden, cc_act_t act, cc_dtype_t dtype, int nranks,
@@ -782,7 +782,9 @@ cc_status_t cc_moe_ffn_int8_workspace_size(const size_t* counts, int nexperts, s
  * e + 127 each (255: NaN), back to back.  Base and rank stride are multiples of
  * 16 bytes.  Rows behind a block's kept ones are neither read nor written; the
  * bytes between a row's parts mean nothing.
- * y, and every other argument, is that of cc_moe_ffn. */
+ * y, and every other argument, is that of cc_moe_ffn; in bf16 GELU is computed to
+ * 2^-15 of its value (to 0 below 2^-126) before h is rounded, so that an h may be
+ * the neighbour of the one there. */
 #define CC_CKPT_BLOCK 32
 cc_status_t cc_moe_ffn_checkpoint(cc_rankbuf_t x, cc_rankbuf_t w_in, cc_rankbuf_t w_out, cc_rankbuf_t ckpt,
                                   cc_rankbuf_t y, const size_t* counts, int nexperts, size_t capacity, size_t width,

@@ -114,9 +114,10 @@ __device__ __forceinline__ float exps(float* x) {
 // tokens and counts those that have any; the next group's logits are under way
 // meanwhile.  16 experts a lane: of 64, 4 lanes hold a token and each sum over
 // them takes 2 moves where a wave a token takes 6 (with 8-byte chunks and moves
-// through LDS 8.0 us where this takes 4.1).  Bound by the latency of a group's
-// loads and exponentials: 8 x 4096 tokens of 64 bf16 4.1 us, 1.0 TB/s; 3 x 1023 of
-// 61 float32 4.7.
+// through LDS 8.0 us where this takes 4.2).  Bound by the latency of a group's
+// loads and exponentials: 8 x 4096 tokens of 64 bf16 4.2 us (at best 3.9), 1.0 TB/s;
+// 3 x 1023 of 61 float32 5.3 (4.7); long batches by memory: 8 x 32768 of 256 bf16,
+// 134 MB, 28 us (26), 4.8 TB/s, float32 48, 5.6 TB/s.
 template <int DT, int L>
 __global__ __launch_bounds__(kBalanceBlock) void k_balance(BalArgs a) {
   constexpr int G = kBalanceBlock / L, C = L * kV;      // tokens at a time, columns
@@ -172,8 +173,9 @@ __global__ __launch_bounds__(kBalanceBlock) void k_balance(BalArgs a) {
 // The sums of a rank's workgroups (or of all ranks'), a workgroup: its threads
 // are C = 64 .. 1024 columns times 1024 / C parts of the rows.  One column's sums,
 // counts and loss then lie in the threads below C, whose waves are joined.  Bound by
-// the latency of a launch and of two rounds of loads: 4.7 us after 8 x 4096 tokens of
-// 64, 3.3 after 3 x 1023 of 61.
+// the latency of a launch and of its rounds of loads: 5.0 us (at best 4.6) after 8 x 4096
+// tokens of 64, 3.6 (3.3) after 3 x 1023 of 61, 10.4 (10.0) after 8 x 32768 of 256,
+// whose 512 rows of sums are 16 rounds.
 constexpr int kJoin = 1024;
 __global__ __launch_bounds__(kJoin) void k_balance_join(BalArgs a) {
   __shared__ float sum[kJoin];
@@ -249,8 +251,9 @@ __global__ __launch_bounds__(kJoin) void k_balance_join(BalArgs a) {
 
 // A group of tokens at a time as in the sums; f from the counts, once a workgroup.
 // Bound by memory from some megabytes on: 8 x 32768 tokens of 256 bf16, 268 MB in and
-// out, 53.6 us, 5.0 TB/s, its vector instructions 51% of the cycles; below that by
-// latency: 8 x 4096 of 64 float32 added to another gradient 7.1 us, 3.5 TB/s.
+// out, 54 us, 5.0 TB/s, its vector instructions 51% of the cycles, float32 91, 5.9 TB/s;
+// below that by latency: 8 x 4096 of 64 float32 added to another gradient 7.5 us (at
+// best 6.8), 3.4 TB/s.
 template <int DT, int L, bool BASE>
 __global__ __launch_bounds__(kBalanceBlock) void k_balance_grad(BalArgs a) {
   constexpr int G = kBalanceBlock / L;
@@ -317,6 +320,13 @@ int lanes_of(int E) {
 
 // Workgroups a rank: each takes `rounds` groups of tokens where there are enough
 // of them to leave `most` workgroups.
+// Measured, a pass in a graph.  Sums and join of 8 x 4096 tokens of 64 bf16 and
+// 3 x 1023 of 61 float32: with 1 round 8.9 and 6.6 us, 2 8.4 and 7.5, 4 9.9 and 9.4; of
+// 8 x 32768 of 256 and 32768 of 1024 bf16: with 256 workgroups in all 50 and 40, 512 38
+// and 44, 1024 43 and 65 (the join's one workgroup reads their sums).  Gradient of
+// 8 x 512, 4096 and 16384 tokens of 64 float32, added: with 1 round 4.3, 7.7 and 24.1, 2
+// 5.2, 7.7 and 22.9, 4 8.2, 11.1 and 23.6; of 8 x 32768 of 256 float32: 512 107, 1024 96,
+// 2048 91, 4096 89.
 uint32_t blocks_of(int N, uint64_t tokens, int E, uint32_t rounds, uint32_t most) {
   const uint64_t per = kBalanceBlock / lanes_of(E), groups = (tokens + per - 1) / per;
   const uint64_t each = std::max<uint64_t>(1, most / N);

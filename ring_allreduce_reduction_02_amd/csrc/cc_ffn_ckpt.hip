@@ -85,7 +85,8 @@ __device__ __forceinline__ void unpack_x(const XRows& a, uint64_t rank, uint32_t
   }
 }
 
-// Both are bound by memory: 60.7k rows of 2048 bf16 73 and 63 us, 5.2 and 6.0 TB/s.
+// Both are bound by memory: 60.7k rows of 2048 bf16 83 and 65 us, at best 73 and 63, 5.2
+// and 6.0 TB/s.
 // (In one kernel with the plan, whose counts lie in the host's memory, the whole
 // step of 64 to 32768 rows took 0-4% less where few rows, 0-2% more where many.)
 template <int DT, bool UNPACK>

@@ -80,8 +80,10 @@ inline FfnGrid ffn_grid(const FfnShape& s, int kind, uint64_t M, uint64_t cols, 
 // units idle.  Cost of equal areas, measured on all six products of 60.7k rows:
 // bf16 2048 x 2048 1, 1.21 and 1.92 (4.62, 5.62 and 8.87 ms), float32, whose
 // products take eight times as long, 1024 x 1024 1, 1 and 1.25 (9.79, 9.81 and
-// 12.24 ms; the weight gradients alone 1, 1 and 1.35, which is counted).  The
-// tiles through registers have the last two sizes.
+// 12.24 ms; the weight gradients alone 1, 1 and 1.35, which is counted).  8-bit
+// integers (element size 1) take bf16's: their product of 2048 x 4096 to bf16 1, 1.14
+// and 1.66 (591, 676 and 983 us), gate and up of 2048 x 2048 1, 1.19 and 1.77, down 1,
+// 1.24 and 1.78.  The tiles through registers have the last two sizes.
 inline int ffn_pick_tile(const FfnShape& s, int kind, uint64_t M, uint64_t cols, bool fast, int cus) {
   constexpr double kArea[2][kFfnTiles] = {{16.0, 4.0 * 1.21, 1.92}, {16.0, 4.0, 1.35}};
   const int first = fast ? 0 : 1;

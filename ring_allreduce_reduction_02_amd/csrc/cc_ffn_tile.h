@@ -14,7 +14,8 @@ namespace cc {
 // checkpoint, the hidden gradient from one, and 8-bit integers (summed in
 // int32; the rows of W or F bytes of cc_ffn_rule.h's element size 1).
 // The checkpoint's cost little beside the products: 16 experts of 2048 x 2048 bf16,
-// 60.7k rows, gate and up 1037 us (1028 that keep bf16), the hidden gradient 675 (639).
+// 60.7k rows, gate and up 1080 us, at best 1030 (1120-1180, 1020 that keep bf16), the
+// hidden gradient 700, 675 (660-680, 640).
 constexpr int K_GATEUP_CK = 5, K_DHID_CK = 6;
 constexpr bool is_gateup(int kind) { return kind == K_GATEUP || kind == K_GATEUP_CK; }
 constexpr bool is_dhid(int kind) { return kind == K_DHID || kind == K_DHID_CK; }
@@ -634,7 +635,7 @@ __device__ __forceinline__ void finish(const G& g, const Part& t, const f32x16 (
 // the column's scale, in float32.  The int32 sum is rounded once to float32, and
 // each scale's product once.
 // Gate and up of 16 experts of 2048 x 2048 (or a product of 4096 columns) for 60.7k
-// rows: 256 x 256 tiles 521-526 us, 1.9 POP/s, the matrix units 51% of the cycles, of
+// rows: 256 x 256 tiles 520-530 us at best, 1.9 POP/s, the matrix units 51% of the cycles, of
 // which this takes about a fifth: 429 us with the sums dropped, 503 with all but the
 // stores.  (128 x 128 tiles, two a unit at a time, 16% slower, 192 x 128 6%; scales
 // loaded before the products, stores through the caches: nothing gained.)
@@ -898,10 +899,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const RowSide& s, 
 
 // Two stages of whole 128-byte lines are in LDS (128 KiB of a 256 x 256 tile),
 // one barrier a stage.  Measured on 8 x 4096 tokens, top-2 of 16 experts,
-// 2048 x 2048 bf16 (60.7k rows): gate and up 1.04 ms (980 TFLOP/s), down 0.48-0.51
-// (1000-1060), hidden gradient 0.65 (780; it reads and writes 1.5 GB more), row
-// gradient 0.87 (1170), weight gradients 0.54 and 1.10 (930).  The matrix units
-// are busy 57, 60, 40, 64 and 49-51% of the cycles, at 1.6, 1.6, 1.9, 1.8 and 1.9
+// 2048 x 2048 bf16 (60.7k rows), at best: gate and up 1.02 ms (1000 TFLOP/s), down
+// 0.47-0.49 (1040-1080), hidden gradient 0.64 (790; it reads and writes 1.5 GB more), row
+// gradient 0.87 (1170), weight gradients 0.56 and 1.12-1.15 (890-910); on average 3-15%
+// more.  The matrix units are busy 57, 61, 41, 65 and 46-49% of the cycles, at 1.5-1.9
 // GHz: the card lowers its clock under this load.  With the loads left out a stage took 1.36 us, with loads that
 // hit the L2 1.58, as it is 1.95.
 // What else was tried there: four stages of 64-byte lines (twice the cache

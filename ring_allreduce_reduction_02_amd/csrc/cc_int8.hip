@@ -116,9 +116,10 @@ __device__ __forceinline__ void quantized_small(u32x4 in, float s, uint32_t* w) 
 }
 
 // A row by WPR waves (1 or 4), R vectors a lane in registers; longer rows (WPR 4)
-// are read twice.  Bound by memory: 81920 rows of 2048 bf16, 503 MB in and out, 82 us,
-// 6.1 TB/s; 60.7k kept rows 67 us, as many compact ones 57.  (With a branch to the
-// float64 quotient behind every element 150 and 168.)
+// are read twice.  Bound by memory: 81920 rows of 2048 bf16, 503 MB in and out, 90 us
+// (at best 79), 5.6 TB/s; 60.7k kept rows 76 (69), as many compact ones 59 (56); float32
+// 163 (153), 839 MB, 5.1 TB/s, 135 (125) and 116 (112).  (With a branch to the float64
+// quotient behind every element 150 and 168 for the first two.)
 template <int DT, int WPR, int R>
 __device__ __forceinline__ void quantize_row(const char* x, uint64_t width, char* q, uint64_t pitch, float* scale,
                                              int product, uint32_t* red) {
