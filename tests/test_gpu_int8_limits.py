@@ -31,3 +31,31 @@ def test_many_experts_of_many_columns(W, dtype):
         near(y.view(E, C)[e], want, (3.01 * U + HALF[dtype] * 1.01) * want.abs() + 1e-38, f"y of expert {e}")
         y.view(E, C)[e] = 7.0
     assert (y == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_block_of_many_experts(dtype):
+    """8192 experts of 3 x 65536, three with rows: what each of them gives alone, bit for bit."""
+    E, W, F, live = 8192, 3, 65536, [0, 4097, 8191]
+    say("8-bit block of many experts", dtype)
+    counts = [[int(e in live) for e in range(E)]]
+    g = gen(5)
+    q_in, s_in = torch.zeros(1, E * 2 * F * W, dtype=torch.int8, device=DEV), torch.zeros(1, E * 2 * F, device=DEV)
+    q_out, s_out = torch.zeros(1, E * W * F, dtype=torch.int8, device=DEV), torch.zeros(1, E * W, device=DEV)
+    x = torch.randn(1, E * W, generator=g, device=DEV).to(TORCH_DT[dtype])
+    for e in live:
+        for q, s, n in ((q_in, s_in, 2 * F * W), (q_out, s_out, W * F)):
+            q.view(E, n)[e] = torch.randint(-127, 128, (n,), generator=g, device=DEV, dtype=torch.int8)
+            s.view(E, -1)[e] = torch.rand(s.numel() // E, generator=g, device=DEV) * 0.01
+    y = torch.full((1, E * W), 7.0, dtype=TORCH_DT[dtype], device=DEV)
+    ccgpu.moe_ffn_int8(x, q_in, s_in, q_out, s_out, y, counts, 1, W, act="gelu",
+                       workspace=ccgpu.make_moe_ffn_int8_workspace(counts, 1, W, F, dtype))
+    torch.cuda.synchronize()
+    for e in live:
+        one = [t.view(E, -1)[e:e + 1].contiguous() for t in (x, q_in, s_in, q_out, s_out)]
+        alone = torch.zeros(1, W, dtype=TORCH_DT[dtype], device=DEV)
+        ccgpu.moe_ffn_int8(*one, alone, [[1]], 1, W, act="gelu", workspace=ccgpu.make_moe_ffn_int8_workspace([[1]], 1, W, F, dtype))
+        torch.cuda.synchronize()
+        assert torch.equal(alone[0], y.view(E, W)[e]) and alone.any()
+        y.view(E, W)[e] = 7.0
+    assert (y == 7.0).all()
